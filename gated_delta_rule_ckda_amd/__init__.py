@@ -14,7 +14,8 @@ import threading
 __all__ = ["chunk_fwd", "chunk_bwd", "chunk_bwd_workspace_size", "recurrent_step",
            "l2norm_debug", "fwd_supported",
            "library_path", "abi_version", "chunk_fwd_save", "CkdaError", "BF16", "F32", "GATE_KDA",
-           "GATE_CKDA", "GATES_F32", "GATES_LOGITS_F32", "GATES_LOGITS_BF16", "ChunkFwdPlan"]
+           "GATE_CKDA", "GATES_F32", "GATES_LOGITS_F32", "GATES_LOGITS_BF16", "ChunkFwdPlan",
+           "decay_fwd", "decay_bwd", "decay_step", "decay_supported"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = os.path.join(_HERE, "libckda.so")
@@ -42,6 +43,14 @@ class FwdDesc(ctypes.Structure):
                 ("gate_range", ctypes.c_int32), ("use_qk_l2norm", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("gate_input", ctypes.c_int32),
                 ("qk_heads", ctypes.c_int32), ("sign_absorb", ctypes.c_int32)]
+
+
+class DecayDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("gate_range", ctypes.c_int32),
+                ("gate_input", ctypes.c_int32), ("qk_heads", ctypes.c_int32),
+                ("alpha_per_head", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 def library_path() -> str:
@@ -88,6 +97,18 @@ def _load():
                                             vp, vp, vp, vp, vp, vp, vp, vp]
         lib.ckda_l2norm_debug.restype = i32
         lib.ckda_l2norm_debug.argtypes = [vp, vp, ctypes.c_int64, i32, i32, vp]
+        dd, sz = ctypes.POINTER(DecayDesc), ctypes.c_size_t
+        lib.ckda_decay_supported.restype = i32
+        lib.ckda_decay_supported.argtypes = [i32, i32]
+        for name in ("ckda_decay_fwd_workspace_size", "ckda_decay_bwd_workspace_size"):
+            getattr(lib, name).restype = sz
+            getattr(lib, name).argtypes = [dd, i32]
+        lib.ckda_decay_fwd.restype = i32
+        lib.ckda_decay_fwd.argtypes = [dd] + [vp] * 9 + [sz, vp]
+        lib.ckda_decay_bwd.restype = i32
+        lib.ckda_decay_bwd.argtypes = [dd] + [vp] * 14 + [sz, vp]
+        lib.ckda_decay_step.restype = i32
+        lib.ckda_decay_step.argtypes = [i32] * 9 + [f32] + [vp] * 8
         lib.ckda_status_string.restype = ctypes.c_char_p
         lib.ckda_status_string.argtypes = [i32]
         lib.ckda_last_error.restype = ctypes.c_char_p
@@ -417,3 +438,185 @@ def l2norm_debug(x, stream=None):
     _check(lib.ckda_l2norm_debug(_ptr(x), _ptr(y), x.numel() // d, d, _dtype_code(x),
                                  _stream(stream)))
     return y
+
+
+# ---- linear attention with one decay a head
+
+def _tensors(device, **named):
+    """Checks that every given tensor is contiguous on `device` (a GPU)."""
+    _require(device.type == "cuda", "tensors must be on a GPU, got %s" % device)
+    for name, t in named.items():
+        if t is not None:
+            _require(t.device == device, "%s is on %s, not on %s" % (name, t.device, device))
+            _require(t.is_contiguous(), "%s must be contiguous" % name)
+
+
+def _state_ok(name, t, shape):
+    import torch
+    if t is not None:
+        _require(t.dtype == torch.float32 and tuple(t.shape) == shape,
+                 "%s must be float32 of shape %s" % (name, list(shape)))
+
+
+class _on:
+    """The tensors' device made current for a call, and the stream it goes to:
+    the caller's, or that device's current one."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guard = torch.cuda.device(device)
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        import torch
+        self.guard.__enter__()
+        s = torch.cuda.current_stream(self.device) if self.stream is None else self.stream
+        _require(s.device == self.device, "the stream belongs to %s, the tensors to %s"
+                 % (s.device, self.device))
+        return ctypes.c_void_p(s.cuda_stream)
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale):
+    """The descriptor of a decay call, after the checks of its inputs' shapes and types."""
+    import torch
+    io = _dtype_code(q)
+    _require(k.dtype == q.dtype and v.dtype == q.dtype, "q, k, v must share a dtype")
+    lead = 1 if cu_seqlens is not None and q.dim() == 3 else 2
+    _require(q.dim() == lead + 2 and v.dim() == lead + 2,
+             "q and v must be [B,T,heads,d] (a packed batch may leave B out)")
+    _require(k.shape == q.shape, "k must match q")
+    _require(v.shape[:lead] == q.shape[:lead], "v must have the tokens of q")
+    H, Hk = v.shape[-2], q.shape[-2]
+    _require(Hk > 0 and H % Hk == 0, "the q/k heads must divide the value heads")
+    per_head = alpha.dim() == 1
+    _require(tuple(alpha.shape) == ((H,) if per_head else tuple(v.shape[:-1])),
+             "alpha must be [H] or one gate a token and head")
+    B, T = (1, q.shape[0]) if lead == 1 else (q.shape[0], q.shape[1])
+    n = B
+    if cu_seqlens is not None:
+        _require(cu_seqlens.dtype == torch.int32 and cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 1,
+                 "cu_seqlens must be an int32 vector")
+        _require(B == 1, "a packed batch has B = 1")
+        n = cu_seqlens.numel() - 1
+    return DecayDesc(B, T, H, q.shape[-1], v.shape[-1], n, io, _gate_code(gate),
+                     _gate_input(gates, alpha, alpha), Hk, int(per_head), float(scale))
+
+
+def _workspace(workspace, need, device):
+    import torch
+    if workspace is None:
+        return torch.empty(max(need, 1), device=device, dtype=torch.uint8)
+    _require(workspace.device == device and workspace.dtype == torch.uint8
+             and workspace.is_contiguous() and workspace.numel() >= need,
+             "workspace must be a uint8 tensor of at least %d bytes on %s" % (need, device))
+    return workspace
+
+
+def decay_supported(dk, dv) -> bool:
+    return bool(_load().ckda_decay_supported(dk, dv))
+
+
+def decay_fwd_workspace_size(desc: DecayDesc, packed: bool) -> int:
+    """Bytes of workspace ckda_decay_fwd needs for `desc` (0: none)."""
+    return int(_load().ckda_decay_fwd_workspace_size(ctypes.byref(desc), int(bool(packed))))
+
+
+def decay_bwd_workspace_size(desc: DecayDesc, packed: bool) -> int:
+    """Bytes of workspace ckda_decay_bwd needs for `desc`."""
+    return int(_load().ckda_decay_bwd_workspace_size(ctypes.byref(desc), int(bool(packed))))
+
+
+def decay_fwd(q, k, v, alpha, *, h0=None, cu_seqlens=None, gate="ckda", gates="values", scale=1.0,
+              output_final_state=True, out=None, final_state=None, workspace=None, stream=None):
+    """Linear attention with one decay a head, S_t = a_t S_{t-1} + k_t v_t^T and
+    o_t = scale S_t^T q_t, over whole prompts.  Dense: q, k [B,T,Hk,dk], v
+    [B,T,H,dv] (Hk divides H); packed (cu_seqlens int32 [N+1]): [1,T,...] or
+    [T,...].  alpha: [B,T,H], or [H] for a fixed decay; gates='values'
+    (float32) or 'logits' (float32 or bfloat16, activated by `gate`).
+    Returns (o, ht) with ht [N,H,dk,dv] float32 (None if not requested).  A
+    workspace that the caller passes must not be shared by calls that overlap."""
+    import torch
+    lib = _load()
+    desc = _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale)
+    dev = q.device
+    _tensors(dev, q=q, k=k, v=v, alpha=alpha, h0=h0, cu_seqlens=cu_seqlens, out=out,
+             final_state=final_state)
+    shape = (desc.num_seqs, desc.H, desc.dk, desc.dv)
+    _state_ok("h0", h0, shape)
+    _state_ok("final_state", final_state, shape)
+    if out is not None:
+        _require(out.dtype == v.dtype and out.shape == v.shape, "out must match v")
+    o = torch.empty_like(v) if out is None else out
+    ht = final_state
+    if output_final_state and ht is None:
+        ht = torch.empty(shape, device=dev, dtype=torch.float32)
+    need = decay_fwd_workspace_size(desc, cu_seqlens is not None)
+    with _on(dev, stream) as s:
+        ws = _workspace(workspace, need, dev) if need else workspace
+        _check(lib.ckda_decay_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha),
+                                  _ptr(cu_seqlens), _ptr(h0), _ptr(o), _ptr(ht), _ptr(ws),
+                                  0 if ws is None else ws.numel(), s))
+    return o, ht
+
+
+def decay_bwd(q, k, v, alpha, dout, *, h0=None, dht=None, cu_seqlens=None, gate="ckda",
+              gates="values", scale=1.0, output_dalpha=True, output_dh0=True, workspace=None,
+              stream=None):
+    """Gradients of decay_fwd for dL/do = dout and dL/dht = dht (None for zero).
+    Returns (dq, dk, dv, dalpha, dh0): the first four in q's dtype, shaped like
+    q, k, v and alpha (with logits, the gradient of the logits; with [H], the
+    sum over all tokens), dh0 [N,H,dk,dv] float32; dalpha and dh0 None unless
+    requested."""
+    import torch
+    lib = _load()
+    desc = _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale)
+    dev = q.device
+    _tensors(dev, q=q, k=k, v=v, alpha=alpha, dout=dout, h0=h0, dht=dht, cu_seqlens=cu_seqlens)
+    shape = (desc.num_seqs, desc.H, desc.dk, desc.dv)
+    _state_ok("h0", h0, shape)
+    _state_ok("dht", dht, shape)
+    _require(dout.dtype == v.dtype and dout.shape == v.shape, "dout must match v")
+    dq, dkk, dvv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dal = torch.empty(alpha.shape, device=dev, dtype=q.dtype) if output_dalpha else None
+    dh0 = torch.empty(shape, device=dev, dtype=torch.float32) if output_dh0 else None
+    need = decay_bwd_workspace_size(desc, cu_seqlens is not None)
+    with _on(dev, stream) as s:
+        ws = _workspace(workspace, need, dev)
+        _check(lib.ckda_decay_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha),
+                                  _ptr(cu_seqlens), _ptr(h0), _ptr(dout), _ptr(dht), _ptr(dq),
+                                  _ptr(dkk), _ptr(dvv), _ptr(dal), _ptr(dh0), _ptr(ws), ws.numel(),
+                                  s))
+    return dq, dkk, dvv, dal, dh0
+
+
+def decay_step(q, k, v, alpha, state, *, gate="ckda", gates="values", scale=1.0, out=None,
+               new_state=None, stream=None):
+    """One token a sequence of decay_fwd's recurrence: q, k [N,Hk,dk], v
+    [N,H,dv], alpha [N,H] or [H], state [N,H,dk,dv] float32, updated in place
+    unless new_state is given.  Returns o [N,H,dv]."""
+    import torch
+    lib = _load()
+    _require(q.dim() == 3 and v.dim() == 3, "q and v must be [N,heads,d]")
+    N, Hk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    _require(k.dtype == q.dtype and v.dtype == q.dtype, "q, k, v must share a dtype")
+    _require(k.shape == q.shape and v.shape[0] == N, "shape mismatch")
+    per_head = alpha.dim() == 1
+    _require(tuple(alpha.shape) == ((H,) if per_head else (N, H)), "alpha must be [N,H] or [H]")
+    dev = q.device
+    _tensors(dev, q=q, k=k, v=v, alpha=alpha, state=state, out=out, new_state=new_state)
+    _state_ok("state", state, (N, H, dk, dv))
+    _state_ok("new_state", new_state, (N, H, dk, dv))
+    if out is not None:
+        _require(out.dtype == v.dtype and out.shape == v.shape, "out must match v")
+    o = torch.empty_like(v) if out is None else out
+    dst = state if new_state is None else new_state
+    with _on(dev, stream) as s:
+        _check(lib.ckda_decay_step(N, H, Hk, dk, dv, _dtype_code(q), _gate_code(gate),
+                                   _gate_input(gates, alpha, alpha), int(per_head), float(scale),
+                                   _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(state), _ptr(dst),
+                                   _ptr(o), s))
+    return o

@@ -536,3 +536,254 @@ ckda_status_t ckda_l2norm_debug(const void* x, float* y, int64_t rows, int32_t d
 }
 
 }  // extern "C"
+
+// ---- decay linear attention ------------------------------------------------
+namespace {
+
+// The tensors of one decay call, for the checks of alignment and overlap.
+struct Tensor {
+  Range r;
+  bool out;      // written
+  bool needed;   // may not be NULL
+};
+
+// Every tensor aligned and given where needed; no output overlaps an input or
+// another output, but for the pair (same_a, same_b), which may be one buffer.
+ckda_status_t check_tensors(const Tensor* ts, int n, int same_a = -1, int same_b = -1) {
+  for (int i = 0; i < n; ++i) {
+    if (ts[i].needed && ts[i].r.lo == 0)
+      return fail(CKDA_ERR_INVALID_ARGUMENT, "%s must not be NULL", ts[i].r.name);
+    if ((ts[i].r.lo & 15u) != 0)
+      return fail(CKDA_ERR_INVALID_ARGUMENT, "%s is not 16-byte aligned", ts[i].r.name);
+  }
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < n; ++j) {
+      if (!ts[i].out || i == j || (ts[j].out && j < i)) continue;
+      if (ts[i].r.lo == 0 || ts[j].r.lo == 0 || !overlap(ts[i].r, ts[j].r)) continue;
+      if (((i == same_a && j == same_b) || (i == same_b && j == same_a)) && ts[i].r.lo == ts[j].r.lo)
+        continue;
+      return fail(CKDA_ERR_INVALID_ARGUMENT, "%s overlaps %s", ts[i].r.name, ts[j].r.name);
+    }
+  return ok();
+}
+
+ckda_status_t check_workspace(const Tensor* ts, int n, const void* ws, size_t bytes, size_t need) {
+  if (need == 0) return ok();
+  if (!ws) return fail(CKDA_ERR_INVALID_ARGUMENT, "workspace is NULL (%zu bytes needed)", need);
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "workspace is not 256-byte aligned");
+  if (bytes < need)
+    return fail(CKDA_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, %zu needed", bytes, need);
+  const Range rw = range("workspace", ws, static_cast<int64_t>(need));
+  for (int i = 0; i < n; ++i)
+    if (ts[i].r.lo != 0 && overlap(rw, ts[i].r))
+      return fail(CKDA_ERR_INVALID_ARGUMENT, "workspace overlaps %s", ts[i].r.name);
+  return ok();
+}
+
+bool valid_decay_sizes(const ckda_decay_desc_t* d) {
+  return d->B > 0 && d->T >= 0 && d->H > 0 && d->dk > 0 && d->dv > 0 && d->num_seqs >= 0 &&
+         (d->io_dtype == CKDA_DTYPE_BF16 || d->io_dtype == CKDA_DTYPE_F32) &&
+         valid_qk_heads(d->H, d->qk_heads) && valid_gate_input(d->gate_input);
+}
+
+ckda::DecayArgs decay_args(const ckda_decay_desc_t* d, const int32_t* cu) {
+  ckda::DecayArgs a{};
+  a.B = d->B;
+  a.T = d->T;
+  a.H = d->H;
+  a.Hk = qk_heads_of(d->H, d->qk_heads);
+  a.dk = d->dk;
+  a.dv = d->dv;
+  a.N = d->num_seqs;
+  a.gate_range = d->gate_range;
+  a.gate_input = d->gate_input;
+  a.per_head = d->alpha_per_head;
+  a.scale = d->scale;
+  a.cu = cu;
+  return a;
+}
+
+ckda_status_t validate_decay(const ckda_decay_desc_t* d, const int32_t* cu) {
+  if (!d) return fail(CKDA_ERR_INVALID_ARGUMENT, "desc is NULL");
+  if (d->B <= 0 || d->T < 0 || d->H <= 0 || d->dk <= 0 || d->dv <= 0 || d->num_seqs < 0)
+    return fail(CKDA_ERR_INVALID_ARGUMENT,
+                "non-positive size: B=%d T=%d H=%d dk=%d dv=%d num_seqs=%d", d->B, d->T, d->H,
+                d->dk, d->dv, d->num_seqs);
+  if (d->io_dtype != CKDA_DTYPE_BF16 && d->io_dtype != CKDA_DTYPE_F32)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "io_dtype %d is not a ckda_dtype_t", d->io_dtype);
+  if (d->gate_range != CKDA_GATE_KDA && d->gate_range != CKDA_GATE_CKDA)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "gate_range %d is not a ckda_gate_t", d->gate_range);
+  if (!valid_gate_input(d->gate_input))
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "gate_input %d is not a ckda_gate_input_t", d->gate_input);
+  if (d->alpha_per_head != 0 && d->alpha_per_head != 1)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "alpha_per_head must be 0 or 1");
+  if (!valid_qk_heads(d->H, d->qk_heads))
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "qk_heads %d does not divide H=%d", d->qk_heads, d->H);
+  if (cu) {
+    if (d->B != 1)
+      return fail(CKDA_ERR_INVALID_ARGUMENT, "cu_seqlens given with B=%d (must be 1)", d->B);
+    if ((reinterpret_cast<uintptr_t>(cu) & 3u) != 0)
+      return fail(CKDA_ERR_INVALID_ARGUMENT, "cu_seqlens is not 4-byte aligned");
+  } else if (d->num_seqs != d->B) {
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "num_seqs=%d must equal B=%d without cu_seqlens",
+                d->num_seqs, d->B);
+  }
+  if (!ckda::decay_supported(d->dk, d->dv))
+    return fail(CKDA_ERR_UNSUPPORTED, "no decay kernel for dk=%d dv=%d (multiples of 8 up to 128)",
+                d->dk, d->dv);
+  if (static_cast<int64_t>(d->B) * d->T >= (int64_t(1) << 31) ||
+      ckda::decay_grid(decay_args(d, cu), d->io_dtype) >= (int64_t(1) << 31))
+    return fail(CKDA_ERR_UNSUPPORTED, "too many (sequence, head) chunks for one launch");
+  return ok();
+}
+
+struct DecaySizes {
+  int64_t tokens, qk, vo, alpha, state;  // elements, elements, elements, bytes, bytes
+  int64_t es;
+};
+DecaySizes decay_sizes(const ckda_decay_desc_t* d) {
+  DecaySizes z;
+  z.tokens = static_cast<int64_t>(d->B) * d->T;
+  z.es = elem_bytes(d->io_dtype);
+  z.qk = z.tokens * qk_heads_of(d->H, d->qk_heads) * d->dk;
+  z.vo = z.tokens * d->H * d->dv;
+  z.alpha = (d->alpha_per_head ? 1 : z.tokens) * d->H * gate_bytes(d->gate_input);
+  z.state = static_cast<int64_t>(d->num_seqs) * d->H * d->dk * d->dv * 4;
+  return z;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t ckda_decay_supported(int32_t dk, int32_t dv) { return ckda::decay_supported(dk, dv) ? 1 : 0; }
+
+size_t ckda_decay_fwd_workspace_size(const ckda_decay_desc_t* d, int32_t packed) {
+  if (!d || !valid_decay_sizes(d) || !ckda::decay_supported(d->dk, d->dv) || d->num_seqs == 0) return 0;
+  static const int32_t given = 0;  // only whether the batch is packed matters here
+  return ckda::decay_segment_bytes(decay_args(d, packed ? &given : nullptr));
+}
+
+size_t ckda_decay_bwd_workspace_size(const ckda_decay_desc_t* d, int32_t packed) {
+  if (!d || !valid_decay_sizes(d) || !ckda::decay_supported(d->dk, d->dv) || d->num_seqs == 0) return 0;
+  static const int32_t given = 0;
+  return ckda::decay_bwd_workspace(decay_args(d, packed ? &given : nullptr), d->io_dtype);
+}
+
+ckda_status_t ckda_decay_fwd(const ckda_decay_desc_t* d, const void* q, const void* k, const void* v,
+                             const void* alpha, const int32_t* cu_seqlens, const float* h0, void* o,
+                             float* ht, void* workspace, size_t workspace_bytes, void* stream) {
+  ckda_status_t st = validate_decay(d, cu_seqlens);
+  if (st != CKDA_OK) return st;
+  const DecaySizes z = decay_sizes(d);
+  const bool some = z.tokens > 0;
+  const Tensor ts[] = {{range("q", q, q ? z.qk * z.es : 0), false, some},
+                       {range("k", k, k ? z.qk * z.es : 0), false, some},
+                       {range("v", v, v ? z.vo * z.es : 0), false, some},
+                       {range("alpha", alpha, alpha ? z.alpha : 0), false, some},
+                       {range("h0", h0, h0 ? z.state : 0), false, false},
+                       {range("o", o, o ? z.vo * z.es : 0), true, some},
+                       {range("ht", ht, ht ? z.state : 0), true, false}};
+  if ((st = check_tensors(ts, 7, 4, 6)) != CKDA_OK) return st;
+  if (cu_seqlens) {
+    const Range rc = range("cu_seqlens", cu_seqlens, 4 * (static_cast<int64_t>(d->num_seqs) + 1));
+    for (int i = 5; i < 7; ++i)
+      if (overlap(ts[i].r, rc))
+        return fail(CKDA_ERR_INVALID_ARGUMENT, "%s overlaps cu_seqlens", ts[i].r.name);
+  }
+  const size_t need = ckda_decay_fwd_workspace_size(d, cu_seqlens ? 1 : 0);
+  if ((st = check_workspace(ts, 7, workspace, workspace_bytes, need)) != CKDA_OK) return st;
+  if (d->num_seqs == 0) return ok();
+  ckda::DecayArgs a = decay_args(d, cu_seqlens);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.alpha = alpha;
+  a.h0 = h0;
+  a.o = o;
+  a.ht = ht;
+  return from_hip(ckda::launch_decay_fwd(a, d->io_dtype, workspace, static_cast<hipStream_t>(stream)));
+}
+
+ckda_status_t ckda_decay_bwd(const ckda_decay_desc_t* d, const void* q, const void* k, const void* v,
+                             const void* alpha, const int32_t* cu_seqlens, const float* h0,
+                             const void* dout, const float* dht, void* dq, void* dk, void* dv,
+                             void* dalpha, float* dh0, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  ckda_status_t st = validate_decay(d, cu_seqlens);
+  if (st != CKDA_OK) return st;
+  const DecaySizes z = decay_sizes(d);
+  const bool some = z.tokens > 0;
+  const int64_t da = (d->alpha_per_head ? 1 : z.tokens) * d->H * z.es;
+  const Tensor ts[] = {{range("q", q, q ? z.qk * z.es : 0), false, some},
+                       {range("k", k, k ? z.qk * z.es : 0), false, some},
+                       {range("v", v, v ? z.vo * z.es : 0), false, some},
+                       {range("alpha", alpha, alpha ? z.alpha : 0), false, some},
+                       {range("h0", h0, h0 ? z.state : 0), false, false},
+                       {range("dout", dout, dout ? z.vo * z.es : 0), false, some},
+                       {range("dht", dht, dht ? z.state : 0), false, false},
+                       {range("dq", dq, dq ? z.qk * z.es : 0), true, some},
+                       {range("dk", dk, dk ? z.qk * z.es : 0), true, some},
+                       {range("dv", dv, dv ? z.vo * z.es : 0), true, some},
+                       {range("dalpha", dalpha, dalpha ? da : 0), true, false},
+                       {range("dh0", dh0, dh0 ? z.state : 0), true, false}};
+  if ((st = check_tensors(ts, 12)) != CKDA_OK) return st;
+  if (cu_seqlens) {
+    const Range rc = range("cu_seqlens", cu_seqlens, 4 * (static_cast<int64_t>(d->num_seqs) + 1));
+    for (int i = 7; i < 12; ++i)
+      if (overlap(ts[i].r, rc))
+        return fail(CKDA_ERR_INVALID_ARGUMENT, "%s overlaps cu_seqlens", ts[i].r.name);
+  }
+  const size_t need = ckda_decay_bwd_workspace_size(d, cu_seqlens ? 1 : 0);
+  if ((st = check_workspace(ts, 12, workspace, workspace_bytes, need)) != CKDA_OK) return st;
+  if (d->num_seqs == 0) return ok();
+  ckda::DecayArgs a = decay_args(d, cu_seqlens);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.alpha = alpha;
+  a.h0 = h0;
+  ckda::DecayGrads g{dout, dht, dq, dk, dv, dalpha, dh0, nullptr};
+  return from_hip(ckda::launch_decay_bwd(a, g, d->io_dtype, workspace, static_cast<hipStream_t>(stream)));
+}
+
+ckda_status_t ckda_decay_step(int32_t N, int32_t H, int32_t qk_heads, int32_t dk, int32_t dv,
+                              int32_t io_dtype, int32_t gate_range, int32_t gate_input,
+                              int32_t alpha_per_head, float scale, const void* q, const void* k,
+                              const void* v, const void* alpha, const float* h0, float* ht, void* o,
+                              void* stream) {
+  if (N < 0 || H <= 0 || dk <= 0 || dv <= 0)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "bad size: N=%d H=%d dk=%d dv=%d", N, H, dk, dv);
+  // one token a sequence is a dense batch of N sequences of one token
+  const ckda_decay_desc_t d{N > 0 ? N : 1, 1, H, dk, dv, N > 0 ? N : 1, io_dtype, gate_range,
+                            gate_input, qk_heads, alpha_per_head, scale};
+  ckda_status_t st = validate_decay(&d, nullptr);
+  if (st != CKDA_OK) return st;
+  const int64_t nh = static_cast<int64_t>(N) * H;
+  if (nh > (int64_t(1) << 21))
+    return fail(CKDA_ERR_UNSUPPORTED, "N*H = %lld exceeds 2^21 for one decode launch",
+                static_cast<long long>(nh));
+  const DecaySizes z = decay_sizes(&d);
+  const bool some = N > 0;
+  const Tensor ts[] = {{range("q", q, z.qk * z.es), false, some},
+                       {range("k", k, z.qk * z.es), false, some},
+                       {range("v", v, z.vo * z.es), false, some},
+                       {range("alpha", alpha, z.alpha), false, some},
+                       {range("h0", h0, z.state), false, some},
+                       {range("o", o, z.vo * z.es), true, some},
+                       {range("ht", ht, z.state), true, some}};
+  if ((st = check_tensors(ts, 7, 4, 6)) != CKDA_OK) return st;
+  if (N == 0) return ok();
+  ckda::DecayArgs a = decay_args(&d, nullptr);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.alpha = alpha;
+  a.h0 = h0;
+  a.o = o;
+  a.ht = ht;
+  return from_hip(ckda::launch_decay_step(a, io_dtype, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -186,6 +186,55 @@ size_t bwd_gates_extra_bytes(int32_t B, int32_t T, int32_t H, int32_t Hk, int32_
 launch_result launch_bwd_full(BwdArgs b, int32_t io_dtype, void* ws, size_t core_bytes,
                               hipStream_t stream, bool recompute = true);
 
+// Decay linear attention (decay.hip, decay_bwd.hip): S_t = a_t S_{t-1} + k_t v_t^T,
+// o_t = scale S_t^T q_t.
+struct DecayArgs {
+  int32_t B, T, H, Hk, dk, dv, N;
+  int32_t gate_range;  // ckda_gate_t
+  int32_t gate_input;  // ckda_gate_input_t
+  int32_t per_head;    // alpha is [H], not [B][T][H]
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* alpha;
+  const int32_t* cu;   // null for a dense batch
+  const float* h0;     // state entering a sequence (the adjoint leaving it, backwards) or null
+  void* o;
+  float* ht;           // state leaving a sequence (the adjoint entering it, backwards) or null
+  // segments of a sequence's chunks run side by side (seg = 0: one a sequence)
+  int32_t seg;         // tokens of a segment, a multiple of the chunk
+  int32_t slots;       // segment slots over all sequences
+  float* entry;        // [slots][H][dk][dv] the state entering a segment
+  float* gain;         // [slots][H] the product of a segment's gates
+  // records of the backward: one a chunk
+  int32_t cslots;      // chunk slots over all sequences
+  void* states;        // [cslots][H][dk][dv] state entering a chunk (io type)
+  void* adjoints;      // [cslots][H][dk][dv] adjoint of the state leaving it (io type)
+  float* dots;         // [cslots][H][nslab] partial sums of <adjoint, entry state>
+};
+bool decay_supported(int32_t dk, int32_t dv);
+// Workspace bytes of the forward, 0 where sequences are not cut.
+size_t decay_segment_bytes(const DecayArgs& a);
+// Workgroups of the largest launch these sizes need (forward or backward).
+int64_t decay_grid(const DecayArgs& a, int32_t io_dtype);
+launch_result launch_decay_fwd(DecayArgs a, int32_t io_dtype, void* ws, hipStream_t s);
+launch_result launch_decay_step(const DecayArgs& a, int32_t io_dtype, hipStream_t s);
+// Backward: gradients in the io type, dalpha shaped like alpha.
+struct DecayGrads {
+  const void* dout;
+  const float* dht;
+  void* dq;
+  void* dk;
+  void* dv;
+  void* dalpha;   // null: not wanted
+  float* dh0;     // null: not wanted
+  float* per_token;  // [B*T][H] gate gradients before their sum (one gate a head)
+};
+size_t decay_bwd_workspace(const DecayArgs& a, int32_t io_dtype);
+launch_result launch_decay_bwd(const DecayArgs& a, DecayGrads g, int32_t io_dtype, void* ws,
+                               hipStream_t s);
+
 // ---- small device helpers shared by the kernels --------------------------
 
 // bf16 <-> f32.  Conversion to bf16 rounds to nearest even (finite inputs).

@@ -1,0 +1,660 @@
+// Decay linear attention: the chunked forward, the state passes that the
+// backward and long prompts run, and the single-token step.
+//
+//     S_t = a_t S_{t-1} + k_t v_t^T,     o_t = scale S_t^T q_t
+#include "decay_ops.h"
+
+namespace ckda {
+namespace {
+
+constexpr int kNT = 256;  // 4 waves
+
+// ---- forward -------------------------------------------------------------------
+// One workgroup walks one (segment, head) over its chunks for DVS columns of
+// the state, which stays in the matrix accumulators in float32; per chunk
+//
+//   P^T = K Q^T                  wave w: the 16 tokens 16w.. of Q
+//   O^T = S^T Q^T E + V^T (P D)^T
+//   S   = g S + K^T (W V)        wave w: DKP/4 rows of S
+//
+// P^T leaves the accumulators as the next product's operand.  K, V and a copy
+// of S in the io type pass through LDS; the next chunk's rows are loaded into
+// registers while this one is computed.
+template <class Op, int DKP, int DVS>
+struct FwdCfg {
+  using T = typename Op::T;
+  static constexpr int C = kDecayChunk, ES = sizeof(T);
+  static constexpr int LDK = frag_stride(DKP, ES), LDV = cross_stride(DVS, ES);
+  static constexpr int O_K = 0, O_V = O_K + C * LDK * ES, O_H = O_V + C * LDV * ES,
+                       O_L = O_H + C * LDV * ES, O_S = O_L + (Fr<Op>::kSplit ? C * LDV * ES : 0),
+                       O_G = align16(O_S + DVS * LDK * ES),
+                       BYTES = O_G + 2 * static_cast<int>(sizeof(Gates<C>));
+};
+
+template <class Op, int DKP, int DVS>
+__global__ __launch_bounds__(kNT, 2) void decay_fwd_kernel(DecayArgs a) {
+  using Cfg = FwdCfg<Op, DKP, DVS>;
+  using X = Fr<Op>;
+  using T = typename Op::T;
+  using F = typename X::F;
+  constexpr int C = Cfg::C, LDK = Cfg::LDK, LDV = Cfg::LDV, KS = X::KS;
+  constexpr int NQ = DKP / KS, MT = DKP / 64, NTL = DVS / 16, EPP = 16 / sizeof(T);
+  extern __shared__ __align__(16) unsigned char smem[];
+  T* sK = reinterpret_cast<T*>(smem + Cfg::O_K);
+  T* sV = reinterpret_cast<T*>(smem + Cfg::O_V);
+  T* sH = reinterpret_cast<T*>(smem + Cfg::O_H);
+  T* sL = reinterpret_cast<T*>(smem + Cfg::O_L);
+  T* sS = reinterpret_cast<T*>(smem + Cfg::O_S);
+  Gates<C>* sG = reinterpret_cast<Gates<C>*>(smem + Cfg::O_G);
+
+  const int t = threadIdx.x, lane = t & 63, w = uniform32(t >> 6), l16 = lane & 15, lq = lane >> 4;
+  const int nslab = (a.dv + DVS - 1) / DVS;
+  int64_t chain;
+  int slab;
+  item_of(blockIdx.x, gridDim.x, nslab, chain, slab);
+  const int slot = static_cast<int>(chain / a.H), h = static_cast<int>(chain % a.H);
+  Piece pc;
+  if (a.seg > 0) {
+    pc = piece_of(a, slot, a.seg, lane);
+    if (pc.n < 0) return;
+  } else {
+    const Seq s = sequence(a, slot);
+    pc = Piece{slot, 0, 1, s.begin, s.len};
+  }
+  const int hk = h / (a.H / a.Hk), c0 = slab * DVS;
+  const int vcols = a.dv - c0 < DVS ? a.dv - c0 : DVS;
+  const int64_t ldq = static_cast<int64_t>(a.Hk) * a.dk, ldv = static_cast<int64_t>(a.H) * a.dv;
+  const T* gq = static_cast<const T*>(a.q) + pc.begin * ldq + static_cast<int64_t>(hk) * a.dk;
+  const T* gk = static_cast<const T*>(a.k) + pc.begin * ldq + static_cast<int64_t>(hk) * a.dk;
+  const T* gv = static_cast<const T*>(a.v) + pc.begin * ldv + static_cast<int64_t>(h) * a.dv + c0;
+  T* go = static_cast<T*>(a.o) + pc.begin * ldv + static_cast<int64_t>(h) * a.dv + c0;
+  const bool ckda = a.gate_range == CKDA_GATE_CKDA;
+  const int nch = (pc.len + C - 1) / C;
+
+  // state tile (m, n): rows dk = row0 + 16 m + 4 lq + i, column c0 + 16 n + l16
+  const int row0 = w * (DKP / 4);
+  const int64_t sbase = (static_cast<int64_t>(pc.n) * a.H + h) * a.dk * a.dv;
+  f32x4 S[MT][NTL];
+  {
+    const float* src = a.seg > 0 ? a.entry + (static_cast<int64_t>(slot) * a.H + h) * a.dk * a.dv
+                                 : (a.h0 ? a.h0 + sbase : nullptr);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = row0 + 16 * m + 4 * lq + i, c = 16 * n + l16;
+          S[m][n][i] = src && r < a.dk && c < vcols ? src[static_cast<int64_t>(r) * a.dv + c0 + c] : 0.f;
+        }
+  }
+  auto stage_state = [&]() {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n)
+        Op::store4(sS + (16 * n + l16) * LDK + row0 + 16 * m + 4 * lq, S[m][n]);
+  };
+
+  RowTile<T, C, DKP, kNT> rk;
+  RowTile<T, C, DVS, kNT> rv;
+  uint4 rq[NQ];
+  auto load_chunk = [&](int c) {
+    const int rows = pc.len - c * C;  // <= 0 past the last chunk: zeros, no loads
+    const int64_t o = static_cast<int64_t>(c) * C;
+    rk.load(gk + o * ldq, ldq, rows, a.dk, t);
+    rv.load(gv + o * ldv, ldv, rows, vcols, t);
+    const int r = 16 * w + l16;
+#pragma unroll
+    for (int s = 0; s < NQ; ++s) {
+      const int c8 = KS * s + EPP * lq;
+      rq[s] = make_uint4(0, 0, 0, 0);
+      if (r < rows && c8 < a.dk) rq[s] = *reinterpret_cast<const uint4*>(gq + (o + r) * ldq + c8);
+    }
+  };
+  auto load_gate = [&](int c) {
+    const int i = c * C + lane;
+    return i < pc.len ? gate_stored(a, pc.begin + i, h) : 0.f;
+  };
+  auto stage_rows = [&](const Gates<C>& G) {
+    rk.store(sK, LDK, t);
+    rv.store(sV, LDV, t);
+    using RV = RowTile<T, C, DVS, kNT>;
+#pragma unroll
+    for (int u = 0; u < RV::NP; ++u) {
+      const int p = t + kNT * u, row = p / RV::PPR, c = (p % RV::PPR) * RV::EPP;
+      store_scaled<T>(rv.r[u], G.W[row], sH + row * LDV + c, sL + row * LDV + c);
+    }
+  };
+
+  if (nch > 0) {
+    load_chunk(0);
+    if (w == 0) gates_fill<C>(sG[0], load_gate(0), lane < pc.len, a.gate_input, ckda, lane);
+    stage_state();
+    __syncthreads();
+    stage_rows(sG[0]);
+  }
+  F fq[NQ];
+  for (int c = 0; c < nch; ++c) {
+#pragma unroll
+    for (int s = 0; s < NQ; ++s) fq[s] = *reinterpret_cast<const F*>(&rq[s]);
+    load_chunk(c + 1);
+    const bool gw = w == ((c + 1) & 3);
+    float xg = 0.f;
+    if (gw) xg = load_gate(c + 1);
+    __syncthreads();  // rows, state copy and gates of chunk c are in LDS
+    const Gates<C>& G = sG[c & 1];
+    const float g = G.g;
+    const bool fast = G.fast != 0;
+    const int r = 16 * w + l16;
+
+    f32x4 p[C / 16];
+#pragma unroll
+    for (int j = 0; j < C / 16; ++j) {
+      p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (j <= w) {
+        const T* rowk = sK + (16 * j + l16) * LDK;
+#pragma unroll
+        for (int s = 0; s < NQ; ++s) Op::mma(p[j], X::row(rowk, s, lq), fq[s]);
+        const int j0 = 16 * j + 4 * lq;
+        if (fast) {
+          const f32x4 ej = *reinterpret_cast<const f32x4*>(&G.ej[j0]);
+          const float er = G.er[r];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[j][i] = j0 + i <= r ? (p[j][i] * er) * ej[i] : 0.f;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float d = d_slow(G, r, j0 + i);
+            p[j][i] = d != 0.f ? p[j][i] * d : 0.f;  // nothing passes a zero gate
+          }
+        }
+      }
+    }
+    F pf[C / KS];
+    Op::template frags<C>(pf, p);
+
+    f32x4 o[NTL];
+    const float e = G.E[r];
+#pragma unroll
+    for (int n = 0; n < NTL; ++n) {
+      o[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const T* rows = sS + (16 * n + l16) * LDK;
+#pragma unroll
+      for (int s = 0; s < NQ; ++s) Op::mma(o[n], X::row(rows, s, lq), fq[s]);
+      o[n] *= e;
+    }
+#pragma unroll
+    for (int ks = 0; ks < C / KS; ++ks)
+      if (KS * ks <= 16 * w) {
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) Op::mma(o[n], X::across(sV, LDV, KS * ks, 16 * n, lane), pf[ks]);
+      }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) S[m][n] *= g;
+#pragma unroll
+    for (int ks = 0; ks < C / KS; ++ks) {
+      F vh[NTL], vl[NTL];
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) {
+        vh[n] = X::across(sH, LDV, KS * ks, 16 * n, lane);
+        if constexpr (X::kSplit) vl[n] = X::across(sL, LDV, KS * ks, 16 * n, lane);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const F ka = X::across(sK, LDK, KS * ks, row0 + 16 * m, lane);
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) {
+          Op::mma(S[m][n], ka, vh[n]);
+          if constexpr (X::kSplit) Op::mma(S[m][n], ka, vl[n]);
+        }
+      }
+    }
+    const int row = c * C + r;
+    if (row < pc.len) {
+      T* dst = go + row * ldv;
+#pragma unroll
+      for (int n = 0; n < NTL; ++n)
+        if (16 * n + 4 * lq < vcols) Op::store4(dst + 16 * n + 4 * lq, o[n] * a.scale);
+    }
+    if (gw) gates_fill<C>(sG[(c + 1) & 1], xg, (c + 1) * C + lane < pc.len, a.gate_input, ckda, lane);
+    __syncthreads();  // chunk c is done with LDS; gates of chunk c + 1 are there
+    stage_state();
+    stage_rows(sG[(c + 1) & 1]);
+  }
+  if (a.ht && pc.s == pc.count - 1) {
+    float* dst = a.ht + sbase;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = row0 + 16 * m + 4 * lq + i, c = 16 * n + l16;
+          if (rr < a.dk && c < vcols) dst[static_cast<int64_t>(rr) * a.dv + c0 + c] = S[m][n][i];
+        }
+  }
+}
+
+// ---- state passes ---------------------------------------------------------------
+// The same walk without the read-out, in either direction:
+//   forward    S <- g S + sum_j k_j (W_j v_j)^T,              x = k, y = v
+//   backwards  S <- g S + sum_i q_i (scale E_i dout_i)^T,     x = q, y = dout,
+// over the chunks from the last to the first.  kSegment starts from zero and
+// leaves a segment's own sum and gate product (joined by decay_join_kernel);
+// kChunks starts from the segment's entry and keeps the state met at every
+// chunk in the io type (backwards with its product with the forward's one),
+// and the state at the end of the walk in float32.
+enum { kSegment = 0, kChunks = 1 };
+
+template <class Op, int DKP, int DVS, int C>
+struct StateCfg {
+  using T = typename Op::T;
+  static constexpr int ES = sizeof(T);
+  static constexpr int LDK = frag_stride(DKP, ES), LDV = cross_stride(DVS, ES);
+  static constexpr int O_K = 0, O_H = O_K + C * LDK * ES, O_L = O_H + C * LDV * ES,
+                       O_G = align16(O_L + (Fr<Op>::kSplit ? C * LDV * ES : 0)),
+                       O_R = O_G + 2 * static_cast<int>(sizeof(Gates<C>)), BYTES = O_R + 16;
+};
+
+template <class Op, int DKP, int DVS, int C, bool REV, int MODE>
+__global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
+  using Cfg = StateCfg<Op, DKP, DVS, C>;
+  using X = Fr<Op>;
+  using T = typename Op::T;
+  using F = typename X::F;
+  constexpr int LDK = Cfg::LDK, LDV = Cfg::LDV, KS = X::KS, MT = DKP / 64, NTL = DVS / 16;
+  extern __shared__ __align__(16) unsigned char smem[];
+  T* sK = reinterpret_cast<T*>(smem + Cfg::O_K);
+  T* sH = reinterpret_cast<T*>(smem + Cfg::O_H);
+  T* sL = reinterpret_cast<T*>(smem + Cfg::O_L);
+  Gates<C>* sG = reinterpret_cast<Gates<C>*>(smem + Cfg::O_G);
+  float* sR = reinterpret_cast<float*>(smem + Cfg::O_R);
+
+  const int t = threadIdx.x, lane = t & 63, w = uniform32(t >> 6), l16 = lane & 15, lq = lane >> 4;
+  const int nslab = (a.dv + DVS - 1) / DVS;
+  int64_t chain;
+  int slab;
+  item_of(blockIdx.x, gridDim.x, nslab, chain, slab);
+  const int slot = static_cast<int>(chain / a.H), h = static_cast<int>(chain % a.H);
+  Piece pc;
+  if (a.seg > 0) {
+    pc = piece_of(a, slot, a.seg, lane);
+    if (pc.n < 0) return;
+  } else {
+    const Seq s = sequence(a, slot);
+    pc = Piece{slot, 0, 1, s.begin, s.len};
+  }
+  // nobody enters a state after the walk's last segment
+  if (MODE == kSegment && pc.s == (REV ? 0 : pc.count - 1)) return;
+  const int hk = h / (a.H / a.Hk), c0 = slab * DVS;
+  const int vcols = a.dv - c0 < DVS ? a.dv - c0 : DVS;
+  const int64_t ldx = static_cast<int64_t>(a.Hk) * a.dk, ldy = static_cast<int64_t>(a.H) * a.dv;
+  const T* gx = static_cast<const T*>(REV ? a.q : a.k) + pc.begin * ldx + static_cast<int64_t>(hk) * a.dk;
+  const T* gy = static_cast<const T*>(REV ? a.o : a.v) + pc.begin * ldy + static_cast<int64_t>(h) * a.dv + c0;
+  const bool ckda = a.gate_range == CKDA_GATE_CKDA;
+  const int nch = (pc.len + C - 1) / C;
+
+  // tile (m, n) of S^T: column dk = row0 + 16 m + l16, rows dv = c0 + 16 n + 4 lq + i
+  const int row0 = w * (DKP / 4);
+  const int64_t seq_state = (static_cast<int64_t>(pc.n) * a.H + h) * a.dk * a.dv;
+  const int64_t seg_state = (static_cast<int64_t>(slot) * a.H + h) * a.dk * a.dv;
+  f32x4 S[MT][NTL];
+  const float* src = MODE == kSegment ? nullptr
+                     : (a.seg > 0 ? a.entry + seg_state : (a.h0 ? a.h0 + seq_state : nullptr));
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NTL; ++n) {
+      const int r = row0 + 16 * m + l16, c = 16 * n + 4 * lq;
+      S[m][n] = src && r < a.dk && c < vcols
+                    ? *reinterpret_cast<const f32x4*>(src + static_cast<int64_t>(r) * a.dv + c0 + c)
+                    : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  auto save = [&](float* dst) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) {
+        const int r = row0 + 16 * m + l16, c = 16 * n + 4 * lq;
+        if (r < a.dk && c < vcols)
+          *reinterpret_cast<f32x4*>(dst + static_cast<int64_t>(r) * a.dv + c0 + c) = S[m][n];
+      }
+  };
+
+  RowTile<T, C, DKP, kNT> rx;
+  RowTile<T, C, DVS, kNT> ry;
+  auto chunk_at = [&](int i) { return REV ? nch - 1 - i : i; };
+  auto load_chunk = [&](int i) {
+    const int c = chunk_at(i);
+    const int rows = i < nch ? pc.len - c * C : 0;
+    const int64_t o = static_cast<int64_t>(i < nch ? c : 0) * C;
+    rx.load(gx + o * ldx, ldx, rows, a.dk, t);
+    ry.load(gy + o * ldy, ldy, rows, vcols, t);
+  };
+  auto gate_ok = [&](int i) { return i < nch && lane < C && chunk_at(i) * C + lane < pc.len; };
+  auto load_gate = [&](int i) {
+    return gate_ok(i) ? gate_stored(a, pc.begin + chunk_at(i) * C + lane, h) : 0.f;
+  };
+  auto stage_rows = [&](const Gates<C>& G) {
+    rx.store(sK, LDK, t);
+    using RY = RowTile<T, C, DVS, kNT>;
+#pragma unroll
+    for (int u = 0; u < RY::NP; ++u) {
+      const int p = t + kNT * u, row = p / RY::PPR, c = (p % RY::PPR) * RY::EPP;
+      store_scaled<T>(ry.r[u], REV ? G.E[row] * a.scale : G.W[row], sH + row * LDV + c,
+                      sL + row * LDV + c);
+    }
+  };
+  int64_t cslot = 0;
+  if (MODE == kChunks) cslot = first_slot(a, pc.n, C) + (a.seg > 0 ? pc.s * (a.seg / C) : 0);
+
+  float gain = 1.f;
+  if (nch > 0) {
+    load_chunk(0);
+    if (w == 0) gates_fill<C>(sG[0], load_gate(0), gate_ok(0), a.gate_input, ckda, lane);
+    __syncthreads();
+    stage_rows(sG[0]);
+  }
+  for (int i = 0; i < nch; ++i) {
+    load_chunk(i + 1);
+    const bool gw = w == ((i + 1) & 3);
+    float xg = 0.f;
+    if (gw) xg = load_gate(i + 1);
+    if (MODE == kChunks) {  // the state met at this chunk
+      const int64_t rec = ((cslot + chunk_at(i)) * a.H + h) * a.dk * a.dv;
+      T* dst = static_cast<T*>(REV ? a.adjoints : a.states) + rec;
+      const T* fwd = static_cast<const T*>(a.states) + rec;
+      float dot = 0.f;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) {
+          const int r = row0 + 16 * m + l16, c = 16 * n + 4 * lq;
+          if (r < a.dk && c < vcols) {
+            const int64_t at = static_cast<int64_t>(r) * a.dv + c0 + c;
+            Op::store4(dst + at, S[m][n]);
+            if (REV) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) dot += S[m][n][e] * static_cast<float>(fwd[at + e]);
+            }
+          }
+        }
+      if (REV) {
+#pragma unroll
+        for (int mm = 32; mm >= 1; mm >>= 1) dot += __shfl_xor(dot, mm, 64);
+        if (lane == 0) sR[w] = dot;
+      }
+    }
+    __syncthreads();  // rows and gates of chunk i are in LDS
+    if (MODE == kChunks && REV && t == 0)
+      a.dots[((cslot + chunk_at(i)) * a.H + h) * nslab + slab] = (sR[0] + sR[1]) + (sR[2] + sR[3]);
+    const float g = sG[i & 1].g;
+    gain *= g;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) S[m][n] *= g;
+#pragma unroll
+    for (int ks = 0; ks < C / KS; ++ks) {
+      F vh[NTL], vl[NTL];
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) {
+        vh[n] = X::across(sH, LDV, KS * ks, 16 * n, lane);
+        if constexpr (X::kSplit) vl[n] = X::across(sL, LDV, KS * ks, 16 * n, lane);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const F ka = X::across(sK, LDK, KS * ks, row0 + 16 * m, lane);
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) {
+          Op::mma(S[m][n], vh[n], ka);
+          if constexpr (X::kSplit) Op::mma(S[m][n], vl[n], ka);
+        }
+      }
+    }
+    if (gw) gates_fill<C>(sG[(i + 1) & 1], xg, gate_ok(i + 1), a.gate_input, ckda, lane);
+    __syncthreads();
+    stage_rows(sG[(i + 1) & 1]);
+  }
+  if (MODE == kSegment) {
+    save(a.entry + seg_state);
+    if (slab == 0 && t == 0) a.gain[static_cast<int64_t>(slot) * a.H + h] = gain;
+  } else if (a.ht && pc.s == (REV ? 0 : pc.count - 1)) {
+    save(a.ht + seq_state);
+  }
+}
+
+// entry[s], the sums of the segments alone, become the states entering them:
+// R <- gain_s R + sum_s along each sequence's segments, elements side by side.
+template <bool REV>
+__global__ __launch_bounds__(kNT) void decay_join_kernel(DecayArgs a) {
+  const int64_t per = static_cast<int64_t>(a.dk) * a.dv / 4;
+  const int parts = static_cast<int>((per + kNT - 1) / kNT);
+  const int64_t nh = blockIdx.x / parts, e = (blockIdx.x % parts) * static_cast<int64_t>(kNT) + threadIdx.x;
+  if (e >= per) return;
+  const int n = static_cast<int>(nh / a.H), h = static_cast<int>(nh % a.H);
+  const Seq q = sequence(a, n);
+  const int first = first_slot(a, n, a.seg), count = q.len > 0 ? (q.len + a.seg - 1) / a.seg : 1;
+  f32x4 R = a.h0 ? reinterpret_cast<const f32x4*>(a.h0)[(static_cast<int64_t>(n) * a.H + h) * per + e]
+                 : f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4* base = reinterpret_cast<f32x4*>(a.entry);
+  for (int i = 0; i < count; ++i) {
+    const int64_t s = static_cast<int64_t>(first + (REV ? count - 1 - i : i)) * a.H + h;
+    f32x4 u = {0.f, 0.f, 0.f, 0.f};
+    float g = 0.f;
+    if (i + 1 < count) {
+      u = base[s * per + e];
+      g = a.gain[s];
+    }
+    base[s * per + e] = R;
+    R = R * g + u;
+  }
+}
+
+// ---- single-token step -----------------------------------------------------------
+//   S <- a S + k v^T,  o = scale S^T q
+// HBM-bound: the state is read once and written once.  One workgroup owns 32
+// columns of one (sequence, head) state; each thread holds one float4 of two
+// rows between the read and the write.  The column sums of o run over the rows
+// a wave holds, then over the waves in LDS.
+struct DecayStepArgs {
+  int32_t N, H, Hk, dk, dv, gate_range, gate_input, per_head;
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* alpha;
+  const float* h0;
+  float* ht;
+  void* o;
+};
+
+template <class IO, int NW>
+__global__ __launch_bounds__(64 * NW) void decay_step_kernel(DecayStepArgs a) {
+  using T = typename IO::storage;
+  __shared__ f32x4 part[NW][8];
+  const int nslab = (a.dv + 31) / 32;
+  int64_t nh;
+  int slab;
+  item_of(blockIdx.x, gridDim.x, nslab, nh, slab);
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int n = static_cast<int>(nh / a.H), h = static_cast<int>(nh % a.H);
+  const int c = slab * 32 + 4 * (lane & 7), r0 = wave * 8 + lane / 8;  // rows r0 + 8 NW i
+  const bool col = c < a.dv;
+  const int64_t sb = nh * a.dk * a.dv + c;
+  f32x4 s[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = r0 + 8 * NW * i;
+    s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (col && r < a.dk)
+      s[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(a.h0 + sb + static_cast<int64_t>(r) * a.dv));
+  }
+  const bool ckda = a.gate_range == CKDA_GATE_CKDA;
+  const float g = load_alpha_rt(a.alpha, a.per_head ? h : nh, a.gate_input, ckda);
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (col) {
+    const T* p = static_cast<const T*>(a.v) + nh * a.dv + c;
+    v = f32x4{IO::load(p, 0), IO::load(p, 1), IO::load(p, 2), IO::load(p, 3)};
+  }
+  const int64_t kb = (static_cast<int64_t>(n) * a.Hk + h / (a.H / a.Hk)) * a.dk;
+  f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = r0 + 8 * NW * i;
+    if (r < a.dk) {
+      const float k = IO::load(static_cast<const T*>(a.k), kb + r);
+      const float q = IO::load(static_cast<const T*>(a.q), kb + r);
+      s[i] = s[i] * g + k * v;
+      y += s[i] * q;
+      if (col)
+        __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(a.ht + sb + static_cast<int64_t>(r) * a.dv));
+    }
+  }
+#pragma unroll
+  for (int m = 8; m < 64; m <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] += __shfl_xor(y[e], m, 64);
+  if (NW > 1) {
+    if (lane < 8) part[wave][lane] = y;
+    __syncthreads();
+    if (t < 8) {
+      y = part[0][t];
+#pragma unroll
+      for (int i = 1; i < NW; ++i) y += part[i][t];
+    }
+  }
+  if (t < 8 && col) IO::store4(static_cast<T*>(a.o) + nh * a.dv + c, y * a.scale);
+}
+
+template <class IO>
+launch_result launch_step_io(const DecayStepArgs& a, hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.N) * a.H * ((a.dv + 31) / 32));
+  if (a.dk <= 16)
+    hipLaunchKernelGGL((decay_step_kernel<IO, 1>), dim3(grid), dim3(64), 0, s, a);
+  else if (a.dk <= 32)
+    hipLaunchKernelGGL((decay_step_kernel<IO, 2>), dim3(grid), dim3(128), 0, s, a);
+  else if (a.dk <= 64)
+    hipLaunchKernelGGL((decay_step_kernel<IO, 4>), dim3(grid), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((decay_step_kernel<IO, 8>), dim3(grid), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
+// ---- launches ----------------------------------------------------------------------
+constexpr int kSlab = kDecaySlab;
+
+template <class Op, int DKP>
+launch_result launch_fwd_t(const DecayArgs& a, int64_t grid, hipStream_t s) {
+  constexpr int lds = FwdCfg<Op, DKP, kSlab>::BYTES;
+  const launch_result e = allow_lds<decay_fwd_kernel<Op, DKP, kSlab>>(lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((decay_fwd_kernel<Op, DKP, kSlab>), dim3(static_cast<unsigned>(grid)), dim3(kNT),
+                     lds, s, a);
+  return hipGetLastError();
+}
+
+template <class Op, int DKP, int C, bool REV, int MODE>
+launch_result launch_state_t(const DecayArgs& a, hipStream_t s) {
+  constexpr int lds = StateCfg<Op, DKP, kSlab, C>::BYTES;
+  const int64_t grid = static_cast<int64_t>(a.seg > 0 ? a.slots : a.N) * a.H * ((a.dv + kSlab - 1) / kSlab);
+  const launch_result e = allow_lds<decay_state_kernel<Op, DKP, kSlab, C, REV, MODE>>(lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((decay_state_kernel<Op, DKP, kSlab, C, REV, MODE>), dim3(static_cast<unsigned>(grid)),
+                     dim3(kNT), lds, s, a);
+  return hipGetLastError();
+}
+
+template <bool REV>
+launch_result launch_join(const DecayArgs& a, hipStream_t s) {
+  const int64_t per = static_cast<int64_t>(a.dk) * a.dv / 4;
+  const int64_t grid = static_cast<int64_t>(a.N) * a.H * ((per + kNT - 1) / kNT);
+  hipLaunchKernelGGL(decay_join_kernel<REV>, dim3(static_cast<unsigned>(grid)), dim3(kNT), 0, s, a);
+  return hipGetLastError();
+}
+
+template <bool REV, int MODE>
+launch_result launch_state(const DecayArgs& a, int32_t io_dtype, hipStream_t s) {
+  if (io_dtype == CKDA_DTYPE_BF16)
+    return a.dk <= 64 ? launch_state_t<OpBF16, 64, decay_bwd_chunk(CKDA_DTYPE_BF16), REV, MODE>(a, s)
+                      : launch_state_t<OpBF16, 128, decay_bwd_chunk(CKDA_DTYPE_BF16), REV, MODE>(a, s);
+  return a.dk <= 64 ? launch_state_t<OpF32, 64, decay_bwd_chunk(CKDA_DTYPE_F32), REV, MODE>(a, s)
+                    : launch_state_t<OpF32, 128, decay_bwd_chunk(CKDA_DTYPE_F32), REV, MODE>(a, s);
+}
+
+}  // namespace
+
+bool decay_supported(int32_t dk, int32_t dv) {
+  return dk >= 8 && dk <= 128 && dk % 8 == 0 && dv >= 8 && dv <= 128 && dv % 8 == 0;
+}
+
+// Tokens of a segment for these sizes (0: sequences are not cut).
+int32_t decay_segment(const DecayArgs& a) {
+  const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
+  const int64_t parts = static_cast<int64_t>(a.H) * ((a.dv + kSlab - 1) / kSlab);
+  if (a.N * parts >= 512 && !a.cu) return 0;
+  int64_t seg = (tokens * parts / 1024 + 63) / 64 * 64;
+  if (seg < 512) seg = 512;
+  return seg < a.T ? static_cast<int32_t>(seg) : 0;
+}
+
+// Lays the segments' records out in `ws`; returns the bytes taken.
+size_t decay_layout_segments(DecayArgs& a, unsigned char* ws) {
+  a.seg = decay_segment(a);
+  a.slots = 0;
+  if (a.seg == 0) return 0;
+  a.slots = static_cast<int32_t>(decay_slots(a, a.seg));
+  const size_t st = static_cast<size_t>(a.slots) * a.H * a.dk * a.dv * 4;
+  a.entry = reinterpret_cast<float*>(ws);
+  a.gain = reinterpret_cast<float*>(ws + st);
+  return st + ((static_cast<size_t>(a.slots) * a.H * 4 + 255) & ~size_t(255));
+}
+
+size_t decay_segment_bytes(const DecayArgs& a) {
+  DecayArgs b = a;
+  return decay_layout_segments(b, nullptr);
+}
+
+launch_result launch_decay_segments(const DecayArgs& a, int32_t io_dtype, bool rev, hipStream_t s) {
+  if (a.seg == 0) return hipSuccess;
+  launch_result e = rev ? launch_state<true, kSegment>(a, io_dtype, s)
+                        : launch_state<false, kSegment>(a, io_dtype, s);
+  if (e != hipSuccess) return e;
+  return rev ? launch_join<true>(a, s) : launch_join<false>(a, s);
+}
+
+launch_result launch_decay_chunks(const DecayArgs& a, int32_t io_dtype, bool rev, hipStream_t s) {
+  return rev ? launch_state<true, kChunks>(a, io_dtype, s) : launch_state<false, kChunks>(a, io_dtype, s);
+}
+
+int64_t decay_grid(const DecayArgs& a, int32_t io_dtype) {
+  const int64_t parts = static_cast<int64_t>(a.H) * ((a.dv + kSlab - 1) / kSlab);
+  const int64_t walks = (a.cu || a.T > 0 ? decay_slots(a, 512) : a.N) * parts;
+  const int64_t chunks = decay_slots(a, decay_bwd_chunk(io_dtype)) * a.H;
+  const int64_t joins = static_cast<int64_t>(a.N) * a.H * ((static_cast<int64_t>(a.dk) * a.dv / 4 + kNT - 1) / kNT);
+  const int64_t m = walks > chunks ? walks : chunks;
+  return m > joins ? m : joins;
+}
+
+int decay_dots_per_chunk(int32_t dv) { return (dv + kSlab - 1) / kSlab; }
+
+launch_result launch_decay_fwd(DecayArgs a, int32_t io_dtype, void* ws, hipStream_t s) {
+  decay_layout_segments(a, static_cast<unsigned char*>(ws));
+  launch_result e = launch_decay_segments(a, io_dtype, false, s);
+  if (e != hipSuccess) return e;
+  const int64_t grid = static_cast<int64_t>(a.seg > 0 ? a.slots : a.N) * a.H * ((a.dv + kSlab - 1) / kSlab);
+  if (io_dtype == CKDA_DTYPE_BF16)
+    return a.dk <= 64 ? launch_fwd_t<OpBF16, 64>(a, grid, s) : launch_fwd_t<OpBF16, 128>(a, grid, s);
+  return a.dk <= 64 ? launch_fwd_t<OpF32, 64>(a, grid, s) : launch_fwd_t<OpF32, 128>(a, grid, s);
+}
+
+launch_result launch_decay_step(const DecayArgs& a, int32_t io_dtype, hipStream_t s) {
+  const DecayStepArgs p{a.N, a.H, a.Hk, a.dk, a.dv, a.gate_range, a.gate_input, a.per_head, a.scale,
+                        a.q, a.k, a.v, a.alpha, a.h0, a.ht, a.o};
+  return io_dtype == CKDA_DTYPE_BF16 ? launch_step_io<io_bf16>(p, s) : launch_step_io<io_f32>(p, s);
+}
+
+}  // namespace ckda

@@ -1,0 +1,364 @@
+// Gradients of the decay linear attention.  With the state S0 entering a chunk
+// and the adjoint A of the state leaving it (both kept by the state passes of
+// decay.hip), D_ij, E_i, W_j as in decay_ops.h, P_ij = q_i . k_j and
+// N_ij = scale dout_i . v_j,
+//
+//   dq_i = scale E_i S0 dout_i + sum_{j <= i} D_ij N_ij k_j
+//   dk_j = W_j A v_j           + sum_{i >= j} D_ij N_ij q_i
+//   dv_j = W_j A^T k_j         + scale sum_{i >= j} D_ij P_ij dout_i
+//
+// and for the gates, with no division by a gate: a_t appears in every pair of
+// a write before it and a read at or after it, so with M_ij = P_ij N_ij,
+// z_i = scale q_i . S0 dout_i, y_j = k_j . A v_j and x = <A, S0>
+//
+//   R_1(i) = z_i,  R_{t+1}(i) = a_t R_t(i) + M_it     (writes before t, read i)
+//   da_t = sum_{i >= t} D_it R_t(i) + W_t X_t,   X_1 = x,  X_{t+1} = a_t X_t + y_t.
+//
+// One workgroup per (chunk, query/key head); it runs over the value heads that
+// share the head and sums their dq and dk in registers.
+#include "decay_ops.h"
+
+namespace ckda {
+namespace {
+
+constexpr int kNT = 256;  // 4 waves
+
+template <class Op, int DP, int C>
+struct GradCfg {
+  using T = typename Op::T;
+  static constexpr int ES = sizeof(T);
+  static constexpr int LD = frag_stride(DP, ES), LDC = frag_stride(C, ES), LDM = C + 1;
+  static constexpr int ROWS = C * LD * ES;
+  static constexpr int O_Q = 0, O_K = ROWS, O_V = 2 * ROWS, O_O = 3 * ROWS, O_A = 4 * ROWS,
+                       O_P = O_A + DP * LD * ES, O_N = O_P + C * LDC * ES,
+                       O_M = O_N + C * LDC * ES, O_Z = O_M + C * LDM * 4, O_Y = O_Z + 4 * C * 4,
+                       O_X = O_Y + 4 * C * 4, O_G = align16(O_X + C * 4 + 16),
+                       BYTES = O_G + static_cast<int>(sizeof(Gates<C>));
+};
+
+template <class Op, int DP, int C>
+__global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGrads gr) {
+  using Cfg = GradCfg<Op, DP, C>;
+  using X = Fr<Op>;
+  using T = typename Op::T;
+  using F = typename X::F;
+  constexpr int LD = Cfg::LD, LDC = Cfg::LDC, LDM = Cfg::LDM, KS = X::KS, EPP = 16 / sizeof(T);
+  constexpr int RT = C / 16, CT = DP / 64, ND = DP / KS, NC = C / KS;
+  extern __shared__ __align__(16) unsigned char smem[];
+  T* sQ = reinterpret_cast<T*>(smem + Cfg::O_Q);
+  T* sK = reinterpret_cast<T*>(smem + Cfg::O_K);
+  T* sV = reinterpret_cast<T*>(smem + Cfg::O_V);
+  T* sO = reinterpret_cast<T*>(smem + Cfg::O_O);
+  T* sA = reinterpret_cast<T*>(smem + Cfg::O_A);  // adjoint state [dk][dv]
+  T* sP = reinterpret_cast<T*>(smem + Cfg::O_P);  // scale D P  [i][j]
+  T* sN = reinterpret_cast<T*>(smem + Cfg::O_N);  // D N        [i][j]
+  float* sM = reinterpret_cast<float*>(smem + Cfg::O_M);
+  float* sZ = reinterpret_cast<float*>(smem + Cfg::O_Z);
+  float* sY = reinterpret_cast<float*>(smem + Cfg::O_Y);
+  float* sAl = reinterpret_cast<float*>(smem + Cfg::O_X);  // gates, then x
+  Gates<C>& G = *reinterpret_cast<Gates<C>*>(smem + Cfg::O_G);
+
+  const int t = threadIdx.x, lane = t & 63, w = uniform32(t >> 6), l16 = lane & 15, lq = lane >> 4;
+  const int64_t slot = blockIdx.x / a.Hk;
+  const int hk = static_cast<int>(blockIdx.x % a.Hk), group = a.H / a.Hk;
+  const Piece pc = piece_of(a, static_cast<int>(slot), C, lane);
+  if (pc.n < 0 || pc.len == 0) return;
+  const int64_t ldq = static_cast<int64_t>(a.Hk) * a.dk, ldv = static_cast<int64_t>(a.H) * a.dv;
+  const int64_t oq = pc.begin * ldq + static_cast<int64_t>(hk) * a.dk;
+  const bool ckda = a.gate_range == CKDA_GATE_CKDA;
+  const int nslab = (a.dv + kDecaySlab - 1) / kDecaySlab;
+  const int col0 = w * (DP / 4);  // this wave's columns of dq, dk, dv
+
+  f32x4 dq[CT][RT], dk[CT][RT];
+#pragma unroll
+  for (int m = 0; m < CT; ++m)
+#pragma unroll
+    for (int n = 0; n < RT; ++n) dq[m][n] = dk[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  RowTile<T, C, DP, kNT> rq, rk, rv, ro;
+  rq.load(static_cast<const T*>(a.q) + oq, ldq, pc.len, a.dk, t);
+  rk.load(static_cast<const T*>(a.k) + oq, ldq, pc.len, a.dk, t);
+  rq.store(sQ, LD, t);
+  rk.store(sK, LD, t);
+
+  for (int hv = 0; hv < group; ++hv) {
+    const int h = hk * group + hv;
+    const int64_t ov = pc.begin * ldv + static_cast<int64_t>(h) * a.dv;
+    const int64_t rec = (slot * a.H + h) * a.dk * a.dv;
+    rv.load(static_cast<const T*>(a.v) + ov, ldv, pc.len, a.dv, t);
+    ro.load(static_cast<const T*>(gr.dout) + ov, ldv, pc.len, a.dv, t);
+    RowTile<T, DP, DP, kNT> ra;
+    ra.load(static_cast<const T*>(a.adjoints) + rec, a.dv, a.dk, a.dv, t);
+    const bool tok = lane < C && lane < pc.len;
+    float xg = 0.f;
+    if (w == 0) {
+      xg = tok ? gate_stored(a, pc.begin + lane, h) : 0.f;
+      gates_fill<C>(G, xg, tok, a.gate_input, ckda, lane);
+      if (lane < C) sAl[lane] = tok ? gate_value(xg, a.gate_input, ckda) : 1.f;
+      if (lane == 0) {
+        float x = 0.f;
+        for (int i = 0; i < nslab; ++i) x += a.dots[(slot * a.H + h) * nslab + i];
+        sAl[C] = x;
+      }
+    }
+    rv.store(sV, LD, t);
+    ro.store(sO, LD, t);
+    ra.store(sA, LD, t);
+    __syncthreads();
+    const bool fast = G.fast != 0;
+
+    // P^T and N^T tiles: column i = 16 ti + l16, rows j = 16 tj + 4 lq + r
+    for (int tile = w; tile < RT * RT; tile += 4) {
+      const int ti = tile / RT, tj = tile % RT, i = 16 * ti + l16, j0 = 16 * tj + 4 * lq;
+      f32x4 p = {0.f, 0.f, 0.f, 0.f}, n = p;
+      if (tj <= ti) {
+#pragma unroll
+        for (int s = 0; s < ND; ++s) {
+          Op::mma(p, X::row(sK + (16 * tj + l16) * LD, s, lq), X::row(sQ + i * LD, s, lq));
+          Op::mma(n, X::row(sV + (16 * tj + l16) * LD, s, lq), X::row(sO + i * LD, s, lq));
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sM[i * LDM + j0 + r] = p[r] * n[r] * a.scale;
+          const float d = (fast ? (j0 + r <= i ? G.er[i] * G.ej[j0 + r] : 0.f) : d_slow(G, i, j0 + r)) * a.scale;
+          p[r] = d != 0.f ? p[r] * d : 0.f;
+          n[r] = d != 0.f ? n[r] * d : 0.f;
+        }
+      }
+      Op::store4(sP + i * LDC + j0, p);
+      Op::store4(sN + i * LDC + j0, n);
+    }
+    __syncthreads();
+
+    // dq: columns dk = col0 + 16 m + 4 lq + r, token 16 n + l16
+    {
+      const T* st = static_cast<const T*>(a.states) + rec;
+      F fa[CT][ND];
+#pragma unroll
+      for (int m = 0; m < CT; ++m) {
+        const int r = col0 + 16 * m + l16;
+#pragma unroll
+        for (int s = 0; s < ND; ++s) {
+          const int c = KS * s + EPP * lq;
+          fa[m][s] = X::zero();
+          if (r < a.dk && c < a.dv) fa[m][s] = *reinterpret_cast<const F*>(st + static_cast<int64_t>(r) * a.dv + c);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < RT; ++n) {
+        const int i = 16 * n + l16;
+        const float e = G.E[i] * a.scale;
+        float z = 0.f;
+#pragma unroll
+        for (int m = 0; m < CT; ++m) {
+          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < ND; ++s) Op::mma(acc, fa[m][s], X::row(sO + i * LD, s, lq));
+          const T* qr = sQ + i * LD + col0 + 16 * m + 4 * lq;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) z += acc[r] * static_cast<float>(qr[r]);
+          dq[m][n] += acc * e;
+#pragma unroll
+          for (int ks = 0; ks < NC; ++ks)
+            if (KS * ks <= 16 * n)
+              Op::mma(dq[m][n], X::across(sK, LD, KS * ks, col0 + 16 * m, lane), X::rowp(sN + i * LDC, ks, lq));
+        }
+        z += __shfl_xor(z, 16, 64);
+        z += __shfl_xor(z, 32, 64);
+        if (lq == 0) sZ[w * C + i] = z * a.scale;
+      }
+    }
+    // dk, token 16 n + l16
+#pragma unroll
+    for (int n = 0; n < RT; ++n) {
+      const int j = 16 * n + l16;
+      const float wj = G.W[j];
+      float y = 0.f;
+#pragma unroll
+      for (int m = 0; m < CT; ++m) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < ND; ++s)
+          Op::mma(acc, X::row(sA + (col0 + 16 * m + l16) * LD, s, lq), X::row(sV + j * LD, s, lq));
+        const T* kr = sK + j * LD + col0 + 16 * m + 4 * lq;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y += acc[r] * static_cast<float>(kr[r]);
+        dk[m][n] += acc * wj;
+#pragma unroll
+        for (int ks = 0; ks < NC; ++ks)
+          if (KS * ks + KS > 16 * n)
+            Op::mma(dk[m][n], X::across(sQ, LD, KS * ks, col0 + 16 * m, lane),
+                    X::across(sN, LDC, KS * ks, 16 * n, lane));
+      }
+      y += __shfl_xor(y, 16, 64);
+      y += __shfl_xor(y, 32, 64);
+      if (lq == 0) sY[w * C + j] = y;
+    }
+    // dv: columns dv = col0 + 16 m + 4 lq + r
+    T* gdv = static_cast<T*>(gr.dv) + ov;
+#pragma unroll
+    for (int n = 0; n < RT; ++n) {
+      const int j = 16 * n + l16;
+      const float wj = G.W[j];
+#pragma unroll
+      for (int m = 0; m < CT; ++m) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < ND; ++s)
+          Op::mma(acc, X::across(sA, LD, KS * s, col0 + 16 * m, lane), X::rowp(sK + j * LD, s, lq));
+        acc *= wj;
+#pragma unroll
+        for (int ks = 0; ks < NC; ++ks)
+          if (KS * ks + KS > 16 * n)
+            Op::mma(acc, X::across(sO, LD, KS * ks, col0 + 16 * m, lane),
+                    X::across(sP, LDC, KS * ks, 16 * n, lane));
+        const int c = col0 + 16 * m + 4 * lq;
+        if (j < pc.len && c < a.dv) Op::store4(gdv + j * ldv + c, acc);
+      }
+    }
+    __syncthreads();  // z, y of all waves; LDS rows may change after the next
+
+    if (w == 0 && gr.dalpha) {
+      const int i = lane < C ? lane : C - 1;
+      float R = (sZ[i] + sZ[C + i]) + (sZ[2 * C + i] + sZ[3 * C + i]);
+      const float y = (sY[i] + sY[C + i]) + (sY[2 * C + i] + sY[3 * C + i]);
+      float Xr = sAl[C], da = 0.f;
+      for (int s = 0; s < C; ++s) {
+        const float al = sAl[s], ys = __shfl(y, s, 64);
+        float m = 0.f, d = 0.f;
+        if (s <= i) {
+          m = sM[i * LDM + s];
+          d = fast ? G.er[i] * G.ej[s] : d_slow(G, i, s);
+          sM[i * LDM + s] = d != 0.f ? d * R : 0.f;
+        }
+        R = al * R + m;
+        if (s == i) da = G.W[s] * Xr;
+        Xr = al * Xr + ys;
+      }
+      wave_lds_sync();
+      for (int r = i; r < C; ++r) da += sM[r * LDM + i];
+      if (tok) {
+        if (a.gate_input != CKDA_GATES_F32) {
+          const float e = expf(-fabsf(xg));
+          da *= (ckda ? 2.f : 1.f) * e / ((1.f + e) * (1.f + e));
+        }
+        const int64_t at = (pc.begin + lane) * a.H + h;
+        if (a.per_head)
+          gr.per_token[at] = da;
+        else
+          static_cast<T*>(gr.dalpha)[at] = static_cast<T>(da);
+      }
+    }
+    __syncthreads();
+  }
+
+  T* gdq = static_cast<T*>(gr.dq) + oq;
+  T* gdk = static_cast<T*>(gr.dk) + oq;
+#pragma unroll
+  for (int n = 0; n < RT; ++n) {
+    const int j = 16 * n + l16;
+    if (j < pc.len) {
+#pragma unroll
+      for (int m = 0; m < CT; ++m) {
+        const int c = col0 + 16 * m + 4 * lq;
+        if (c < a.dk) {
+          Op::store4(gdq + j * ldq + c, dq[m][n]);
+          Op::store4(gdk + j * ldq + c, dk[m][n]);
+        }
+      }
+    }
+  }
+}
+
+// dalpha [H] from the tokens' gradients, in a fixed order: thread t of a
+// head's workgroup takes tokens t, t + 1024, ..., then a tree over threads.
+template <class IO>
+__global__ __launch_bounds__(1024) void decay_gate_sum_kernel(DecayArgs a, const float* per_token,
+                                                             void* dalpha) {
+  __shared__ float part[16];
+  const int h = blockIdx.x, t = threadIdx.x;
+  const int64_t n = a.cu ? cu_at(a, a.N) : static_cast<int64_t>(a.B) * a.T;
+  float s = 0.f;
+  for (int64_t i = t; i < n; i += 1024) s += per_token[i * a.H + h];
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) s += __shfl_xor(s, m, 64);
+  if ((t & 63) == 0) part[t >> 6] = s;
+  __syncthreads();
+  if (t == 0) {
+    for (int i = 1; i < 16; ++i) s += part[i];
+    using T = typename IO::storage;
+    IO::store(static_cast<T*>(dalpha), h, s);
+  }
+}
+
+template <class Op, int DP, int C>
+launch_result launch_grad_t(const DecayArgs& a, const DecayGrads& g, hipStream_t s) {
+  constexpr int lds = GradCfg<Op, DP, C>::BYTES;
+  static_assert(lds <= 160 * 1024, "LDS of a CU");
+  const launch_result e = allow_lds<decay_grad_kernel<Op, DP, C>>(lds);
+  if (e != hipSuccess) return e;
+  const int64_t grid = static_cast<int64_t>(a.cslots) * a.Hk;
+  hipLaunchKernelGGL((decay_grad_kernel<Op, DP, C>), dim3(static_cast<unsigned>(grid)), dim3(kNT), lds, s,
+                     a, g);
+  return hipGetLastError();
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Workspace: segments' records (used forwards, then again backwards), then
+// the chunks' states, adjoints and partial dots, then the tokens' gate
+// gradients of a head's one gate.
+size_t lay_out(DecayArgs& a, DecayGrads& g, int32_t io_dtype, unsigned char* ws) {
+  size_t off = up256(decay_layout_segments(a, ws));
+  const int C = decay_bwd_chunk(io_dtype);
+  const size_t es = io_dtype == CKDA_DTYPE_BF16 ? 2 : 4;
+  a.cslots = static_cast<int32_t>(decay_slots(a, C));
+  const size_t chains = static_cast<size_t>(a.cslots) * a.H;
+  a.states = ws + off;
+  off += up256(chains * a.dk * a.dv * es);
+  a.adjoints = ws + off;
+  off += up256(chains * a.dk * a.dv * es);
+  a.dots = reinterpret_cast<float*>(ws + off);
+  off += up256(chains * decay_dots_per_chunk(a.dv) * 4);
+  g.per_token = reinterpret_cast<float*>(ws + off);
+  if (a.per_head) off += up256(static_cast<size_t>(a.B) * a.T * a.H * 4);
+  return off;
+}
+
+}  // namespace
+
+size_t decay_bwd_workspace(const DecayArgs& a, int32_t io_dtype) {
+  DecayArgs b = a;
+  DecayGrads g{};
+  return lay_out(b, g, io_dtype, nullptr);
+}
+
+launch_result launch_decay_bwd(const DecayArgs& a, DecayGrads g, int32_t io_dtype, void* ws,
+                               hipStream_t s) {
+  DecayArgs f = a;
+  lay_out(f, g, io_dtype, static_cast<unsigned char*>(ws));
+  f.ht = nullptr;
+  launch_result e = launch_decay_segments(f, io_dtype, false, s);
+  if (e != hipSuccess) return e;
+  if ((e = launch_decay_chunks(f, io_dtype, false, s)) != hipSuccess) return e;
+  DecayArgs r = f;
+  r.h0 = g.dht;
+  r.ht = g.dh0;
+  r.o = const_cast<void*>(g.dout);
+  if ((e = launch_decay_segments(r, io_dtype, true, s)) != hipSuccess) return e;
+  if ((e = launch_decay_chunks(r, io_dtype, true, s)) != hipSuccess) return e;
+  constexpr int CB = decay_bwd_chunk(CKDA_DTYPE_BF16), CF = decay_bwd_chunk(CKDA_DTYPE_F32);
+  const bool wide = a.dk > 64 || a.dv > 64;
+  if (io_dtype == CKDA_DTYPE_BF16)
+    e = wide ? launch_grad_t<OpBF16, 128, CB>(f, g, s) : launch_grad_t<OpBF16, 64, CB>(f, g, s);
+  else
+    e = wide ? launch_grad_t<OpF32, 128, CF>(f, g, s) : launch_grad_t<OpF32, 64, CF>(f, g, s);
+  if (e != hipSuccess || !g.dalpha || !a.per_head) return e;
+  if (io_dtype == CKDA_DTYPE_BF16)
+    hipLaunchKernelGGL(decay_gate_sum_kernel<io_bf16>, dim3(a.H), dim3(1024), 0, s, f, g.per_token, g.dalpha);
+  else
+    hipLaunchKernelGGL(decay_gate_sum_kernel<io_f32>, dim3(a.H), dim3(1024), 0, s, f, g.per_token, g.dalpha);
+  return hipGetLastError();
+}
+
+}  // namespace ckda

@@ -1,0 +1,380 @@
+// Device building blocks of the decay linear attention
+//
+//     S_t = a_t S_{t-1} + k_t v_t^T,     o_t = scale S_t^T q_t
+//
+// (one gate a head and token, or one a head): the products of gates inside a
+// chunk, the spans of tokens a workgroup works on, tiles of rows on their way
+// from memory to LDS, and operand fragments read across the rows of LDS.
+//
+// A chunk of C tokens entered with the state S0 is, with D_ij = a_{j+1}..a_i
+// for j <= i (0 otherwise), E_i = a_1..a_i, W_j = a_{j+1}..a_C and g = E_C,
+//
+//     o_i = scale (E_i S0^T q_i + sum_{j <= i} D_ij (q_i . k_j) v_j)
+//     S_C = g S0 + sum_j W_j k_j v_j^T
+//
+// exactly the recurrence for any gates, zeros and negative ones included.
+#pragma once
+
+#include <atomic>
+
+#include "mfma_ops.h"
+
+namespace ckda {
+
+
+// ---- spans -------------------------------------------------------------------
+// Sequence n owns the tokens [begin, begin + len).  cu_seqlens is clamped to
+// [0, T], so a malformed one cannot lead outside the tensors.
+struct Seq {
+  int64_t begin;
+  int32_t len;
+};
+__device__ __forceinline__ int32_t cu_at(const DecayArgs& a, int i) {
+  const int32_t c = a.cu[i];
+  return c < 0 ? 0 : (c > a.T ? a.T : c);
+}
+__device__ __forceinline__ Seq sequence(const DecayArgs& a, int n) {
+  if (!a.cu) return Seq{static_cast<int64_t>(n) * a.T, a.T};
+  const int32_t b = cu_at(a, n), e = cu_at(a, n + 1);
+  return Seq{b, e > b ? e - b : 0};
+}
+
+// Sequences are cut into pieces of L tokens (at least one a sequence), and
+// piece s of sequence n has slot first_slot(n, L) + s.  A packed sequence
+// starting at token b takes slots from floor(b / L) + n on: those ranges never
+// meet and need no sum over the lengths before.
+__device__ __forceinline__ int32_t first_slot(const DecayArgs& a, int n, int L) {
+  if (!a.cu) return n * (a.T > 0 ? (a.T + L - 1) / L : 1);
+  return cu_at(a, n) / L + n;
+}
+struct Piece {
+  int32_t n;       // sequence, -1 for an unused slot
+  int32_t s, count;  // piece s of `count` of the sequence
+  int64_t begin;   // first token
+  int32_t len;
+};
+// The piece of a slot, the same in all lanes of a wave: dense by division,
+// packed by a search that tests 64 sequences at a time.
+__device__ __forceinline__ Piece piece_of(const DecayArgs& a, int slot, int L, int lane) {
+  Piece p;
+  if (!a.cu) {
+    const int per = a.T > 0 ? (a.T + L - 1) / L : 1;
+    p.n = slot / per;
+  } else {
+    int lo = 0, cnt = a.N;
+    while (cnt > 1) {
+      const int step = (cnt + 63) / 64;
+      const int off = lane * step;
+      const bool below = off < cnt && first_slot(a, lo + off, L) <= slot;
+      int m = __popcll(__ballot(below));
+      m = m > 0 ? m - 1 : 0;
+      const int left = cnt - m * step;
+      lo += m * step;
+      cnt = left < step ? left : step;
+    }
+    p.n = uniform32(lo);
+  }
+  const Seq q = sequence(a, p.n);
+  p.s = slot - first_slot(a, p.n, L);
+  p.count = q.len > 0 ? (q.len + L - 1) / L : 1;
+  if (p.s < 0 || p.s >= p.count) {
+    p.n = -1;
+    p.len = 0;
+    return p;
+  }
+  p.begin = q.begin + static_cast<int64_t>(p.s) * L;
+  const int rest = q.len - p.s * L;
+  p.len = rest < L ? rest : L;
+  return p;
+}
+
+// ---- gates -------------------------------------------------------------------
+constexpr float kLog2e = 1.4426950408889634f;
+
+// log2|a| of a gate, whether it is negative, and whether it is exactly zero
+// (then the logarithm is 0 and the zero is tracked apart).  The logarithm
+// comes from the logit itself where there is one: forming the gate first
+// would lose the distance of a gate from 1, which a memory of thousands of
+// tokens multiplies.
+struct GateLog {
+  float l2;
+  bool neg, zero;
+};
+__device__ __forceinline__ float log2_of(float a) {  // a > 0
+  return (a > 0.5f && a < 2.f) ? log1pf(a - 1.f) * kLog2e : log2f(a);
+}
+__device__ __forceinline__ GateLog gate_log(float x, int gate_input, bool ckda) {
+  GateLog r;
+  if (gate_input == CKDA_GATES_F32) {
+    r.neg = x < 0.f;
+    r.zero = x == 0.f;
+    r.l2 = r.zero ? 0.f : log2_of(fabsf(x));
+  } else if (!ckda) {  // sigmoid
+    const float e = expf(-fabsf(x));
+    r.neg = false;
+    r.zero = x == -INFINITY;
+    r.l2 = r.zero ? 0.f : ((x < 0.f ? x : 0.f) - log1pf(e)) * kLog2e;
+  } else {  // 2 sigmoid - 1 = tanh(x / 2)
+    const float m = fabsf(x), e = expf(-m);
+    r.neg = x < 0.f;
+    r.zero = x == 0.f;
+    r.l2 = r.zero ? 0.f
+                  : (m < 0.5f ? log2f(alpha_from_logit(m, true))
+                              : (log1pf(-e) - log1pf(e)) * kLog2e);
+  }
+  return r;
+}
+// the gate itself (for the recurrences that multiply by it)
+__device__ __forceinline__ float gate_value(float x, int gate_input, bool ckda) {
+  return gate_input == CKDA_GATES_F32 ? x : alpha_from_logit(x, ckda);
+}
+// alpha as it is stored, widened
+__device__ __forceinline__ float gate_stored(const DecayArgs& a, int64_t token, int h) {
+  const int64_t i = a.per_head ? h : token * a.H + h;
+  return a.gate_input == CKDA_GATES_LOGITS_BF16 ? gate_raw<gate_logit_bf16>(a.alpha, i)
+                                                : gate_raw<gate_f32>(a.alpha, i);
+}
+
+// 2^x of a double whose integer part may leave float's exponent range
+__device__ __forceinline__ float exp2_wide(double x) {
+  const double n = rint(x);
+  return ldexpf(__builtin_amdgcn_exp2f(static_cast<float>(x - n)), static_cast<int>(n));
+}
+
+// A chunk's gates in LDS.  L is the running sum of log2|a| (kept in double:
+// with gates near 0.1 a float sum of 64 of them is off by 1e-5), split into an
+// integer and a fraction so that differences of two are exact to float.
+// `fast`: no zero gate and all running products within 2^+-60 of the middle
+// one, so D_ij = er_i ej_j (signs included); else d_slow forms each.
+template <int C>
+struct alignas(16) Gates {
+  float E[C], W[C];    // products from the chunk's start, to its end
+  float er[C], ej[C];
+  float hi[C], lo[C], sg[C];
+  int z[C];            // last zero gate at or before i (-1: none)
+  float g;             // product of all
+  int fast;
+};
+
+// One wave fills G from its lanes' gates (lane i: token i; tokens past the
+// chunk's length count as gates of 1).
+template <int C>
+__device__ __forceinline__ void gates_fill(Gates<C>& G, float x, bool valid, int gate_input,
+                                           bool ckda, int lane) {
+  const GateLog gl = gate_log(x, gate_input, ckda);
+  const uint64_t zm = __ballot(valid && gl.zero), nm = __ballot(valid && gl.neg);
+  double L = valid ? static_cast<double>(gl.l2) : 0.0;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double y = __shfl_up(L, d, 64);
+    L += lane >= d ? y : 0.0;
+  }
+  const double end = __shfl(L, 63, 64), mid = __shfl(L, C / 2 - 1, 64);
+  const uint64_t upto = ~0ull >> (63 - lane);
+  const uint64_t zz = zm & upto;
+  const int z = zz ? 63 - __clzll(zz) : -1;
+  const int zend = zm ? 63 - __clzll(zm) : -1;
+  const float sg = (__popcll(nm & upto) & 1) ? -1.f : 1.f;
+  const float sgend = (__popcll(nm) & 1) ? -1.f : 1.f;
+  const bool far = !(fabs(L - mid) <= 60.0);
+  const bool fast = zm == 0 && __ballot(far) == 0;
+  if (lane < C) {
+    const double n = rint(L);
+    G.E[lane] = z < 0 ? sg * exp2_wide(L) : 0.f;
+    G.W[lane] = zend <= lane ? sg * sgend * exp2_wide(end - L) : 0.f;
+    G.er[lane] = fast ? sg * exp2_wide(L - mid) : 0.f;
+    G.ej[lane] = fast ? sg * exp2_wide(mid - L) : 0.f;
+    G.hi[lane] = static_cast<float>(n);
+    G.lo[lane] = static_cast<float>(L - n);
+    G.sg[lane] = sg;
+    G.z[lane] = z;
+  }
+  if (lane == 0) {
+    G.g = zend < 0 ? sgend * exp2_wide(end) : 0.f;
+    G.fast = fast;
+  }
+}
+
+// D_ij for j <= i where the chunk is not `fast`
+template <int C>
+__device__ __forceinline__ float d_slow(const Gates<C>& G, int i, int j) {
+  const float e = __builtin_amdgcn_exp2f((G.hi[i] - G.hi[j]) + (G.lo[i] - G.lo[j]));
+  return (j <= i && G.z[i] <= j) ? G.sg[i] * G.sg[j] * e : 0.f;
+}
+
+// ---- tiles of rows, memory -> registers -> LDS ------------------------------
+// ROWS x COLS elements of T in 16-byte pieces by NT threads; pieces outside
+// the first `rows` rows or `cols` columns (a multiple of a piece) are zeros.
+template <class T, int ROWS, int COLS, int NT>
+struct RowTile {
+  static constexpr int EPP = 16 / sizeof(T), PPR = COLS / EPP, NP = ROWS * PPR / NT;
+  static_assert(ROWS * PPR % NT == 0, "whole pieces a thread");
+  uint4 r[NP];
+  __device__ __forceinline__ void load(const T* base, int64_t ld, int rows, int cols, int t) {
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+      const int p = t + NT * u, row = p / PPR, c = (p % PPR) * EPP;
+      r[u] = make_uint4(0, 0, 0, 0);
+      if (row < rows && c < cols) r[u] = *reinterpret_cast<const uint4*>(base + row * ld + c);
+    }
+  }
+  __device__ __forceinline__ void store(T* lds, int ldl, int t) const {
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+      const int p = t + NT * u, row = p / PPR, c = (p % PPR) * EPP;
+      *reinterpret_cast<uint4*>(lds + row * ldl + c) = r[u];
+    }
+  }
+};
+
+// LDS row stride for tiles that are read across their rows (four rows of 16
+// columns a lane group and read): for rows of 64 bytes 96, else the stride
+// of row fragments; eight rows then fall into different banks.
+constexpr int cross_stride(int n, int es) { return n * es == 64 ? 96 / es : frag_stride(n, es); }
+
+// ---- operand fragments --------------------------------------------------------
+// Beside the row fragments of mfma_ops.h, fragments read ACROSS rows: from
+// X[k][n] in LDS, lane (l16, lq) takes column n0 + l16 and the K-values of the
+// accumulators' order (16-row tile, lq, i), so products of accumulators with
+// them need no pass through LDS.  `row`: natural K order; `rowp`: a row in
+// the accumulators' K order.
+template <class Op>
+struct Fr;
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <>
+struct Fr<OpBF16> {
+  using Op = OpBF16;
+  using T = __bf16;
+  using F = bf16x8;
+  static constexpr int KS = 32;
+  static constexpr bool kSplit = true;
+  using IO = io_bf16;
+  static __device__ __forceinline__ s16x4 tr4(const T* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)(const_cast<T*>(p)));
+  }
+  static __device__ __forceinline__ F across(const T* x, int ld, int k0, int n0, int lane) {
+    const int l16 = lane & 15, lq = lane >> 4;
+    const T* p = x + (k0 + 4 * lq + (l16 >> 2)) * ld + n0 + 4 * (l16 & 3);
+    union {
+      s16x4 s[2];
+      F f;
+    } u;
+    u.s[0] = tr4(p);
+    u.s[1] = tr4(p + 16 * ld);
+    return u.f;
+  }
+  static __device__ __forceinline__ F row(const T* r, int s, int lq) {
+    return *reinterpret_cast<const F*>(r + 32 * s + 8 * lq);
+  }
+  static __device__ __forceinline__ F rowp(const T* r, int s, int lq) {
+    union {
+      bf16x4 h[2];
+      F f;
+    } u;
+    u.h[0] = *reinterpret_cast<const bf16x4*>(r + 32 * s + 4 * lq);
+    u.h[1] = *reinterpret_cast<const bf16x4*>(r + 32 * s + 16 + 4 * lq);
+    return u.f;
+  }
+  // zeros outside the row (guarded loads from memory)
+  static __device__ __forceinline__ F zero() { return F{}; }
+};
+
+template <>
+struct Fr<OpF32> {
+  using Op = OpF32;
+  using T = float;
+  using F = f32x4;
+  static constexpr int KS = 16;
+  static constexpr bool kSplit = false;
+  using IO = io_f32;
+  static __device__ __forceinline__ F across(const T* x, int ld, int k0, int n0, int lane) {
+    const T* p = x + (k0 + 4 * (lane >> 4)) * ld + n0 + (lane & 15);
+    return F{p[0], p[ld], p[2 * ld], p[3 * ld]};
+  }
+  static __device__ __forceinline__ F row(const T* r, int s, int lq) {
+    return *reinterpret_cast<const F*>(r + 16 * s + 4 * lq);
+  }
+  static __device__ __forceinline__ F rowp(const T* r, int s, int lq) { return row(r, s, lq); }
+  static __device__ __forceinline__ F zero() { return F{}; }
+};
+
+// element e of a 16-byte piece, widened
+template <class T>
+__device__ __forceinline__ float piece_elem(const uint4& u, int e) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if constexpr (sizeof(T) == 2)
+    return __uint_as_float((e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
+  else
+    return __uint_as_float(w[e]);
+}
+
+// A piece times w, stored for the state update.  bf16: as two terms, the
+// product's nearest bf16 and what is left (2^-18 of it is lost), because the
+// state is kept, and handed out, in float32; k and v themselves are exact.
+template <class T>
+__device__ __forceinline__ void store_scaled(const uint4& u, float w, T* hi, T* lo) {
+  constexpr int E = 16 / sizeof(T);
+  alignas(16) T h[E];
+  alignas(16) T l[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float x = piece_elem<T>(u, e) * w;
+    h[e] = static_cast<T>(x);
+    if constexpr (sizeof(T) == 2) l[e] = static_cast<T>(x - static_cast<float>(h[e]));
+  }
+  *reinterpret_cast<uint4*>(hi) = *reinterpret_cast<const uint4*>(h);
+  if constexpr (sizeof(T) == 2) *reinterpret_cast<uint4*>(lo) = *reinterpret_cast<const uint4*>(l);
+}
+
+// Work items of a grid: `outer` items of `inner` parts.  Workgroups go to the
+// 8 XCDs in turn, so the parts of one item are placed 8 workgroups apart: they
+// share what they read through one L2.
+__device__ __forceinline__ void item_of(int64_t block, int64_t grid, int inner, int64_t& outer,
+                                        int& part) {
+  if (inner > 1 && grid % (8 * static_cast<int64_t>(inner)) == 0) {
+    const int64_t r = block / 8;
+    part = static_cast<int>(r % inner);
+    outer = (r / inner) * 8 + block % 8;
+  } else {
+    part = static_cast<int>(block % inner);
+    outer = block / inner;
+  }
+}
+
+// ---- host side ----------------------------------------------------------------
+// Lets `Kernel` take more than 64 KB of LDS, once for each device.
+template <auto Kernel>
+launch_result allow_lds(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  const hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return hipSuccess;
+  const hipError_t r = hipFuncSetAttribute(reinterpret_cast<const void*>(Kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (r == hipSuccess) done.fetch_or(bit, std::memory_order_release);
+  return r;
+}
+constexpr int kDecayChunk = 64;
+constexpr int kDecaySlab = 32;  // state columns a workgroup of the state walks
+// chunk of the backward's records and gradients
+constexpr int decay_bwd_chunk(int32_t io_dtype) { return io_dtype == CKDA_DTYPE_BF16 ? 64 : 32; }
+// slots of pieces of L tokens
+inline int64_t decay_slots(const DecayArgs& a, int L) {
+  if (a.cu) return a.T / L + static_cast<int64_t>(a.N);
+  return static_cast<int64_t>(a.N) * (a.T > 0 ? (a.T + L - 1) / L : 1);
+}
+
+size_t decay_layout_segments(DecayArgs& a, unsigned char* ws);
+int decay_dots_per_chunk(int32_t dv);
+// Segment entries (nothing where sequences are not cut), then the walks that
+// keep the state met at every chunk.  Backwards, a.o holds dout, a.h0 the
+// adjoint of the final states and a.ht receives that of the initial ones.
+launch_result launch_decay_segments(const DecayArgs& a, int32_t io_dtype, bool rev, hipStream_t s);
+launch_result launch_decay_chunks(const DecayArgs& a, int32_t io_dtype, bool rev, hipStream_t s);
+
+}  // namespace ckda

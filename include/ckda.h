@@ -54,7 +54,7 @@
 extern "C" {
 #endif
 
-#define CKDA_ABI_VERSION 9
+#define CKDA_ABI_VERSION 10
 
 typedef enum {
   CKDA_OK = 0,
@@ -362,6 +362,87 @@ ckda_status_t ckda_recurrent_step(int32_t N, int32_t H, int32_t qk_heads, int32_
  */
 ckda_status_t ckda_l2norm_debug(const void* x, float* y, int64_t rows,
                                 int32_t d, int32_t dtype, void* stream);
+
+/*
+ * Linear attention with one decay a head: the recurrence without the delta
+ * correction and with a scalar gate,
+ *
+ *     S_t = a_t S_{t-1} + k_t v_t^T,      o_t = scale * S_t^T q_t,
+ *
+ * with the layouts, packing, gate inputs and states of the delta-rule calls
+ * above, so that layers of both kinds share a program's buffers:
+ *   q, k : [B][T][Hk][dk]   v, o : [B][T][H][dv]   h0, ht : [num_seqs][H][dk][dv] float32
+ *   alpha : [B][T][H], or [H] with alpha_per_head = 1 (a fixed decay); what it
+ *     holds is gate_input's (gates in float32, or logits activated by
+ *     gate_range: KDA a = sigmoid, CKDA a = 2 sigmoid - 1).
+ * Gates are taken as written: zeros restart the state exactly, negative gates
+ * flip it, and a gate's distance from 1 is kept (the products of gates run
+ * through logarithms formed from 1 - a, or from the logit itself).
+ * A non-finite value in a token's q, k, v or gate reaches the outputs of its
+ * own block of 64 tokens (32 in float32 gradients) and of later tokens of its
+ * sequence (earlier ones, for gradients); never another sequence.  Tokens
+ * past cu_seqlens[num_seqs] of a packed batch are neither read nor written;
+ * cu_seqlens is clamped to [0, T] on the device.
+ * Supported: dk and dv multiples of 8 from 8 to 128, in any combination, both
+ * io dtypes; others return CKDA_ERR_UNSUPPORTED, as do B * T of 2^31 or more
+ * and launches of 2^31 or more workgroups.
+ */
+typedef struct {
+  int32_t B, T, H, dk, dv;
+  int32_t num_seqs;       /* B for a dense batch */
+  int32_t io_dtype;       /* ckda_dtype_t */
+  int32_t gate_range;     /* ckda_gate_t, for logits */
+  int32_t gate_input;     /* ckda_gate_input_t */
+  int32_t qk_heads;       /* Hk, heads of q and k; 0 = H */
+  int32_t alpha_per_head; /* 0: alpha [B][T][H]; 1: alpha [H] */
+  float scale;
+} ckda_decay_desc_t;
+
+/* 1 if the decay calls have kernels for these head sizes, else 0. */
+int32_t ckda_decay_supported(int32_t dk, int32_t dv);
+
+/*
+ * The forward over whole sequences.  h0 NULL: zero initial states; ht NULL:
+ * final states not written; h0 and ht may be the same buffer.  The workspace
+ * (0 bytes where there are sequences and heads enough to fill the GPU; then
+ * NULL is fine) holds the states entering the segments that long sequences
+ * are cut into: 256-byte aligned, overlapping no tensor.
+ */
+size_t ckda_decay_fwd_workspace_size(const ckda_decay_desc_t* desc, int32_t packed);
+ckda_status_t ckda_decay_fwd(const ckda_decay_desc_t* desc, const void* q, const void* k,
+                             const void* v, const void* alpha, const int32_t* cu_seqlens,
+                             const float* h0, void* o, float* ht, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients, given dout = dL/do (io dtype) and dht = dL/dht (float32,
+ * NULL for zero).  dq, dk, dv and dalpha come in the io dtype, shaped like q,
+ * k, v and alpha (bf16 inputs: the products run on bf16 operands and sums in
+ * float32, rounded once at the end); dh0 in float32.  With logits dalpha is
+ * the gradient of the logits; with alpha_per_head it is summed over all
+ * tokens.  dalpha and dh0 may be NULL (not wanted).  dq and dk of a q/k head
+ * sum over the value heads that read it.  dalpha is formed with no division
+ * by a gate, so zero gates have the gradient of the recurrence.  Every sum
+ * runs in a fixed order.
+ */
+size_t ckda_decay_bwd_workspace_size(const ckda_decay_desc_t* desc, int32_t packed);
+ckda_status_t ckda_decay_bwd(const ckda_decay_desc_t* desc, const void* q, const void* k,
+                             const void* v, const void* alpha, const int32_t* cu_seqlens,
+                             const float* h0, const void* dout, const float* dht, void* dq,
+                             void* dk, void* dv, void* dalpha, float* dh0, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * One token for each of N sequences:
+ *   q, k : [N][Hk][dk]   v, o : [N][H][dv]   alpha : [N][H] or [H]
+ *   h0, ht : [N][H][dk][dv] float32; h0 == ht (in place) is allowed.
+ * N * H up to 2^21.
+ */
+ckda_status_t ckda_decay_step(int32_t N, int32_t H, int32_t qk_heads, int32_t dk, int32_t dv,
+                              int32_t io_dtype, int32_t gate_range, int32_t gate_input,
+                              int32_t alpha_per_head, float scale, const void* q, const void* k,
+                              const void* v, const void* alpha, const float* h0, float* ht,
+                              void* o, void* stream);
 
 /* Static description of a status code. */
 const char* ckda_status_string(int32_t status);
