@@ -15,7 +15,8 @@ __all__ = ["chunk_fwd", "chunk_bwd", "chunk_bwd_workspace_size", "recurrent_step
            "l2norm_debug", "fwd_supported",
            "library_path", "abi_version", "chunk_fwd_save", "CkdaError", "BF16", "F32", "GATE_KDA",
            "GATE_CKDA", "GATES_F32", "GATES_LOGITS_F32", "GATES_LOGITS_BF16", "ChunkFwdPlan",
-           "decay_fwd", "decay_bwd", "decay_step", "decay_supported"]
+           "decay_fwd", "decay_bwd", "decay_step", "decay_supported",
+           "block_norm", "block_norm_bwd"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = os.path.join(_HERE, "libckda.so")
@@ -109,6 +110,13 @@ def _load():
         lib.ckda_decay_bwd.argtypes = [dd] + [vp] * 14 + [sz, vp]
         lib.ckda_decay_step.restype = i32
         lib.ckda_decay_step.argtypes = [i32] * 9 + [f32] + [vp] * 8
+        i64 = ctypes.c_int64
+        lib.ckda_block_norm.restype = i32
+        lib.ckda_block_norm.argtypes = [i64, i32, i32, i32, f32] + [vp] * 9
+        lib.ckda_block_norm_bwd_workspace_size.restype = sz
+        lib.ckda_block_norm_bwd_workspace_size.argtypes = [i64, i32, i32]
+        lib.ckda_block_norm_bwd.restype = i32
+        lib.ckda_block_norm_bwd.argtypes = [i64, i32, i32, i32, f32] + [vp] * 15 + [sz, vp]
         lib.ckda_status_string.restype = ctypes.c_char_p
         lib.ckda_status_string.argtypes = [i32]
         lib.ckda_last_error.restype = ctypes.c_char_p
@@ -620,3 +628,85 @@ def decay_step(q, k, v, alpha, state, *, gate="ckda", gates="values", scale=1.0,
                                    _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(state), _ptr(dst),
                                    _ptr(o), s))
     return o
+
+
+# ---- the norms around a block, with its gate and residual scale
+
+_ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
+
+
+def _norm_args(y, weight, gate, act, residual, scale, next_weight, **more):
+    """Checks of the norm calls' tensors; returns (rows, d, activation code)."""
+    import torch
+    _require(y.dim() >= 1 and y.shape[-1] > 0, "y must be [..., d]")
+    _require(act in _ACTS, "act must be 'none', 'sigmoid' or 'silu'")
+    d = y.shape[-1]
+    _tensors(y.device, y=y, weight=weight, gate=gate, residual=residual, scale=scale,
+             next_weight=next_weight, **more)
+    for name, t in dict(gate=gate, residual=residual, **more).items():
+        _require(t is None or (t.dtype == y.dtype and t.shape == y.shape), "%s must match y" % name)
+    for name, t in (("weight", weight), ("scale", scale), ("next_weight", next_weight)):
+        _require(t is None or (t.dtype == torch.float32 and tuple(t.shape) == (d,)),
+                 "%s must be float32 [%d]" % (name, d))
+    return y.numel() // d, d, 0 if gate is None else _ACTS[act]
+
+
+def block_norm(y, weight, *, gate=None, act="sigmoid", residual=None, scale=None,
+               next_weight=None, eps=1e-6, out=None, next_out=None, stream=None):
+    """The norm after a block, its output gate, the residual stream and the norm
+    before the next block, over the last axis of y [..., d]:
+        u = rmsnorm(y) * weight        (y itself if weight is None)
+        v = u * act(gate)              (act 'sigmoid' or 'silu'; gate shaped like y)
+        h = residual + scale * v       (scale a channel)
+        n = rmsnorm(h) * next_weight
+    y, gate and residual in bfloat16 or float32, weight, scale and next_weight
+    float32 [d].  Any part may be left out.  Returns (h, n), n None without
+    next_weight.  out may be the residual itself (updated in place)."""
+    import torch
+    lib = _load()
+    io = _dtype_code(y)
+    rows, d, code = _norm_args(y, weight, gate, act, residual, scale, next_weight, out=out,
+                               next_out=next_out)
+    _require(gate is None or code != 0, "a gate needs act 'sigmoid' or 'silu'")
+    _require(next_out is None or next_weight is not None, "next_out needs next_weight")
+    h = torch.empty_like(y) if out is None else out
+    n = next_out
+    if next_weight is not None and n is None:
+        n = torch.empty_like(y)
+    with _on(y.device, stream) as s:
+        _check(lib.ckda_block_norm(rows, d, io, code, float(eps), _ptr(y), _ptr(weight),
+                                   _ptr(gate), _ptr(residual), _ptr(scale), _ptr(next_weight),
+                                   _ptr(h), _ptr(n), s))
+    return h, n
+
+
+def block_norm_bwd(y, weight, dh, *, dnext=None, gate=None, act="sigmoid", residual=None,
+                   scale=None, next_weight=None, eps=1e-6, workspace=None, stream=None):
+    """Gradients of block_norm for dL/dh = dh and dL/dn = dnext (given exactly
+    with next_weight).  Returns (dy, dweight, dgate, dresidual, dscale,
+    dnext_weight), None where the input was left out; dy, dgate and dresidual
+    in y's dtype, the others float32 [d].  Without next_weight dresidual is dh
+    itself."""
+    import torch
+    lib = _load()
+    io = _dtype_code(y)
+    rows, d, code = _norm_args(y, weight, gate, act, residual, scale, next_weight, dh=dh, dnext=dnext)
+    _require(gate is None or code != 0, "a gate needs act 'sigmoid' or 'silu'")
+    _require((dnext is None) == (next_weight is None), "dnext is given exactly with next_weight")
+    new = lambda like: None if like is None else torch.empty_like(like)
+    dy, dw, dg, ds, dw2 = (new(t) for t in (y, weight, gate, scale, next_weight))
+    if rows == 0:
+        for t in (dw, ds, dw2):
+            if t is not None:
+                t.zero_()
+        return dy, dw, dg, None if residual is None else dh, ds, dw2
+    dx = dh if residual is not None and next_weight is None else new(residual)
+    need = int(lib.ckda_block_norm_bwd_workspace_size(rows, d, io))
+    with _on(y.device, stream) as s:
+        ws = _workspace(workspace, need, y.device)
+        _check(lib.ckda_block_norm_bwd(rows, d, io, code, float(eps), _ptr(y), _ptr(weight),
+                                       _ptr(gate), _ptr(residual), _ptr(scale), _ptr(next_weight),
+                                       _ptr(dh), _ptr(dnext), _ptr(dy), _ptr(dw), _ptr(dg),
+                                       None if dx is dh else _ptr(dx), _ptr(ds), _ptr(dw2),
+                                       _ptr(ws), ws.numel(), s))
+    return dy, dw, dg, dx, ds, dw2

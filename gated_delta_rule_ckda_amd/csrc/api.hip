@@ -787,3 +787,88 @@ ckda_status_t ckda_decay_step(int32_t N, int32_t H, int32_t qk_heads, int32_t dk
 }
 
 }  // extern "C"
+
+// ---- norms around a block -----------------------------------------------------
+namespace {
+
+ckda_status_t validate_norm(int64_t rows, int32_t d, int32_t io_dtype, int32_t act, float eps,
+                            const void* g) {
+  if (rows < 0 || d <= 0)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "bad size: rows=%lld d=%d", static_cast<long long>(rows), d);
+  if (io_dtype != CKDA_DTYPE_BF16 && io_dtype != CKDA_DTYPE_F32)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "io_dtype %d is not a ckda_dtype_t", io_dtype);
+  if (act < CKDA_NORM_GATE_NONE || act > CKDA_NORM_GATE_SILU)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "act %d is not a ckda_norm_act_t", act);
+  if (rows > 0 && (act == CKDA_NORM_GATE_NONE) != (g == nullptr))
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "g is given exactly with an activation");
+  if (!(eps >= 0.f) || eps > 3.0e38f)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "eps must be finite and not negative");
+  if (d > 16384) return fail(CKDA_ERR_UNSUPPORTED, "no norm kernel for d=%d (at most 16384)", d);
+  if (rows > (int64_t(1) << 46) / d)
+    return fail(CKDA_ERR_UNSUPPORTED, "rows * d is over 2^46");
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ckda_block_norm_bwd_workspace_size(int64_t rows, int32_t d, int32_t io_dtype) {
+  if (rows <= 0 || d <= 0 || d > 16384) return 0;
+  if (io_dtype != CKDA_DTYPE_BF16 && io_dtype != CKDA_DTYPE_F32) return 0;
+  return ckda::norm_bwd_workspace(rows, d, io_dtype);
+}
+
+ckda_status_t ckda_block_norm(int64_t rows, int32_t d, int32_t io_dtype, int32_t act, float eps,
+                              const void* y, const float* w, const void* g, const void* x,
+                              const float* s, const float* w2, void* h, void* n, void* stream) {
+  ckda_status_t st = validate_norm(rows, d, io_dtype, act, eps, g);
+  if (st != CKDA_OK) return st;
+  if ((w2 == nullptr) != (n == nullptr) && rows > 0)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "n is given exactly with w2");
+  const int64_t b = rows * d * elem_bytes(io_dtype), v = 4 * static_cast<int64_t>(d);
+  const bool some = rows > 0;
+  const Tensor ts[] = {{range("y", y, y ? b : 0), false, some}, {range("w", w, w ? v : 0), false, false},
+                       {range("g", g, g ? b : 0), false, false}, {range("x", x, x ? b : 0), false, false},
+                       {range("s", s, s ? v : 0), false, false}, {range("w2", w2, w2 ? v : 0), false, false},
+                       {range("h", h, h ? b : 0), true, some},   {range("n", n, n ? b : 0), true, false}};
+  if ((st = check_tensors(ts, 8, 3, 6)) != CKDA_OK) return st;
+  if (rows == 0) return ok();
+  const ckda::NormArgs a{rows, d, act, eps, y, w, g, x, s, w2, h, n};
+  return from_hip(ckda::launch_norm_fwd(a, io_dtype, static_cast<hipStream_t>(stream)));
+}
+
+ckda_status_t ckda_block_norm_bwd(int64_t rows, int32_t d, int32_t io_dtype, int32_t act, float eps,
+                                  const void* y, const float* w, const void* g, const void* x,
+                                  const float* s, const float* w2, const void* dh, const void* dn,
+                                  void* dy, float* dw, void* dg, void* dx, float* ds, float* dw2,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  ckda_status_t st = validate_norm(rows, d, io_dtype, act, eps, g);
+  if (st != CKDA_OK) return st;
+  if (rows == 0)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "no rows: the sums over rows would not be written");
+  if ((w2 == nullptr) != (dn == nullptr) || (w2 == nullptr) != (dw2 == nullptr))
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "dn and dw2 are given exactly with w2");
+  if ((w == nullptr) != (dw == nullptr))
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "dw is given exactly with w");
+  if ((s == nullptr) != (ds == nullptr))
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "ds is given exactly with s");
+  if ((g == nullptr) != (dg == nullptr))
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "dg is given exactly with g");
+  const int64_t b = rows * d * elem_bytes(io_dtype), v = 4 * static_cast<int64_t>(d);
+  const Tensor ts[] = {{range("y", y, y ? b : 0), false, true},   {range("w", w, w ? v : 0), false, false},
+                       {range("g", g, g ? b : 0), false, false},  {range("x", x, x ? b : 0), false, false},
+                       {range("s", s, s ? v : 0), false, false},  {range("w2", w2, w2 ? v : 0), false, false},
+                       {range("dh", dh, dh ? b : 0), false, true}, {range("dn", dn, dn ? b : 0), false, false},
+                       {range("dy", dy, dy ? b : 0), true, true}, {range("dw", dw, dw ? v : 0), true, false},
+                       {range("dg", dg, dg ? b : 0), true, false}, {range("dx", dx, dx ? b : 0), true, false},
+                       {range("ds", ds, ds ? v : 0), true, false}, {range("dw2", dw2, dw2 ? v : 0), true, false}};
+  if ((st = check_tensors(ts, 14)) != CKDA_OK) return st;
+  const size_t need = ckda_block_norm_bwd_workspace_size(rows, d, io_dtype);
+  if ((st = check_workspace(ts, 14, workspace, workspace_bytes, need)) != CKDA_OK) return st;
+  const ckda::NormArgs a{rows, d, act, eps, y, w, g, x, s, w2, nullptr, nullptr};
+  const ckda::NormGrads gr{dh, dn, dy, dw, dg, dx, ds, dw2, nullptr};
+  return from_hip(ckda::launch_norm_bwd(a, gr, io_dtype, workspace, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

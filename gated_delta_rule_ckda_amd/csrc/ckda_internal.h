@@ -235,6 +235,37 @@ size_t decay_bwd_workspace(const DecayArgs& a, int32_t io_dtype);
 launch_result launch_decay_bwd(const DecayArgs& a, DecayGrads g, int32_t io_dtype, void* ws,
                                hipStream_t s);
 
+// The norms around a block with its gate and residual scale (norm.hip); null:
+// that part is absent.
+struct NormArgs {
+  int64_t rows;
+  int32_t d;
+  int32_t act;      // ckda_norm_act_t
+  float eps;
+  const void* y;    // [rows][d] io type, as g, x, h and n
+  const float* w;   // [d], as s and w2
+  const void* g;
+  const void* x;
+  const float* s;
+  const float* w2;
+  void* h;
+  void* n;
+};
+struct NormGrads {
+  const void* dh;
+  const void* dn;
+  void* dy;
+  float* dw;
+  void* dg;
+  void* dx;
+  float* ds;
+  float* dw2;
+  float* part;      // [workgroups][3][d]
+};
+size_t norm_bwd_workspace(int64_t rows, int32_t d, int32_t io_dtype);
+launch_result launch_norm_fwd(const NormArgs& a, int32_t io_dtype, hipStream_t s);
+launch_result launch_norm_bwd(const NormArgs& a, NormGrads g, int32_t io_dtype, void* ws, hipStream_t s);
+
 // ---- small device helpers shared by the kernels --------------------------
 
 // bf16 <-> f32.  Conversion to bf16 rounds to nearest even (finite inputs).

@@ -444,6 +444,51 @@ ckda_status_t ckda_decay_step(int32_t N, int32_t H, int32_t qk_heads, int32_t dk
                               const void* v, const void* alpha, const float* h0, float* ht,
                               void* o, void* stream);
 
+/*
+ * The norms before and after a block, fused with its gate and residual scale.
+ * Each of `rows` rows of d elements, in float32:
+ *
+ *   u = y / sqrt(mean(y^2) + eps) * w     norm after the block (w NULL: u = y)
+ *   v = u * act(g)                        its output gate (g NULL: v = u)
+ *   h = x + s * v                         residual stream and its scale a
+ *                                         channel (x NULL: s * v; s NULL: 1)
+ *   n = h / sqrt(mean(h^2) + eps) * w2    norm before the next block, formed
+ *                                         from h before its rounding (w2 and n
+ *                                         NULL: not computed)
+ *
+ * y, g, x, h, n: [rows][d] in the io dtype; w, s, w2: [d] float32.  A gated
+ * norm of every head of an attention output takes the heads as rows (rows =
+ * tokens * H, d = dv).  h may be x's buffer (the stream updated in place);
+ * other overlaps with an output are refused.  d from 1 to 16384, any; rows
+ * whose d is a multiple of 8 (bf16) or 4 (float32) move in 16-byte accesses.
+ * A gate of -inf gives v = 0 with both activations.
+ */
+typedef enum {
+  CKDA_NORM_GATE_NONE = 0,    /* g must be NULL */
+  CKDA_NORM_GATE_SIGMOID = 1, /* act(g) = sigmoid(g) */
+  CKDA_NORM_GATE_SILU = 2     /* act(g) = g sigmoid(g) */
+} ckda_norm_act_t;
+
+ckda_status_t ckda_block_norm(int64_t rows, int32_t d, int32_t io_dtype, int32_t act, float eps,
+                              const void* y, const float* w, const void* g, const void* x,
+                              const float* s, const float* w2, void* h, void* n, void* stream);
+
+/*
+ * Its gradients for dh = dL/dh and dn = dL/dn (io dtype; dn NULL exactly
+ * where w2 is), from the forward's inputs.  dy, dg, dx in the io dtype; dw,
+ * ds, dw2 [d] float32, summed over the rows in a fixed order.  dg, dw, ds and
+ * dw2 are given exactly where g, w, s and w2 are; dx may be NULL (without w2
+ * it equals dh), and x is read only with w2.  No output overlaps an input or
+ * another output.  `workspace`: ckda_block_norm_bwd_workspace_size bytes, a
+ * column sum a workgroup; 256-byte aligned.
+ */
+size_t ckda_block_norm_bwd_workspace_size(int64_t rows, int32_t d, int32_t io_dtype);
+ckda_status_t ckda_block_norm_bwd(int64_t rows, int32_t d, int32_t io_dtype, int32_t act, float eps,
+                                  const void* y, const float* w, const void* g, const void* x,
+                                  const float* s, const float* w2, const void* dh, const void* dn,
+                                  void* dy, float* dw, void* dg, void* dx, float* ds, float* dw2,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* ckda_status_string(int32_t status);
 
