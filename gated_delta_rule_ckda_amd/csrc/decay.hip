@@ -2,6 +2,8 @@
 // backward and long prompts run, and the single-token step.
 //
 //     S_t = a_t S_{t-1} + k_t v_t^T,     o_t = scale S_t^T q_t
+#include <type_traits>
+
 #include "decay_ops.h"
 
 namespace ckda {
@@ -11,43 +13,48 @@ constexpr int kNT = 256;  // 4 waves
 
 // ---- forward -------------------------------------------------------------------
 // One workgroup walks one (segment, head) over its chunks for DVS columns of
-// the state, which stays in the matrix accumulators in float32; per chunk
+// the state; per chunk
 //
-//   P^T = K Q^T                  wave w: the 16 tokens 16w.. of Q
-//   O^T = S^T Q^T E + V^T (P D)^T
-//   S   = g S + K^T (W V)        wave w: DKP/4 rows of S
+//   P^T = K Q^T
+//   O^T = E S^T Q^T + V^T (D P)^T
+//   S   = g S + K^T (W V)
 //
-// P^T leaves the accumulators as the next product's operand.  K, V and a copy
-// of S in the io type pass through LDS; the next chunk's rows are loaded into
-// registers while this one is computed.
+// Half of the eight waves read out (wave w: the 16 tokens 16w.. of Q), half
+// keep the state (wave w: DKP/4 of its rows, in the matrix accumulators, in
+// float32): the two run side by side on one chunk, since the read-out takes
+// the state from before it.  P^T leaves the accumulators as the next
+// product's operand.  K, V, W V and a copy of S in the io type pass through
+// LDS; the next chunk's rows are loaded into registers meanwhile.
 template <class Op, int DKP, int DVS>
 struct FwdCfg {
   using T = typename Op::T;
-  static constexpr int C = kDecayChunk, ES = sizeof(T);
+  static constexpr int C = kDecayChunk, ES = sizeof(T), NT = 512;
   static constexpr int LDK = frag_stride(DKP, ES), LDV = cross_stride(DVS, ES);
   static constexpr int O_K = 0, O_V = O_K + C * LDK * ES, O_H = O_V + C * LDV * ES,
-                       O_L = O_H + C * LDV * ES, O_S = O_L + (Fr<Op>::kSplit ? C * LDV * ES : 0),
-                       O_G = align16(O_S + DVS * LDK * ES),
+                       O_S = O_H + Fr<Op>::kTerms * C * LDV * ES, O_G = align16(O_S + DVS * LDK * ES),
                        BYTES = O_G + 2 * static_cast<int>(sizeof(Gates<C>));
+  static constexpr int WAVES = ES == 2 ? 4 : 2;  // a SIMD
 };
 
 template <class Op, int DKP, int DVS>
-__global__ __launch_bounds__(kNT, 2) void decay_fwd_kernel(DecayArgs a) {
+__global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::WAVES)) void decay_fwd_kernel(
+    DecayArgs a) {
   using Cfg = FwdCfg<Op, DKP, DVS>;
   using X = Fr<Op>;
   using T = typename Op::T;
   using F = typename X::F;
-  constexpr int C = Cfg::C, LDK = Cfg::LDK, LDV = Cfg::LDV, KS = X::KS;
+  constexpr int C = Cfg::C, LDK = Cfg::LDK, LDV = Cfg::LDV, KS = X::KS, NW = 256;
   constexpr int NQ = DKP / KS, MT = DKP / 64, NTL = DVS / 16, EPP = 16 / sizeof(T);
   extern __shared__ __align__(16) unsigned char smem[];
   T* sK = reinterpret_cast<T*>(smem + Cfg::O_K);
   T* sV = reinterpret_cast<T*>(smem + Cfg::O_V);
   T* sH = reinterpret_cast<T*>(smem + Cfg::O_H);
-  T* sL = reinterpret_cast<T*>(smem + Cfg::O_L);
   T* sS = reinterpret_cast<T*>(smem + Cfg::O_S);
   Gates<C>* sG = reinterpret_cast<Gates<C>*>(smem + Cfg::O_G);
 
-  const int t = threadIdx.x, lane = t & 63, w = uniform32(t >> 6), l16 = lane & 15, lq = lane >> 4;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, lq = lane >> 4;
+  const int wave = uniform32(threadIdx.x >> 6), w = wave & 3, t = threadIdx.x & (NW - 1);
+  const bool reads_out = wave < 4;
   const int nslab = (a.dv + DVS - 1) / DVS;
   int64_t chain;
   int slab;
@@ -63,21 +70,111 @@ __global__ __launch_bounds__(kNT, 2) void decay_fwd_kernel(DecayArgs a) {
   }
   const int hk = h / (a.H / a.Hk), c0 = slab * DVS;
   const int vcols = a.dv - c0 < DVS ? a.dv - c0 : DVS;
-  const int64_t ldq = static_cast<int64_t>(a.Hk) * a.dk, ldv = static_cast<int64_t>(a.H) * a.dv;
-  const T* gq = static_cast<const T*>(a.q) + pc.begin * ldq + static_cast<int64_t>(hk) * a.dk;
-  const T* gk = static_cast<const T*>(a.k) + pc.begin * ldq + static_cast<int64_t>(hk) * a.dk;
-  const T* gv = static_cast<const T*>(a.v) + pc.begin * ldv + static_cast<int64_t>(h) * a.dv + c0;
-  T* go = static_cast<T*>(a.o) + pc.begin * ldv + static_cast<int64_t>(h) * a.dv + c0;
-  const bool ckda = a.gate_range == CKDA_GATE_CKDA;
+  const int ldq = a.Hk * a.dk, ldv = a.H * a.dv;
+  const int64_t oq = pc.begin * ldq + static_cast<int64_t>(hk) * a.dk;
+  const int64_t ov = pc.begin * ldv + static_cast<int64_t>(h) * a.dv + c0;
   const int nch = (pc.len + C - 1) / C;
+  auto first_token = [&](int c) { return c < nch ? static_cast<int64_t>(c) * C : 0; };
+
+  if (reads_out) {
+    const T* gq = static_cast<const T*>(a.q) + oq;
+    const T* gk = static_cast<const T*>(a.k) + oq;
+    T* go = static_cast<T*>(a.o) + ov;
+    const int r = 16 * w + l16;  // this lane's token
+    RowTile<T, C, DKP, NW> rk;
+    rk.init(ldq, a.dk, t);
+    uint4 rq[NQ];
+    int offq[NQ];
+#pragma unroll
+    for (int s = 0; s < NQ; ++s) {
+      const int col = KS * s + EPP * lq;
+      offq[s] = col < a.dk ? (r * ldq + col) * Cfg::ES : kNoOffset;
+    }
+    auto load = [&](int c) {  // zeros past the last chunk
+      const int rows = c < nch ? pc.len - c * C : 0;
+      rk.load(gk + first_token(c) * ldq, ldq, rows, a.dk);
+      const rsrc_t rs = rows_rsrc(gq + first_token(c) * ldq, ldq, rows, a.dk, C);
+#pragma unroll
+      for (int s = 0; s < NQ; ++s) rq[s] = load_piece(rs, offq[s]);
+    };
+    if (nch > 0) {
+      load(0);
+      __syncthreads();
+      rk.store(sK, LDK, t);
+    }
+    for (int c = 0; c < nch; ++c) {
+      F fq[NQ];
+#pragma unroll
+      for (int s = 0; s < NQ; ++s) fq[s] = *reinterpret_cast<const F*>(&rq[s]);
+      load(c + 1);
+      __syncthreads();  // rows, state copy and gates of chunk c are in LDS
+      const Gates<C>& G = sG[c & 1];
+      const bool fast = G.fast != 0;
+      f32x4 p[C / 16];
+#pragma unroll
+      for (int j = 0; j < C / 16; ++j) p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      auto tile_pair = [&](auto J) {
+        constexpr int j0 = decltype(J)::value;
+#pragma unroll
+        for (int j = j0; j < j0 + 2; ++j) {
+          const T* rowk = sK + (16 * j + l16) * LDK;
+#pragma unroll
+          for (int s = 0; s < NQ; ++s) Op::mma(p[j], X::row(rowk, s, lq), fq[s]);
+        }
+      };
+      tile_pair(std::integral_constant<int, 0>{});
+      if (w >= 2) tile_pair(std::integral_constant<int, 2>{});
+      // where D factors, its row part multiplies the sum instead of each term
+      float row = 1.f;
+      if (fast) {
+        row = G.er[r];
+#pragma unroll
+        for (int j = 0; j < C / 16; ++j) {
+          p[j] *= *reinterpret_cast<const f32x4*>(&G.ej[16 * j + 4 * lq]);
+          if (j >= w) {  // this wave's diagonal tile, or past it
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[j][i] = 16 * j + 4 * lq + i <= r ? p[j][i] : 0.f;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < C / 16; ++j) p[j] = decayed(p[j], decay_of(G, r, 16 * j + 4 * lq, false));
+      }
+      F pf[C / KS];
+      Op::template frags<C>(pf, p);
+      f32x4 o[NTL], x[NTL];
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) {
+        o[n] = x[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const T* rows = sS + (16 * n + l16) * LDK;
+#pragma unroll
+        for (int s = 0; s < NQ; ++s) Op::mma(x[n], X::row(rows, s, lq), fq[s]);
+      }
+#pragma unroll
+      for (int ks = 0; ks < C / KS; ++ks)
+        if (2 * ks < C / KS || w >= 2) {
+#pragma unroll
+          for (int n = 0; n < NTL; ++n) Op::mma(o[n], X::across(sV, LDV, KS * ks, 16 * n, lane), pf[ks]);
+        }
+      const float e = G.E[r] * a.scale;
+      row *= a.scale;
+      if (c * C + r < pc.len) {
+        T* dst = go + static_cast<int64_t>(c * C + r) * ldv;
+#pragma unroll
+        for (int n = 0; n < NTL; ++n)
+          if (16 * n + 4 * lq < vcols) Op::store4(dst + 16 * n + 4 * lq, x[n] * e + o[n] * row);
+      }
+      __syncthreads();  // chunk c is done with LDS; gates of chunk c + 1 are there
+      rk.store(sK, LDK, t);
+    }
+    return;
+  }
 
   // state tile (m, n): rows dk = row0 + 16 m + 4 lq + i, column c0 + 16 n + l16
   const int row0 = w * (DKP / 4);
   const int64_t sbase = (static_cast<int64_t>(pc.n) * a.H + h) * a.dk * a.dv;
   f32x4 S[MT][NTL];
-  {
-    const float* src = a.seg > 0 ? a.entry + (static_cast<int64_t>(slot) * a.H + h) * a.dk * a.dv
-                                 : (a.h0 ? a.h0 + sbase : nullptr);
+  auto each = [&](auto f) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -85,9 +182,12 @@ __global__ __launch_bounds__(kNT, 2) void decay_fwd_kernel(DecayArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = row0 + 16 * m + 4 * lq + i, c = 16 * n + l16;
-          S[m][n][i] = src && r < a.dk && c < vcols ? src[static_cast<int64_t>(r) * a.dv + c0 + c] : 0.f;
+          f(S[m][n], i, r < a.dk && c < vcols, static_cast<int64_t>(r) * a.dv + c0 + c);
         }
-  }
+  };
+  const float* src = a.seg > 0 ? a.entry + (static_cast<int64_t>(slot) * a.H + h) * a.dk * a.dv
+                               : (a.h0 ? a.h0 + sbase : nullptr);
+  each([&](f32x4& x, int i, bool in, int64_t at) { x[i] = src && in ? src[at] : 0.f; });
   auto stage_state = [&]() {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -95,146 +195,69 @@ __global__ __launch_bounds__(kNT, 2) void decay_fwd_kernel(DecayArgs a) {
       for (int n = 0; n < NTL; ++n)
         Op::store4(sS + (16 * n + l16) * LDK + row0 + 16 * m + 4 * lq, S[m][n]);
   };
-
-  RowTile<T, C, DKP, kNT> rk;
-  RowTile<T, C, DVS, kNT> rv;
-  uint4 rq[NQ];
-  auto load_chunk = [&](int c) {
-    const int rows = pc.len - c * C;  // <= 0 past the last chunk: zeros, no loads
-    const int64_t o = static_cast<int64_t>(c) * C;
-    rk.load(gk + o * ldq, ldq, rows, a.dk, t);
-    rv.load(gv + o * ldv, ldv, rows, vcols, t);
-    const int r = 16 * w + l16;
-#pragma unroll
-    for (int s = 0; s < NQ; ++s) {
-      const int c8 = KS * s + EPP * lq;
-      rq[s] = make_uint4(0, 0, 0, 0);
-      if (r < rows && c8 < a.dk) rq[s] = *reinterpret_cast<const uint4*>(gq + (o + r) * ldq + c8);
-    }
+  const bool ckda = a.gate_range == CKDA_GATE_CKDA;
+  const T* gv = static_cast<const T*>(a.v) + ov;
+  using RV = RowTile<T, C, DVS, NW>;
+  RV rv;
+  rv.init(ldv, vcols, t);
+  auto load = [&](int c) {
+    rv.load(gv + first_token(c) * ldv, ldv, c < nch ? pc.len - c * C : 0, vcols);
   };
   auto load_gate = [&](int c) {
-    const int i = c * C + lane;
-    return i < pc.len ? gate_stored(a, pc.begin + i, h) : 0.f;
+    return load_gate_bits(a, pc.begin + first_token(c), c < nch ? pc.len - c * C : 0, h, lane);
+  };
+  auto fill_gates = [&](int c, uint32_t bits) {
+    gates_fill<C>(sG[c & 1], gate_of_bits(bits, a.gate_input), c * C + lane < pc.len, a.gate_input, ckda, lane);
   };
   auto stage_rows = [&](const Gates<C>& G) {
-    rk.store(sK, LDK, t);
     rv.store(sV, LDV, t);
-    using RV = RowTile<T, C, DVS, kNT>;
 #pragma unroll
     for (int u = 0; u < RV::NP; ++u) {
-      const int p = t + kNT * u, row = p / RV::PPR, c = (p % RV::PPR) * RV::EPP;
-      store_scaled<T>(rv.r[u], G.W[row], sH + row * LDV + c, sL + row * LDV + c);
+      const int p = t + NW * u, row = p / RV::PPR, c = (p % RV::PPR) * RV::EPP;
+      store_scaled<T>(rv.r[u], G.W[row], sH + row * LDV + c, C * LDV);
     }
   };
-
   if (nch > 0) {
-    load_chunk(0);
-    if (w == 0) gates_fill<C>(sG[0], load_gate(0), lane < pc.len, a.gate_input, ckda, lane);
+    const uint32_t bits = load_gate(0);
+    load(0);
+    if (w == 0) fill_gates(0, bits);
     stage_state();
     __syncthreads();
     stage_rows(sG[0]);
   }
-  F fq[NQ];
   for (int c = 0; c < nch; ++c) {
-#pragma unroll
-    for (int s = 0; s < NQ; ++s) fq[s] = *reinterpret_cast<const F*>(&rq[s]);
-    load_chunk(c + 1);
-    const bool gw = w == ((c + 1) & 3);
-    float xg = 0.f;
-    if (gw) xg = load_gate(c + 1);
+    const uint32_t bits = load_gate(c + 1);
+    load(c + 1);
     __syncthreads();  // rows, state copy and gates of chunk c are in LDS
-    const Gates<C>& G = sG[c & 1];
-    const float g = G.g;
-    const bool fast = G.fast != 0;
-    const int r = 16 * w + l16;
-
-    f32x4 p[C / 16];
-#pragma unroll
-    for (int j = 0; j < C / 16; ++j) {
-      p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (j <= w) {
-        const T* rowk = sK + (16 * j + l16) * LDK;
-#pragma unroll
-        for (int s = 0; s < NQ; ++s) Op::mma(p[j], X::row(rowk, s, lq), fq[s]);
-        const int j0 = 16 * j + 4 * lq;
-        if (fast) {
-          const f32x4 ej = *reinterpret_cast<const f32x4*>(&G.ej[j0]);
-          const float er = G.er[r];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[j][i] = j0 + i <= r ? (p[j][i] * er) * ej[i] : 0.f;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float d = d_slow(G, r, j0 + i);
-            p[j][i] = d != 0.f ? p[j][i] * d : 0.f;  // nothing passes a zero gate
-          }
-        }
-      }
-    }
-    F pf[C / KS];
-    Op::template frags<C>(pf, p);
-
-    f32x4 o[NTL];
-    const float e = G.E[r];
-#pragma unroll
-    for (int n = 0; n < NTL; ++n) {
-      o[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const T* rows = sS + (16 * n + l16) * LDK;
-#pragma unroll
-      for (int s = 0; s < NQ; ++s) Op::mma(o[n], X::row(rows, s, lq), fq[s]);
-      o[n] *= e;
-    }
-#pragma unroll
-    for (int ks = 0; ks < C / KS; ++ks)
-      if (KS * ks <= 16 * w) {
-#pragma unroll
-        for (int n = 0; n < NTL; ++n) Op::mma(o[n], X::across(sV, LDV, KS * ks, 16 * n, lane), pf[ks]);
-      }
+    const float g = sG[c & 1].g;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NTL; ++n) S[m][n] *= g;
 #pragma unroll
     for (int ks = 0; ks < C / KS; ++ks) {
-      F vh[NTL], vl[NTL];
+      F ka[MT];
 #pragma unroll
-      for (int n = 0; n < NTL; ++n) {
-        vh[n] = X::across(sH, LDV, KS * ks, 16 * n, lane);
-        if constexpr (X::kSplit) vl[n] = X::across(sL, LDV, KS * ks, 16 * n, lane);
-      }
+      for (int m = 0; m < MT; ++m) ka[m] = X::across(sK, LDK, KS * ks, row0 + 16 * m, lane);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const F ka = X::across(sK, LDK, KS * ks, row0 + 16 * m, lane);
+      for (int p = 0; p < X::kTerms; ++p)
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
-          Op::mma(S[m][n], ka, vh[n]);
-          if constexpr (X::kSplit) Op::mma(S[m][n], ka, vl[n]);
-        }
-      }
-    }
-    const int row = c * C + r;
-    if (row < pc.len) {
-      T* dst = go + row * ldv;
+          const F vb = X::across(sH + p * C * LDV, LDV, KS * ks, 16 * n, lane);
 #pragma unroll
-      for (int n = 0; n < NTL; ++n)
-        if (16 * n + 4 * lq < vcols) Op::store4(dst + 16 * n + 4 * lq, o[n] * a.scale);
+          for (int m = 0; m < MT; ++m) Op::mma(S[m][n], ka[m], vb);
+        }
     }
-    if (gw) gates_fill<C>(sG[(c + 1) & 1], xg, (c + 1) * C + lane < pc.len, a.gate_input, ckda, lane);
+    if (w == ((c + 1) & 3)) fill_gates(c + 1, bits);
     __syncthreads();  // chunk c is done with LDS; gates of chunk c + 1 are there
     stage_state();
     stage_rows(sG[(c + 1) & 1]);
   }
   if (a.ht && pc.s == pc.count - 1) {
     float* dst = a.ht + sbase;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NTL; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = row0 + 16 * m + 4 * lq + i, c = 16 * n + l16;
-          if (rr < a.dk && c < vcols) dst[static_cast<int64_t>(rr) * a.dv + c0 + c] = S[m][n][i];
-        }
+    each([&](const f32x4& x, int i, bool in, int64_t at) {
+      if (in) dst[at] = x[i];
+    });
   }
 }
 
@@ -254,8 +277,8 @@ struct StateCfg {
   using T = typename Op::T;
   static constexpr int ES = sizeof(T);
   static constexpr int LDK = frag_stride(DKP, ES), LDV = cross_stride(DVS, ES);
-  static constexpr int O_K = 0, O_H = O_K + C * LDK * ES, O_L = O_H + C * LDV * ES,
-                       O_G = align16(O_L + (Fr<Op>::kSplit ? C * LDV * ES : 0)),
+  static constexpr int O_K = 0, O_H = O_K + C * LDK * ES,
+                       O_G = align16(O_H + Fr<Op>::kTerms * C * LDV * ES),
                        O_R = O_G + 2 * static_cast<int>(sizeof(Gates<C>)), BYTES = O_R + 16;
 };
 
@@ -269,7 +292,6 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   T* sK = reinterpret_cast<T*>(smem + Cfg::O_K);
   T* sH = reinterpret_cast<T*>(smem + Cfg::O_H);
-  T* sL = reinterpret_cast<T*>(smem + Cfg::O_L);
   Gates<C>* sG = reinterpret_cast<Gates<C>*>(smem + Cfg::O_G);
   float* sR = reinterpret_cast<float*>(smem + Cfg::O_R);
 
@@ -291,7 +313,7 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
   if (MODE == kSegment && pc.s == (REV ? 0 : pc.count - 1)) return;
   const int hk = h / (a.H / a.Hk), c0 = slab * DVS;
   const int vcols = a.dv - c0 < DVS ? a.dv - c0 : DVS;
-  const int64_t ldx = static_cast<int64_t>(a.Hk) * a.dk, ldy = static_cast<int64_t>(a.H) * a.dv;
+  const int ldx = a.Hk * a.dk, ldy = a.H * a.dv;
   const T* gx = static_cast<const T*>(REV ? a.q : a.k) + pc.begin * ldx + static_cast<int64_t>(hk) * a.dk;
   const T* gy = static_cast<const T*>(REV ? a.o : a.v) + pc.begin * ldy + static_cast<int64_t>(h) * a.dv + c0;
   const bool ckda = a.gate_range == CKDA_GATE_CKDA;
@@ -326,17 +348,23 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
 
   RowTile<T, C, DKP, kNT> rx;
   RowTile<T, C, DVS, kNT> ry;
+  rx.init(ldx, a.dk, t);
+  ry.init(ldy, vcols, t);
   auto chunk_at = [&](int i) { return REV ? nch - 1 - i : i; };
   auto load_chunk = [&](int i) {
     const int c = chunk_at(i);
     const int rows = i < nch ? pc.len - c * C : 0;
     const int64_t o = static_cast<int64_t>(i < nch ? c : 0) * C;
-    rx.load(gx + o * ldx, ldx, rows, a.dk, t);
-    ry.load(gy + o * ldy, ldy, rows, vcols, t);
+    rx.load(gx + o * ldx, ldx, rows, a.dk);
+    ry.load(gy + o * ldy, ldy, rows, vcols);
   };
-  auto gate_ok = [&](int i) { return i < nch && lane < C && chunk_at(i) * C + lane < pc.len; };
   auto load_gate = [&](int i) {
-    return gate_ok(i) ? gate_stored(a, pc.begin + chunk_at(i) * C + lane, h) : 0.f;
+    const int c = i < nch ? chunk_at(i) : 0, rows = i < nch ? pc.len - c * C : 0;
+    return load_gate_bits(a, pc.begin + static_cast<int64_t>(c) * C, rows < C ? rows : C, h, lane);
+  };
+  auto fill_gates = [&](int i, uint32_t bits) {
+    const bool ok = i < nch && lane < C && chunk_at(i) * C + lane < pc.len;
+    gates_fill<C>(sG[i & 1], gate_of_bits(bits, a.gate_input), ok, a.gate_input, ckda, lane);
   };
   auto stage_rows = [&](const Gates<C>& G) {
     rx.store(sK, LDK, t);
@@ -344,8 +372,7 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
 #pragma unroll
     for (int u = 0; u < RY::NP; ++u) {
       const int p = t + kNT * u, row = p / RY::PPR, c = (p % RY::PPR) * RY::EPP;
-      store_scaled<T>(ry.r[u], REV ? G.E[row] * a.scale : G.W[row], sH + row * LDV + c,
-                      sL + row * LDV + c);
+      store_scaled<T>(ry.r[u], REV ? G.E[row] * a.scale : G.W[row], sH + row * LDV + c, C * LDV);
     }
   };
   int64_t cslot = 0;
@@ -353,16 +380,15 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
 
   float gain = 1.f;
   if (nch > 0) {
+    const uint32_t bits = load_gate(0);
     load_chunk(0);
-    if (w == 0) gates_fill<C>(sG[0], load_gate(0), gate_ok(0), a.gate_input, ckda, lane);
+    if (w == 0) fill_gates(0, bits);
     __syncthreads();
     stage_rows(sG[0]);
   }
   for (int i = 0; i < nch; ++i) {
+    const uint32_t bits = load_gate(i + 1);
     load_chunk(i + 1);
-    const bool gw = w == ((i + 1) & 3);
-    float xg = 0.f;
-    if (gw) xg = load_gate(i + 1);
     if (MODE == kChunks) {  // the state met at this chunk
       const int64_t rec = ((cslot + chunk_at(i)) * a.H + h) * a.dk * a.dv;
       T* dst = static_cast<T*>(REV ? a.adjoints : a.states) + rec;
@@ -399,23 +425,19 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
       for (int n = 0; n < NTL; ++n) S[m][n] *= g;
 #pragma unroll
     for (int ks = 0; ks < C / KS; ++ks) {
-      F vh[NTL], vl[NTL];
+      F ka[MT];
 #pragma unroll
-      for (int n = 0; n < NTL; ++n) {
-        vh[n] = X::across(sH, LDV, KS * ks, 16 * n, lane);
-        if constexpr (X::kSplit) vl[n] = X::across(sL, LDV, KS * ks, 16 * n, lane);
-      }
+      for (int m = 0; m < MT; ++m) ka[m] = X::across(sK, LDK, KS * ks, row0 + 16 * m, lane);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const F ka = X::across(sK, LDK, KS * ks, row0 + 16 * m, lane);
+      for (int p = 0; p < X::kTerms; ++p)
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
-          Op::mma(S[m][n], vh[n], ka);
-          if constexpr (X::kSplit) Op::mma(S[m][n], vl[n], ka);
+          const F vb = X::across(sH + p * C * LDV, LDV, KS * ks, 16 * n, lane);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) Op::mma(S[m][n], vb, ka[m]);
         }
-      }
     }
-    if (gw) gates_fill<C>(sG[(i + 1) & 1], xg, gate_ok(i + 1), a.gate_input, ckda, lane);
+    if (w == ((i + 1) & 3)) fill_gates(i + 1, bits);
     __syncthreads();
     stage_rows(sG[(i + 1) & 1]);
   }
@@ -552,8 +574,8 @@ launch_result launch_fwd_t(const DecayArgs& a, int64_t grid, hipStream_t s) {
   constexpr int lds = FwdCfg<Op, DKP, kSlab>::BYTES;
   const launch_result e = allow_lds<decay_fwd_kernel<Op, DKP, kSlab>>(lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((decay_fwd_kernel<Op, DKP, kSlab>), dim3(static_cast<unsigned>(grid)), dim3(kNT),
-                     lds, s, a);
+  hipLaunchKernelGGL((decay_fwd_kernel<Op, DKP, kSlab>), dim3(static_cast<unsigned>(grid)),
+                     dim3(FwdCfg<Op, DKP, kSlab>::NT), lds, s, a);
   return hipGetLastError();
 }
 

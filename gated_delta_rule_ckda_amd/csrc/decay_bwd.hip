@@ -63,8 +63,8 @@ __global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGr
   const int hk = static_cast<int>(blockIdx.x % a.Hk), group = a.H / a.Hk;
   const Piece pc = piece_of(a, static_cast<int>(slot), C, lane);
   if (pc.n < 0 || pc.len == 0) return;
-  const int64_t ldq = static_cast<int64_t>(a.Hk) * a.dk, ldv = static_cast<int64_t>(a.H) * a.dv;
-  const int64_t oq = pc.begin * ldq + static_cast<int64_t>(hk) * a.dk;
+  const int ldq = a.Hk * a.dk, ldv = a.H * a.dv;
+  const int64_t oq = pc.begin * static_cast<int64_t>(ldq) + static_cast<int64_t>(hk) * a.dk;
   const bool ckda = a.gate_range == CKDA_GATE_CKDA;
   const int nslab = (a.dv + kDecaySlab - 1) / kDecaySlab;
   const int col0 = w * (DP / 4);  // this wave's columns of dq, dk, dv
@@ -76,8 +76,12 @@ __global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGr
     for (int n = 0; n < RT; ++n) dq[m][n] = dk[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   RowTile<T, C, DP, kNT> rq, rk, rv, ro;
-  rq.load(static_cast<const T*>(a.q) + oq, ldq, pc.len, a.dk, t);
-  rk.load(static_cast<const T*>(a.k) + oq, ldq, pc.len, a.dk, t);
+  rq.init(ldq, a.dk, t);
+  rk.init(ldq, a.dk, t);
+  rv.init(ldv, a.dv, t);
+  ro.init(ldv, a.dv, t);
+  rq.load(static_cast<const T*>(a.q) + oq, ldq, pc.len, a.dk);
+  rk.load(static_cast<const T*>(a.k) + oq, ldq, pc.len, a.dk);
   rq.store(sQ, LD, t);
   rk.store(sK, LD, t);
 
@@ -85,10 +89,11 @@ __global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGr
     const int h = hk * group + hv;
     const int64_t ov = pc.begin * ldv + static_cast<int64_t>(h) * a.dv;
     const int64_t rec = (slot * a.H + h) * a.dk * a.dv;
-    rv.load(static_cast<const T*>(a.v) + ov, ldv, pc.len, a.dv, t);
-    ro.load(static_cast<const T*>(gr.dout) + ov, ldv, pc.len, a.dv, t);
+    rv.load(static_cast<const T*>(a.v) + ov, ldv, pc.len, a.dv);
+    ro.load(static_cast<const T*>(gr.dout) + ov, ldv, pc.len, a.dv);
     RowTile<T, DP, DP, kNT> ra;
-    ra.load(static_cast<const T*>(a.adjoints) + rec, a.dv, a.dk, a.dv, t);
+    ra.init(a.dv, a.dv, t);
+    ra.load(static_cast<const T*>(a.adjoints) + rec, a.dv, a.dk, a.dv);
     const bool tok = lane < C && lane < pc.len;
     float xg = 0.f;
     if (w == 0) {
@@ -118,12 +123,10 @@ __global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGr
           Op::mma(n, X::row(sV + (16 * tj + l16) * LD, s, lq), X::row(sO + i * LD, s, lq));
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          sM[i * LDM + j0 + r] = p[r] * n[r] * a.scale;
-          const float d = (fast ? (j0 + r <= i ? G.er[i] * G.ej[j0 + r] : 0.f) : d_slow(G, i, j0 + r)) * a.scale;
-          p[r] = d != 0.f ? p[r] * d : 0.f;
-          n[r] = d != 0.f ? n[r] * d : 0.f;
-        }
+        for (int r = 0; r < 4; ++r) sM[i * LDM + j0 + r] = p[r] * n[r] * a.scale;
+        const f32x4 d = decay_of(G, i, j0, fast) * a.scale;
+        p = decayed(p, d);
+        n = decayed(n, d);
       }
       Op::store4(sP + i * LDC + j0, p);
       Op::store4(sN + i * LDC + j0, n);
@@ -213,7 +216,7 @@ __global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGr
             Op::mma(acc, X::across(sO, LD, KS * ks, col0 + 16 * m, lane),
                     X::across(sP, LDC, KS * ks, 16 * n, lane));
         const int c = col0 + 16 * m + 4 * lq;
-        if (j < pc.len && c < a.dv) Op::store4(gdv + j * ldv + c, acc);
+        if (j < pc.len && c < a.dv) Op::store4(gdv + static_cast<int64_t>(j) * ldv + c, acc);
       }
     }
     __syncthreads();  // z, y of all waves; LDS rows may change after the next
@@ -223,17 +226,17 @@ __global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGr
       float R = (sZ[i] + sZ[C + i]) + (sZ[2 * C + i] + sZ[3 * C + i]);
       const float y = (sY[i] + sY[C + i]) + (sY[2 * C + i] + sY[3 * C + i]);
       float Xr = sAl[C], da = 0.f;
-      for (int s = 0; s < C; ++s) {
-        const float al = sAl[s], ys = __shfl(y, s, 64);
-        float m = 0.f, d = 0.f;
-        if (s <= i) {
-          m = sM[i * LDM + s];
-          d = fast ? G.er[i] * G.ej[s] : d_slow(G, i, s);
-          sM[i * LDM + s] = d != 0.f ? d * R : 0.f;
+      for (int s0 = 0; s0 < C; s0 += 4) {
+        const f32x4 d = decay_of(G, i, s0, fast);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int s = s0 + e;
+          const float al = sAl[s], ys = __shfl(y, s, 64), m = sM[i * LDM + s];
+          sM[i * LDM + s] = d[e] != 0.f ? d[e] * R : 0.f;  // past the diagonal: 0
+          R = al * R + m;
+          da = s == i ? G.W[s] * Xr : da;
+          Xr = al * Xr + ys;
         }
-        R = al * R + m;
-        if (s == i) da = G.W[s] * Xr;
-        Xr = al * Xr + ys;
       }
       wave_lds_sync();
       for (int r = i; r < C; ++r) da += sM[r * LDM + i];
@@ -262,8 +265,8 @@ __global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGr
       for (int m = 0; m < CT; ++m) {
         const int c = col0 + 16 * m + 4 * lq;
         if (c < a.dk) {
-          Op::store4(gdq + j * ldq + c, dq[m][n]);
-          Op::store4(gdk + j * ldq + c, dk[m][n]);
+          Op::store4(gdq + static_cast<int64_t>(j) * ldq + c, dq[m][n]);
+          Op::store4(gdk + static_cast<int64_t>(j) * ldq + c, dk[m][n]);
         }
       }
     }

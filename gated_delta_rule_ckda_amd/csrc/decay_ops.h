@@ -100,28 +100,34 @@ struct GateLog {
   float l2;
   bool neg, zero;
 };
+// v_log_f32 is within 1.2e-7 of the value over all normal floats, also next to
+// 1 (measured); smaller ones are scaled up first.
 __device__ __forceinline__ float log2_of(float a) {  // a > 0
-  return (a > 0.5f && a < 2.f) ? log1pf(a - 1.f) * kLog2e : log2f(a);
+  const bool tiny = a < 0x1p-100f;
+  return __builtin_amdgcn_logf(tiny ? a * 0x1p64f : a) - (tiny ? 64.f : 0.f);
+}
+// log2(1 + y), -1 < y <= 1: the rounding of 1 + y is undone by the factor
+__device__ __forceinline__ float log2_1p(float y) {
+  const float u = 1.f + y, r = u - 1.f;
+  return r == 0.f ? y * kLog2e : __builtin_amdgcn_logf(u) * (y * __builtin_amdgcn_rcpf(r));
 }
 __device__ __forceinline__ GateLog gate_log(float x, int gate_input, bool ckda) {
   GateLog r;
   if (gate_input == CKDA_GATES_F32) {
     r.neg = x < 0.f;
     r.zero = x == 0.f;
-    r.l2 = r.zero ? 0.f : log2_of(fabsf(x));
+    r.l2 = log2_of(fabsf(x));
   } else if (!ckda) {  // sigmoid
-    const float e = expf(-fabsf(x));
     r.neg = false;
     r.zero = x == -INFINITY;
-    r.l2 = r.zero ? 0.f : ((x < 0.f ? x : 0.f) - log1pf(e)) * kLog2e;
+    r.l2 = (x < 0.f ? x * kLog2e : 0.f) - log2_1p(exp_neg(fabsf(x)));
   } else {  // 2 sigmoid - 1 = tanh(x / 2)
-    const float m = fabsf(x), e = expf(-m);
+    const float m = fabsf(x), e = exp_neg(m);
     r.neg = x < 0.f;
     r.zero = x == 0.f;
-    r.l2 = r.zero ? 0.f
-                  : (m < 0.5f ? log2f(alpha_from_logit(m, true))
-                              : (log1pf(-e) - log1pf(e)) * kLog2e);
+    r.l2 = m < 0.5f ? log2_of(alpha_from_logit(m, true)) : log2_1p(-e) - log2_1p(e);
   }
+  if (r.zero) r.l2 = 0.f;
   return r;
 }
 // the gate itself (for the recurrences that multiply by it)
@@ -135,6 +141,30 @@ __device__ __forceinline__ float gate_stored(const DecayArgs& a, int64_t token, 
                                                 : gate_raw<gate_f32>(a.alpha, i);
 }
 
+// Inclusive sum over the lanes of a wave.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_moved(double x) {  // 0 where no lane moves in
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+__device__ __forceinline__ double wave_scan(double x) {
+  x += dpp_moved<0x111, 0xf>(x);  // within rows of 16 lanes: from 1, 2, 4, 8 below
+  x += dpp_moved<0x112, 0xf>(x);
+  x += dpp_moved<0x114, 0xf>(x);
+  x += dpp_moved<0x118, 0xf>(x);
+  x += dpp_moved<0x142, 0xa>(x);  // row 0's last lane into row 1, 2's into 3
+  x += dpp_moved<0x143, 0xc>(x);  // lane 31 into rows 2 and 3
+  return x;
+}
+__device__ __forceinline__ double lane_value(double x, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), l);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), l);
+  return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+
 // 2^x of a double whose integer part may leave float's exponent range
 __device__ __forceinline__ float exp2_wide(double x) {
   const double n = rint(x);
@@ -145,13 +175,13 @@ __device__ __forceinline__ float exp2_wide(double x) {
 // with gates near 0.1 a float sum of 64 of them is off by 1e-5), split into an
 // integer and a fraction so that differences of two are exact to float.
 // `fast`: no zero gate and all running products within 2^+-60 of the middle
-// one, so D_ij = er_i ej_j (signs included); else d_slow forms each.
+// one, so D_ij = er_i ej_j (signs included).
 template <int C>
 struct alignas(16) Gates {
   float E[C], W[C];    // products from the chunk's start, to its end
-  float er[C], ej[C];
-  float hi[C], lo[C], sg[C];
-  int z[C];            // last zero gate at or before i (-1: none)
+  float er[C], ej[C];  // with `fast`
+  float hi[C], lo[C], sg[C];  // without
+  int z[C];            // without: last zero gate at or before i (-1: none)
   float g;             // product of all
   int fast;
 };
@@ -163,13 +193,8 @@ __device__ __forceinline__ void gates_fill(Gates<C>& G, float x, bool valid, int
                                            bool ckda, int lane) {
   const GateLog gl = gate_log(x, gate_input, ckda);
   const uint64_t zm = __ballot(valid && gl.zero), nm = __ballot(valid && gl.neg);
-  double L = valid ? static_cast<double>(gl.l2) : 0.0;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double y = __shfl_up(L, d, 64);
-    L += lane >= d ? y : 0.0;
-  }
-  const double end = __shfl(L, 63, 64), mid = __shfl(L, C / 2 - 1, 64);
+  const double L = wave_scan(valid ? static_cast<double>(gl.l2) : 0.0);
+  const double end = lane_value(L, 63), mid = lane_value(L, C / 2 - 1);
   const uint64_t upto = ~0ull >> (63 - lane);
   const uint64_t zz = zm & upto;
   const int z = zz ? 63 - __clzll(zz) : -1;
@@ -178,45 +203,101 @@ __device__ __forceinline__ void gates_fill(Gates<C>& G, float x, bool valid, int
   const float sgend = (__popcll(nm) & 1) ? -1.f : 1.f;
   const bool far = !(fabs(L - mid) <= 60.0);
   const bool fast = zm == 0 && __ballot(far) == 0;
-  if (lane < C) {
+  if (fast) {  // powers of differences up to 60, the others from them
+    const float er = sg * __builtin_amdgcn_exp2f(static_cast<float>(L - mid));
+    const float ej = __builtin_amdgcn_rcpf(er);
+    const float g = sgend * exp2_wide(end), em = exp2_wide(mid), ee = sgend * exp2_wide(end - mid);
+    if (lane < C) {
+      G.E[lane] = er * em;
+      G.W[lane] = ej * ee;
+      G.er[lane] = er;
+      G.ej[lane] = ej;
+    }
+    if (lane == 0) {
+      G.g = g;
+      G.fast = 1;
+    }
+  } else {
     const double n = rint(L);
-    G.E[lane] = z < 0 ? sg * exp2_wide(L) : 0.f;
-    G.W[lane] = zend <= lane ? sg * sgend * exp2_wide(end - L) : 0.f;
-    G.er[lane] = fast ? sg * exp2_wide(L - mid) : 0.f;
-    G.ej[lane] = fast ? sg * exp2_wide(mid - L) : 0.f;
-    G.hi[lane] = static_cast<float>(n);
-    G.lo[lane] = static_cast<float>(L - n);
-    G.sg[lane] = sg;
-    G.z[lane] = z;
-  }
-  if (lane == 0) {
-    G.g = zend < 0 ? sgend * exp2_wide(end) : 0.f;
-    G.fast = fast;
+    if (lane < C) {
+      G.E[lane] = z < 0 ? sg * exp2_wide(L) : 0.f;
+      G.W[lane] = zend <= lane ? sg * sgend * exp2_wide(end - L) : 0.f;
+      G.hi[lane] = static_cast<float>(n);
+      G.lo[lane] = static_cast<float>(L - n);
+      G.sg[lane] = sg;
+      G.z[lane] = z;
+    }
+    if (lane == 0) {
+      G.g = zend < 0 ? sgend * exp2_wide(end) : 0.f;
+      G.fast = 0;
+    }
   }
 }
 
-// D_ij for j <= i where the chunk is not `fast`
+// D_ij for one i and j = j0 .. j0 + 3 (j0 a multiple of 4), 0 for j > i
 template <int C>
-__device__ __forceinline__ float d_slow(const Gates<C>& G, int i, int j) {
-  const float e = __builtin_amdgcn_exp2f((G.hi[i] - G.hi[j]) + (G.lo[i] - G.lo[j]));
-  return (j <= i && G.z[i] <= j) ? G.sg[i] * G.sg[j] * e : 0.f;
+__device__ __forceinline__ f32x4 decay_of(const Gates<C>& G, int i, int j0, bool fast) {
+  f32x4 d;
+  if (fast) {
+    d = *reinterpret_cast<const f32x4*>(&G.ej[j0]) * G.er[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = j0 + e <= i ? d[e] : 0.f;
+  } else {
+    const f32x4 hi = *reinterpret_cast<const f32x4*>(&G.hi[j0]);
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(&G.lo[j0]);
+    const f32x4 sg = *reinterpret_cast<const f32x4*>(&G.sg[j0]) * G.sg[i];
+    const float h = G.hi[i], l = G.lo[i];
+    const int z = G.z[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = sg[e] * __builtin_amdgcn_exp2f((h - hi[e]) + (l - lo[e]));
+      d[e] = (j0 + e <= i && z <= j0 + e) ? x : 0.f;
+    }
+  }
+  return d;
+}
+// x D, nothing passing a D of exactly 0 (a zero gate, j > i)
+__device__ __forceinline__ f32x4 decayed(f32x4 x, f32x4 d) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = d[e] != 0.f ? x[e] * d[e] : 0.f;
+  return x;
 }
 
 // ---- tiles of rows, memory -> registers -> LDS ------------------------------
-// ROWS x COLS elements of T in 16-byte pieces by NT threads; pieces outside
-// the first `rows` rows or `cols` columns (a multiple of a piece) are zeros.
+// ROWS x COLS elements of T in 16-byte pieces by NT threads, read through a
+// buffer resource that ends with the last valid row's last column: rows past
+// it read as zeros without a branch, and pieces past the first `cols` columns
+// (a multiple of a piece) carry an offset past any resource.  A thread's
+// offsets are formed once; ld in elements, ROWS * ld * sizeof(T) < 2^31.
+constexpr int kNoOffset = 0x7ffffff0;
+template <class T>
+__device__ __forceinline__ rsrc_t rows_rsrc(const T* base, int ld, int rows, int cols, int most) {
+  const int r = rows < most ? rows : most;
+  const T* b = reinterpret_cast<const T*>(uniform64(reinterpret_cast<int64_t>(base)));
+  return make_rsrc(b, uniform32(r > 0 ? ((r - 1) * ld + cols) * static_cast<int>(sizeof(T)) : 0));
+}
+__device__ __forceinline__ uint4 load_piece(rsrc_t r, int off) {
+  uint4 x;
+  ldraw<16>(r, off, reinterpret_cast<uint32_t*>(&x));
+  return x;
+}
 template <class T, int ROWS, int COLS, int NT>
 struct RowTile {
   static constexpr int EPP = 16 / sizeof(T), PPR = COLS / EPP, NP = ROWS * PPR / NT;
   static_assert(ROWS * PPR % NT == 0, "whole pieces a thread");
   uint4 r[NP];
-  __device__ __forceinline__ void load(const T* base, int64_t ld, int rows, int cols, int t) {
+  int off[NP];
+  __device__ __forceinline__ void init(int ld, int cols, int t) {
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       const int p = t + NT * u, row = p / PPR, c = (p % PPR) * EPP;
-      r[u] = make_uint4(0, 0, 0, 0);
-      if (row < rows && c < cols) r[u] = *reinterpret_cast<const uint4*>(base + row * ld + c);
+      off[u] = c < cols ? (row * ld + c) * static_cast<int>(sizeof(T)) : kNoOffset;
     }
+  }
+  __device__ __forceinline__ void load(const T* base, int ld, int rows, int cols) {
+    const rsrc_t rs = rows_rsrc(base, ld, rows, cols, ROWS);
+#pragma unroll
+    for (int u = 0; u < NP; ++u) r[u] = load_piece(rs, off[u]);
   }
   __device__ __forceinline__ void store(T* lds, int ldl, int t) const {
 #pragma unroll
@@ -231,6 +312,27 @@ struct RowTile {
 // columns a lane group and read): for rows of 64 bytes 96, else the stride
 // of row fragments; eight rows then fall into different banks.
 constexpr int cross_stride(int n, int es) { return n * es == 64 ? 96 / es : frag_stride(n, es); }
+
+// The stored gate of token `lane` of `rows` tokens from `token` on, as raw
+// bits (0 past them): issued with a chunk's rows and decoded after them.
+__device__ __forceinline__ uint32_t load_gate_bits(const DecayArgs& a, int64_t token, int rows, int h,
+                                                   int lane) {
+  const int gs = a.gate_input == CKDA_GATES_LOGITS_BF16 ? 2 : 4;
+  const int64_t at = (a.per_head ? 0 : (rows > 0 ? token : 0) * a.H) + h;
+  const unsigned char* b = static_cast<const unsigned char*>(a.alpha) + at * gs;
+  const int ld = a.per_head ? 0 : a.H, n = rows < 64 ? rows : 64;
+  const rsrc_t r = make_rsrc(reinterpret_cast<const void*>(uniform64(reinterpret_cast<int64_t>(b))),
+                             uniform32(n > 0 ? ((n - 1) * ld + 1) * gs : 0));
+  uint32_t x;
+  if (gs == 2)
+    ldraw<2>(r, lane * ld * gs, &x);
+  else
+    ldraw<4>(r, lane * ld * gs, &x);
+  return x;
+}
+__device__ __forceinline__ float gate_of_bits(uint32_t x, int gate_input) {
+  return __uint_as_float(gate_input == CKDA_GATES_LOGITS_BF16 ? x << 16 : x);
+}
 
 // ---- operand fragments --------------------------------------------------------
 // Beside the row fragments of mfma_ops.h, fragments read ACROSS rows: from
@@ -249,7 +351,7 @@ struct Fr<OpBF16> {
   using T = __bf16;
   using F = bf16x8;
   static constexpr int KS = 32;
-  static constexpr bool kSplit = true;
+  static constexpr int kTerms = 3;  // of a weighted operand
   using IO = io_bf16;
   static __device__ __forceinline__ s16x4 tr4(const T* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -288,7 +390,7 @@ struct Fr<OpF32> {
   using T = float;
   using F = f32x4;
   static constexpr int KS = 16;
-  static constexpr bool kSplit = false;
+  static constexpr int kTerms = 1;
   using IO = io_f32;
   static __device__ __forceinline__ F across(const T* x, int ld, int k0, int n0, int lane) {
     const T* p = x + (k0 + 4 * (lane >> 4)) * ld + n0 + (lane & 15);
@@ -311,22 +413,26 @@ __device__ __forceinline__ float piece_elem(const uint4& u, int e) {
     return __uint_as_float(w[e]);
 }
 
-// A piece times w, stored for the state update.  bf16: as two terms, the
-// product's nearest bf16 and what is left (2^-18 of it is lost), because the
-// state is kept, and handed out, in float32; k and v themselves are exact.
+// A piece times w, stored for the state update.  bf16: as three terms, each
+// the nearest bf16 of what the ones before leave (2^-24 of it is lost: as
+// float32), because the state is kept, and handed out, in float32; k and v
+// themselves are exact.  Two terms would leave 2e-6 of the state.
 template <class T>
-__device__ __forceinline__ void store_scaled(const uint4& u, float w, T* hi, T* lo) {
-  constexpr int E = 16 / sizeof(T);
-  alignas(16) T h[E];
-  alignas(16) T l[E];
+__device__ __forceinline__ void store_scaled(const uint4& u, float w, T* dst, int plane) {
+  constexpr int E = 16 / sizeof(T), NP = sizeof(T) == 2 ? 3 : 1;
+  alignas(16) T h[NP][E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const float x = piece_elem<T>(u, e) * w;
-    h[e] = static_cast<T>(x);
-    if constexpr (sizeof(T) == 2) l[e] = static_cast<T>(x - static_cast<float>(h[e]));
+    float x = piece_elem<T>(u, e) * w;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      h[p][e] = static_cast<T>(x);
+      if constexpr (NP > 1) x -= static_cast<float>(h[p][e]);
+    }
   }
-  *reinterpret_cast<uint4*>(hi) = *reinterpret_cast<const uint4*>(h);
-  if constexpr (sizeof(T) == 2) *reinterpret_cast<uint4*>(lo) = *reinterpret_cast<const uint4*>(l);
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+    *reinterpret_cast<uint4*>(dst + p * plane) = *reinterpret_cast<const uint4*>(h[p]);
 }
 
 // Work items of a grid: `outer` items of `inner` parts.  Workgroups go to the

@@ -384,7 +384,8 @@ ckda_status_t ckda_l2norm_debug(const void* x, float* y, int64_t rows,
  * past cu_seqlens[num_seqs] of a packed batch are neither read nor written;
  * cu_seqlens is clamped to [0, T] on the device.
  * Supported: dk and dv multiples of 8 from 8 to 128, in any combination, both
- * io dtypes; others return CKDA_ERR_UNSUPPORTED, as do B * T of 2^31 or more
+ * io dtypes; others return CKDA_ERR_UNSUPPORTED, as do H * max(dk, dv) of 2^22 or
+ * more, B * T of 2^31 or more
  * and launches of 2^31 or more workgroups.
  */
 typedef struct {

@@ -103,6 +103,6 @@ def bound_out(dtype, value, mag, dk, T):
 
 
 def bound_state(dtype, mag, dk, T):
-    """A float32 state: in bf16 the weighted operand goes in as two terms,
-    which lose 2^-16 of it."""
-    return (2.0 ** -16 if dtype == "bf16" else 0.0) * mag + 2 * sums(dk, T) * mag + 1e-30
+    """A float32 state (in bf16 the weighted operand goes in as three terms, 24
+    bits in all, so both types keep float32's accuracy)."""
+    return 2 * sums(dk, T) * mag + 1e-30
