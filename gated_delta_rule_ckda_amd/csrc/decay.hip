@@ -76,37 +76,30 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
   const int nch = (pc.len + C - 1) / C;
   auto first_token = [&](int c) { return c < nch ? static_cast<int64_t>(c) * C : 0; };
 
+  // Each role's loop takes two chunks a turn, so that the registers a chunk's
+  // rows wait in are fixed: they are loaded two chunks ahead.
   if (reads_out) {
     const T* gq = static_cast<const T*>(a.q) + oq;
-    const T* gk = static_cast<const T*>(a.k) + oq;
     T* go = static_cast<T*>(a.o) + ov;
     const int r = 16 * w + l16;  // this lane's token
-    RowTile<T, C, DKP, NW> rk;
-    rk.init(ldq, a.dk, t);
-    uint4 rq[NQ];
+    uint4 rq[2][NQ];
     int offq[NQ];
 #pragma unroll
     for (int s = 0; s < NQ; ++s) {
       const int col = KS * s + EPP * lq;
       offq[s] = col < a.dk ? (r * ldq + col) * Cfg::ES : kNoOffset;
     }
-    auto load = [&](int c) {  // zeros past the last chunk
-      const int rows = c < nch ? pc.len - c * C : 0;
-      rk.load(gk + first_token(c) * ldq, ldq, rows, a.dk);
-      const rsrc_t rs = rows_rsrc(gq + first_token(c) * ldq, ldq, rows, a.dk, C);
+    auto load = [&](auto P, int c) {  // zeros past the last chunk
+      constexpr int b = decltype(P)::value;
+      const rsrc_t rs = rows_rsrc(gq + first_token(c) * ldq, ldq, c < nch ? pc.len - c * C : 0, a.dk, C);
 #pragma unroll
-      for (int s = 0; s < NQ; ++s) rq[s] = load_piece(rs, offq[s]);
+      for (int s = 0; s < NQ; ++s) rq[b][s] = load_piece(rs, offq[s]);
     };
-    if (nch > 0) {
-      load(0);
-      __syncthreads();
-      rk.store(sK, LDK, t);
-    }
-    for (int c = 0; c < nch; ++c) {
+    auto step = [&](auto P, int c) {
+      constexpr int b = decltype(P)::value;
       F fq[NQ];
 #pragma unroll
-      for (int s = 0; s < NQ; ++s) fq[s] = *reinterpret_cast<const F*>(&rq[s]);
-      load(c + 1);
+      for (int s = 0; s < NQ; ++s) fq[s] = *reinterpret_cast<const F*>(&rq[b][s]);
       __syncthreads();  // rows, state copy and gates of chunk c are in LDS
       const Gates<C>& G = sG[c & 1];
       const bool fast = G.fast != 0;
@@ -124,6 +117,17 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
       };
       tile_pair(std::integral_constant<int, 0>{});
       if (w >= 2) tile_pair(std::integral_constant<int, 2>{});
+      // tile n of the output holds, in lane (l16, lq), columns EPL lq + 4 n + i
+      // of token l16: EPL = 4 NTL columns in a row
+      f32x4 o[NTL], x[NTL];
+#pragma unroll
+      for (int n = 0; n < NTL; ++n) {
+        o[n] = x[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const T* rows = sS + (4 * NTL * (l16 >> 2) + 4 * n + (l16 & 3)) * LDK;
+#pragma unroll
+        for (int s = 0; s < NQ; ++s) Op::mma(x[n], X::row(rows, s, lq), fq[s]);
+      }
+      load(P, c + 2);
       // where D factors, its row part multiplies the sum instead of each term
       float row = 1.f;
       if (fast) {
@@ -142,30 +146,35 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
       }
       F pf[C / KS];
       Op::template frags<C>(pf, p);
-      f32x4 o[NTL], x[NTL];
-#pragma unroll
-      for (int n = 0; n < NTL; ++n) {
-        o[n] = x[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const T* rows = sS + (16 * n + l16) * LDK;
-#pragma unroll
-        for (int s = 0; s < NQ; ++s) Op::mma(x[n], X::row(rows, s, lq), fq[s]);
-      }
 #pragma unroll
       for (int ks = 0; ks < C / KS; ++ks)
         if (2 * ks < C / KS || w >= 2) {
 #pragma unroll
-          for (int n = 0; n < NTL; ++n) Op::mma(o[n], X::across(sV, LDV, KS * ks, 16 * n, lane), pf[ks]);
+          for (int n = 0; n < NTL; ++n)
+            Op::mma(o[n], X::across(sV, LDV, KS * ks, 4 * n, lane, 4 * NTL), pf[ks]);
         }
       const float e = G.E[r] * a.scale;
       row *= a.scale;
       if (c * C + r < pc.len) {
-        T* dst = go + static_cast<int64_t>(c * C + r) * ldv;
+        T* dst = go + static_cast<int64_t>(c * C + r) * ldv + 4 * NTL * lq;
+        alignas(16) T y[4 * NTL];
 #pragma unroll
-        for (int n = 0; n < NTL; ++n)
-          if (16 * n + 4 * lq < vcols) Op::store4(dst + 16 * n + 4 * lq, x[n] * e + o[n] * row);
+        for (int n = 0; n < NTL; ++n) Op::store4(y + 4 * n, x[n] * e + o[n] * row);
+#pragma unroll
+        for (int u = 0; u < 4 * NTL / EPP; ++u)
+          if (4 * NTL * lq + EPP * u < vcols)
+            *reinterpret_cast<uint4*>(dst + EPP * u) = *reinterpret_cast<const uint4*>(y + EPP * u);
       }
       __syncthreads();  // chunk c is done with LDS; gates of chunk c + 1 are there
-      rk.store(sK, LDK, t);
+    };
+    if (nch > 0) {
+      load(std::integral_constant<int, 0>{}, 0);
+      load(std::integral_constant<int, 1>{}, 1);
+      __syncthreads();
+    }
+    for (int c = 0; c < nch; c += 2) {
+      step(std::integral_constant<int, 0>{}, c);
+      if (c + 1 < nch) step(std::integral_constant<int, 1>{}, c + 1);
     }
     return;
   }
@@ -196,38 +205,42 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
         Op::store4(sS + (16 * n + l16) * LDK + row0 + 16 * m + 4 * lq, S[m][n]);
   };
   const bool ckda = a.gate_range == CKDA_GATE_CKDA;
+  const T* gk = static_cast<const T*>(a.k) + oq;
   const T* gv = static_cast<const T*>(a.v) + ov;
+  using RK = RowTile<T, C, DKP, NW>;
   using RV = RowTile<T, C, DVS, NW>;
-  RV rv;
-  rv.init(ldv, vcols, t);
-  auto load = [&](int c) {
-    rv.load(gv + first_token(c) * ldv, ldv, c < nch ? pc.len - c * C : 0, vcols);
+  RK tk;
+  RV tv;
+  tk.init(ldq, a.dk, t);
+  tv.init(ldv, vcols, t);
+  typename RK::Regs rk[2];
+  typename RV::Regs rv[2];
+  uint32_t bits[2];
+  auto load = [&](auto P, int c) {
+    constexpr int b = decltype(P)::value;
+    const int rows = c < nch ? pc.len - c * C : 0;
+    bits[b] = load_gate_bits(a, pc.begin + first_token(c), rows, h, lane);
+    tv.load(rv[b], gv + first_token(c) * ldv, ldv, rows, vcols);
+    tk.load(rk[b], gk + first_token(c) * ldq, ldq, rows, a.dk);
   };
-  auto load_gate = [&](int c) {
-    return load_gate_bits(a, pc.begin + first_token(c), c < nch ? pc.len - c * C : 0, h, lane);
+  auto fill_gates = [&](int c, uint32_t x) {
+    gates_fill<C>(sG[c & 1], gate_of_bits(x, a.gate_input), c * C + lane < pc.len, a.gate_input, ckda, lane);
   };
-  auto fill_gates = [&](int c, uint32_t bits) {
-    gates_fill<C>(sG[c & 1], gate_of_bits(bits, a.gate_input), c * C + lane < pc.len, a.gate_input, ckda, lane);
-  };
-  auto stage_rows = [&](const Gates<C>& G) {
-    rv.store(sV, LDV, t);
+  auto stage_rows = [&](auto P, const Gates<C>& G) {
+    constexpr int b = decltype(P)::value;
+    tv.store(rv[b], sV, LDV, t);
 #pragma unroll
     for (int u = 0; u < RV::NP; ++u) {
       const int p = t + NW * u, row = p / RV::PPR, c = (p % RV::PPR) * RV::EPP;
-      store_scaled<T>(rv.r[u], G.W[row], sH + row * LDV + c, C * LDV);
+      store_scaled<T>(rv[b].r[u], G.W[row], sH + row * LDV + c, C * LDV);
     }
+    tk.store(rk[b], sK, LDK, t);
   };
-  if (nch > 0) {
-    const uint32_t bits = load_gate(0);
-    load(0);
-    if (w == 0) fill_gates(0, bits);
-    stage_state();
-    __syncthreads();
-    stage_rows(sG[0]);
-  }
-  for (int c = 0; c < nch; ++c) {
-    const uint32_t bits = load_gate(c + 1);
-    load(c + 1);
+  using P0 = std::integral_constant<int, 0>;
+  using P1 = std::integral_constant<int, 1>;
+  // chunk c, whose rows were in registers P and are in LDS now
+  auto step = [&](auto P, auto Q, int c) {
+    load(P, c + 2);
     __syncthreads();  // rows, state copy and gates of chunk c are in LDS
     const float g = sG[c & 1].g;
 #pragma unroll
@@ -248,10 +261,22 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
           for (int m = 0; m < MT; ++m) Op::mma(S[m][n], ka[m], vb);
         }
     }
-    if (w == ((c + 1) & 3)) fill_gates(c + 1, bits);
+    if (w == ((c + 1) & 3)) fill_gates(c + 1, bits[decltype(Q)::value]);
     __syncthreads();  // chunk c is done with LDS; gates of chunk c + 1 are there
     stage_state();
-    stage_rows(sG[(c + 1) & 1]);
+    stage_rows(Q, sG[(c + 1) & 1]);
+  };
+  if (nch > 0) {
+    load(P0{}, 0);
+    load(P1{}, 1);
+    if (w == 0) fill_gates(0, bits[0]);
+    stage_state();
+    __syncthreads();
+    stage_rows(P0{}, sG[0]);
+  }
+  for (int c = 0; c < nch; c += 2) {
+    step(P0{}, P1{}, c);
+    if (c + 1 < nch) step(P1{}, P0{}, c + 1);
   }
   if (a.ht && pc.s == pc.count - 1) {
     float* dst = a.ht + sbase;
@@ -346,17 +371,21 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
       }
   };
 
-  RowTile<T, C, DKP, kNT> rx;
-  RowTile<T, C, DVS, kNT> ry;
-  rx.init(ldx, a.dk, t);
-  ry.init(ldy, vcols, t);
+  using RX = RowTile<T, C, DKP, kNT>;
+  using RY = RowTile<T, C, DVS, kNT>;
+  RX tx;
+  RY ty;
+  tx.init(ldx, a.dk, t);
+  ty.init(ldy, vcols, t);
+  typename RX::Regs rx;
+  typename RY::Regs ry;
   auto chunk_at = [&](int i) { return REV ? nch - 1 - i : i; };
   auto load_chunk = [&](int i) {
     const int c = chunk_at(i);
     const int rows = i < nch ? pc.len - c * C : 0;
     const int64_t o = static_cast<int64_t>(i < nch ? c : 0) * C;
-    rx.load(gx + o * ldx, ldx, rows, a.dk);
-    ry.load(gy + o * ldy, ldy, rows, vcols);
+    tx.load(rx, gx + o * ldx, ldx, rows, a.dk);
+    ty.load(ry, gy + o * ldy, ldy, rows, vcols);
   };
   auto load_gate = [&](int i) {
     const int c = i < nch ? chunk_at(i) : 0, rows = i < nch ? pc.len - c * C : 0;
@@ -367,8 +396,7 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
     gates_fill<C>(sG[i & 1], gate_of_bits(bits, a.gate_input), ok, a.gate_input, ckda, lane);
   };
   auto stage_rows = [&](const Gates<C>& G) {
-    rx.store(sK, LDK, t);
-    using RY = RowTile<T, C, DVS, kNT>;
+    tx.store(rx, sK, LDK, t);
 #pragma unroll
     for (int u = 0; u < RY::NP; ++u) {
       const int p = t + kNT * u, row = p / RY::PPR, c = (p % RY::PPR) * RY::EPP;

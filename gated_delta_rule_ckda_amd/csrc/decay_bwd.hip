@@ -75,25 +75,27 @@ __global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGr
 #pragma unroll
     for (int n = 0; n < RT; ++n) dq[m][n] = dk[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  RowTile<T, C, DP, kNT> rq, rk, rv, ro;
-  rq.init(ldq, a.dk, t);
-  rk.init(ldq, a.dk, t);
-  rv.init(ldv, a.dv, t);
-  ro.init(ldv, a.dv, t);
-  rq.load(static_cast<const T*>(a.q) + oq, ldq, pc.len, a.dk);
-  rk.load(static_cast<const T*>(a.k) + oq, ldq, pc.len, a.dk);
-  rq.store(sQ, LD, t);
-  rk.store(sK, LD, t);
+  using R = RowTile<T, C, DP, kNT>;
+  using RA = RowTile<T, DP, DP, kNT>;
+  R tq, tv;
+  RA ta;
+  typename R::Regs rq, rk, rv, ro;
+  typename RA::Regs ra;
+  tq.init(ldq, a.dk, t);
+  tv.init(ldv, a.dv, t);
+  ta.init(a.dv, a.dv, t);
+  tq.load(rq, static_cast<const T*>(a.q) + oq, ldq, pc.len, a.dk);
+  tq.load(rk, static_cast<const T*>(a.k) + oq, ldq, pc.len, a.dk);
+  tq.store(rq, sQ, LD, t);
+  tq.store(rk, sK, LD, t);
 
   for (int hv = 0; hv < group; ++hv) {
     const int h = hk * group + hv;
     const int64_t ov = pc.begin * ldv + static_cast<int64_t>(h) * a.dv;
     const int64_t rec = (slot * a.H + h) * a.dk * a.dv;
-    rv.load(static_cast<const T*>(a.v) + ov, ldv, pc.len, a.dv);
-    ro.load(static_cast<const T*>(gr.dout) + ov, ldv, pc.len, a.dv);
-    RowTile<T, DP, DP, kNT> ra;
-    ra.init(a.dv, a.dv, t);
-    ra.load(static_cast<const T*>(a.adjoints) + rec, a.dv, a.dk, a.dv);
+    tv.load(rv, static_cast<const T*>(a.v) + ov, ldv, pc.len, a.dv);
+    tv.load(ro, static_cast<const T*>(gr.dout) + ov, ldv, pc.len, a.dv);
+    ta.load(ra, static_cast<const T*>(a.adjoints) + rec, a.dv, a.dk, a.dv);
     const bool tok = lane < C && lane < pc.len;
     float xg = 0.f;
     if (w == 0) {
@@ -106,9 +108,9 @@ __global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGr
         sAl[C] = x;
       }
     }
-    rv.store(sV, LD, t);
-    ro.store(sO, LD, t);
-    ra.store(sA, LD, t);
+    tv.store(rv, sV, LD, t);
+    tv.store(ro, sO, LD, t);
+    ta.store(ra, sA, LD, t);
     __syncthreads();
     const bool fast = G.fast != 0;
 

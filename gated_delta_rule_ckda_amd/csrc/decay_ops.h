@@ -285,7 +285,9 @@ template <class T, int ROWS, int COLS, int NT>
 struct RowTile {
   static constexpr int EPP = 16 / sizeof(T), PPR = COLS / EPP, NP = ROWS * PPR / NT;
   static_assert(ROWS * PPR % NT == 0, "whole pieces a thread");
-  uint4 r[NP];
+  struct Regs {
+    uint4 r[NP];
+  };
   int off[NP];
   __device__ __forceinline__ void init(int ld, int cols, int t) {
 #pragma unroll
@@ -294,16 +296,16 @@ struct RowTile {
       off[u] = c < cols ? (row * ld + c) * static_cast<int>(sizeof(T)) : kNoOffset;
     }
   }
-  __device__ __forceinline__ void load(const T* base, int ld, int rows, int cols) {
+  __device__ __forceinline__ void load(Regs& d, const T* base, int ld, int rows, int cols) const {
     const rsrc_t rs = rows_rsrc(base, ld, rows, cols, ROWS);
 #pragma unroll
-    for (int u = 0; u < NP; ++u) r[u] = load_piece(rs, off[u]);
+    for (int u = 0; u < NP; ++u) d.r[u] = load_piece(rs, off[u]);
   }
-  __device__ __forceinline__ void store(T* lds, int ldl, int t) const {
+  static __device__ __forceinline__ void store(const Regs& d, T* lds, int ldl, int t) {
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       const int p = t + NT * u, row = p / PPR, c = (p % PPR) * EPP;
-      *reinterpret_cast<uint4*>(lds + row * ldl + c) = r[u];
+      *reinterpret_cast<uint4*>(lds + row * ldl + c) = d.r[u];
     }
   }
 };
@@ -357,9 +359,11 @@ struct Fr<OpBF16> {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
         (__attribute__((address_space(3))) s16x4*)(const_cast<T*>(p)));
   }
-  static __device__ __forceinline__ F across(const T* x, int ld, int k0, int n0, int lane) {
+  // the 16 columns in groups of 4, `apart` columns apart: lane l16 takes column
+  // n0 + apart (l16 / 4) + l16 % 4
+  static __device__ __forceinline__ F across(const T* x, int ld, int k0, int n0, int lane, int apart = 4) {
     const int l16 = lane & 15, lq = lane >> 4;
-    const T* p = x + (k0 + 4 * lq + (l16 >> 2)) * ld + n0 + 4 * (l16 & 3);
+    const T* p = x + (k0 + 4 * lq + (l16 >> 2)) * ld + n0 + apart * (l16 & 3);
     union {
       s16x4 s[2];
       F f;
@@ -392,8 +396,8 @@ struct Fr<OpF32> {
   static constexpr int KS = 16;
   static constexpr int kTerms = 1;
   using IO = io_f32;
-  static __device__ __forceinline__ F across(const T* x, int ld, int k0, int n0, int lane) {
-    const T* p = x + (k0 + 4 * (lane >> 4)) * ld + n0 + (lane & 15);
+  static __device__ __forceinline__ F across(const T* x, int ld, int k0, int n0, int lane, int apart = 4) {
+    const T* p = x + (k0 + 4 * (lane >> 4)) * ld + n0 + apart * ((lane & 15) >> 2) + (lane & 3);
     return F{p[0], p[ld], p[2 * ld], p[3 * ld]};
   }
   static __device__ __forceinline__ F row(const T* r, int s, int lq) {
