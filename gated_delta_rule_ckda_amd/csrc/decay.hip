@@ -344,30 +344,35 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
   const bool ckda = a.gate_range == CKDA_GATE_CKDA;
   const int nch = (pc.len + C - 1) / C;
 
-  // tile (m, n) of S^T: column dk = row0 + 16 m + l16, rows dv = c0 + 16 n + 4 lq + i
+  // tile (m, n) of S^T: column dk = row0 + 16 m + l16, rows dv = c0 + RUN lq +
+  // 4 n + i: a lane holds RUN columns of the state in a row
+  constexpr int RUN = 4 * NTL;
+  typedef T Run __attribute__((ext_vector_type(RUN)));
   const int row0 = w * (DKP / 4);
   const int64_t seq_state = (static_cast<int64_t>(pc.n) * a.H + h) * a.dk * a.dv;
   const int64_t seg_state = (static_cast<int64_t>(slot) * a.H + h) * a.dk * a.dv;
   f32x4 S[MT][NTL];
+  // place of S[m][n] in a state, -1 outside it
+  auto place = [&](int m, int n) {
+    const int r = row0 + 16 * m + l16, c = RUN * lq + 4 * n;
+    return r < a.dk && c < vcols ? r * a.dv + c0 + c : -1;
+  };
   const float* src = MODE == kSegment ? nullptr
                      : (a.seg > 0 ? a.entry + seg_state : (a.h0 ? a.h0 + seq_state : nullptr));
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NTL; ++n) {
-      const int r = row0 + 16 * m + l16, c = 16 * n + 4 * lq;
-      S[m][n] = src && r < a.dk && c < vcols
-                    ? *reinterpret_cast<const f32x4*>(src + static_cast<int64_t>(r) * a.dv + c0 + c)
-                    : f32x4{0.f, 0.f, 0.f, 0.f};
+      const int at = place(m, n);
+      S[m][n] = src && at >= 0 ? *reinterpret_cast<const f32x4*>(src + at) : f32x4{0.f, 0.f, 0.f, 0.f};
     }
   auto save = [&](float* dst) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NTL; ++n) {
-        const int r = row0 + 16 * m + l16, c = 16 * n + 4 * lq;
-        if (r < a.dk && c < vcols)
-          *reinterpret_cast<f32x4*>(dst + static_cast<int64_t>(r) * a.dv + c0 + c) = S[m][n];
+        const int at = place(m, n);
+        if (at >= 0) *reinterpret_cast<f32x4*>(dst + at) = S[m][n];
       }
   };
 
@@ -377,71 +382,79 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
   RY ty;
   tx.init(ldx, a.dk, t);
   ty.init(ldy, vcols, t);
-  typename RX::Regs rx;
-  typename RY::Regs ry;
-  auto chunk_at = [&](int i) { return REV ? nch - 1 - i : i; };
-  auto load_chunk = [&](int i) {
-    const int c = chunk_at(i);
-    const int rows = i < nch ? pc.len - c * C : 0;
-    const int64_t o = static_cast<int64_t>(i < nch ? c : 0) * C;
-    tx.load(rx, gx + o * ldx, ldx, rows, a.dk);
-    ty.load(ry, gy + o * ldy, ldy, rows, vcols);
-  };
-  auto load_gate = [&](int i) {
-    const int c = i < nch ? chunk_at(i) : 0, rows = i < nch ? pc.len - c * C : 0;
-    return load_gate_bits(a, pc.begin + static_cast<int64_t>(c) * C, rows < C ? rows : C, h, lane);
-  };
-  auto fill_gates = [&](int i, uint32_t bits) {
-    const bool ok = i < nch && lane < C && chunk_at(i) * C + lane < pc.len;
-    gates_fill<C>(sG[i & 1], gate_of_bits(bits, a.gate_input), ok, a.gate_input, ckda, lane);
-  };
-  auto stage_rows = [&](const Gates<C>& G) {
-    tx.store(rx, sK, LDK, t);
-#pragma unroll
-    for (int u = 0; u < RY::NP; ++u) {
-      const int p = t + kNT * u, row = p / RY::PPR, c = (p % RY::PPR) * RY::EPP;
-      store_scaled<T>(ry.r[u], REV ? G.E[row] * a.scale : G.W[row], sH + row * LDV + c, C * LDV);
-    }
-  };
+  // rows wait in registers two chunks ahead; the loop takes two chunks a turn
+  typename RX::Regs rx[2];
+  typename RY::Regs ry[2];
+  uint32_t bits[2];
+  uint4 rf[2][MT][RUN * sizeof(T) / 16];  // backwards: the forward's state at the chunk
   int64_t cslot = 0;
   if (MODE == kChunks) cslot = first_slot(a, pc.n, C) + (a.seg > 0 ? pc.s * (a.seg / C) : 0);
-
-  float gain = 1.f;
-  if (nch > 0) {
-    const uint32_t bits = load_gate(0);
-    load_chunk(0);
-    if (w == 0) fill_gates(0, bits);
-    __syncthreads();
-    stage_rows(sG[0]);
-  }
-  for (int i = 0; i < nch; ++i) {
-    const uint32_t bits = load_gate(i + 1);
-    load_chunk(i + 1);
-    if (MODE == kChunks) {  // the state met at this chunk
-      const int64_t rec = ((cslot + chunk_at(i)) * a.H + h) * a.dk * a.dv;
-      T* dst = static_cast<T*>(REV ? a.adjoints : a.states) + rec;
-      const T* fwd = static_cast<const T*>(a.states) + rec;
-      float dot = 0.f;
+  auto chunk_at = [&](int i) { return i < nch ? (REV ? nch - 1 - i : i) : 0; };
+  auto record = [&](int i) { return ((cslot + chunk_at(i)) * a.H + h) * a.dk * a.dv; };
+  auto load_chunk = [&](auto P, int i) {  // zeros past the last
+    constexpr int b = decltype(P)::value;
+    const int c = chunk_at(i), left = i < nch ? pc.len - c * C : 0, rows = left < C ? left : C;
+    const int64_t o = static_cast<int64_t>(c) * C;
+    bits[b] = load_gate_bits(a, pc.begin + o, rows, h, lane);
+    tx.load(rx[b], gx + o * ldx, ldx, rows, a.dk);
+    ty.load(ry[b], gy + o * ldy, ldy, rows, vcols);
+    if constexpr (REV && MODE == kChunks) {
+      const T* fwd = static_cast<const T*>(a.states) + record(i);
+      const rsrc_t r = rows_rsrc(fwd, a.dv, i < nch ? a.dk : 0, a.dv, DKP);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < NTL; ++n) {
-          const int r = row0 + 16 * m + l16, c = 16 * n + 4 * lq;
-          if (r < a.dk && c < vcols) {
-            const int64_t at = static_cast<int64_t>(r) * a.dv + c0 + c;
-            Op::store4(dst + at, S[m][n]);
-            if (REV) {
+        for (int u = 0; u < RUN * static_cast<int>(sizeof(T)) / 16; ++u) {
+          const int at = place(m, u * (4 / static_cast<int>(sizeof(T))));
+          rf[b][m][u] = load_piece(r, at >= 0 ? at * static_cast<int>(sizeof(T)) : kNoOffset);
+        }
+    }
+  };
+  auto fill_gates = [&](int i, uint32_t x) {
+    const bool ok = i < nch && lane < C && chunk_at(i) * C + lane < pc.len;
+    gates_fill<C>(sG[i & 1], gate_of_bits(x, a.gate_input), ok, a.gate_input, ckda, lane);
+  };
+  auto stage_rows = [&](auto P, const Gates<C>& G) {
+    constexpr int b = decltype(P)::value;
+    tx.store(rx[b], sK, LDK, t);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) dot += S[m][n][e] * static_cast<float>(fwd[at + e]);
-            }
+    for (int u = 0; u < RY::NP; ++u) {
+      const int p = t + kNT * u, row = p / RY::PPR, c = (p % RY::PPR) * RY::EPP;
+      store_scaled<T>(ry[b].r[u], REV ? G.E[row] * a.scale : G.W[row], sH + row * LDV + c, C * LDV);
+    }
+  };
+  using P0 = std::integral_constant<int, 0>;
+  using P1 = std::integral_constant<int, 1>;
+
+  float gain = 1.f;
+  auto step = [&](auto P, auto Q, int i) {
+    if (MODE == kChunks) {  // the state met at this chunk
+      T* dst = static_cast<T*>(REV ? a.adjoints : a.states) + record(i);
+      float dot = 0.f;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        alignas(16) T y[RUN];
+#pragma unroll
+        for (int n = 0; n < NTL; ++n) Op::store4(y + 4 * n, S[m][n]);
+#pragma unroll
+        for (int u = 0; u < RUN * static_cast<int>(sizeof(T)) / 16; ++u) {
+          const int at = place(m, u * (4 / static_cast<int>(sizeof(T))));
+          if (at >= 0) *reinterpret_cast<uint4*>(dst + at) = reinterpret_cast<const uint4*>(y)[u];
+          if (REV) {
+            constexpr int E = 16 / sizeof(T);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              dot += S[m][(u * E + e) / 4][(u * E + e) % 4] * piece_elem<T>(rf[decltype(P)::value][m][u], e);
           }
         }
+      }
       if (REV) {
 #pragma unroll
         for (int mm = 32; mm >= 1; mm >>= 1) dot += __shfl_xor(dot, mm, 64);
         if (lane == 0) sR[w] = dot;
       }
     }
+    load_chunk(P, i + 2);
     __syncthreads();  // rows and gates of chunk i are in LDS
     if (MODE == kChunks && REV && t == 0)
       a.dots[((cslot + chunk_at(i)) * a.H + h) * nslab + slab] = (sR[0] + sR[1]) + (sR[2] + sR[3]);
@@ -460,14 +473,25 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
       for (int p = 0; p < X::kTerms; ++p)
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
-          const F vb = X::across(sH + p * C * LDV, LDV, KS * ks, 16 * n, lane);
+          const F vb = X::across(sH + p * C * LDV, LDV, KS * ks, 4 * n, lane, RUN);
 #pragma unroll
           for (int m = 0; m < MT; ++m) Op::mma(S[m][n], vb, ka[m]);
         }
     }
-    if (w == ((i + 1) & 3)) fill_gates(i + 1, bits);
+    if (w == ((i + 1) & 3)) fill_gates(i + 1, bits[decltype(Q)::value]);
     __syncthreads();
-    stage_rows(sG[(i + 1) & 1]);
+    stage_rows(Q, sG[(i + 1) & 1]);
+  };
+  if (nch > 0) {
+    load_chunk(P0{}, 0);
+    load_chunk(P1{}, 1);
+    if (w == 0) fill_gates(0, bits[0]);
+    __syncthreads();
+    stage_rows(P0{}, sG[0]);
+  }
+  for (int i = 0; i < nch; i += 2) {
+    step(P0{}, P1{}, i);
+    if (i + 1 < nch) step(P1{}, P0{}, i + 1);
   }
   if (MODE == kSegment) {
     save(a.entry + seg_state);

@@ -7,21 +7,31 @@
 //   dk_j = W_j A v_j           + sum_{i >= j} D_ij N_ij q_i
 //   dv_j = W_j A^T k_j         + scale sum_{i >= j} D_ij P_ij dout_i
 //
-// and for the gates, with no division by a gate: a_t appears in every pair of
-// a write before it and a read at or after it, so with M_ij = P_ij N_ij,
-// z_i = scale q_i . S0 dout_i, y_j = k_j . A v_j and x = <A, S0>
+// and for the gates: a_t appears in every pair of a write before it and a read
+// at or after it.  With M_ij = P_ij N_ij, z_i = scale q_i . S0 dout_i,
+// y_j = k_j . A v_j and x = <A, S0>,
+//
+//   a_t da_t = sum_{i >= t} (E_i z_i + sum_{j < t} D_ij M_ij) + sum_{j < t} W_j y_j + g x:
+//
+// sums of terms that all hold the factor a_t, with nothing subtracted, so that
+// dividing by it costs no accuracy.  In a chunk with zero gates, or products
+// beyond 2^60, the factor is left out instead,
 //
 //   R_1(i) = z_i,  R_{t+1}(i) = a_t R_t(i) + M_it     (writes before t, read i)
 //   da_t = sum_{i >= t} D_it R_t(i) + W_t X_t,   X_1 = x,  X_{t+1} = a_t X_t + y_t.
 //
-// One workgroup per (chunk, query/key head); it runs over the value heads that
-// share the head and sums their dq and dk in registers.
+// A workgroup takes (chunk, query/key head) items in turn and runs over the
+// value heads that share the head, summing their dq and dk in registers; a
+// wave owns DP / 8 columns of dq, dk and dv for all tokens.  One workgroup
+// fills a CU's LDS, so the next head's or item's rows are on their way into
+// registers while one is computed.
 #include "decay_ops.h"
 
 namespace ckda {
 namespace {
 
-constexpr int kNT = 256;  // 4 waves
+constexpr int kNT = 512;  // 8 waves
+constexpr int kWaves = kNT / 64;
 
 template <class Op, int DP, int C>
 struct GradCfg {
@@ -31,19 +41,21 @@ struct GradCfg {
   static constexpr int ROWS = C * LD * ES;
   static constexpr int O_Q = 0, O_K = ROWS, O_V = 2 * ROWS, O_O = 3 * ROWS, O_A = 4 * ROWS,
                        O_P = O_A + DP * LD * ES, O_N = O_P + C * LDC * ES,
-                       O_M = O_N + C * LDC * ES, O_Z = O_M + C * LDM * 4, O_Y = O_Z + 4 * C * 4,
-                       O_X = O_Y + 4 * C * 4, O_G = align16(O_X + C * 4 + 16),
+                       O_M = O_N + C * LDC * ES, O_Z = O_M + C * LDM * 4, O_Y = O_Z + kWaves * C * 4,
+                       O_X = O_Y + kWaves * C * 4, O_G = align16(O_X + C * 4 + 16),
                        BYTES = O_G + static_cast<int>(sizeof(Gates<C>));
 };
 
 template <class Op, int DP, int C>
-__global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGrads gr) {
+__global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGrads gr) {
   using Cfg = GradCfg<Op, DP, C>;
   using X = Fr<Op>;
   using T = typename Op::T;
   using F = typename X::F;
   constexpr int LD = Cfg::LD, LDC = Cfg::LDC, LDM = Cfg::LDM, KS = X::KS, EPP = 16 / sizeof(T);
-  constexpr int RT = C / 16, CT = DP / 64, ND = DP / KS, NC = C / KS;
+  // tiles of 16 columns: DP / 16 of them over 8 waves (with 4, half of the waves take none)
+  constexpr int RT = C / 16, ND = DP / KS, NC = C / KS, CW = DP / 16;
+  static_assert(CW == 4 || CW == 8, "column tiles");
   extern __shared__ __align__(16) unsigned char smem[];
   T* sQ = reinterpret_cast<T*>(smem + Cfg::O_Q);
   T* sK = reinterpret_cast<T*>(smem + Cfg::O_K);
@@ -52,71 +64,118 @@ __global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGr
   T* sA = reinterpret_cast<T*>(smem + Cfg::O_A);  // adjoint state [dk][dv]
   T* sP = reinterpret_cast<T*>(smem + Cfg::O_P);  // scale D P  [i][j]
   T* sN = reinterpret_cast<T*>(smem + Cfg::O_N);  // D N        [i][j]
-  float* sM = reinterpret_cast<float*>(smem + Cfg::O_M);
-  float* sZ = reinterpret_cast<float*>(smem + Cfg::O_Z);
+  float* sM = reinterpret_cast<float*>(smem + Cfg::O_M);   // D M with fast gates, else M
+  float* sZ = reinterpret_cast<float*>(smem + Cfg::O_Z);   // waves' parts of z, then of da
   float* sY = reinterpret_cast<float*>(smem + Cfg::O_Y);
   float* sAl = reinterpret_cast<float*>(smem + Cfg::O_X);  // gates, then x
   Gates<C>& G = *reinterpret_cast<Gates<C>*>(smem + Cfg::O_G);
 
   const int t = threadIdx.x, lane = t & 63, w = uniform32(t >> 6), l16 = lane & 15, lq = lane >> 4;
-  const int64_t slot = blockIdx.x / a.Hk;
-  const int hk = static_cast<int>(blockIdx.x % a.Hk), group = a.H / a.Hk;
-  const Piece pc = piece_of(a, static_cast<int>(slot), C, lane);
-  if (pc.n < 0 || pc.len == 0) return;
+  const int group = a.H / a.Hk;
   const int ldq = a.Hk * a.dk, ldv = a.H * a.dv;
-  const int64_t oq = pc.begin * static_cast<int64_t>(ldq) + static_cast<int64_t>(hk) * a.dk;
   const bool ckda = a.gate_range == CKDA_GATE_CKDA;
   const int nslab = (a.dv + kDecaySlab - 1) / kDecaySlab;
-  const int col0 = w * (DP / 4);  // this wave's columns of dq, dk, dv
+  // with 4 column tiles, waves 4..7 take the upper half of the tokens
+  const int col0 = 16 * (w % CW), n0 = CW == 8 ? 0 : (w / 4) * (RT / 2);
+  constexpr int NT = CW == 8 ? RT : RT / 2;  // token tiles a wave
+  const int64_t items = static_cast<int64_t>(a.cslots) * a.Hk;
 
-  f32x4 dq[CT][RT], dk[CT][RT];
-#pragma unroll
-  for (int m = 0; m < CT; ++m)
-#pragma unroll
-    for (int n = 0; n < RT; ++n) dq[m][n] = dk[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-
+  // one (item, value head): where its rows are
+  struct Work {
+    int64_t item;
+    int hv;
+    Piece pc;
+  };
+  auto seek = [&](Work& k) {  // the first item at or after k.item that has tokens
+    for (; k.item < items; k.item += gridDim.x) {
+      k.pc = piece_of(a, static_cast<int>(k.item / a.Hk), C, lane);
+      if (k.pc.n >= 0 && k.pc.len > 0) return;
+    }
+  };
+  auto advance = [&](Work& k) {
+    if (++k.hv < group) return;
+    k.hv = 0;
+    k.item += gridDim.x;
+    seek(k);
+  };
   using R = RowTile<T, C, DP, kNT>;
   using RA = RowTile<T, DP, DP, kNT>;
   R tq, tv;
   RA ta;
-  typename R::Regs rq, rk, rv, ro;
-  typename RA::Regs ra;
   tq.init(ldq, a.dk, t);
   tv.init(ldv, a.dv, t);
   ta.init(a.dv, a.dv, t);
-  tq.load(rq, static_cast<const T*>(a.q) + oq, ldq, pc.len, a.dk);
-  tq.load(rk, static_cast<const T*>(a.k) + oq, ldq, pc.len, a.dk);
-  tq.store(rq, sQ, LD, t);
-  tq.store(rk, sK, LD, t);
+  int offs[ND];  // this wave's rows of the state, as operands
+#pragma unroll
+  for (int s = 0; s < ND; ++s) {
+    const int r = col0 + l16, c = KS * s + EPP * lq;
+    offs[s] = r < a.dk && c < a.dv ? (r * a.dv + c) * Cfg::ES : kNoOffset;
+  }
+  typename R::Regs rq, rk, rv, ro;
+  typename RA::Regs ra;
+  uint4 rs[ND];
+  uint32_t bits = 0;
+  float rx = 0.f;
+  auto load = [&](const Work& k) {  // nothing past the last item
+    const bool in = k.item < items;
+    const int hk = in ? static_cast<int>(k.item % a.Hk) : 0, h = hk * group + k.hv, rows = in ? k.pc.len : 0;
+    const int64_t tok = in ? k.pc.begin : 0, chain = (in ? k.item / a.Hk : 0) * a.H + h;
+    bits = load_gate_bits(a, tok, rows, h, lane);
+    if (k.hv == 0) {
+      const int64_t oq = tok * ldq + static_cast<int64_t>(hk) * a.dk;
+      tq.load(rq, static_cast<const T*>(a.q) + oq, ldq, rows, a.dk);
+      tq.load(rk, static_cast<const T*>(a.k) + oq, ldq, rows, a.dk);
+    }
+    const int64_t ov = tok * ldv + static_cast<int64_t>(h) * a.dv;
+    tv.load(rv, static_cast<const T*>(a.v) + ov, ldv, rows, a.dv);
+    tv.load(ro, static_cast<const T*>(gr.dout) + ov, ldv, rows, a.dv);
+    const int64_t rec = chain * a.dk * a.dv;
+    ta.load(ra, static_cast<const T*>(a.adjoints) + rec, a.dv, in ? a.dk : 0, a.dv);
+    const rsrc_t r = rows_rsrc(static_cast<const T*>(a.states) + rec, a.dv, in ? a.dk : 0, a.dv, DP);
+#pragma unroll
+    for (int s = 0; s < ND; ++s) rs[s] = load_piece(r, offs[s]);
+    rx = 0.f;
+    if (in)
+      for (int i = 0; i < nslab; ++i) rx += a.dots[chain * nslab + i];
+  };
 
-  for (int hv = 0; hv < group; ++hv) {
-    const int h = hk * group + hv;
-    const int64_t ov = pc.begin * ldv + static_cast<int64_t>(h) * a.dv;
-    const int64_t rec = (slot * a.H + h) * a.dk * a.dv;
-    tv.load(rv, static_cast<const T*>(a.v) + ov, ldv, pc.len, a.dv);
-    tv.load(ro, static_cast<const T*>(gr.dout) + ov, ldv, pc.len, a.dv);
-    ta.load(ra, static_cast<const T*>(a.adjoints) + rec, a.dv, a.dk, a.dv);
+  Work cur{blockIdx.x, 0, {}};
+  seek(cur);
+  if (cur.item >= items) return;
+  load(cur);
+  f32x4 dq[NT], dk[NT];
+  while (cur.item < items) {
+    const Piece pc = cur.pc;
+    const int hk = static_cast<int>(cur.item % a.Hk), h = hk * group + cur.hv;
+    const bool first = cur.hv == 0, last = cur.hv == group - 1;
     const bool tok = lane < C && lane < pc.len;
-    float xg = 0.f;
-    if (w == 0) {
-      xg = tok ? gate_stored(a, pc.begin + lane, h) : 0.f;
-      gates_fill<C>(G, xg, tok, a.gate_input, ckda, lane);
-      if (lane < C) sAl[lane] = tok ? gate_value(xg, a.gate_input, ckda) : 1.f;
-      if (lane == 0) {
-        float x = 0.f;
-        for (int i = 0; i < nslab; ++i) x += a.dots[(slot * a.H + h) * nslab + i];
-        sAl[C] = x;
-      }
+    const float xg = gate_of_bits(bits, a.gate_input);
+    if (first) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) dq[n] = dk[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+      tq.store(rq, sQ, LD, t);
+      tq.store(rk, sK, LD, t);
     }
     tv.store(rv, sV, LD, t);
     tv.store(ro, sO, LD, t);
     ta.store(ra, sA, LD, t);
+    F fs[ND];
+#pragma unroll
+    for (int s = 0; s < ND; ++s) fs[s] = *reinterpret_cast<const F*>(&rs[s]);
+    if (w == 0) {
+      gates_fill<C>(G, xg, tok, a.gate_input, ckda, lane);
+      if (lane < C) sAl[lane] = tok ? gate_value(xg, a.gate_input, ckda) : 1.f;
+      if (lane == 0) sAl[C] = rx;
+    }
+    Work next = cur;
+    advance(next);
+    load(next);
     __syncthreads();
     const bool fast = G.fast != 0;
 
     // P^T and N^T tiles: column i = 16 ti + l16, rows j = 16 tj + 4 lq + r
-    for (int tile = w; tile < RT * RT; tile += 4) {
-      const int ti = tile / RT, tj = tile % RT, i = 16 * ti + l16, j0 = 16 * tj + 4 * lq;
+    for (int tile = w; tile < RT * RT; tile += kWaves) {
+      const int ti = RT - 1 - tile / RT, tj = tile % RT, i = 16 * ti + l16, j0 = 16 * tj + 4 * lq;
       f32x4 p = {0.f, 0.f, 0.f, 0.f}, n = p;
       if (tj <= ti) {
 #pragma unroll
@@ -124,154 +183,171 @@ __global__ __launch_bounds__(kNT, 1) void decay_grad_kernel(DecayArgs a, DecayGr
           Op::mma(p, X::row(sK + (16 * tj + l16) * LD, s, lq), X::row(sQ + i * LD, s, lq));
           Op::mma(n, X::row(sV + (16 * tj + l16) * LD, s, lq), X::row(sO + i * LD, s, lq));
         }
+        const f32x4 d = decay_of(G, i, j0, fast);
+        n *= a.scale;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sM[i * LDM + j0 + r] = p[r] * n[r] * a.scale;
-        const f32x4 d = decay_of(G, i, j0, fast) * a.scale;
-        p = decayed(p, d);
+        for (int r = 0; r < 4; ++r) sM[i * LDM + j0 + r] = fast ? (d[r] != 0.f ? p[r] * d[r] * n[r] : 0.f) : p[r] * n[r];
+        p = decayed(p, d) * a.scale;
         n = decayed(n, d);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sM[i * LDM + j0 + r] = 0.f;
       }
       Op::store4(sP + i * LDC + j0, p);
       Op::store4(sN + i * LDC + j0, n);
     }
     __syncthreads();
 
-    // dq: columns dk = col0 + 16 m + 4 lq + r, token 16 n + l16
+    // dq: columns dk = col0 + 4 lq + r, token 16 n + l16
     {
-      const T* st = static_cast<const T*>(a.states) + rec;
-      F fa[CT][ND];
+      F fk[NC];
 #pragma unroll
-      for (int m = 0; m < CT; ++m) {
-        const int r = col0 + 16 * m + l16;
+      for (int ks = 0; ks < NC; ++ks) fk[ks] = X::across(sK, LD, KS * ks, col0, lane);
 #pragma unroll
-        for (int s = 0; s < ND; ++s) {
-          const int c = KS * s + EPP * lq;
-          fa[m][s] = X::zero();
-          if (r < a.dk && c < a.dv) fa[m][s] = *reinterpret_cast<const F*>(st + static_cast<int64_t>(r) * a.dv + c);
-        }
-      }
+      for (int nn = 0; nn < NT; ++nn) {
+        const int i = 16 * (n0 + nn) + l16;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int n = 0; n < RT; ++n) {
-        const int i = 16 * n + l16;
-        const float e = G.E[i] * a.scale;
+        for (int s = 0; s < ND; ++s) Op::mma(acc, fs[s], X::row(sO + i * LD, s, lq));
+        const T* qr = sQ + i * LD + col0 + 4 * lq;
         float z = 0.f;
 #pragma unroll
-        for (int m = 0; m < CT; ++m) {
-          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < 4; ++r) z += acc[r] * static_cast<float>(qr[r]);
+        dq[nn] += acc * (G.E[i] * a.scale);
 #pragma unroll
-          for (int s = 0; s < ND; ++s) Op::mma(acc, fa[m][s], X::row(sO + i * LD, s, lq));
-          const T* qr = sQ + i * LD + col0 + 16 * m + 4 * lq;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) z += acc[r] * static_cast<float>(qr[r]);
-          dq[m][n] += acc * e;
-#pragma unroll
-          for (int ks = 0; ks < NC; ++ks)
-            if (KS * ks <= 16 * n)
-              Op::mma(dq[m][n], X::across(sK, LD, KS * ks, col0 + 16 * m, lane), X::rowp(sN + i * LDC, ks, lq));
-        }
+        for (int ks = 0; ks < NC; ++ks) Op::mma(dq[nn], fk[ks], X::rowp(sN + i * LDC, ks, lq));
         z += __shfl_xor(z, 16, 64);
         z += __shfl_xor(z, 32, 64);
-        if (lq == 0) sZ[w * C + i] = z * a.scale;
+        if (lq == 0) sZ[(w % CW) * C + i] = z * a.scale;
       }
     }
+    __builtin_amdgcn_sched_barrier(0);  // hoisted across, the operands spill
     // dk, token 16 n + l16
+    {
+      F fa[ND], fq[NC];
 #pragma unroll
-    for (int n = 0; n < RT; ++n) {
-      const int j = 16 * n + l16;
-      const float wj = G.W[j];
-      float y = 0.f;
+      for (int s = 0; s < ND; ++s) fa[s] = X::row(sA + (col0 + l16) * LD, s, lq);
 #pragma unroll
-      for (int m = 0; m < CT; ++m) {
+      for (int ks = 0; ks < NC; ++ks) fq[ks] = X::across(sQ, LD, KS * ks, col0, lane);
+#pragma unroll
+      for (int nn = 0; nn < NT; ++nn) {
+        const int j = 16 * (n0 + nn) + l16;
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < ND; ++s)
-          Op::mma(acc, X::row(sA + (col0 + 16 * m + l16) * LD, s, lq), X::row(sV + j * LD, s, lq));
-        const T* kr = sK + j * LD + col0 + 16 * m + 4 * lq;
+        for (int s = 0; s < ND; ++s) Op::mma(acc, fa[s], X::row(sV + j * LD, s, lq));
+        const T* kr = sK + j * LD + col0 + 4 * lq;
+        float y = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) y += acc[r] * static_cast<float>(kr[r]);
-        dk[m][n] += acc * wj;
+        dk[nn] += acc * G.W[j];
 #pragma unroll
-        for (int ks = 0; ks < NC; ++ks)
-          if (KS * ks + KS > 16 * n)
-            Op::mma(dk[m][n], X::across(sQ, LD, KS * ks, col0 + 16 * m, lane),
-                    X::across(sN, LDC, KS * ks, 16 * n, lane));
+        for (int ks = 0; ks < NC; ++ks) Op::mma(dk[nn], fq[ks], X::across(sN, LDC, KS * ks, 16 * (n0 + nn), lane));
+        y += __shfl_xor(y, 16, 64);
+        y += __shfl_xor(y, 32, 64);
+        if (lq == 0) sY[(w % CW) * C + j] = y;
       }
-      y += __shfl_xor(y, 16, 64);
-      y += __shfl_xor(y, 32, 64);
-      if (lq == 0) sY[w * C + j] = y;
     }
-    // dv: columns dv = col0 + 16 m + 4 lq + r
-    T* gdv = static_cast<T*>(gr.dv) + ov;
+    __builtin_amdgcn_sched_barrier(0);
+    // dv: columns dv = col0 + 4 lq + r
+    {
+      F fa[ND], fo[NC];
 #pragma unroll
-    for (int n = 0; n < RT; ++n) {
-      const int j = 16 * n + l16;
-      const float wj = G.W[j];
+      for (int s = 0; s < ND; ++s) fa[s] = X::across(sA, LD, KS * s, col0, lane);
 #pragma unroll
-      for (int m = 0; m < CT; ++m) {
+      for (int ks = 0; ks < NC; ++ks) fo[ks] = X::across(sO, LD, KS * ks, col0, lane);
+      T* gdv = static_cast<T*>(gr.dv) + pc.begin * ldv + static_cast<int64_t>(h) * a.dv + col0 + 4 * lq;
+#pragma unroll
+      for (int nn = 0; nn < NT; ++nn) {
+        const int j = 16 * (n0 + nn) + l16;
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < ND; ++s)
-          Op::mma(acc, X::across(sA, LD, KS * s, col0 + 16 * m, lane), X::rowp(sK + j * LD, s, lq));
-        acc *= wj;
+        for (int s = 0; s < ND; ++s) Op::mma(acc, fa[s], X::rowp(sK + j * LD, s, lq));
+        acc *= G.W[j];
 #pragma unroll
-        for (int ks = 0; ks < NC; ++ks)
-          if (KS * ks + KS > 16 * n)
-            Op::mma(acc, X::across(sO, LD, KS * ks, col0 + 16 * m, lane),
-                    X::across(sP, LDC, KS * ks, 16 * n, lane));
-        const int c = col0 + 16 * m + 4 * lq;
-        if (j < pc.len && c < a.dv) Op::store4(gdv + static_cast<int64_t>(j) * ldv + c, acc);
+        for (int ks = 0; ks < NC; ++ks) Op::mma(acc, fo[ks], X::across(sP, LDC, KS * ks, 16 * (n0 + nn), lane));
+        if (j < pc.len && col0 + 4 * lq < a.dv) Op::store4(gdv + static_cast<int64_t>(j) * ldv, acc);
       }
     }
-    __syncthreads();  // z, y of all waves; LDS rows may change after the next
+    if (last) {
+      const int64_t oq = pc.begin * ldq + static_cast<int64_t>(hk) * a.dk + col0 + 4 * lq;
+      T* gdq = static_cast<T*>(gr.dq) + oq;
+      T* gdk = static_cast<T*>(gr.dk) + oq;
+#pragma unroll
+      for (int nn = 0; nn < NT; ++nn) {
+        const int j = 16 * (n0 + nn) + l16;
+        if (j < pc.len && col0 + 4 * lq < a.dk) {
+          Op::store4(gdq + static_cast<int64_t>(j) * ldq, dq[nn]);
+          Op::store4(gdk + static_cast<int64_t>(j) * ldq, dk[nn]);
+        }
+      }
+    }
+    __syncthreads();  // z, y and M are in LDS
 
-    if (w == 0 && gr.dalpha) {
+    if (gr.dalpha) {
       const int i = lane < C ? lane : C - 1;
-      float R = (sZ[i] + sZ[C + i]) + (sZ[2 * C + i] + sZ[3 * C + i]);
-      const float y = (sY[i] + sY[C + i]) + (sY[2 * C + i] + sY[3 * C + i]);
-      float Xr = sAl[C], da = 0.f;
-      for (int s0 = 0; s0 < C; s0 += 4) {
-        const f32x4 d = decay_of(G, i, s0, fast);
+      float z = 0.f, y = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int s = s0 + e;
-          const float al = sAl[s], ys = __shfl(y, s, 64), m = sM[i * LDM + s];
-          sM[i * LDM + s] = d[e] != 0.f ? d[e] * R : 0.f;  // past the diagonal: 0
-          R = al * R + m;
-          da = s == i ? G.W[s] * Xr : da;
-          Xr = al * Xr + ys;
+      for (int k = 0; k < CW; ++k) {
+        z += sZ[k * C + i];
+        y += sY[k * C + i];
+      }
+      float da = 0.f;
+      if (fast) {
+        // wave w: reads w, w + 8, ... (lane t: the writes before t)
+        const float ez = G.E[i] * z;
+#pragma unroll
+        for (int u = 0; u < C / kWaves; ++u) {
+          const int r = w + kWaves * u;
+          const float before = wave_scan(lane > 0 && lane <= C ? sM[r * LDM + lane - 1] : 0.f);
+          const float e = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ez), r));
+          da += lane <= r ? before + e : 0.f;
+        }
+        if (w == 0) {
+          const float wy = __shfl_up(lane < C ? G.W[i] * y : 0.f, 1, 64);
+          da += wave_scan(lane > 0 ? wy : 0.f) + G.g * sAl[C];
         }
       }
-      wave_lds_sync();
-      for (int r = i; r < C; ++r) da += sM[r * LDM + i];
-      if (tok) {
-        if (a.gate_input != CKDA_GATES_F32) {
-          const float e = expf(-fabsf(xg));
-          da *= (ckda ? 2.f : 1.f) * e / ((1.f + e) * (1.f + e));
+      __syncthreads();  // z is read: its place takes the waves' parts of da
+      if (fast && lane < C) sZ[w * C + lane] = da;
+      __syncthreads();
+      if (w == 0) {
+        if (fast) {
+          da = 0.f;
+#pragma unroll
+          for (int k = 0; k < kWaves; ++k) da += sZ[k * C + i];
+          da *= 1.f / sAl[i];
+        } else {
+          float Rr = z, Xr = sAl[C];
+          for (int s0 = 0; s0 < C; s0 += 4) {
+            const f32x4 d = decay_of(G, i, s0, false);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int s = s0 + e;
+              const float al = sAl[s], ys = __shfl(y, s, 64), m = sM[i * LDM + s];
+              sM[i * LDM + s] = d[e] != 0.f ? d[e] * Rr : 0.f;  // past the diagonal: 0
+              Rr = al * Rr + m;
+              da = s == i ? G.W[s] * Xr : da;
+              Xr = al * Xr + ys;
+            }
+          }
+          wave_lds_sync();
+          for (int r = i; r < C; ++r) da += sM[r * LDM + i];
         }
-        const int64_t at = (pc.begin + lane) * a.H + h;
-        if (a.per_head)
-          gr.per_token[at] = da;
-        else
-          static_cast<T*>(gr.dalpha)[at] = static_cast<T>(da);
+        if (tok) {
+          if (a.gate_input != CKDA_GATES_F32) {
+            const float e = expf(-fabsf(xg));
+            da *= (ckda ? 2.f : 1.f) * e / ((1.f + e) * (1.f + e));
+          }
+          const int64_t at = (pc.begin + lane) * a.H + h;
+          if (a.per_head)
+            gr.per_token[at] = da;
+          else
+            static_cast<T*>(gr.dalpha)[at] = static_cast<T>(da);
+        }
       }
     }
-    __syncthreads();
-  }
-
-  T* gdq = static_cast<T*>(gr.dq) + oq;
-  T* gdk = static_cast<T*>(gr.dk) + oq;
-#pragma unroll
-  for (int n = 0; n < RT; ++n) {
-    const int j = 16 * n + l16;
-    if (j < pc.len) {
-#pragma unroll
-      for (int m = 0; m < CT; ++m) {
-        const int c = col0 + 16 * m + 4 * lq;
-        if (c < a.dk) {
-          Op::store4(gdq + static_cast<int64_t>(j) * ldq + c, dq[m][n]);
-          Op::store4(gdk + static_cast<int64_t>(j) * ldq + c, dk[m][n]);
-        }
-      }
-    }
+    __syncthreads();  // LDS is free
+    cur = next;
   }
 }
 
@@ -302,7 +378,9 @@ launch_result launch_grad_t(const DecayArgs& a, const DecayGrads& g, hipStream_t
   static_assert(lds <= 160 * 1024, "LDS of a CU");
   const launch_result e = allow_lds<decay_grad_kernel<Op, DP, C>>(lds);
   if (e != hipSuccess) return e;
-  const int64_t grid = static_cast<int64_t>(a.cslots) * a.Hk;
+  // as many workgroups as are resident on 256 CUs, each taking items in turn
+  const int64_t items = static_cast<int64_t>(a.cslots) * a.Hk, most = 256 * (160 * 1024 / lds < 2 ? 1 : 2);
+  const int64_t grid = items < most ? items : most;
   hipLaunchKernelGGL((decay_grad_kernel<Op, DP, C>), dim3(static_cast<unsigned>(grid)), dim3(kNT), lds, s,
                      a, g);
   return hipGetLastError();

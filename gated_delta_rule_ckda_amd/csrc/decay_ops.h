@@ -158,6 +158,19 @@ __device__ __forceinline__ double wave_scan(double x) {
   x += dpp_moved<0x143, 0xc>(x);  // lane 31 into rows 2 and 3
   return x;
 }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_moved(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float wave_scan(float x) {
+  x += dpp_moved<0x111, 0xf>(x);
+  x += dpp_moved<0x112, 0xf>(x);
+  x += dpp_moved<0x114, 0xf>(x);
+  x += dpp_moved<0x118, 0xf>(x);
+  x += dpp_moved<0x142, 0xa>(x);
+  x += dpp_moved<0x143, 0xc>(x);
+  return x;
+}
 __device__ __forceinline__ double lane_value(double x, int l) {
   const uint64_t u = __builtin_bit_cast(uint64_t, x);
   const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), l);
