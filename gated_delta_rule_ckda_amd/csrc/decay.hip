@@ -32,7 +32,7 @@ struct FwdCfg {
   static constexpr int LDK = frag_stride(DKP, ES), LDV = cross_stride(DVS, ES);
   static constexpr int O_K = 0, O_V = O_K + C * LDK * ES, O_H = O_V + C * LDV * ES,
                        O_S = O_H + Fr<Op>::kTerms * C * LDV * ES, O_G = align16(O_S + DVS * LDK * ES),
-                       BYTES = O_G + 2 * static_cast<int>(sizeof(Gates<C>));
+                       BYTES = O_G + 8 * static_cast<int>(sizeof(Gates<C>));
   static constexpr int WAVES = ES == 2 ? 4 : 2;  // a SIMD
 };
 
@@ -101,7 +101,7 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
 #pragma unroll
       for (int s = 0; s < NQ; ++s) fq[s] = *reinterpret_cast<const F*>(&rq[b][s]);
       __syncthreads();  // rows, state copy and gates of chunk c are in LDS
-      const Gates<C>& G = sG[c & 1];
+      const Gates<C>& G = sG[c & 7];
       const bool fast = G.fast != 0;
       f32x4 p[C / 16];
 #pragma unroll
@@ -131,10 +131,10 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
       // where D factors, its row part multiplies the sum instead of each term
       float row = 1.f;
       if (fast) {
-        row = G.er[r];
+        row = G.u[r];
 #pragma unroll
         for (int j = 0; j < C / 16; ++j) {
-          p[j] *= *reinterpret_cast<const f32x4*>(&G.ej[16 * j + 4 * lq]);
+          p[j] *= *reinterpret_cast<const f32x4*>(&G.v[16 * j + 4 * lq]);
           if (j >= w) {  // this wave's diagonal tile, or past it
 #pragma unroll
             for (int i = 0; i < 4; ++i) p[j][i] = 16 * j + 4 * lq + i <= r ? p[j][i] : 0.f;
@@ -215,16 +215,23 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
   tv.init(ldv, vcols, t);
   typename RK::Regs rk[2];
   typename RV::Regs rv[2];
-  uint32_t bits[2];
   auto load = [&](auto P, int c) {
     constexpr int b = decltype(P)::value;
     const int rows = c < nch ? pc.len - c * C : 0;
-    bits[b] = load_gate_bits(a, pc.begin + first_token(c), rows, h, lane);
     tv.load(rv[b], gv + first_token(c) * ldv, ldv, rows, vcols);
     tk.load(rk[b], gk + first_token(c) * ldq, ldq, rows, a.dk);
   };
-  auto fill_gates = [&](int c, uint32_t x) {
-    gates_fill<C>(sG[c & 1], gate_of_bits(x, a.gate_input), c * C + lane < pc.len, a.gate_input, ckda, lane);
+  // Gates four chunks at a time, one a wave: formed one after the other they
+  // were the longest part of a chunk's step.
+  uint32_t bits;
+  auto load_gates = [&](int c) {
+    const int cw = c + w;
+    bits = load_gate_bits(a, pc.begin + first_token(cw), cw < nch ? pc.len - cw * C : 0, h, lane);
+  };
+  auto fill_gates = [&](int c) {
+    const int cw = c + w;
+    gates_fill<C>(sG[cw & 7], gate_of_bits(bits, a.gate_input), cw < nch && cw * C + lane < pc.len, a.gate_input,
+                  ckda, lane);
   };
   auto stage_rows = [&](auto P, const Gates<C>& G) {
     constexpr int b = decltype(P)::value;
@@ -242,7 +249,7 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
   auto step = [&](auto P, auto Q, int c) {
     load(P, c + 2);
     __syncthreads();  // rows, state copy and gates of chunk c are in LDS
-    const float g = sG[c & 1].g;
+    const float g = sG[c & 7].g;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -261,15 +268,17 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
           for (int m = 0; m < MT; ++m) Op::mma(S[m][n], ka[m], vb);
         }
     }
-    if (w == ((c + 1) & 3)) fill_gates(c + 1, bits[decltype(Q)::value]);
+    if ((c & 3) == 1) load_gates(c + 3);
+    if ((c & 3) == 3) fill_gates(c + 1);
     __syncthreads();  // chunk c is done with LDS; gates of chunk c + 1 are there
     stage_state();
-    stage_rows(Q, sG[(c + 1) & 1]);
+    stage_rows(Q, sG[(c + 1) & 7]);
   };
   if (nch > 0) {
+    load_gates(0);
     load(P0{}, 0);
     load(P1{}, 1);
-    if (w == 0) fill_gates(0, bits[0]);
+    fill_gates(0);
     stage_state();
     __syncthreads();
     stage_rows(P0{}, sG[0]);
@@ -304,7 +313,7 @@ struct StateCfg {
   static constexpr int LDK = frag_stride(DKP, ES), LDV = cross_stride(DVS, ES);
   static constexpr int O_K = 0, O_H = O_K + C * LDK * ES,
                        O_G = align16(O_H + Fr<Op>::kTerms * C * LDV * ES),
-                       O_R = O_G + 2 * static_cast<int>(sizeof(Gates<C>)), BYTES = O_R + 16;
+                       O_R = O_G + 8 * static_cast<int>(sizeof(Gates<C>)), BYTES = O_R + 16;
 };
 
 template <class Op, int DKP, int DVS, int C, bool REV, int MODE>
@@ -347,7 +356,6 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
   // tile (m, n) of S^T: column dk = row0 + 16 m + l16, rows dv = c0 + RUN lq +
   // 4 n + i: a lane holds RUN columns of the state in a row
   constexpr int RUN = 4 * NTL;
-  typedef T Run __attribute__((ext_vector_type(RUN)));
   const int row0 = w * (DKP / 4);
   const int64_t seq_state = (static_cast<int64_t>(pc.n) * a.H + h) * a.dk * a.dv;
   const int64_t seg_state = (static_cast<int64_t>(slot) * a.H + h) * a.dk * a.dv;
@@ -385,7 +393,6 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
   // rows wait in registers two chunks ahead; the loop takes two chunks a turn
   typename RX::Regs rx[2];
   typename RY::Regs ry[2];
-  uint32_t bits[2];
   uint4 rf[2][MT][RUN * sizeof(T) / 16];  // backwards: the forward's state at the chunk
   int64_t cslot = 0;
   if (MODE == kChunks) cslot = first_slot(a, pc.n, C) + (a.seg > 0 ? pc.s * (a.seg / C) : 0);
@@ -395,7 +402,6 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
     constexpr int b = decltype(P)::value;
     const int c = chunk_at(i), left = i < nch ? pc.len - c * C : 0, rows = left < C ? left : C;
     const int64_t o = static_cast<int64_t>(c) * C;
-    bits[b] = load_gate_bits(a, pc.begin + o, rows, h, lane);
     tx.load(rx[b], gx + o * ldx, ldx, rows, a.dk);
     ty.load(ry[b], gy + o * ldy, ldy, rows, vcols);
     if constexpr (REV && MODE == kChunks) {
@@ -410,9 +416,15 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
         }
     }
   };
-  auto fill_gates = [&](int i, uint32_t x) {
-    const bool ok = i < nch && lane < C && chunk_at(i) * C + lane < pc.len;
-    gates_fill<C>(sG[i & 1], gate_of_bits(x, a.gate_input), ok, a.gate_input, ckda, lane);
+  uint32_t bits;  // gates four chunks at a time, one a wave
+  auto load_gates = [&](int i) {
+    const int iw = i + w, c = chunk_at(iw), left = iw < nch ? pc.len - c * C : 0;
+    bits = load_gate_bits(a, pc.begin + static_cast<int64_t>(c) * C, left < C ? left : C, h, lane);
+  };
+  auto fill_gates = [&](int i) {
+    const int iw = i + w;
+    const bool ok = iw < nch && lane < C && chunk_at(iw) * C + lane < pc.len;
+    gates_fill<C>(sG[iw & 7], gate_of_bits(bits, a.gate_input), ok, a.gate_input, ckda, lane);
   };
   auto stage_rows = [&](auto P, const Gates<C>& G) {
     constexpr int b = decltype(P)::value;
@@ -458,7 +470,7 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
     __syncthreads();  // rows and gates of chunk i are in LDS
     if (MODE == kChunks && REV && t == 0)
       a.dots[((cslot + chunk_at(i)) * a.H + h) * nslab + slab] = (sR[0] + sR[1]) + (sR[2] + sR[3]);
-    const float g = sG[i & 1].g;
+    const float g = sG[i & 7].g;
     gain *= g;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -478,14 +490,16 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
           for (int m = 0; m < MT; ++m) Op::mma(S[m][n], vb, ka[m]);
         }
     }
-    if (w == ((i + 1) & 3)) fill_gates(i + 1, bits[decltype(Q)::value]);
+    if ((i & 3) == 1) load_gates(i + 3);
+    if ((i & 3) == 3) fill_gates(i + 1);
     __syncthreads();
-    stage_rows(Q, sG[(i + 1) & 1]);
+    stage_rows(Q, sG[(i + 1) & 7]);
   };
   if (nch > 0) {
+    load_gates(0);
     load_chunk(P0{}, 0);
     load_chunk(P1{}, 1);
-    if (w == 0) fill_gates(0, bits[0]);
+    fill_gates(0);
     __syncthreads();
     stage_rows(P0{}, sG[0]);
   }

@@ -42,8 +42,8 @@ struct GradCfg {
   static constexpr int O_Q = 0, O_K = ROWS, O_V = 2 * ROWS, O_O = 3 * ROWS, O_A = 4 * ROWS,
                        O_P = O_A + DP * LD * ES, O_N = O_P + C * LDC * ES,
                        O_M = O_N + C * LDC * ES, O_Z = O_M + C * LDM * 4, O_Y = O_Z + kWaves * C * 4,
-                       O_X = O_Y + kWaves * C * 4, O_G = align16(O_X + C * 4 + 16),
-                       BYTES = O_G + static_cast<int>(sizeof(Gates<C>));
+                       O_X = O_Y + kWaves * C * 4, O_G = align16(O_X + 2 * (C + 4) * 4),
+                       BYTES = O_G + 2 * static_cast<int>(sizeof(Gates<C>));
 };
 
 template <class Op, int DP, int C>
@@ -67,8 +67,8 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
   float* sM = reinterpret_cast<float*>(smem + Cfg::O_M);   // D M with fast gates, else M
   float* sZ = reinterpret_cast<float*>(smem + Cfg::O_Z);   // waves' parts of z, then of da
   float* sY = reinterpret_cast<float*>(smem + Cfg::O_Y);
-  float* sAl = reinterpret_cast<float*>(smem + Cfg::O_X);  // gates, then x
-  Gates<C>& G = *reinterpret_cast<Gates<C>*>(smem + Cfg::O_G);
+  float* sX = reinterpret_cast<float*>(smem + Cfg::O_X);  // gates, then x; two of them
+  Gates<C>* sG = reinterpret_cast<Gates<C>*>(smem + Cfg::O_G);
 
   const int t = threadIdx.x, lane = t & 63, w = uniform32(t >> 6), l16 = lane & 15, lq = lane >> 4;
   const int group = a.H / a.Hk;
@@ -143,8 +143,19 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
   seek(cur);
   if (cur.item >= items) return;
   load(cur);
+  // the gates of what `load` fetched last, into place b, by one wave
+  auto fill = [&](const Work& k, int b) {
+    const bool ok = k.item < items && lane < C && lane < k.pc.len;
+    const float x = gate_of_bits(bits, a.gate_input);
+    gates_fill<C>(sG[b], x, ok, a.gate_input, ckda, lane);
+    if (lane < C) sX[b * (C + 4) + lane] = ok ? gate_value(x, a.gate_input, ckda) : 1.f;
+    if (lane == 0) sX[b * (C + 4) + C] = rx;
+  };
+  if (w == 1) fill(cur, 0);
   f32x4 dq[NT], dk[NT];
-  while (cur.item < items) {
+  for (int turn = 0; cur.item < items; turn ^= 1) {
+    const Gates<C>& G = sG[turn];
+    const float* sAl = sX + turn * (C + 4);
     const Piece pc = cur.pc;
     const int hk = static_cast<int>(cur.item % a.Hk), h = hk * group + cur.hv;
     const bool first = cur.hv == 0, last = cur.hv == group - 1;
@@ -162,11 +173,6 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
     F fs[ND];
 #pragma unroll
     for (int s = 0; s < ND; ++s) fs[s] = *reinterpret_cast<const F*>(&rs[s]);
-    if (w == 0) {
-      gates_fill<C>(G, xg, tok, a.gate_input, ckda, lane);
-      if (lane < C) sAl[lane] = tok ? gate_value(xg, a.gate_input, ckda) : 1.f;
-      if (lane == 0) sAl[C] = rx;
-    }
     Work next = cur;
     advance(next);
     load(next);
@@ -346,7 +352,8 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
         }
       }
     }
-    __syncthreads();  // LDS is free
+    if (w == 1) fill(next, turn ^ 1);
+    __syncthreads();  // LDS is free; the next gates are there
     cur = next;
   }
 }

@@ -191,11 +191,11 @@ __device__ __forceinline__ float exp2_wide(double x) {
 // one, so D_ij = er_i ej_j (signs included).
 template <int C>
 struct alignas(16) Gates {
-  float E[C], W[C];    // products from the chunk's start, to its end
-  float er[C], ej[C];  // with `fast`
-  float hi[C], lo[C], sg[C];  // without
-  int z[C];            // without: last zero gate at or before i (-1: none)
-  float g;             // product of all
+  float E[C], W[C];  // products from the chunk's start, to its end
+  float u[C], v[C];  // er, ej; without `fast` the integer and fraction of L
+  int sz[C];         // without `fast`: 2 z + (1 where the running sign is negative),
+                     // z the last zero gate at or before i (-1: none)
+  float g;           // product of all
   int fast;
 };
 
@@ -223,8 +223,8 @@ __device__ __forceinline__ void gates_fill(Gates<C>& G, float x, bool valid, int
     if (lane < C) {
       G.E[lane] = er * em;
       G.W[lane] = ej * ee;
-      G.er[lane] = er;
-      G.ej[lane] = ej;
+      G.u[lane] = er;
+      G.v[lane] = ej;
     }
     if (lane == 0) {
       G.g = g;
@@ -235,10 +235,9 @@ __device__ __forceinline__ void gates_fill(Gates<C>& G, float x, bool valid, int
     if (lane < C) {
       G.E[lane] = z < 0 ? sg * exp2_wide(L) : 0.f;
       G.W[lane] = zend <= lane ? sg * sgend * exp2_wide(end - L) : 0.f;
-      G.hi[lane] = static_cast<float>(n);
-      G.lo[lane] = static_cast<float>(L - n);
-      G.sg[lane] = sg;
-      G.z[lane] = z;
+      G.u[lane] = static_cast<float>(n);
+      G.v[lane] = static_cast<float>(L - n);
+      G.sz[lane] = 2 * z + (sg < 0.f ? 1 : 0);
     }
     if (lane == 0) {
       G.g = zend < 0 ? sgend * exp2_wide(end) : 0.f;
@@ -252,19 +251,20 @@ template <int C>
 __device__ __forceinline__ f32x4 decay_of(const Gates<C>& G, int i, int j0, bool fast) {
   f32x4 d;
   if (fast) {
-    d = *reinterpret_cast<const f32x4*>(&G.ej[j0]) * G.er[i];
+    d = *reinterpret_cast<const f32x4*>(&G.v[j0]) * G.u[i];
 #pragma unroll
     for (int e = 0; e < 4; ++e) d[e] = j0 + e <= i ? d[e] : 0.f;
   } else {
-    const f32x4 hi = *reinterpret_cast<const f32x4*>(&G.hi[j0]);
-    const f32x4 lo = *reinterpret_cast<const f32x4*>(&G.lo[j0]);
-    const f32x4 sg = *reinterpret_cast<const f32x4*>(&G.sg[j0]) * G.sg[i];
-    const float h = G.hi[i], l = G.lo[i];
-    const int z = G.z[i];
+    const f32x4 hi = *reinterpret_cast<const f32x4*>(&G.u[j0]);
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(&G.v[j0]);
+    const int4 sz = *reinterpret_cast<const int4*>(&G.sz[j0]);
+    const int szj[4] = {sz.x, sz.y, sz.z, sz.w};
+    const float h = G.u[i], l = G.v[i];
+    const int si = G.sz[i], z = si >> 1;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float x = sg[e] * __builtin_amdgcn_exp2f((h - hi[e]) + (l - lo[e]));
-      d[e] = (j0 + e <= i && z <= j0 + e) ? x : 0.f;
+      const float x = __builtin_amdgcn_exp2f((h - hi[e]) + (l - lo[e]));
+      d[e] = (j0 + e <= i && z <= j0 + e) ? (((si ^ szj[e]) & 1) ? -x : x) : 0.f;
     }
   }
   return d;
