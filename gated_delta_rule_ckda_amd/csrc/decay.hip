@@ -89,6 +89,12 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
       const int col = KS * s + EPP * lq;
       offq[s] = col < a.dk ? (r * ldq + col) * Cfg::ES : kNoOffset;
     }
+    int offo[4 * NTL / EPP];
+#pragma unroll
+    for (int u = 0; u < 4 * NTL / EPP; ++u) {
+      const int col = 4 * NTL * lq + EPP * u;
+      offo[u] = col < vcols ? (r * ldv + col) * Cfg::ES : kNoOffset;
+    }
     auto load = [&](auto P, int c) {  // zeros past the last chunk
       constexpr int b = decltype(P)::value;
       const rsrc_t rs = rows_rsrc(gq + first_token(c) * ldq, ldq, c < nch ? pc.len - c * C : 0, a.dk, C);
@@ -155,16 +161,13 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
         }
       const float e = G.E[r] * a.scale;
       row *= a.scale;
-      if (c * C + r < pc.len) {
-        T* dst = go + static_cast<int64_t>(c * C + r) * ldv + 4 * NTL * lq;
-        alignas(16) T y[4 * NTL];
+      const rsrc_t ro = rows_rsrc(go + first_token(c) * ldv, ldv, pc.len - c * C, vcols, C);
+      alignas(16) T y[4 * NTL];
 #pragma unroll
-        for (int n = 0; n < NTL; ++n) Op::store4(y + 4 * n, x[n] * e + o[n] * row);
+      for (int n = 0; n < NTL; ++n) Op::store4(y + 4 * n, x[n] * e + o[n] * row);
 #pragma unroll
-        for (int u = 0; u < 4 * NTL / EPP; ++u)
-          if (4 * NTL * lq + EPP * u < vcols)
-            *reinterpret_cast<uint4*>(dst + EPP * u) = *reinterpret_cast<const uint4*>(y + EPP * u);
-      }
+      for (int u = 0; u < 4 * NTL / EPP; ++u)
+        store_piece(ro, offo[u], *reinterpret_cast<const uint4*>(y + EPP * u));
       __syncthreads();  // chunk c is done with LDS; gates of chunk c + 1 are there
     };
     if (nch > 0) {
@@ -441,7 +444,7 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
   float gain = 1.f;
   auto step = [&](auto P, auto Q, int i) {
     if (MODE == kChunks) {  // the state met at this chunk
-      T* dst = static_cast<T*>(REV ? a.adjoints : a.states) + record(i);
+      const rsrc_t dst = rows_rsrc(static_cast<const T*>(REV ? a.adjoints : a.states) + record(i), a.dv, a.dk, a.dv, DKP);
       float dot = 0.f;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -451,7 +454,7 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
 #pragma unroll
         for (int u = 0; u < RUN * static_cast<int>(sizeof(T)) / 16; ++u) {
           const int at = place(m, u * (4 / static_cast<int>(sizeof(T))));
-          if (at >= 0) *reinterpret_cast<uint4*>(dst + at) = reinterpret_cast<const uint4*>(y)[u];
+          store_piece(dst, at >= 0 ? at * static_cast<int>(sizeof(T)) : kNoOffset, reinterpret_cast<const uint4*>(y)[u]);
           if (REV) {
             constexpr int E = 16 / sizeof(T);
 #pragma unroll

@@ -261,7 +261,8 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
       for (int s = 0; s < ND; ++s) fa[s] = X::across(sA, LD, KS * s, col0, lane);
 #pragma unroll
       for (int ks = 0; ks < NC; ++ks) fo[ks] = X::across(sO, LD, KS * ks, col0, lane);
-      T* gdv = static_cast<T*>(gr.dv) + pc.begin * ldv + static_cast<int64_t>(h) * a.dv + col0 + 4 * lq;
+      const rsrc_t gdv = rows_rsrc(static_cast<const T*>(gr.dv) + pc.begin * ldv + static_cast<int64_t>(h) * a.dv, ldv,
+                                   pc.len, a.dv, C);
 #pragma unroll
       for (int nn = 0; nn < NT; ++nn) {
         const int j = 16 * (n0 + nn) + l16;
@@ -271,20 +272,20 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
         acc *= G.W[j];
 #pragma unroll
         for (int ks = 0; ks < NC; ++ks) Op::mma(acc, fo[ks], X::across(sP, LDC, KS * ks, 16 * (n0 + nn), lane));
-        if (j < pc.len && col0 + 4 * lq < a.dv) Op::store4(gdv + static_cast<int64_t>(j) * ldv, acc);
+        const int col = col0 + 4 * lq;
+        store_four<Op>(gdv, col < a.dv ? (j * ldv + col) * Cfg::ES : kNoOffset, acc);
       }
     }
     if (last) {
-      const int64_t oq = pc.begin * ldq + static_cast<int64_t>(hk) * a.dk + col0 + 4 * lq;
-      T* gdq = static_cast<T*>(gr.dq) + oq;
-      T* gdk = static_cast<T*>(gr.dk) + oq;
+      const int64_t oq = pc.begin * ldq + static_cast<int64_t>(hk) * a.dk;
+      const rsrc_t gdq = rows_rsrc(static_cast<const T*>(gr.dq) + oq, ldq, pc.len, a.dk, C);
+      const rsrc_t gdk = rows_rsrc(static_cast<const T*>(gr.dk) + oq, ldq, pc.len, a.dk, C);
 #pragma unroll
       for (int nn = 0; nn < NT; ++nn) {
-        const int j = 16 * (n0 + nn) + l16;
-        if (j < pc.len && col0 + 4 * lq < a.dk) {
-          Op::store4(gdq + static_cast<int64_t>(j) * ldq, dq[nn]);
-          Op::store4(gdk + static_cast<int64_t>(j) * ldq, dk[nn]);
-        }
+        const int j = 16 * (n0 + nn) + l16, col = col0 + 4 * lq;
+        const int off = col < a.dk ? (j * ldq + col) * Cfg::ES : kNoOffset;
+        store_four<Op>(gdq, off, dq[nn]);
+        store_four<Op>(gdk, off, dk[nn]);
       }
     }
     __syncthreads();  // z, y and M are in LDS

@@ -294,6 +294,23 @@ __device__ __forceinline__ uint4 load_piece(rsrc_t r, int off) {
   ldraw<16>(r, off, reinterpret_cast<uint32_t*>(&x));
   return x;
 }
+// Stores through such a resource drop what lies past it.
+__device__ __forceinline__ void store_piece(rsrc_t r, int off, const uint4& x) {
+  typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+  __builtin_amdgcn_raw_buffer_store_b128(u32x4{x.x, x.y, x.z, x.w}, r, off, 0, 0);
+}
+// 4 values in the type of Op (8 or 16 bytes)
+template <class Op>
+__device__ __forceinline__ void store_four(rsrc_t r, int off, const f32x4& x) {
+  alignas(16) typename Op::T y[4];
+  Op::store4(y, x);
+  if constexpr (sizeof(typename Op::T) == 2) {
+    typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+    __builtin_amdgcn_raw_buffer_store_b64(*reinterpret_cast<const u32x2*>(y), r, off, 0, 0);
+  } else {
+    store_piece(r, off, *reinterpret_cast<const uint4*>(y));
+  }
+}
 template <class T, int ROWS, int COLS, int NT>
 struct RowTile {
   static constexpr int EPP = 16 / sizeof(T), PPR = COLS / EPP, NP = ROWS * PPR / NT;
