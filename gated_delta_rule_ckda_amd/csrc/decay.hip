@@ -74,7 +74,7 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
   const int64_t oq = pc.begin * ldq + static_cast<int64_t>(hk) * a.dk;
   const int64_t ov = pc.begin * ldv + static_cast<int64_t>(h) * a.dv + c0;
   const int nch = (pc.len + C - 1) / C;
-  auto first_token = [&](int c) { return c < nch ? static_cast<int64_t>(c) * C : 0; };
+  auto first_token = [&](int c) { return static_cast<int64_t>(c) * C; };  // past the end: nothing is read there
 
   // Each role's loop takes two chunks a turn, so that the registers a chunk's
   // rows wait in are fixed: they are loaded two chunks ahead.
@@ -97,7 +97,7 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
     }
     auto load = [&](auto P, int c) {  // zeros past the last chunk
       constexpr int b = decltype(P)::value;
-      const rsrc_t rs = rows_rsrc(gq + first_token(c) * ldq, ldq, c < nch ? pc.len - c * C : 0, a.dk, C);
+      const rsrc_t rs = rows_rsrc(gq + first_token(c) * ldq, ldq, pc.len - c * C, a.dk, C);
 #pragma unroll
       for (int s = 0; s < NQ; ++s) rq[b][s] = load_piece(rs, offq[s]);
     };
@@ -175,10 +175,12 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
       load(std::integral_constant<int, 1>{}, 1);
       __syncthreads();
     }
-    for (int c = 0; c < nch; c += 2) {
+    int c = 0;
+    for (; c + 1 < nch; c += 2) {
       step(std::integral_constant<int, 0>{}, c);
-      if (c + 1 < nch) step(std::integral_constant<int, 1>{}, c + 1);
+      step(std::integral_constant<int, 1>{}, c + 1);
     }
+    if (c < nch) step(std::integral_constant<int, 0>{}, c);
     return;
   }
 
@@ -220,20 +222,20 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
   typename RV::Regs rv[2];
   auto load = [&](auto P, int c) {
     constexpr int b = decltype(P)::value;
-    const int rows = c < nch ? pc.len - c * C : 0;
+    const int rows = pc.len - c * C;
     tv.load(rv[b], gv + first_token(c) * ldv, ldv, rows, vcols);
     tk.load(rk[b], gk + first_token(c) * ldq, ldq, rows, a.dk);
   };
   // Gates four chunks at a time, one a wave: formed one after the other they
   // were the longest part of a chunk's step.
-  uint32_t bits;
+  GateBits bits;
   auto load_gates = [&](int c) {
     const int cw = c + w;
-    bits = load_gate_bits(a, pc.begin + first_token(cw), cw < nch ? pc.len - cw * C : 0, h, lane);
+    bits = load_gate_bits(a, pc.begin + first_token(cw), pc.len - cw * C, h, lane);
   };
   auto fill_gates = [&](int c) {
     const int cw = c + w;
-    gates_fill<C>(sG[cw & 7], gate_of_bits(bits, a.gate_input), cw < nch && cw * C + lane < pc.len, a.gate_input,
+    gates_fill<C>(sG[cw & 7], gate_of_bits(bits, a.gate_input), cw * C + lane < pc.len, a.gate_input,
                   ckda, lane);
   };
   auto stage_rows = [&](auto P, const Gates<C>& G) {
@@ -286,10 +288,12 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
     __syncthreads();
     stage_rows(P0{}, sG[0]);
   }
-  for (int c = 0; c < nch; c += 2) {
+  int c = 0;
+  for (; c + 1 < nch; c += 2) {
     step(P0{}, P1{}, c);
-    if (c + 1 < nch) step(P1{}, P0{}, c + 1);
+    step(P1{}, P0{}, c + 1);
   }
+  if (c < nch) step(P0{}, P1{}, c);
   if (a.ht && pc.s == pc.count - 1) {
     float* dst = a.ht + sbase;
     each([&](const f32x4& x, int i, bool in, int64_t at) {
@@ -399,12 +403,16 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
   uint4 rf[2][MT][RUN * sizeof(T) / 16];  // backwards: the forward's state at the chunk
   int64_t cslot = 0;
   if (MODE == kChunks) cslot = first_slot(a, pc.n, C) + (a.seg > 0 ? pc.s * (a.seg / C) : 0);
-  auto chunk_at = [&](int i) { return i < nch ? (REV ? nch - 1 - i : i) : 0; };
+  auto chunk_at = [&](int i) { return REV ? nch - 1 - i : i; };
+  auto rows_at = [&](int i) {  // none past the last
+    const int left = REV ? min(pc.len - (nch - 1 - i) * C, C) : pc.len - i * C;
+    return i < nch ? left : 0;
+  };
   auto record = [&](int i) { return ((cslot + chunk_at(i)) * a.H + h) * a.dk * a.dv; };
   auto load_chunk = [&](auto P, int i) {  // zeros past the last
     constexpr int b = decltype(P)::value;
-    const int c = chunk_at(i), left = i < nch ? pc.len - c * C : 0, rows = left < C ? left : C;
-    const int64_t o = static_cast<int64_t>(c) * C;
+    const int rows = rows_at(i);
+    const int64_t o = static_cast<int64_t>(chunk_at(i)) * C;
     tx.load(rx[b], gx + o * ldx, ldx, rows, a.dk);
     ty.load(ry[b], gy + o * ldy, ldy, rows, vcols);
     if constexpr (REV && MODE == kChunks) {
@@ -419,10 +427,10 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
         }
     }
   };
-  uint32_t bits;  // gates four chunks at a time, one a wave
+  GateBits bits;  // gates four chunks at a time, one a wave
   auto load_gates = [&](int i) {
-    const int iw = i + w, c = chunk_at(iw), left = iw < nch ? pc.len - c * C : 0;
-    bits = load_gate_bits(a, pc.begin + static_cast<int64_t>(c) * C, left < C ? left : C, h, lane);
+    const int iw = i + w;
+    bits = load_gate_bits(a, pc.begin + static_cast<int64_t>(chunk_at(iw)) * C, min(rows_at(iw), C), h, lane);
   };
   auto fill_gates = [&](int i) {
     const int iw = i + w;
@@ -506,10 +514,12 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
     __syncthreads();
     stage_rows(P0{}, sG[0]);
   }
-  for (int i = 0; i < nch; i += 2) {
+  int i = 0;
+  for (; i + 1 < nch; i += 2) {
     step(P0{}, P1{}, i);
-    if (i + 1 < nch) step(P1{}, P0{}, i + 1);
+    step(P1{}, P0{}, i + 1);
   }
+  if (i < nch) step(P0{}, P1{}, i);
   if (MODE == kSegment) {
     save(a.entry + seg_state);
     if (slab == 0 && t == 0) a.gain[static_cast<int64_t>(slot) * a.H + h] = gain;

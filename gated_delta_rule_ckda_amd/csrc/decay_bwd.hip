@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
   typename R::Regs rq, rk, rv, ro;
   typename RA::Regs ra;
   uint4 rs[ND];
-  uint32_t bits = 0;
+  GateBits bits;
   float rx = 0.f;
   auto load = [&](const Work& k) {  // nothing past the last item
     const bool in = k.item < items;

@@ -285,9 +285,10 @@ __device__ __forceinline__ f32x4 decayed(f32x4 x, f32x4 d) {
 constexpr int kNoOffset = 0x7ffffff0;
 template <class T>
 __device__ __forceinline__ rsrc_t rows_rsrc(const T* base, int ld, int rows, int cols, int most) {
-  const int r = rows < most ? rows : most;
+  // no branch (a wait after one would count the path with fewer loads)
+  const int r = min(rows, most), bytes = ((r - 1) * ld + cols) * static_cast<int>(sizeof(T));
   const T* b = reinterpret_cast<const T*>(uniform64(reinterpret_cast<int64_t>(base)));
-  return make_rsrc(b, uniform32(r > 0 ? ((r - 1) * ld + cols) * static_cast<int>(sizeof(T)) : 0));
+  return make_rsrc(b, uniform32(bytes & ~((r - 1) >> 31)));
 }
 __device__ __forceinline__ uint4 load_piece(rsrc_t r, int off) {
   uint4 x;
@@ -347,23 +348,25 @@ constexpr int cross_stride(int n, int es) { return n * es == 64 ? 96 / es : frag
 
 // The stored gate of token `lane` of `rows` tokens from `token` on, as raw
 // bits (0 past them): issued with a chunk's rows and decoded after them.
-__device__ __forceinline__ uint32_t load_gate_bits(const DecayArgs& a, int64_t token, int rows, int h,
+struct GateBits {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ GateBits load_gate_bits(const DecayArgs& a, int64_t token, int rows, int h,
                                                    int lane) {
+  // two loads of two bytes each, at any type, in the place of a branch on it
   const int gs = a.gate_input == CKDA_GATES_LOGITS_BF16 ? 2 : 4;
-  const int64_t at = (a.per_head ? 0 : (rows > 0 ? token : 0) * a.H) + h;
+  const int64_t at = (a.per_head ? 0 : token * a.H) + h;
   const unsigned char* b = static_cast<const unsigned char*>(a.alpha) + at * gs;
-  const int ld = a.per_head ? 0 : a.H, n = rows < 64 ? rows : 64;
+  const int ld = a.per_head ? 0 : a.H, n = min(rows, 64), bytes = ((n - 1) * ld + 1) * gs;
   const rsrc_t r = make_rsrc(reinterpret_cast<const void*>(uniform64(reinterpret_cast<int64_t>(b))),
-                             uniform32(n > 0 ? ((n - 1) * ld + 1) * gs : 0));
-  uint32_t x;
-  if (gs == 2)
-    ldraw<2>(r, lane * ld * gs, &x);
-  else
-    ldraw<4>(r, lane * ld * gs, &x);
+                             uniform32(bytes & ~((n - 1) >> 31)));
+  GateBits x;
+  ldraw<2>(r, lane * ld * gs, &x.lo);
+  ldraw<2>(r, lane * ld * gs + (gs - 2), &x.hi);  // of a bf16 gate, its bits again
   return x;
 }
-__device__ __forceinline__ float gate_of_bits(uint32_t x, int gate_input) {
-  return __uint_as_float(gate_input == CKDA_GATES_LOGITS_BF16 ? x << 16 : x);
+__device__ __forceinline__ float gate_of_bits(const GateBits& x, int gate_input) {
+  return __uint_as_float((x.hi << 16) | (gate_input == CKDA_GATES_LOGITS_BF16 ? 0 : x.lo));
 }
 
 // ---- operand fragments --------------------------------------------------------
