@@ -19,42 +19,43 @@ constexpr int kNT = 256;  // 4 waves
 //   O^T = E S^T Q^T + V^T (D P)^T
 //   S   = g S + K^T (W V)
 //
-// Half of the eight waves read out (wave w: the 16 tokens 16w.. of Q), half
-// keep the state (wave w: DKP/4 of its rows, in the matrix accumulators, in
-// float32): the two run side by side on one chunk, since the read-out takes
-// the state from before it.  P^T leaves the accumulators as the next
-// product's operand.  K, V, W V and a copy of S in the io type pass through
-// LDS; the next chunk's rows are loaded into registers meanwhile.
+// Four waves read out (wave w: the 16 tokens 16w.. of Q, all DVS columns); four
+// for every 32 columns keep the state (DKP/4 rows each, in the matrix
+// accumulators, in float32) and bring K and V in.  The two kinds run side by
+// side on one chunk, since the read-out takes the state from before it, and
+// everything they hand on in LDS (K, V, W V, a copy of S in the io type) is
+// held twice, so that a chunk's step has one barrier: with one copy the
+// hand-over itself, between two barriers, took as long as the products.  P^T
+// leaves the accumulators as the next product's operand.
 template <class Op, int DKP, int DVS>
 struct FwdCfg {
   using T = typename Op::T;
-  static constexpr int C = kDecayChunk, ES = sizeof(T), NT = 512;
-  static constexpr int LDK = frag_stride(DKP, ES), LDV = cross_stride(DVS, ES);
-  static constexpr int O_K = 0, O_V = O_K + C * LDK * ES, O_H = O_V + C * LDV * ES,
-                       O_S = O_H + Fr<Op>::kTerms * C * LDV * ES, O_G = align16(O_S + DVS * LDK * ES),
+  static constexpr int C = kDecayChunk, ES = sizeof(T), NU = DVS / 8, NT = 64 * (4 + NU);
+  static constexpr int LDK = frag_stride(DKP, ES), LDV = cross_stride(DVS, ES), LDS = DKP + 16 / ES;
+  static constexpr int NV = 1 + Fr<Op>::kTerms;  // V, then the terms of W V
+  static constexpr int KB = C * LDK * ES, VB = NV * C * LDV * ES, SB = DVS * LDS * ES;
+  static constexpr int O_K = 0, O_V = O_K + 2 * KB, O_S = O_V + 2 * VB, O_G = align16(O_S + 2 * SB),
                        BYTES = O_G + 8 * static_cast<int>(sizeof(Gates<C>));
-  static constexpr int WAVES = ES == 2 ? 4 : 2;  // a SIMD
+  static_assert(BYTES <= 160 * 1024, "LDS of a CU");
 };
 
 template <class Op, int DKP, int DVS>
-__global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::WAVES)) void decay_fwd_kernel(
-    DecayArgs a) {
+__global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT)) void decay_fwd_kernel(DecayArgs a) {
   using Cfg = FwdCfg<Op, DKP, DVS>;
   using X = Fr<Op>;
   using T = typename Op::T;
   using F = typename X::F;
-  constexpr int C = Cfg::C, LDK = Cfg::LDK, LDV = Cfg::LDV, KS = X::KS, NW = 256;
-  constexpr int NQ = DKP / KS, MT = DKP / 64, NTL = DVS / 16, EPP = 16 / sizeof(T);
+  constexpr int C = Cfg::C, LDK = Cfg::LDK, LDV = Cfg::LDV, KS = X::KS, NW = 64 * Cfg::NU;
+  constexpr int NQ = DKP / KS, MT = DKP / 64, NTO = DVS / 16, NTS = 2, EPP = 16 / sizeof(T);
   extern __shared__ __align__(16) unsigned char smem[];
-  T* sK = reinterpret_cast<T*>(smem + Cfg::O_K);
-  T* sV = reinterpret_cast<T*>(smem + Cfg::O_V);
-  T* sH = reinterpret_cast<T*>(smem + Cfg::O_H);
-  T* sS = reinterpret_cast<T*>(smem + Cfg::O_S);
+  // by the chunk's parity
+  auto sK = [&](int c) { return reinterpret_cast<T*>(smem + Cfg::O_K + (c & 1) * Cfg::KB); };
+  auto sV = [&](int c) { return reinterpret_cast<T*>(smem + Cfg::O_V + (c & 1) * Cfg::VB); };
+  auto sS = [&](int c) { return reinterpret_cast<T*>(smem + Cfg::O_S + (c & 1) * Cfg::SB); };
   Gates<C>* sG = reinterpret_cast<Gates<C>*>(smem + Cfg::O_G);
 
   const int lane = threadIdx.x & 63, l16 = lane & 15, lq = lane >> 4;
-  const int wave = uniform32(threadIdx.x >> 6), w = wave & 3, t = threadIdx.x & (NW - 1);
-  const bool reads_out = wave < 4;
+  const int wave = uniform32(threadIdx.x >> 6);
   const int nslab = (a.dv + DVS - 1) / DVS;
   int64_t chain;
   int slab;
@@ -76,39 +77,43 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
   const int nch = (pc.len + C - 1) / C;
   auto first_token = [&](int c) { return static_cast<int64_t>(c) * C; };  // past the end: nothing is read there
 
-  // Each role's loop takes two chunks a turn, so that the registers a chunk's
-  // rows wait in are fixed: they are loaded two chunks ahead.
-  if (reads_out) {
-    const T* gq = static_cast<const T*>(a.q) + oq;
+  if (wave < 4) {  // ---- read-out
+    const int w = wave, r = 16 * w + l16;  // this lane's token
     T* go = static_cast<T*>(a.o) + ov;
-    const int r = 16 * w + l16;  // this lane's token
-    uint4 rq[2][NQ];
+    // tile n of the output holds, in lane (l16, lq), columns RUN lq + 4 n + i of
+    // token l16: RUN columns in a row
+    constexpr int RUN = 4 * NTO;
+    int offo[RUN / EPP];
+#pragma unroll
+    for (int u = 0; u < RUN / EPP; ++u) {
+      const int col = RUN * lq + EPP * u;
+      offo[u] = col < vcols ? (r * ldv + col) * Cfg::ES : kNoOffset;
+    }
+    const T* gq = static_cast<const T*>(a.q) + oq;
+    uint4 rq[NQ];
     int offq[NQ];
 #pragma unroll
     for (int s = 0; s < NQ; ++s) {
       const int col = KS * s + EPP * lq;
       offq[s] = col < a.dk ? (r * ldq + col) * Cfg::ES : kNoOffset;
     }
-    int offo[4 * NTL / EPP];
-#pragma unroll
-    for (int u = 0; u < 4 * NTL / EPP; ++u) {
-      const int col = 4 * NTL * lq + EPP * u;
-      offo[u] = col < vcols ? (r * ldv + col) * Cfg::ES : kNoOffset;
-    }
-    auto load = [&](auto P, int c) {  // zeros past the last chunk
-      constexpr int b = decltype(P)::value;
+    auto load = [&](int c) {
       const rsrc_t rs = rows_rsrc(gq + first_token(c) * ldq, ldq, pc.len - c * C, a.dk, C);
 #pragma unroll
-      for (int s = 0; s < NQ; ++s) rq[b][s] = load_piece(rs, offq[s]);
+      for (int s = 0; s < NQ; ++s) rq[s] = load_piece(rs, offq[s]);
     };
-    auto step = [&](auto P, int c) {
-      constexpr int b = decltype(P)::value;
-      F fq[NQ];
-#pragma unroll
-      for (int s = 0; s < NQ; ++s) fq[s] = *reinterpret_cast<const F*>(&rq[b][s]);
+    if (nch > 0) {
+      load(0);
+      __syncthreads();
+    }
+    for (int c = 0; c < nch; ++c) {
       __syncthreads();  // rows, state copy and gates of chunk c are in LDS
       const Gates<C>& G = sG[c & 7];
       const bool fast = G.fast != 0;
+      const T *tK = sK(c), *tV = sV(c), *tS = sS(c);
+      F fq[NQ];
+#pragma unroll
+      for (int s = 0; s < NQ; ++s) fq[s] = *reinterpret_cast<const F*>(&rq[s]);
       f32x4 p[C / 16];
 #pragma unroll
       for (int j = 0; j < C / 16; ++j) p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -116,24 +121,22 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
         constexpr int j0 = decltype(J)::value;
 #pragma unroll
         for (int j = j0; j < j0 + 2; ++j) {
-          const T* rowk = sK + (16 * j + l16) * LDK;
+          const T* rowk = tK + (16 * j + l16) * LDK;
 #pragma unroll
           for (int s = 0; s < NQ; ++s) Op::mma(p[j], X::row(rowk, s, lq), fq[s]);
         }
       };
       tile_pair(std::integral_constant<int, 0>{});
       if (w >= 2) tile_pair(std::integral_constant<int, 2>{});
-      // tile n of the output holds, in lane (l16, lq), columns EPL lq + 4 n + i
-      // of token l16: EPL = 4 NTL columns in a row
-      f32x4 o[NTL], x[NTL];
+      f32x4 o[NTO], x[NTO];
 #pragma unroll
-      for (int n = 0; n < NTL; ++n) {
+      for (int n = 0; n < NTO; ++n) {
         o[n] = x[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const T* rows = sS + (4 * NTL * (l16 >> 2) + 4 * n + (l16 & 3)) * LDK;
+        const T* rows = tS + (RUN * (l16 >> 2) + 4 * n + (l16 & 3)) * Cfg::LDS;
 #pragma unroll
         for (int s = 0; s < NQ; ++s) Op::mma(x[n], X::row(rows, s, lq), fq[s]);
       }
-      load(P, c + 2);
+      load(c + 1);
       // where D factors, its row part multiplies the sum instead of each term
       float row = 1.f;
       if (fast) {
@@ -156,58 +159,45 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
       for (int ks = 0; ks < C / KS; ++ks)
         if (2 * ks < C / KS || w >= 2) {
 #pragma unroll
-          for (int n = 0; n < NTL; ++n)
-            Op::mma(o[n], X::across(sV, LDV, KS * ks, 4 * n, lane, 4 * NTL), pf[ks]);
+          for (int n = 0; n < NTO; ++n) Op::mma(o[n], X::across(tV, LDV, KS * ks, 4 * n, lane, RUN), pf[ks]);
         }
       const float e = G.E[r] * a.scale;
       row *= a.scale;
       const rsrc_t ro = rows_rsrc(go + first_token(c) * ldv, ldv, pc.len - c * C, vcols, C);
-      alignas(16) T y[4 * NTL];
+      alignas(16) T y[RUN];
 #pragma unroll
-      for (int n = 0; n < NTL; ++n) Op::store4(y + 4 * n, x[n] * e + o[n] * row);
+      for (int n = 0; n < NTO; ++n) Op::store4(y + 4 * n, x[n] * e + o[n] * row);
 #pragma unroll
-      for (int u = 0; u < 4 * NTL / EPP; ++u)
-        store_piece(ro, offo[u], *reinterpret_cast<const uint4*>(y + EPP * u));
-      __syncthreads();  // chunk c is done with LDS; gates of chunk c + 1 are there
-    };
-    if (nch > 0) {
-      load(std::integral_constant<int, 0>{}, 0);
-      load(std::integral_constant<int, 1>{}, 1);
-      __syncthreads();
+      for (int u = 0; u < RUN / EPP; ++u) store_piece(ro, offo[u], *reinterpret_cast<const uint4*>(y + EPP * u));
     }
-    int c = 0;
-    for (; c + 1 < nch; c += 2) {
-      step(std::integral_constant<int, 0>{}, c);
-      step(std::integral_constant<int, 1>{}, c + 1);
-    }
-    if (c < nch) step(std::integral_constant<int, 0>{}, c);
     return;
   }
 
-  // state tile (m, n): rows dk = row0 + 16 m + 4 lq + i, column c0 + 16 n + l16
-  const int row0 = w * (DKP / 4);
+  // ---- state tile (m, n): rows dk = row0 + 16 m + 4 lq + i, column c0 + colw + 16 n + l16
+  const int w = (wave - 4) & 3, t = threadIdx.x - 256;
+  const int row0 = w * (DKP / 4), colw = 32 * ((wave - 4) >> 2);
   const int64_t sbase = (static_cast<int64_t>(pc.n) * a.H + h) * a.dk * a.dv;
-  f32x4 S[MT][NTL];
+  f32x4 S[MT][NTS];
   auto each = [&](auto f) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < NTL; ++n)
+      for (int n = 0; n < NTS; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = row0 + 16 * m + 4 * lq + i, c = 16 * n + l16;
+          const int r = row0 + 16 * m + 4 * lq + i, c = colw + 16 * n + l16;
           f(S[m][n], i, r < a.dk && c < vcols, static_cast<int64_t>(r) * a.dv + c0 + c);
         }
   };
   const float* src = a.seg > 0 ? a.entry + (static_cast<int64_t>(slot) * a.H + h) * a.dk * a.dv
                                : (a.h0 ? a.h0 + sbase : nullptr);
   each([&](f32x4& x, int i, bool in, int64_t at) { x[i] = src && in ? src[at] : 0.f; });
-  auto stage_state = [&]() {
+  auto stage_state = [&](int c) {  // as chunk c meets it
+    T* dst = sS(c) + (colw + l16) * Cfg::LDS + row0 + 4 * lq;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < NTL; ++n)
-        Op::store4(sS + (16 * n + l16) * LDK + row0 + 16 * m + 4 * lq, S[m][n]);
+      for (int n = 0; n < NTS; ++n) Op::store4(dst + 16 * n * Cfg::LDS + 16 * m, S[m][n]);
   };
   const bool ckda = a.gate_range == CKDA_GATE_CKDA;
   const T* gk = static_cast<const T*>(a.k) + oq;
@@ -218,6 +208,8 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
   RV tv;
   tk.init(ldq, a.dk, t);
   tv.init(ldv, vcols, t);
+  // Rows wait in registers for two chunks; the loop takes two a turn, so that
+  // the registers are fixed.
   typename RK::Regs rk[2];
   typename RV::Regs rv[2];
   auto load = [&](auto P, int c) {
@@ -235,18 +227,20 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
   };
   auto fill_gates = [&](int c) {
     const int cw = c + w;
-    gates_fill<C>(sG[cw & 7], gate_of_bits(bits, a.gate_input), cw * C + lane < pc.len, a.gate_input,
-                  ckda, lane);
+    if (colw == 0)
+      gates_fill<C>(sG[cw & 7], gate_of_bits(bits, a.gate_input), cw * C + lane < pc.len, a.gate_input, ckda, lane);
   };
-  auto stage_rows = [&](auto P, const Gates<C>& G) {
+  auto stage_rows = [&](auto P, int c) {
     constexpr int b = decltype(P)::value;
-    tv.store(rv[b], sV, LDV, t);
+    T* dst = sV(c);
+    const Gates<C>& G = sG[c & 7];
+    tv.store(rv[b], dst, LDV, t);
 #pragma unroll
     for (int u = 0; u < RV::NP; ++u) {
-      const int p = t + NW * u, row = p / RV::PPR, c = (p % RV::PPR) * RV::EPP;
-      store_scaled<T>(rv[b].r[u], G.W[row], sH + row * LDV + c, C * LDV);
+      const int p = t + NW * u, row = p / RV::PPR, col = (p % RV::PPR) * RV::EPP;
+      store_scaled<T>(rv[b].r[u], G.W[row], dst + C * LDV + row * LDV + col, C * LDV);
     }
-    tk.store(rk[b], sK, LDK, t);
+    tk.store(rk[b], sK(c), LDK, t);
   };
   using P0 = std::integral_constant<int, 0>;
   using P1 = std::integral_constant<int, 1>;
@@ -255,38 +249,38 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT), (FwdCfg<Op, DKP, DVS>::
     load(P, c + 2);
     __syncthreads();  // rows, state copy and gates of chunk c are in LDS
     const float g = sG[c & 7].g;
+    const T *tK = sK(c), *tH = sV(c) + C * LDV;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < NTL; ++n) S[m][n] *= g;
+      for (int n = 0; n < NTS; ++n) S[m][n] *= g;
 #pragma unroll
     for (int ks = 0; ks < C / KS; ++ks) {
       F ka[MT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) ka[m] = X::across(sK, LDK, KS * ks, row0 + 16 * m, lane);
+      for (int m = 0; m < MT; ++m) ka[m] = X::across(tK, LDK, KS * ks, row0 + 16 * m, lane);
 #pragma unroll
       for (int p = 0; p < X::kTerms; ++p)
 #pragma unroll
-        for (int n = 0; n < NTL; ++n) {
-          const F vb = X::across(sH + p * C * LDV, LDV, KS * ks, 16 * n, lane);
+        for (int n = 0; n < NTS; ++n) {
+          const F vb = X::across(tH + p * C * LDV, LDV, KS * ks, colw + 16 * n, lane);
 #pragma unroll
           for (int m = 0; m < MT; ++m) Op::mma(S[m][n], ka[m], vb);
         }
     }
-    if ((c & 3) == 1) load_gates(c + 3);
-    if ((c & 3) == 3) fill_gates(c + 1);
-    __syncthreads();  // chunk c is done with LDS; gates of chunk c + 1 are there
-    stage_state();
-    stage_rows(Q, sG[(c + 1) & 7]);
+    stage_state(c + 1);
+    stage_rows(Q, c + 1);
+    if ((c & 3) == 0) load_gates(c + 4);
+    if ((c & 3) == 2) fill_gates(c + 2);  // ready when chunk c + 2 is staged, a barrier on
   };
   if (nch > 0) {
     load_gates(0);
     load(P0{}, 0);
     load(P1{}, 1);
     fill_gates(0);
-    stage_state();
+    stage_state(0);
     __syncthreads();
-    stage_rows(P0{}, sG[0]);
+    stage_rows(P0{}, 0);
   }
   int c = 0;
   for (; c + 1 < nch; c += 2) {
@@ -648,14 +642,23 @@ launch_result launch_step_io(const DecayStepArgs& a, hipStream_t s) {
 // ---- launches ----------------------------------------------------------------------
 constexpr int kSlab = kDecaySlab;
 
-template <class Op, int DKP>
-launch_result launch_fwd_t(const DecayArgs& a, int64_t grid, hipStream_t s) {
-  constexpr int lds = FwdCfg<Op, DKP, kSlab>::BYTES;
-  const launch_result e = allow_lds<decay_fwd_kernel<Op, DKP, kSlab>>(lds);
+template <class Op, int DKP, int DVS>
+launch_result launch_fwd_t(const DecayArgs& a, hipStream_t s) {
+  using Cfg = FwdCfg<Op, DKP, DVS>;
+  const launch_result e = allow_lds<decay_fwd_kernel<Op, DKP, DVS>>(Cfg::BYTES);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((decay_fwd_kernel<Op, DKP, kSlab>), dim3(static_cast<unsigned>(grid)),
-                     dim3(FwdCfg<Op, DKP, kSlab>::NT), lds, s, a);
+  const int64_t grid = static_cast<int64_t>(a.seg > 0 ? a.slots : a.N) * a.H * ((a.dv + DVS - 1) / DVS);
+  hipLaunchKernelGGL((decay_fwd_kernel<Op, DKP, DVS>), dim3(static_cast<unsigned>(grid)), dim3(Cfg::NT),
+                     Cfg::BYTES, s, a);
   return hipGetLastError();
+}
+template <class Op>
+launch_result launch_fwd_op(const DecayArgs& a, hipStream_t s) {
+  // slabs of 64 columns form Q K^T half as often as slabs of 32; in float32
+  // with rows of 128 only 32 fit the LDS
+  constexpr int wide = sizeof(typename Op::T) == 2 ? 64 : 32;
+  if (a.dk <= 64) return a.dv <= 32 ? launch_fwd_t<Op, 64, 32>(a, s) : launch_fwd_t<Op, 64, 64>(a, s);
+  return a.dv <= 32 ? launch_fwd_t<Op, 128, 32>(a, s) : launch_fwd_t<Op, 128, wide>(a, s);
 }
 
 template <class Op, int DKP, int C, bool REV, int MODE>
@@ -695,9 +698,9 @@ bool decay_supported(int32_t dk, int32_t dv) {
 // Tokens of a segment for these sizes (0: sequences are not cut).
 int32_t decay_segment(const DecayArgs& a) {
   const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
-  const int64_t parts = static_cast<int64_t>(a.H) * ((a.dv + kSlab - 1) / kSlab);
-  if (a.N * parts >= 512 && !a.cu) return 0;
-  int64_t seg = (tokens * parts / 1024 + 63) / 64 * 64;
+  const int64_t parts = static_cast<int64_t>(a.H) * ((a.dv + 63) / 64);
+  if (a.N * parts >= 256 && !a.cu) return 0;
+  int64_t seg = (tokens * parts / 256 + 63) / 64 * 64;
   if (seg < 512) seg = 512;
   return seg < a.T ? static_cast<int32_t>(seg) : 0;
 }
@@ -746,10 +749,7 @@ launch_result launch_decay_fwd(DecayArgs a, int32_t io_dtype, void* ws, hipStrea
   decay_layout_segments(a, static_cast<unsigned char*>(ws));
   launch_result e = launch_decay_segments(a, io_dtype, false, s);
   if (e != hipSuccess) return e;
-  const int64_t grid = static_cast<int64_t>(a.seg > 0 ? a.slots : a.N) * a.H * ((a.dv + kSlab - 1) / kSlab);
-  if (io_dtype == CKDA_DTYPE_BF16)
-    return a.dk <= 64 ? launch_fwd_t<OpBF16, 64>(a, grid, s) : launch_fwd_t<OpBF16, 128>(a, grid, s);
-  return a.dk <= 64 ? launch_fwd_t<OpF32, 64>(a, grid, s) : launch_fwd_t<OpF32, 128>(a, grid, s);
+  return io_dtype == CKDA_DTYPE_BF16 ? launch_fwd_op<OpBF16>(a, s) : launch_fwd_op<OpF32>(a, s);
 }
 
 launch_result launch_decay_step(const DecayArgs& a, int32_t io_dtype, hipStream_t s) {

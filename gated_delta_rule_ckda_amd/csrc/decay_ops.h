@@ -342,9 +342,8 @@ struct RowTile {
 };
 
 // LDS row stride for tiles that are read across their rows (four rows of 16
-// columns a lane group and read): for rows of 64 bytes 96, else the stride
-// of row fragments; eight rows then fall into different banks.
-constexpr int cross_stride(int n, int es) { return n * es == 64 ? 96 / es : frag_stride(n, es); }
+// columns a lane group and read): 16 bytes past the row.
+constexpr int cross_stride(int n, int es) { return n + 16 / es; }
 
 // The stored gate of token `lane` of `rows` tokens from `token` on, as raw
 // bits (0 past them): issued with a chunk's rows and decoded after them.
