@@ -310,27 +310,27 @@ enum { kSegment = 0, kChunks = 1 };
 template <class Op, int DKP, int DVS, int C>
 struct StateCfg {
   using T = typename Op::T;
-  static constexpr int ES = sizeof(T);
+  static constexpr int ES = sizeof(T), NT = 8 * DVS;  // four waves for every 32 columns
   static constexpr int LDK = frag_stride(DKP, ES), LDV = cross_stride(DVS, ES);
-  static constexpr int O_K = 0, O_H = O_K + C * LDK * ES,
-                       O_G = align16(O_H + Fr<Op>::kTerms * C * LDV * ES),
-                       O_R = O_G + 8 * static_cast<int>(sizeof(Gates<C>)), BYTES = O_R + 16;
+  static constexpr int KB = C * LDK * ES, VB = Fr<Op>::kTerms * C * LDV * ES;
+  static constexpr int O_K = 0, O_H = O_K + 2 * KB, O_G = align16(O_H + 2 * VB),
+                       O_R = O_G + 8 * static_cast<int>(sizeof(Gates<C>)), BYTES = O_R + 2 * 16 * 4;
 };
 
 template <class Op, int DKP, int DVS, int C, bool REV, int MODE>
-__global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
+__global__ __launch_bounds__((StateCfg<Op, DKP, DVS, C>::NT)) void decay_state_kernel(DecayArgs a) {
   using Cfg = StateCfg<Op, DKP, DVS, C>;
   using X = Fr<Op>;
   using T = typename Op::T;
   using F = typename X::F;
-  constexpr int LDK = Cfg::LDK, LDV = Cfg::LDV, KS = X::KS, MT = DKP / 64, NTL = DVS / 16;
+  constexpr int LDK = Cfg::LDK, LDV = Cfg::LDV, KS = X::KS, MT = DKP / 64, NTL = 2, NT = Cfg::NT;
   extern __shared__ __align__(16) unsigned char smem[];
-  T* sK = reinterpret_cast<T*>(smem + Cfg::O_K);
-  T* sH = reinterpret_cast<T*>(smem + Cfg::O_H);
+  auto sK = [&](int i) { return reinterpret_cast<T*>(smem + Cfg::O_K + (i & 1) * Cfg::KB); };
+  auto sH = [&](int i) { return reinterpret_cast<T*>(smem + Cfg::O_H + (i & 1) * Cfg::VB); };
   Gates<C>* sG = reinterpret_cast<Gates<C>*>(smem + Cfg::O_G);
   float* sR = reinterpret_cast<float*>(smem + Cfg::O_R);
 
-  const int t = threadIdx.x, lane = t & 63, w = uniform32(t >> 6), l16 = lane & 15, lq = lane >> 4;
+  const int t = threadIdx.x, lane = t & 63, wave = uniform32(t >> 6), w = wave & 3, l16 = lane & 15, lq = lane >> 4;
   const int nslab = (a.dv + DVS - 1) / DVS;
   int64_t chain;
   int slab;
@@ -354,16 +354,16 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
   const bool ckda = a.gate_range == CKDA_GATE_CKDA;
   const int nch = (pc.len + C - 1) / C;
 
-  // tile (m, n) of S^T: column dk = row0 + 16 m + l16, rows dv = c0 + RUN lq +
-  // 4 n + i: a lane holds RUN columns of the state in a row
+  // tile (m, n) of S^T: column dk = row0 + 16 m + l16, rows dv = c0 + colw +
+  // RUN lq + 4 n + i: a lane holds RUN columns of the state in a row
   constexpr int RUN = 4 * NTL;
-  const int row0 = w * (DKP / 4);
+  const int row0 = w * (DKP / 4), colw = 32 * (wave >> 2);
   const int64_t seq_state = (static_cast<int64_t>(pc.n) * a.H + h) * a.dk * a.dv;
   const int64_t seg_state = (static_cast<int64_t>(slot) * a.H + h) * a.dk * a.dv;
   f32x4 S[MT][NTL];
   // place of S[m][n] in a state, -1 outside it
   auto place = [&](int m, int n) {
-    const int r = row0 + 16 * m + l16, c = RUN * lq + 4 * n;
+    const int r = row0 + 16 * m + l16, c = colw + RUN * lq + 4 * n;
     return r < a.dk && c < vcols ? r * a.dv + c0 + c : -1;
   };
   const float* src = MODE == kSegment ? nullptr
@@ -385,8 +385,8 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
       }
   };
 
-  using RX = RowTile<T, C, DKP, kNT>;
-  using RY = RowTile<T, C, DVS, kNT>;
+  using RX = RowTile<T, C, DKP, NT>;
+  using RY = RowTile<T, C, DVS, NT>;
   RX tx;
   RY ty;
   tx.init(ldx, a.dk, t);
@@ -429,16 +429,17 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
   auto fill_gates = [&](int i) {
     const int iw = i + w;
     const bool ok = iw < nch && lane < C && chunk_at(iw) * C + lane < pc.len;
-    gates_fill<C>(sG[iw & 7], gate_of_bits(bits, a.gate_input), ok, a.gate_input, ckda, lane);
+    if (colw == 0) gates_fill<C>(sG[iw & 7], gate_of_bits(bits, a.gate_input), ok, a.gate_input, ckda, lane);
   };
-  auto stage_rows = [&](auto P, const Gates<C>& G) {
+  auto stage_rows = [&](auto P, int i) {
     constexpr int b = decltype(P)::value;
-    tx.store(rx[b], sK, LDK, t);
+    const Gates<C>& G = sG[i & 7];
 #pragma unroll
     for (int u = 0; u < RY::NP; ++u) {
-      const int p = t + kNT * u, row = p / RY::PPR, c = (p % RY::PPR) * RY::EPP;
-      store_scaled<T>(ry[b].r[u], REV ? G.E[row] * a.scale : G.W[row], sH + row * LDV + c, C * LDV);
+      const int p = t + NT * u, row = p / RY::PPR, c = (p % RY::PPR) * RY::EPP;
+      store_scaled<T>(ry[b].r[u], REV ? G.E[row] * a.scale : G.W[row], sH(i) + row * LDV + c, C * LDV);
     }
+    tx.store(rx[b], sK(i), LDK, t);
   };
   using P0 = std::integral_constant<int, 0>;
   using P1 = std::integral_constant<int, 1>;
@@ -468,13 +469,17 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
       if (REV) {
 #pragma unroll
         for (int mm = 32; mm >= 1; mm >>= 1) dot += __shfl_xor(dot, mm, 64);
-        if (lane == 0) sR[w] = dot;
+        if (lane == 0) sR[16 * (i & 1) + wave] = dot;
       }
     }
     load_chunk(P, i + 2);
     __syncthreads();  // rows and gates of chunk i are in LDS
-    if (MODE == kChunks && REV && t == 0)
-      a.dots[((cslot + chunk_at(i)) * a.H + h) * nslab + slab] = (sR[0] + sR[1]) + (sR[2] + sR[3]);
+    if (MODE == kChunks && REV && t == 0) {
+      float x = 0.f;
+#pragma unroll
+      for (int k = 0; k < NT / 64; ++k) x += sR[16 * (i & 1) + k];
+      a.dots[((cslot + chunk_at(i)) * a.H + h) * nslab + slab] = x;
+    }
     const float g = sG[i & 7].g;
     gain *= g;
 #pragma unroll
@@ -485,20 +490,19 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
     for (int ks = 0; ks < C / KS; ++ks) {
       F ka[MT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) ka[m] = X::across(sK, LDK, KS * ks, row0 + 16 * m, lane);
+      for (int m = 0; m < MT; ++m) ka[m] = X::across(sK(i), LDK, KS * ks, row0 + 16 * m, lane);
 #pragma unroll
       for (int p = 0; p < X::kTerms; ++p)
 #pragma unroll
         for (int n = 0; n < NTL; ++n) {
-          const F vb = X::across(sH + p * C * LDV, LDV, KS * ks, 4 * n, lane, RUN);
+          const F vb = X::across(sH(i) + p * C * LDV, LDV, KS * ks, colw + 4 * n, lane, RUN);
 #pragma unroll
           for (int m = 0; m < MT; ++m) Op::mma(S[m][n], vb, ka[m]);
         }
     }
-    if ((i & 3) == 1) load_gates(i + 3);
-    if ((i & 3) == 3) fill_gates(i + 1);
-    __syncthreads();
-    stage_rows(Q, sG[(i + 1) & 7]);
+    stage_rows(Q, i + 1);
+    if ((i & 3) == 0) load_gates(i + 4);
+    if ((i & 3) == 2) fill_gates(i + 2);
   };
   if (nch > 0) {
     load_gates(0);
@@ -506,7 +510,7 @@ __global__ __launch_bounds__(kNT, 2) void decay_state_kernel(DecayArgs a) {
     load_chunk(P1{}, 1);
     fill_gates(0);
     __syncthreads();
-    stage_rows(P0{}, sG[0]);
+    stage_rows(P0{}, 0);
   }
   int i = 0;
   for (; i + 1 < nch; i += 2) {
@@ -640,7 +644,6 @@ launch_result launch_step_io(const DecayStepArgs& a, hipStream_t s) {
 }
 
 // ---- launches ----------------------------------------------------------------------
-constexpr int kSlab = kDecaySlab;
 
 template <class Op, int DKP, int DVS>
 launch_result launch_fwd_t(const DecayArgs& a, hipStream_t s) {
@@ -661,14 +664,15 @@ launch_result launch_fwd_op(const DecayArgs& a, hipStream_t s) {
   return a.dv <= 32 ? launch_fwd_t<Op, 128, 32>(a, s) : launch_fwd_t<Op, 128, wide>(a, s);
 }
 
-template <class Op, int DKP, int C, bool REV, int MODE>
+template <class Op, int DKP, int DVS, int C, bool REV, int MODE>
 launch_result launch_state_t(const DecayArgs& a, hipStream_t s) {
-  constexpr int lds = StateCfg<Op, DKP, kSlab, C>::BYTES;
-  const int64_t grid = static_cast<int64_t>(a.seg > 0 ? a.slots : a.N) * a.H * ((a.dv + kSlab - 1) / kSlab);
-  const launch_result e = allow_lds<decay_state_kernel<Op, DKP, kSlab, C, REV, MODE>>(lds);
+  using Cfg = StateCfg<Op, DKP, DVS, C>;
+  constexpr int lds = Cfg::BYTES;
+  const int64_t grid = static_cast<int64_t>(a.seg > 0 ? a.slots : a.N) * a.H * ((a.dv + DVS - 1) / DVS);
+  const launch_result e = allow_lds<decay_state_kernel<Op, DKP, DVS, C, REV, MODE>>(lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((decay_state_kernel<Op, DKP, kSlab, C, REV, MODE>), dim3(static_cast<unsigned>(grid)),
-                     dim3(kNT), lds, s, a);
+  hipLaunchKernelGGL((decay_state_kernel<Op, DKP, DVS, C, REV, MODE>), dim3(static_cast<unsigned>(grid)),
+                     dim3(Cfg::NT), lds, s, a);
   return hipGetLastError();
 }
 
@@ -680,13 +684,17 @@ launch_result launch_join(const DecayArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <class Op, bool REV, int MODE>
+launch_result launch_state_op(const DecayArgs& a, hipStream_t s) {
+  constexpr int C = decay_bwd_chunk(sizeof(typename Op::T) == 2 ? CKDA_DTYPE_BF16 : CKDA_DTYPE_F32);
+  if (decay_slab(a.dv) == 32)
+    return a.dk <= 64 ? launch_state_t<Op, 64, 32, C, REV, MODE>(a, s) : launch_state_t<Op, 128, 32, C, REV, MODE>(a, s);
+  return a.dk <= 64 ? launch_state_t<Op, 64, 64, C, REV, MODE>(a, s) : launch_state_t<Op, 128, 64, C, REV, MODE>(a, s);
+}
 template <bool REV, int MODE>
 launch_result launch_state(const DecayArgs& a, int32_t io_dtype, hipStream_t s) {
-  if (io_dtype == CKDA_DTYPE_BF16)
-    return a.dk <= 64 ? launch_state_t<OpBF16, 64, decay_bwd_chunk(CKDA_DTYPE_BF16), REV, MODE>(a, s)
-                      : launch_state_t<OpBF16, 128, decay_bwd_chunk(CKDA_DTYPE_BF16), REV, MODE>(a, s);
-  return a.dk <= 64 ? launch_state_t<OpF32, 64, decay_bwd_chunk(CKDA_DTYPE_F32), REV, MODE>(a, s)
-                    : launch_state_t<OpF32, 128, decay_bwd_chunk(CKDA_DTYPE_F32), REV, MODE>(a, s);
+  return io_dtype == CKDA_DTYPE_BF16 ? launch_state_op<OpBF16, REV, MODE>(a, s)
+                                     : launch_state_op<OpF32, REV, MODE>(a, s);
 }
 
 }  // namespace
@@ -700,7 +708,7 @@ int32_t decay_segment(const DecayArgs& a) {
   const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
   const int64_t parts = static_cast<int64_t>(a.H) * ((a.dv + 63) / 64);
   if (a.N * parts >= 256 && !a.cu) return 0;
-  int64_t seg = (tokens * parts / 256 + 63) / 64 * 64;
+  int64_t seg = (tokens * parts / (a.cu ? 768 : 256) + 63) / 64 * 64;
   if (seg < 512) seg = 512;
   return seg < a.T ? static_cast<int32_t>(seg) : 0;
 }
@@ -735,7 +743,7 @@ launch_result launch_decay_chunks(const DecayArgs& a, int32_t io_dtype, bool rev
 }
 
 int64_t decay_grid(const DecayArgs& a, int32_t io_dtype) {
-  const int64_t parts = static_cast<int64_t>(a.H) * ((a.dv + kSlab - 1) / kSlab);
+  const int64_t parts = static_cast<int64_t>(a.H) * ((a.dv + 31) / 32);
   const int64_t walks = (a.cu || a.T > 0 ? decay_slots(a, 512) : a.N) * parts;
   const int64_t chunks = decay_slots(a, decay_bwd_chunk(io_dtype)) * a.H;
   const int64_t joins = static_cast<int64_t>(a.N) * a.H * ((static_cast<int64_t>(a.dk) * a.dv / 4 + kNT - 1) / kNT);
@@ -743,7 +751,7 @@ int64_t decay_grid(const DecayArgs& a, int32_t io_dtype) {
   return m > joins ? m : joins;
 }
 
-int decay_dots_per_chunk(int32_t dv) { return (dv + kSlab - 1) / kSlab; }
+int decay_dots_per_chunk(int32_t dv) { return (dv + decay_slab(dv) - 1) / decay_slab(dv); }
 
 launch_result launch_decay_fwd(DecayArgs a, int32_t io_dtype, void* ws, hipStream_t s) {
   decay_layout_segments(a, static_cast<unsigned char*>(ws));

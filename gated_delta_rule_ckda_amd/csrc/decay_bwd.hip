@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
   const int group = a.H / a.Hk;
   const int ldq = a.Hk * a.dk, ldv = a.H * a.dv;
   const bool ckda = a.gate_range == CKDA_GATE_CKDA;
-  const int nslab = (a.dv + kDecaySlab - 1) / kDecaySlab;
+  const int nslab = (a.dv + decay_slab(a.dv) - 1) / decay_slab(a.dv);
   // with 4 column tiles, waves 4..7 take the upper half of the tokens
   const int col0 = 16 * (w % CW), n0 = CW == 8 ? 0 : (w / 4) * (RT / 2);
   constexpr int NT = CW == 8 ? RT : RT / 2;  // token tiles a wave

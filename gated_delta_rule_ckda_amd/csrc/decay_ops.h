@@ -502,7 +502,8 @@ launch_result allow_lds(int bytes) {
   return r;
 }
 constexpr int kDecayChunk = 64;
-constexpr int kDecaySlab = 32;  // state columns a workgroup of the state walks
+// state columns a workgroup of the state walks takes
+__host__ __device__ constexpr int decay_slab(int dv) { return dv <= 32 ? 32 : 64; }
 // chunk of the backward's records and gradients
 constexpr int decay_bwd_chunk(int32_t io_dtype) { return io_dtype == CKDA_DTYPE_BF16 ? 64 : 32; }
 // slots of pieces of L tokens
