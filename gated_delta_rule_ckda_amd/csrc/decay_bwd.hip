@@ -78,17 +78,19 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
   // with 4 column tiles, waves 4..7 take the upper half of the tokens
   const int col0 = 16 * (w % CW), n0 = CW == 8 ? 0 : (w / 4) * (RT / 2);
   constexpr int NT = CW == 8 ? RT : RT / 2;  // token tiles a wave
-  const int64_t items = static_cast<int64_t>(a.cslots) * a.Hk;
+  const unsigned items = static_cast<unsigned>(a.cslots) * a.Hk;  // below 2^31
 
   // one (item, value head): where its rows are
   struct Work {
-    int64_t item;
-    int hv;
+    unsigned item;
+    int slot, hk, hv;
     Piece pc;
   };
   auto seek = [&](Work& k) {  // the first item at or after k.item that has tokens
     for (; k.item < items; k.item += gridDim.x) {
-      k.pc = piece_of(a, static_cast<int>(k.item / a.Hk), C, lane);
+      k.slot = k.item / static_cast<unsigned>(a.Hk);
+      k.hk = k.item - k.slot * a.Hk;
+      k.pc = piece_of(a, k.slot, C, lane);
       if (k.pc.n >= 0 && k.pc.len > 0) return;
     }
   };
@@ -115,41 +117,53 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
   typename RA::Regs ra;
   uint4 rs[ND];
   GateBits bits;
-  float rx = 0.f;
-  auto load = [&](const Work& k) {  // nothing past the last item
+  uint32_t rx[2];  // slabs' parts of x (dv <= 128: two at most)
+  // A CU takes in some 16 bytes a clock, and a load that finds its queue full
+  // holds its wave: the next rows are asked for in parts, between the products.
+  auto chain_of = [&](const Work& k) { return (k.item < items ? k.slot : 0) * static_cast<int64_t>(a.H) + k.hk * group + k.hv; };
+  auto load_qk = [&](const Work& k) {  // nothing past the last item, in all three
     const bool in = k.item < items;
-    const int hk = in ? static_cast<int>(k.item % a.Hk) : 0, h = hk * group + k.hv, rows = in ? k.pc.len : 0;
-    const int64_t tok = in ? k.pc.begin : 0, chain = (in ? k.item / a.Hk : 0) * a.H + h;
-    bits = load_gate_bits(a, tok, rows, h, lane);
+    const int rows = in ? k.pc.len : 0;
+    const int64_t tok = in ? k.pc.begin : 0;
+    bits = load_gate_bits(a, tok, rows, in ? k.hk * group + k.hv : 0, lane);
+    const rsrc_t rd = make_rsrc(reinterpret_cast<const void*>(uniform64(reinterpret_cast<int64_t>(a.dots + (in ? chain_of(k) : 0) * nslab))),
+                                uniform32(in ? 4 * nslab : 0));
+    ldraw<4>(rd, 0, &rx[0]);
+    ldraw<4>(rd, 4, &rx[1]);
     if (k.hv == 0) {
-      const int64_t oq = tok * ldq + static_cast<int64_t>(hk) * a.dk;
+      const int64_t oq = tok * ldq + static_cast<int64_t>(in ? k.hk : 0) * a.dk;
       tq.load(rq, static_cast<const T*>(a.q) + oq, ldq, rows, a.dk);
       tq.load(rk, static_cast<const T*>(a.k) + oq, ldq, rows, a.dk);
     }
-    const int64_t ov = tok * ldv + static_cast<int64_t>(h) * a.dv;
-    tv.load(rv, static_cast<const T*>(a.v) + ov, ldv, rows, a.dv);
-    tv.load(ro, static_cast<const T*>(gr.dout) + ov, ldv, rows, a.dv);
-    const int64_t rec = chain * a.dk * a.dv;
+  };
+  auto load_vo = [&](const Work& k) {
+    const bool in = k.item < items;
+    const int64_t ov = in ? k.pc.begin * ldv + static_cast<int64_t>(k.hk * group + k.hv) * a.dv : 0;
+    tv.load(rv, static_cast<const T*>(a.v) + ov, ldv, in ? k.pc.len : 0, a.dv);
+    tv.load(ro, static_cast<const T*>(gr.dout) + ov, ldv, in ? k.pc.len : 0, a.dv);
+  };
+  auto load_states = [&](const Work& k) {
+    const bool in = k.item < items;
+    const int64_t rec = (in ? chain_of(k) : 0) * a.dk * a.dv;
     ta.load(ra, static_cast<const T*>(a.adjoints) + rec, a.dv, in ? a.dk : 0, a.dv);
     const rsrc_t r = rows_rsrc(static_cast<const T*>(a.states) + rec, a.dv, in ? a.dk : 0, a.dv, DP);
 #pragma unroll
     for (int s = 0; s < ND; ++s) rs[s] = load_piece(r, offs[s]);
-    rx = 0.f;
-    if (in)
-      for (int i = 0; i < nslab; ++i) rx += a.dots[chain * nslab + i];
   };
 
-  Work cur{blockIdx.x, 0, {}};
+  Work cur{blockIdx.x, 0, 0, 0, {}};
   seek(cur);
   if (cur.item >= items) return;
-  load(cur);
+  load_qk(cur);
+  load_vo(cur);
+  load_states(cur);
   // the gates of what `load` fetched last, into place b, by one wave
   auto fill = [&](const Work& k, int b) {
     const bool ok = k.item < items && lane < C && lane < k.pc.len;
     const float x = gate_of_bits(bits, a.gate_input);
     gates_fill<C>(sG[b], x, ok, a.gate_input, ckda, lane);
     if (lane < C) sX[b * (C + 4) + lane] = ok ? gate_value(x, a.gate_input, ckda) : 1.f;
-    if (lane == 0) sX[b * (C + 4) + C] = rx;
+    if (lane == 0) sX[b * (C + 4) + C] = __uint_as_float(rx[0]) + __uint_as_float(rx[1]);
   };
   if (w == 1) fill(cur, 0);
   f32x4 dq[NT], dk[NT];
@@ -157,7 +171,7 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
     const Gates<C>& G = sG[turn];
     const float* sAl = sX + turn * (C + 4);
     const Piece pc = cur.pc;
-    const int hk = static_cast<int>(cur.item % a.Hk), h = hk * group + cur.hv;
+    const int hk = cur.hk, h = hk * group + cur.hv;
     const bool first = cur.hv == 0, last = cur.hv == group - 1;
     const bool tok = lane < C && lane < pc.len;
     const float xg = gate_of_bits(bits, a.gate_input);
@@ -173,10 +187,9 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
     F fs[ND];
 #pragma unroll
     for (int s = 0; s < ND; ++s) fs[s] = *reinterpret_cast<const F*>(&rs[s]);
+    __syncthreads();
     Work next = cur;
     advance(next);
-    load(next);
-    __syncthreads();
     const bool fast = G.fast != 0;
 
     // P^T and N^T tiles: column i = 16 ti + l16, rows j = 16 tj + 4 lq + r
@@ -204,6 +217,8 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
     }
     __syncthreads();
 
+    load_qk(next);
+    __builtin_amdgcn_sched_barrier(0);
     // dq: columns dk = col0 + 4 lq + r, token 16 n + l16
     {
       F fk[NC];
@@ -227,6 +242,7 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
         if (lq == 0) sZ[(w % CW) * C + i] = z * a.scale;
       }
     }
+    load_vo(next);
     __builtin_amdgcn_sched_barrier(0);  // hoisted across, the operands spill
     // dk, token 16 n + l16
     {
@@ -253,6 +269,7 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
         if (lq == 0) sY[(w % CW) * C + j] = y;
       }
     }
+    load_states(next);
     __builtin_amdgcn_sched_barrier(0);
     // dv: columns dv = col0 + 4 lq + r
     {
