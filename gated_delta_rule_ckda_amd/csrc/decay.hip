@@ -246,7 +246,6 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT)) void decay_fwd_kernel(D
   using P1 = std::integral_constant<int, 1>;
   // chunk c, whose rows were in registers P and are in LDS now
   auto step = [&](auto P, auto Q, int c) {
-    load(P, c + 2);
     __syncthreads();  // rows, state copy and gates of chunk c are in LDS
     const float g = sG[c & 7].g;
     const T *tK = sK(c), *tH = sV(c) + C * LDV;
@@ -268,6 +267,7 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT)) void decay_fwd_kernel(D
           for (int m = 0; m < MT; ++m) Op::mma(S[m][n], ka[m], vb);
         }
     }
+    load(P, c + 2);
     stage_state(c + 1);
     stage_rows(Q, c + 1);
     if ((c & 3) == 0) load_gates(c + 4);
@@ -472,7 +472,6 @@ __global__ __launch_bounds__((StateCfg<Op, DKP, DVS, C>::NT)) void decay_state_k
         if (lane == 0) sR[16 * (i & 1) + wave] = dot;
       }
     }
-    load_chunk(P, i + 2);
     __syncthreads();  // rows and gates of chunk i are in LDS
     if (MODE == kChunks && REV && t == 0) {
       float x = 0.f;
@@ -500,6 +499,7 @@ __global__ __launch_bounds__((StateCfg<Op, DKP, DVS, C>::NT)) void decay_state_k
           for (int m = 0; m < MT; ++m) Op::mma(S[m][n], vb, ka[m]);
         }
     }
+    load_chunk(P, i + 2);
     stage_rows(Q, i + 1);
     if ((i & 3) == 0) load_gates(i + 4);
     if ((i & 3) == 2) fill_gates(i + 2);
@@ -687,6 +687,9 @@ launch_result launch_join(const DecayArgs& a, hipStream_t s) {
 template <class Op, bool REV, int MODE>
 launch_result launch_state_op(const DecayArgs& a, hipStream_t s) {
   constexpr int C = decay_bwd_chunk(sizeof(typename Op::T) == 2 ? CKDA_DTYPE_BF16 : CKDA_DTYPE_F32);
+  // a segment's own sum: all columns in one workgroup, which reads k once
+  if constexpr (MODE == kSegment)
+    if (a.dk > 64 && a.dv > 64) return launch_state_t<Op, 128, 128, C, REV, MODE>(a, s);
   if (decay_slab(a.dv) == 32)
     return a.dk <= 64 ? launch_state_t<Op, 64, 32, C, REV, MODE>(a, s) : launch_state_t<Op, 128, 32, C, REV, MODE>(a, s);
   return a.dk <= 64 ? launch_state_t<Op, 64, 64, C, REV, MODE>(a, s) : launch_state_t<Op, 128, 64, C, REV, MODE>(a, s);
@@ -708,7 +711,7 @@ int32_t decay_segment(const DecayArgs& a) {
   const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
   const int64_t parts = static_cast<int64_t>(a.H) * ((a.dv + 63) / 64);
   if (a.N * parts >= 256 && !a.cu) return 0;
-  int64_t seg = (tokens * parts / (a.cu ? 768 : 256) + 63) / 64 * 64;
+  int64_t seg = (tokens * a.H / (a.cu ? 384 : 256) + 63) / 64 * 64;
   if (seg < 512) seg = 512;
   return seg < a.T ? static_cast<int32_t>(seg) : 0;
 }

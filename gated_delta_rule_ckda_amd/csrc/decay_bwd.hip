@@ -272,14 +272,13 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
     load_states(next);
     __builtin_amdgcn_sched_barrier(0);
     // dv: columns dv = col0 + 4 lq + r
+    f32x4 dv[NT];
     {
       F fa[ND], fo[NC];
 #pragma unroll
       for (int s = 0; s < ND; ++s) fa[s] = X::across(sA, LD, KS * s, col0, lane);
 #pragma unroll
       for (int ks = 0; ks < NC; ++ks) fo[ks] = X::across(sO, LD, KS * ks, col0, lane);
-      const rsrc_t gdv = rows_rsrc(static_cast<const T*>(gr.dv) + pc.begin * ldv + static_cast<int64_t>(h) * a.dv, ldv,
-                                   pc.len, a.dv, C);
 #pragma unroll
       for (int nn = 0; nn < NT; ++nn) {
         const int j = 16 * (n0 + nn) + l16;
@@ -289,33 +288,30 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
         acc *= G.W[j];
 #pragma unroll
         for (int ks = 0; ks < NC; ++ks) Op::mma(acc, fo[ks], X::across(sP, LDC, KS * ks, 16 * (n0 + nn), lane));
-        const int col = col0 + 4 * lq;
-        store_four<Op>(gdv, col < a.dv ? (j * ldv + col) * Cfg::ES : kNoOffset, acc);
+        dv[nn] = acc;
       }
     }
-    if (last) {
-      const int64_t oq = pc.begin * ldq + static_cast<int64_t>(hk) * a.dk;
-      const rsrc_t gdq = rows_rsrc(static_cast<const T*>(gr.dq) + oq, ldq, pc.len, a.dk, C);
-      const rsrc_t gdk = rows_rsrc(static_cast<const T*>(gr.dk) + oq, ldq, pc.len, a.dk, C);
-#pragma unroll
-      for (int nn = 0; nn < NT; ++nn) {
-        const int j = 16 * (n0 + nn) + l16, col = col0 + 4 * lq;
-        const int off = col < a.dk ? (j * ldq + col) * Cfg::ES : kNoOffset;
-        store_four<Op>(gdq, off, dq[nn]);
-        store_four<Op>(gdk, off, dk[nn]);
-      }
-    }
-    __syncthreads();  // z, y and M are in LDS
+    __syncthreads();  // z, y and M are in LDS; the rows there are done with
 
+    // the gradients leave through LDS as whole rows
+#pragma unroll
+    for (int nn = 0; nn < NT; ++nn) {
+      const int at = (16 * (n0 + nn) + l16) * LD + col0 + 4 * lq;
+      Op::store4(sV + at, dv[nn]);
+      if (last) {
+        Op::store4(sQ + at, dq[nn]);
+        Op::store4(sK + at, dk[nn]);
+      }
+    }
+    const int i = lane < C ? lane : C - 1;  // this lane's token, for the gates
+    float da = 0.f;
     if (gr.dalpha) {
-      const int i = lane < C ? lane : C - 1;
       float z = 0.f, y = 0.f;
 #pragma unroll
       for (int k = 0; k < CW; ++k) {
         z += sZ[k * C + i];
         y += sY[k * C + i];
       }
-      float da = 0.f;
       if (fast) {
         // wave w: reads w, w + 8, ... (lane t: the writes before t)
         const float ez = G.E[i] * z;
@@ -330,8 +326,40 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
           const float wy = __shfl_up(lane < C ? G.W[i] * y : 0.f, 1, 64);
           da += wave_scan(lane > 0 ? wy : 0.f) + G.g * sAl[C];
         }
+      } else if (w == 0) {  // one gate after the other
+        float Rr = z, Xr = sAl[C];
+        for (int s0 = 0; s0 < C; s0 += 4) {
+          const f32x4 d = decay_of(G, i, s0, false);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int s = s0 + e;
+            const float al = sAl[s], ys = __shfl(y, s, 64), m = sM[i * LDM + s];
+            sM[i * LDM + s] = d[e] != 0.f ? d[e] * Rr : 0.f;  // past the diagonal: 0
+            Rr = al * Rr + m;
+            da = s == i ? G.W[s] * Xr : da;
+            Xr = al * Xr + ys;
+          }
+        }
+        wave_lds_sync();
+        for (int r = i; r < C; ++r) da += sM[r * LDM + i];
       }
-      __syncthreads();  // z is read: its place takes the waves' parts of da
+    }
+    __syncthreads();  // the gradients are in LDS; z is read: its place takes the waves' parts of da
+    auto flush = [&](const T* from, const R& tile, void* to, int64_t at, int ld, int cols) {
+      const rsrc_t r = rows_rsrc(static_cast<const T*>(to) + at, ld, pc.len, cols, C);
+#pragma unroll
+      for (int u = 0; u < R::NP; ++u) {
+        const int p = t + kNT * u;
+        store_piece(r, tile.off[u], *reinterpret_cast<const uint4*>(from + (p / R::PPR) * LD + (p % R::PPR) * R::EPP));
+      }
+    };
+    flush(sV, tv, gr.dv, pc.begin * ldv + static_cast<int64_t>(h) * a.dv, ldv, a.dv);
+    if (last) {
+      const int64_t oq = pc.begin * ldq + static_cast<int64_t>(hk) * a.dk;
+      flush(sQ, tq, gr.dq, oq, ldq, a.dk);
+      flush(sK, tq, gr.dk, oq, ldq, a.dk);
+    }
+    if (gr.dalpha) {
       if (fast && lane < C) sZ[w * C + lane] = da;
       __syncthreads();
       if (w == 0) {
@@ -340,22 +368,6 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
 #pragma unroll
           for (int k = 0; k < kWaves; ++k) da += sZ[k * C + i];
           da *= 1.f / sAl[i];
-        } else {
-          float Rr = z, Xr = sAl[C];
-          for (int s0 = 0; s0 < C; s0 += 4) {
-            const f32x4 d = decay_of(G, i, s0, false);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int s = s0 + e;
-              const float al = sAl[s], ys = __shfl(y, s, 64), m = sM[i * LDM + s];
-              sM[i * LDM + s] = d[e] != 0.f ? d[e] * Rr : 0.f;  // past the diagonal: 0
-              Rr = al * Rr + m;
-              da = s == i ? G.W[s] * Xr : da;
-              Xr = al * Xr + ys;
-            }
-          }
-          wave_lds_sync();
-          for (int r = i; r < C; ++r) da += sM[r * LDM + i];
         }
         if (tok) {
           if (a.gate_input != CKDA_GATES_F32) {
