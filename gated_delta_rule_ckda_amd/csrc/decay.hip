@@ -310,7 +310,9 @@ enum { kSegment = 0, kChunks = 1 };
 template <class Op, int DKP, int DVS, int C>
 struct StateCfg {
   using T = typename Op::T;
-  static constexpr int ES = sizeof(T), NT = 8 * DVS;  // four waves for every 32 columns
+  // WK waves for every 32 columns, each with DKP / WK rows: fewer where all
+  // columns are here, since each reads its columns' terms of the whole chunk
+  static constexpr int ES = sizeof(T), WK = DVS == 128 ? 2 : 4, NT = 64 * WK * (DVS / 32);
   static constexpr int LDK = frag_stride(DKP, ES), LDV = cross_stride(DVS, ES);
   static constexpr int KB = C * LDK * ES, VB = Fr<Op>::kTerms * C * LDV * ES;
   static constexpr int O_K = 0, O_H = O_K + 2 * KB, O_G = align16(O_H + 2 * VB),
@@ -323,7 +325,7 @@ __global__ __launch_bounds__((StateCfg<Op, DKP, DVS, C>::NT)) void decay_state_k
   using X = Fr<Op>;
   using T = typename Op::T;
   using F = typename X::F;
-  constexpr int LDK = Cfg::LDK, LDV = Cfg::LDV, KS = X::KS, MT = DKP / 64, NTL = 2, NT = Cfg::NT;
+  constexpr int LDK = Cfg::LDK, LDV = Cfg::LDV, KS = X::KS, MT = DKP / 16 / Cfg::WK, NTL = 2, NT = Cfg::NT;
   extern __shared__ __align__(16) unsigned char smem[];
   auto sK = [&](int i) { return reinterpret_cast<T*>(smem + Cfg::O_K + (i & 1) * Cfg::KB); };
   auto sH = [&](int i) { return reinterpret_cast<T*>(smem + Cfg::O_H + (i & 1) * Cfg::VB); };
@@ -357,7 +359,7 @@ __global__ __launch_bounds__((StateCfg<Op, DKP, DVS, C>::NT)) void decay_state_k
   // tile (m, n) of S^T: column dk = row0 + 16 m + l16, rows dv = c0 + colw +
   // RUN lq + 4 n + i: a lane holds RUN columns of the state in a row
   constexpr int RUN = 4 * NTL;
-  const int row0 = w * (DKP / 4), colw = 32 * (wave >> 2);
+  const int row0 = (wave % Cfg::WK) * (DKP / Cfg::WK), colw = 32 * (wave / Cfg::WK);
   const int64_t seq_state = (static_cast<int64_t>(pc.n) * a.H + h) * a.dk * a.dv;
   const int64_t seg_state = (static_cast<int64_t>(slot) * a.H + h) * a.dk * a.dv;
   f32x4 S[MT][NTL];
@@ -429,7 +431,7 @@ __global__ __launch_bounds__((StateCfg<Op, DKP, DVS, C>::NT)) void decay_state_k
   auto fill_gates = [&](int i) {
     const int iw = i + w;
     const bool ok = iw < nch && lane < C && chunk_at(iw) * C + lane < pc.len;
-    if (colw == 0) gates_fill<C>(sG[iw & 7], gate_of_bits(bits, a.gate_input), ok, a.gate_input, ckda, lane);
+    if (wave < 4) gates_fill<C>(sG[iw & 7], gate_of_bits(bits, a.gate_input), ok, a.gate_input, ckda, lane);
   };
   auto stage_rows = [&](auto P, int i) {
     constexpr int b = decltype(P)::value;
