@@ -8,6 +8,7 @@ library is missing the calls raise -- there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -455,8 +456,28 @@ def _tensors(device, **named):
     _require(device.type == "cuda", "tensors must be on a GPU, got %s" % device)
     for name, t in named.items():
         if t is not None:
-            _require(t.device == device, "%s is on %s, not on %s" % (name, t.device, device))
-            _require(t.is_contiguous(), "%s must be contiguous" % name)
+            if t.device != device:
+                raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+            if not t.is_contiguous():
+                raise ValueError("%s must be contiguous" % name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(device, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current, on the caller's stream
+    or that device's current one."""
+    import torch
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    if s.device != device:
+        raise ValueError("the stream belongs to %s, the tensors to %s" % (s.device, device))
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, s.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, s.cuda_stream))
 
 
 def _state_ok(name, t, shape):
@@ -487,30 +508,40 @@ class _on:
         return self.guard.__exit__(*exc)
 
 
+@functools.lru_cache(maxsize=256)
+def _decay_plan(packed, *fields):
+    """The descriptor of these sizes and the workspaces it needs (forward, backward)."""
+    desc = DecayDesc(*fields)
+    lib = _load()
+    return (desc, int(lib.ckda_decay_fwd_workspace_size(ctypes.byref(desc), packed)),
+            int(lib.ckda_decay_bwd_workspace_size(ctypes.byref(desc), packed)))
+
+
 def _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale):
-    """The descriptor of a decay call, after the checks of its inputs' shapes and types."""
+    """The plan of a decay call, after the checks of its inputs' shapes and types."""
     import torch
     io = _dtype_code(q)
+    qs, vs = q.shape, v.shape
     _require(k.dtype == q.dtype and v.dtype == q.dtype, "q, k, v must share a dtype")
-    lead = 1 if cu_seqlens is not None and q.dim() == 3 else 2
-    _require(q.dim() == lead + 2 and v.dim() == lead + 2,
+    lead = 1 if cu_seqlens is not None and len(qs) == 3 else 2
+    _require(len(qs) == lead + 2 and len(vs) == lead + 2,
              "q and v must be [B,T,heads,d] (a packed batch may leave B out)")
-    _require(k.shape == q.shape, "k must match q")
-    _require(v.shape[:lead] == q.shape[:lead], "v must have the tokens of q")
-    H, Hk = v.shape[-2], q.shape[-2]
+    _require(k.shape == qs, "k must match q")
+    _require(vs[:lead] == qs[:lead], "v must have the tokens of q")
+    H, Hk = vs[-2], qs[-2]
     _require(Hk > 0 and H % Hk == 0, "the q/k heads must divide the value heads")
     per_head = alpha.dim() == 1
-    _require(tuple(alpha.shape) == ((H,) if per_head else tuple(v.shape[:-1])),
+    _require(alpha.shape == ((H,) if per_head else vs[:-1]),
              "alpha must be [H] or one gate a token and head")
-    B, T = (1, q.shape[0]) if lead == 1 else (q.shape[0], q.shape[1])
+    B, T = (1, qs[0]) if lead == 1 else (qs[0], qs[1])
     n = B
     if cu_seqlens is not None:
         _require(cu_seqlens.dtype == torch.int32 and cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 1,
                  "cu_seqlens must be an int32 vector")
         _require(B == 1, "a packed batch has B = 1")
         n = cu_seqlens.numel() - 1
-    return DecayDesc(B, T, H, q.shape[-1], v.shape[-1], n, io, _gate_code(gate),
-                     _gate_input(gates, alpha, alpha), Hk, int(per_head), float(scale))
+    return _decay_plan(int(cu_seqlens is not None), B, T, H, qs[-1], vs[-1], n, io, _gate_code(gate),
+                       _gate_input(gates, alpha, alpha), Hk, int(per_head), float(scale))
 
 
 def _workspace(workspace, need, device):
@@ -548,7 +579,7 @@ def decay_fwd(q, k, v, alpha, *, h0=None, cu_seqlens=None, gate="ckda", gates="v
     workspace that the caller passes must not be shared by calls that overlap."""
     import torch
     lib = _load()
-    desc = _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale)
+    desc, need_fwd, need_bwd = _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale)
     dev = q.device
     _tensors(dev, q=q, k=k, v=v, alpha=alpha, h0=h0, cu_seqlens=cu_seqlens, out=out,
              final_state=final_state)
@@ -561,12 +592,10 @@ def decay_fwd(q, k, v, alpha, *, h0=None, cu_seqlens=None, gate="ckda", gates="v
     ht = final_state
     if output_final_state and ht is None:
         ht = torch.empty(shape, device=dev, dtype=torch.float32)
-    need = decay_fwd_workspace_size(desc, cu_seqlens is not None)
-    with _on(dev, stream) as s:
-        ws = _workspace(workspace, need, dev) if need else workspace
-        _check(lib.ckda_decay_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha),
-                                  _ptr(cu_seqlens), _ptr(h0), _ptr(o), _ptr(ht), _ptr(ws),
-                                  0 if ws is None else ws.numel(), s))
+    ws = _workspace(workspace, need_fwd, dev) if need_fwd else None
+    _launch(dev, stream, lib.ckda_decay_fwd, ctypes.byref(desc), _addr(q), _addr(k), _addr(v),
+            _addr(alpha), _addr(cu_seqlens), _addr(h0), _addr(o), _addr(ht), _addr(ws),
+            0 if ws is None else ws.numel())
     return o, ht
 
 
@@ -580,7 +609,7 @@ def decay_bwd(q, k, v, alpha, dout, *, h0=None, dht=None, cu_seqlens=None, gate=
     requested."""
     import torch
     lib = _load()
-    desc = _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale)
+    desc, need_fwd, need_bwd = _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale)
     dev = q.device
     _tensors(dev, q=q, k=k, v=v, alpha=alpha, dout=dout, h0=h0, dht=dht, cu_seqlens=cu_seqlens)
     shape = (desc.num_seqs, desc.H, desc.dk, desc.dv)
@@ -590,13 +619,10 @@ def decay_bwd(q, k, v, alpha, dout, *, h0=None, dht=None, cu_seqlens=None, gate=
     dq, dkk, dvv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     dal = torch.empty(alpha.shape, device=dev, dtype=q.dtype) if output_dalpha else None
     dh0 = torch.empty(shape, device=dev, dtype=torch.float32) if output_dh0 else None
-    need = decay_bwd_workspace_size(desc, cu_seqlens is not None)
-    with _on(dev, stream) as s:
-        ws = _workspace(workspace, need, dev)
-        _check(lib.ckda_decay_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha),
-                                  _ptr(cu_seqlens), _ptr(h0), _ptr(dout), _ptr(dht), _ptr(dq),
-                                  _ptr(dkk), _ptr(dvv), _ptr(dal), _ptr(dh0), _ptr(ws), ws.numel(),
-                                  s))
+    ws = _workspace(workspace, need_bwd, dev)
+    _launch(dev, stream, lib.ckda_decay_bwd, ctypes.byref(desc), _addr(q), _addr(k), _addr(v),
+            _addr(alpha), _addr(cu_seqlens), _addr(h0), _addr(dout), _addr(dht), _addr(dq),
+            _addr(dkk), _addr(dvv), _addr(dal), _addr(dh0), _addr(ws), ws.numel())
     return dq, dkk, dvv, dal, dh0
 
 
@@ -622,11 +648,9 @@ def decay_step(q, k, v, alpha, state, *, gate="ckda", gates="values", scale=1.0,
         _require(out.dtype == v.dtype and out.shape == v.shape, "out must match v")
     o = torch.empty_like(v) if out is None else out
     dst = state if new_state is None else new_state
-    with _on(dev, stream) as s:
-        _check(lib.ckda_decay_step(N, H, Hk, dk, dv, _dtype_code(q), _gate_code(gate),
-                                   _gate_input(gates, alpha, alpha), int(per_head), float(scale),
-                                   _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(state), _ptr(dst),
-                                   _ptr(o), s))
+    _launch(dev, stream, lib.ckda_decay_step, N, H, Hk, dk, dv, _dtype_code(q), _gate_code(gate),
+            _gate_input(gates, alpha, alpha), int(per_head), float(scale), _addr(q), _addr(k),
+            _addr(v), _addr(alpha), _addr(state), _addr(dst), _addr(o))
     return o
 
 
@@ -644,10 +668,11 @@ def _norm_args(y, weight, gate, act, residual, scale, next_weight, **more):
     _tensors(y.device, y=y, weight=weight, gate=gate, residual=residual, scale=scale,
              next_weight=next_weight, **more)
     for name, t in dict(gate=gate, residual=residual, **more).items():
-        _require(t is None or (t.dtype == y.dtype and t.shape == y.shape), "%s must match y" % name)
+        if t is not None and (t.dtype != y.dtype or t.shape != y.shape):
+            raise ValueError("%s must match y" % name)
     for name, t in (("weight", weight), ("scale", scale), ("next_weight", next_weight)):
-        _require(t is None or (t.dtype == torch.float32 and tuple(t.shape) == (d,)),
-                 "%s must be float32 [%d]" % (name, d))
+        if t is not None and (t.dtype != torch.float32 or t.shape != (d,)):
+            raise ValueError("%s must be float32 [%d]" % (name, d))
     return y.numel() // d, d, 0 if gate is None else _ACTS[act]
 
 
@@ -673,10 +698,9 @@ def block_norm(y, weight, *, gate=None, act="sigmoid", residual=None, scale=None
     n = next_out
     if next_weight is not None and n is None:
         n = torch.empty_like(y)
-    with _on(y.device, stream) as s:
-        _check(lib.ckda_block_norm(rows, d, io, code, float(eps), _ptr(y), _ptr(weight),
-                                   _ptr(gate), _ptr(residual), _ptr(scale), _ptr(next_weight),
-                                   _ptr(h), _ptr(n), s))
+    _launch(y.device, stream, lib.ckda_block_norm, rows, d, io, code, float(eps), _addr(y),
+            _addr(weight), _addr(gate), _addr(residual), _addr(scale), _addr(next_weight), _addr(h),
+            _addr(n))
     return h, n
 
 
@@ -702,11 +726,9 @@ def block_norm_bwd(y, weight, dh, *, dnext=None, gate=None, act="sigmoid", resid
         return dy, dw, dg, None if residual is None else dh, ds, dw2
     dx = dh if residual is not None and next_weight is None else new(residual)
     need = int(lib.ckda_block_norm_bwd_workspace_size(rows, d, io))
-    with _on(y.device, stream) as s:
-        ws = _workspace(workspace, need, y.device)
-        _check(lib.ckda_block_norm_bwd(rows, d, io, code, float(eps), _ptr(y), _ptr(weight),
-                                       _ptr(gate), _ptr(residual), _ptr(scale), _ptr(next_weight),
-                                       _ptr(dh), _ptr(dnext), _ptr(dy), _ptr(dw), _ptr(dg),
-                                       None if dx is dh else _ptr(dx), _ptr(ds), _ptr(dw2),
-                                       _ptr(ws), ws.numel(), s))
+    ws = _workspace(workspace, need, y.device)
+    _launch(y.device, stream, lib.ckda_block_norm_bwd, rows, d, io, code, float(eps), _addr(y),
+            _addr(weight), _addr(gate), _addr(residual), _addr(scale), _addr(next_weight),
+            _addr(dh), _addr(dnext), _addr(dy), _addr(dw), _addr(dg),
+            None if dx is dh else _addr(dx), _addr(ds), _addr(dw2), _addr(ws), ws.numel())
     return dy, dw, dg, dx, ds, dw2

@@ -662,8 +662,11 @@ launch_result launch_fwd_op(const DecayArgs& a, hipStream_t s) {
   // slabs of 64 columns form Q K^T half as often as slabs of 32; in float32
   // with rows of 128 only 32 fit the LDS
   constexpr int wide = sizeof(typename Op::T) == 2 ? 64 : 32;
-  if (a.dk <= 64) return a.dv <= 32 ? launch_fwd_t<Op, 64, 32>(a, s) : launch_fwd_t<Op, 64, 64>(a, s);
-  return a.dv <= 32 ? launch_fwd_t<Op, 128, 32>(a, s) : launch_fwd_t<Op, 128, wide>(a, s);
+  // few workgroups: half the columns each shorten a chunk's step
+  const int64_t walks = static_cast<int64_t>(a.seg > 0 ? a.slots : a.N) * a.H * ((a.dv + 63) / 64);
+  const bool narrow = a.dv <= 32 || walks <= 128;
+  if (a.dk <= 64) return narrow ? launch_fwd_t<Op, 64, 32>(a, s) : launch_fwd_t<Op, 64, 64>(a, s);
+  return narrow ? launch_fwd_t<Op, 128, 32>(a, s) : launch_fwd_t<Op, 128, wide>(a, s);
 }
 
 template <class Op, int DKP, int DVS, int C, bool REV, int MODE>

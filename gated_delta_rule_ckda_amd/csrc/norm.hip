@@ -207,25 +207,38 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, NormGrads g, i
     }
   }
   const float inv_d = 1.f / a.d;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * rpb) {
-    const int64_t row = r0 + t / tpr;
-    const bool live = row < a.rows;
-    typename X::V vy[K], vg[K], vx[K], vh[K], vn[K];
+  // the next row's elements are loaded while one is computed: its three sums
+  // over threads would otherwise leave the memory idle
+  struct Raw {
+    typename X::V y[K], g[K], x[K], h[K], n[K];
+  };
+  auto load = [&](int64_t row) {
+    Raw v;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int64_t i = row * a.d + (lane + tpr * k) * VEC;
-      vy[k] = typename X::V{};
-      vg[k] = vx[k] = vh[k] = vn[k] = vy[k];
-      if (live && ok[k]) {
-        vy[k] = X::load(a.y, i);
-        vh[k] = X::load(g.dh, i);
-        if (a.g) vg[k] = X::load(a.g, i);
+      v.y[k] = typename X::V{};
+      v.g[k] = v.x[k] = v.h[k] = v.n[k] = v.y[k];
+      if (row < a.rows && ok[k]) {
+        v.y[k] = X::load(a.y, i);
+        v.h[k] = X::load(g.dh, i);
+        if (a.g) v.g[k] = X::load(a.g, i);
         if (a.w2) {
-          if (a.x) vx[k] = X::load(a.x, i);
-          vn[k] = X::load(g.dn, i);
+          if (a.x) v.x[k] = X::load(a.x, i);
+          v.n[k] = X::load(g.dn, i);
         }
       }
     }
+    return v;
+  };
+  const int64_t hop = static_cast<int64_t>(gridDim.x) * rpb;
+  Raw ahead = load(static_cast<int64_t>(blockIdx.x) * rpb + t / tpr);
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < a.rows; r0 += hop) {
+    const int64_t row = r0 + t / tpr;
+    const bool live = row < a.rows;
+    const Raw now = ahead;
+    const auto &vy = now.y, &vg = now.g, &vx = now.x, &vh = now.h, &vn = now.n;
+    ahead = load(row + hop);
     float r1 = 1.f;
     if (a.w) {
       float ss[1] = {0.f};
@@ -353,21 +366,21 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, NormGrads g, i
   }
 }
 
-// out[c] = sum over workgroups of part[.][q][c], 64 columns a workgroup, its
-// 16 waves taking every 16th row; the waves' sums are added in order.
+// out[c] = sum over workgroups of part[.][q][c]: 32 columns a workgroup, its
+// 32 groups of lanes taking every 32nd workgroup's; their sums are added in order.
 __global__ __launch_bounds__(1024) void norm_cols_kernel(const float* part, int parts, int d, float* dw,
                                                         float* ds, float* dw2) {
-  __shared__ float red[16][64];
-  const int q = blockIdx.y, c = blockIdx.x * 64 + (threadIdx.x & 63), wave = threadIdx.x >> 6;
+  __shared__ float red[32][33];
+  const int q = blockIdx.y, l = threadIdx.x & 31, c = blockIdx.x * 32 + l, grp = threadIdx.x >> 5;
   float* out = q == 0 ? dw : (q == 1 ? ds : dw2);
   if (!out) return;
   float v = 0.f;
   if (c < d)
-    for (int p = wave; p < parts; p += 16) v += part[(static_cast<int64_t>(p) * 3 + q) * d + c];
-  red[wave][threadIdx.x & 63] = v;
+    for (int p = grp; p < parts; p += 32) v += part[(static_cast<int64_t>(p) * 3 + q) * d + c];
+  red[grp][l] = v;
   __syncthreads();
-  if (wave == 0 && c < d) {
-    for (int i = 1; i < 16; ++i) v += red[i][threadIdx.x];
+  if (grp == 0 && c < d) {
+    for (int i = 1; i < 32; ++i) v += red[i][l];
     out[c] = v;
   }
 }
@@ -408,7 +421,7 @@ launch_result launch_one(const NormArgs& a, const NormGrads* g, const Shape& s, 
                      a, *g, s.tpr);
   const launch_result e = hipGetLastError();
   if (e != hipSuccess || (!g->dw && !g->ds && !g->dw2)) return e;
-  hipLaunchKernelGGL(norm_cols_kernel, dim3((a.d + 63) / 64, 3), dim3(1024), 0, st, g->part,
+  hipLaunchKernelGGL(norm_cols_kernel, dim3((a.d + 31) / 32, 3), dim3(1024), 0, st, g->part,
                      static_cast<int>(grid), a.d, g->dw, g->ds, g->dw2);
   return hipGetLastError();
 }
