@@ -207,38 +207,25 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, NormGrads g, i
     }
   }
   const float inv_d = 1.f / a.d;
-  // the next row's elements are loaded while one is computed: its three sums
-  // over threads would otherwise leave the memory idle
-  struct Raw {
-    typename X::V y[K], g[K], x[K], h[K], n[K];
-  };
-  auto load = [&](int64_t row) {
-    Raw v;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * rpb) {
+    const int64_t row = r0 + t / tpr;
+    const bool live = row < a.rows;
+    typename X::V vy[K], vg[K], vx[K], vh[K], vn[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int64_t i = row * a.d + (lane + tpr * k) * VEC;
-      v.y[k] = typename X::V{};
-      v.g[k] = v.x[k] = v.h[k] = v.n[k] = v.y[k];
-      if (row < a.rows && ok[k]) {
-        v.y[k] = X::load(a.y, i);
-        v.h[k] = X::load(g.dh, i);
-        if (a.g) v.g[k] = X::load(a.g, i);
+      vy[k] = typename X::V{};
+      vg[k] = vx[k] = vh[k] = vn[k] = vy[k];
+      if (live && ok[k]) {
+        vy[k] = X::load(a.y, i);
+        vh[k] = X::load(g.dh, i);
+        if (a.g) vg[k] = X::load(a.g, i);
         if (a.w2) {
-          if (a.x) v.x[k] = X::load(a.x, i);
-          v.n[k] = X::load(g.dn, i);
+          if (a.x) vx[k] = X::load(a.x, i);
+          vn[k] = X::load(g.dn, i);
         }
       }
     }
-    return v;
-  };
-  const int64_t hop = static_cast<int64_t>(gridDim.x) * rpb;
-  Raw ahead = load(static_cast<int64_t>(blockIdx.x) * rpb + t / tpr);
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < a.rows; r0 += hop) {
-    const int64_t row = r0 + t / tpr;
-    const bool live = row < a.rows;
-    const Raw now = ahead;
-    const auto &vy = now.y, &vg = now.g, &vx = now.x, &vh = now.h, &vn = now.n;
-    ahead = load(row + hop);
     float r1 = 1.f;
     if (a.w) {
       float ss[1] = {0.f};
@@ -249,7 +236,7 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, NormGrads g, i
       row_sum<1, NT>(ss, tpr, red, half);
       r1 = 1.f / sqrtf(ss[0] * inv_d + a.eps);
     }
-    float D[EPL], act[EPL];
+    float D[EPL], act[EPL], dact[EPL];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -257,9 +244,11 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, NormGrads g, i
         const int j = k * VEC + e;
         D[j] = X::get(vh[k], e);
         act[j] = 1.f;
+        dact[j] = 0.f;
         if (a.g) {
-          const float gg = X::get(vg[k], e), p = sigmoid_of<IO>(gg);
+          const float gg = X::get(vg[k], e), p = sigmoid_of<IO>(gg), q = p * (1.f - p);
           act[j] = a.act == kActSilu ? (p == 0.f ? 0.f : gg * p) : p;
+          dact[j] = a.act == kActSilu ? (p == 0.f ? 0.f : p + gg * q) : q;
         }
       }
     if (a.w2) {
@@ -303,12 +292,7 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, NormGrads g, i
         const float yn = X::get(vy[k], e) * r1, u = yn * w[j];
         ds[j] += D[j] * u * act[j];
         const float dv = D[j] * s[j];
-        dg[j] = 0.f;
-        if (a.g) {
-          const float gg = X::get(vg[k], e), p = sigmoid_of<IO>(gg);
-          const float da = a.act == kActSilu ? (p == 0.f ? 0.f : p * (1.f + gg * (1.f - p))) : p * (1.f - p);
-          dg[j] = dv * u * da;
-        }
+        dg[j] = dv * u * dact[j];
         const float du = dv * act[j];
         dw[j] += du * yn;
         D[j] = du * w[j];
@@ -405,7 +389,13 @@ int64_t grid_of(int64_t rows, const Shape& s, int64_t most) {
   return steps < most ? steps : most;
 }
 
-constexpr int64_t kFwdGroups = 2048, kBwdGroups = 1024;
+// Workgroups: as many as the 256 CUs hold at once, each walking over rows.  One
+// more round of them with few rows left costs as much as a full one (gradients
+// of 32768 rows of 2048 in bf16: 217 us with 1024 workgroups of four a CU, 289
+// with 1024 where three fitted; forward of 524288 rows of 128: 71 us with 1024,
+// 82 with 2048).
+constexpr int64_t kFwdGroups = 1024;
+int64_t bwd_groups(const Shape& s) { return s.nt == 1024 ? 256 : (s.epl == 8 ? 1024 : 512); }
 
 template <class IO, int VEC, int EPL, int NT>
 launch_result launch_one(const NormArgs& a, const NormGrads* g, const Shape& s, hipStream_t st) {
@@ -414,7 +404,7 @@ launch_result launch_one(const NormArgs& a, const NormGrads* g, const Shape& s, 
                        dim3(static_cast<unsigned>(grid_of(a.rows, s, kFwdGroups))), dim3(NT), 0, st, a, s.tpr);
     return hipGetLastError();
   }
-  const int64_t grid = grid_of(a.rows, s, kBwdGroups);
+  const int64_t grid = grid_of(a.rows, s, bwd_groups(s));
   const int rpb = NT / s.tpr;
   const size_t lds = rpb > 1 ? static_cast<size_t>(rpb) * a.d * 4 : 0;
   hipLaunchKernelGGL((norm_bwd_kernel<IO, VEC, EPL, NT>), dim3(static_cast<unsigned>(grid)), dim3(NT), lds, st,
@@ -451,7 +441,7 @@ launch_result launch(const NormArgs& a, const NormGrads* g, int32_t io_dtype, hi
 
 size_t norm_bwd_workspace(int64_t rows, int32_t d, int32_t io_dtype) {
   const Shape s = shape_of(d, io_dtype == CKDA_DTYPE_BF16 ? 2 : 4);
-  return static_cast<size_t>(grid_of(rows, s, kBwdGroups)) * 3 * d * 4;
+  return static_cast<size_t>(grid_of(rows, s, bwd_groups(s))) * 3 * d * 4;
 }
 
 launch_result launch_norm_fwd(const NormArgs& a, int32_t io_dtype, hipStream_t s) {

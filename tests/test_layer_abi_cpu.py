@@ -1,0 +1,225 @@
+"""The decay and norm calls reject bad arguments on the host before any HIP call
+(dummy, never-dereferenced pointers; no GPU is touched), and the binding before
+the library; the float64 references behind the parity tests against differences."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_ckda_amd as ck
+from tests import decay_fp64 as dref
+from tests import norm_fp64 as nref
+
+BASE = 0x7F0000000000
+NAMES = ["q", "k", "v", "alpha", "h0", "o", "ht", "dout", "dht", "dq", "dk", "dv", "dalpha", "dh0", "ws"]
+P = {n: ctypes.c_void_p(BASE + i * (1 << 33)) for i, n in enumerate(NAMES)}
+CU = ctypes.c_void_p(BASE + 40 * (1 << 33))
+
+
+def desc(**kw):
+    d = dict(B=2, T=64, H=4, dk=128, dv=128, num_seqs=2, io_dtype=ck.BF16, gate_range=ck.GATE_KDA,
+             gate_input=ck.GATES_F32, qk_heads=2, alpha_per_head=0, scale=1.0)
+    d.update(kw)
+    return ck.DecayDesc(**d)
+
+
+def call(which, d, cu=None, bytes_=1 << 33, **over):
+    p = dict(P, **over)
+    lib = ck._load()
+    ref = None if d is None else ctypes.byref(d)
+    if which == "fwd":
+        st = lib.ckda_decay_fwd(ref, p["q"], p["k"], p["v"], p["alpha"], cu, p["h0"], p["o"], p["ht"],
+                                p["ws"], bytes_, None)
+    else:
+        st = lib.ckda_decay_bwd(ref, p["q"], p["k"], p["v"], p["alpha"], cu, p["h0"], p["dout"],
+                                p["dht"], p["dq"], p["dk"], p["dv"], p["dalpha"], p["dh0"], p["ws"],
+                                bytes_, None)
+    return st, lib.ckda_last_error().decode()
+
+
+@pytest.mark.parametrize("which", ["fwd", "bwd"])
+@pytest.mark.parametrize("over,status,needle", [
+    (dict(B=0), 1, "non-positive"), (dict(T=-1), 1, "non-positive"), (dict(dv=0), 1, "non-positive"),
+    (dict(io_dtype=3), 1, "io_dtype"), (dict(gate_range=2), 1, "gate_range"),
+    (dict(gate_input=4), 1, "gate_input"), (dict(alpha_per_head=2), 1, "alpha_per_head"),
+    (dict(qk_heads=3), 1, "qk_heads"), (dict(num_seqs=3), 1, "num_seqs"),
+    (dict(dk=12), 2, "multiples of 8"), (dict(dv=136), 2, "multiples of 8"),
+    (dict(B=1 << 16, num_seqs=1 << 16, T=1 << 15), 2, "too many"),
+    (dict(H=1 << 16, qk_heads=1 << 16), 2, "2^22"),
+])
+def test_decay_rejects_bad_descriptors(which, over, status, needle):
+    st, msg = call(which, desc(**over))
+    assert st == status and needle in msg, msg
+
+
+def test_decay_null_alignment_overlap():
+    assert call("fwd", None)[0] == 1
+    for n in ("q", "k", "v", "alpha", "o"):
+        st, msg = call("fwd", desc(), **{n: None})
+        assert st == 1 and n + " must not be NULL" in msg
+    st, msg = call("fwd", desc(), k=ctypes.c_void_p(P["k"].value + 8))
+    assert st == 1 and "aligned" in msg
+    for n in ("q", "v", "alpha", "h0"):
+        st, msg = call("fwd", desc(), o=P[n])
+        assert st == 1 and "o overlaps " + n in msg
+    st, msg = call("fwd", desc(), ht=ctypes.c_void_p(P["h0"].value + 64))
+    assert st == 1 and "overlaps" in msg
+    for n in ("dq", "dk", "dv", "dout"):
+        st, msg = call("bwd", desc(), **{n: None})
+        assert st == 1 and n in msg
+    st, msg = call("bwd", desc(), dq=P["dk"])
+    assert st == 1 and "overlaps" in msg
+    st, msg = call("bwd", desc(), dh0=P["dht"])
+    assert st == 1 and "overlaps" in msg
+    st, msg = call("bwd", desc(B=1, num_seqs=1), cu=P["dv"])
+    assert st == 1 and "cu_seqlens" in msg
+    st, msg = call("fwd", desc(), cu=CU)
+    assert st == 1 and "B=2" in msg
+
+
+def test_decay_workspaces():
+    d = desc(B=1, num_seqs=1, T=100000)
+    lib = ck._load()
+    need = lib.ckda_decay_fwd_workspace_size(ctypes.byref(d), 0)
+    assert need > 0
+    assert call("fwd", d, bytes_=need - 1) == (3, "workspace has %d bytes, %d needed" % (need - 1, need))
+    assert call("fwd", d, ws=None)[0] == 1
+    assert "256-byte" in call("fwd", d, ws=ctypes.c_void_p(P["ws"].value + 16))[1]
+    assert "workspace overlaps v" in call("fwd", d, ws=P["v"])[1]
+    need = lib.ckda_decay_bwd_workspace_size(ctypes.byref(desc()), 0)
+    # a state and an adjoint a chunk in bf16, at least
+    assert need >= 2 * 2 * 4 * 128 * 128 * 2
+    assert call("bwd", desc(), bytes_=need - 1)[0] == 3
+    assert lib.ckda_decay_fwd_workspace_size(None, 0) == 0
+    assert lib.ckda_decay_bwd_workspace_size(ctypes.byref(desc(dk=20)), 0) == 0
+
+
+def test_decay_nothing_to_do():
+    assert call("fwd", desc(B=1, num_seqs=0, T=0), cu=CU)[0] == 0
+    assert call("bwd", desc(B=1, num_seqs=0, T=0), cu=CU)[0] == 0
+
+
+def step(N=3, H=4, Hk=2, dk=64, dv=64, io=ck.BF16, gate=0, gi=0, per=0, **over):
+    p = dict(P, **over)
+    lib = ck._load()
+    st = lib.ckda_decay_step(N, H, Hk, dk, dv, io, gate, gi, per, 1.0, p["q"], p["k"], p["v"], p["alpha"],
+                             p["h0"], p["ht"], p["o"], None)
+    return st, lib.ckda_last_error().decode()
+
+
+def test_step_rejections():
+    assert step(N=0)[0] == 0
+    for kw, status in ((dict(N=-1), 1), (dict(H=0), 1), (dict(Hk=3), 1), (dict(dk=9), 2), (dict(io=2), 1),
+                       (dict(gate=5), 1), (dict(gi=3), 1), (dict(per=2), 1), (dict(N=1 << 20), 2),
+                       (dict(q=None), 1), (dict(h0=None), 1), (dict(ht=None), 1), (dict(o=P["v"]), 1),
+                       (dict(ht=ctypes.c_void_p(P["h0"].value + 16)), 1), (dict(ht=P["k"]), 1)):
+        assert step(**kw)[0] == status, kw
+
+
+def norm(rows=4, d=64, io=ck.BF16, act=1, eps=1e-6, **over):
+    p = dict(y=P["q"], w=P["k"], g=P["v"], x=P["alpha"], s=P["h0"], w2=P["o"], h=P["ht"], n=P["dout"])
+    p.update(over)
+    lib = ck._load()
+    st = lib.ckda_block_norm(rows, d, io, act, eps, *[p[m] for m in ("y", "w", "g", "x", "s", "w2", "h", "n")], None)
+    return st, lib.ckda_last_error().decode()
+
+
+def norm_bwd(rows=4, d=64, io=ck.BF16, act=1, eps=1e-6, bytes_=1 << 33, **over):
+    p = {m: ctypes.c_void_p(BASE + (50 + i) * (1 << 33)) for i, m in enumerate(
+        "y w g x s w2 dh dn dy dw dg dx ds dw2 ws".split())}
+    p.update(over)
+    lib = ck._load()
+    st = lib.ckda_block_norm_bwd(rows, d, io, act, eps, *[p[m] for m in
+                                 "y w g x s w2 dh dn dy dw dg dx ds dw2 ws".split()], bytes_, None)
+    return st, lib.ckda_last_error().decode()
+
+
+def test_norm_rejections():
+    assert norm(rows=0)[0] == 0
+    for kw, status in ((dict(rows=-1), 1), (dict(d=0), 1), (dict(d=16385), 2), (dict(io=7), 1), (dict(act=3), 1),
+                       (dict(act=0), 1), (dict(g=None), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1),
+                       (dict(eps=float("inf")), 1), (dict(n=None), 1), (dict(w2=None), 1), (dict(y=None), 1),
+                       (dict(h=None), 1), (dict(h=P["q"]), 1), (dict(n=P["alpha"]), 1), (dict(n=P["ht"]), 1),
+                       (dict(y=ctypes.c_void_p(BASE + 2)), 1), (dict(rows=1 << 45), 2)):
+        assert norm(**kw)[0] == status, kw
+    for kw, status in ((dict(rows=0), 1), (dict(dn=None), 1), (dict(dw2=None), 1), (dict(dw=None), 1),
+                       (dict(ds=None), 1), (dict(dg=None), 1), (dict(act=0), 1), (dict(bytes_=16), 3),
+                       (dict(ws=None), 1), (dict(dy=None), 1), (dict(dh=None), 1)):
+        assert norm_bwd(**kw)[0] == status, kw
+    p = ctypes.c_void_p(BASE + 50 * (1 << 33))
+    assert norm_bwd(dx=p)[0] == 1 and "dx overlaps y" in norm_bwd(dx=p)[1]
+
+
+def test_binding_rejects_before_the_library():
+    """Shapes, types and devices are checked in Python (tensors on the CPU here)."""
+    z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt)
+    q, v, al = z(1, 8, 2, 16), z(1, 8, 4, 16), z(1, 8, 4)
+    with pytest.raises(ValueError, match="GPU"):
+        ck.decay_fwd(q, q, v, al)
+    for bad in (dict(k=z(1, 8, 2, 8)), dict(v=z(1, 7, 4, 16)), dict(v=z(1, 8, 3, 16)), dict(alpha=z(1, 8, 2)),
+                dict(alpha=z(1, 8, 4, dt=torch.bfloat16)), dict(k=z(1, 8, 2, 16, dt=torch.bfloat16)),
+                dict(cu_seqlens=z(3))):
+        kw = dict(q=q, k=q, v=v, alpha=al)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            ck.decay_fwd(**kw)
+    with pytest.raises(TypeError):
+        ck.decay_fwd(q.half(), q.half(), v.half(), al)
+    with pytest.raises(ValueError, match="gate"):
+        ck.decay_fwd(q, q, v, al, gate="relu")
+    y, w = z(4, 32), z(32)
+    for kw in (dict(weight=z(31)), dict(gate=z(4, 31)), dict(act="relu"), dict(residual=z(3, 32)),
+               dict(scale=z(32, dt=torch.bfloat16))):
+        args = dict(dict(weight=w), **kw)
+        with pytest.raises(ValueError):
+            ck.block_norm(y, **args)
+    with pytest.raises(ValueError, match="GPU"):
+        ck.block_norm(y, w)
+
+
+@pytest.mark.parametrize("zeros", [0.0, 0.2])
+def test_decay_reference_against_differences(zeros):
+    """The reference's gradients (zero and negative gates among them) against
+    central differences, exact for the gates (the loss is multilinear in them)."""
+    rng = np.random.default_rng(0)
+    B, T, Hk, H, dk, dv = 1, 9, 1, 2, 3, 4
+    cu = np.array([0, 4, 4, 9])
+    p = dict(q=rng.standard_normal((B, T, Hk, dk)), k=rng.standard_normal((B, T, Hk, dk)),
+             v=rng.standard_normal((B, T, H, dv)), a=rng.uniform(-1, 1, (B, T, H)), h0=rng.standard_normal((3, H, dk, dv)))
+    p["a"][rng.random(p["a"].shape) < zeros] = 0.0
+    do, dht = rng.standard_normal((B, T, H, dv)), rng.standard_normal((3, H, dk, dv))
+
+    def loss(p):
+        o, ht = dref.fwd(p["q"], p["k"], p["v"], p["a"], p["h0"], cu, 0.7)[:2]
+        return (o * do).sum() + (ht * dht).sum()
+
+    got = dict(zip(("q", "k", "v", "a", "h0"), dref.bwd(p["q"], p["k"], p["v"], p["a"], do, p["h0"], dht, cu, 0.7)[0]))
+    for name in got:
+        for i in np.ndindex(p[name].shape):
+            up, down = (dict(p, **{name: p[name].copy()}) for _ in (0, 1))
+            up[name][i] += 1e-4
+            down[name][i] -= 1e-4
+            want = (loss(up) - loss(down)) / 2e-4
+            assert abs(got[name][i] - want) < 1e-7 * max(1, abs(want)), (name, i)
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_norm_reference_against_differences(act):
+    rng = np.random.default_rng(1)
+    p = {m: rng.standard_normal((3, 5)) for m in ("y", "g", "x")}
+    p.update({m: 1 + 0.3 * rng.standard_normal(5) for m in ("w", "s", "w2")})
+    dh, dn = rng.standard_normal((2, 3, 5))
+
+    def loss(p):
+        h, n = nref.fwd(p["y"], p["w"], p["g"], act, p["x"], p["s"], p["w2"], 1e-3)[0]
+        return (h * dh).sum() + (n * dn).sum()
+
+    got = nref.bwd(p["y"], p["w"], dh, dn, p["g"], act, p["x"], p["s"], p["w2"], 1e-3)[0]
+    for name in p:
+        for i in np.ndindex(p[name].shape):
+            up, down = (dict(p, **{name: p[name].copy()}) for _ in (0, 1))
+            up[name][i] += 1e-5
+            down[name][i] -= 1e-5
+            want = (loss(up) - loss(down)) / 2e-5
+            assert abs(got["d" + name][i] - want) < 1e-7 * max(1, abs(want)), (name, i)
