@@ -183,7 +183,7 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormArgs a, int tpr) {
 // Gradients; each workgroup leaves its rows' sums for dw, ds, dw2 in
 // part[workgroup][3][d].
 template <class IO, int VEC, int EPL, int NT>
-__global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a, NormGrads g, int tpr) {
+__global__ __launch_bounds__(NT, (EPL == 8 ? 3 : 1)) void norm_bwd_kernel(NormArgs a, NormGrads g, int tpr) {
   constexpr int K = EPL / VEC;
   using X = Vec<IO, VEC>;
   __shared__ float red[4 * (NT / 64)];
@@ -377,6 +377,8 @@ Shape shape_of(int d, int es) {
   Shape s;
   s.vec = 16 / es;
   while (d % s.vec != 0) s.vec /= 2;
+  // past 8192 the gradients' registers spill a little at 16 elements a thread,
+  // and by kilobytes at 32 in 512 threads
   s.nt = d > 8192 ? 1024 : 256;
   s.epl = d <= 2048 ? 8 : (d <= 4096 || d > 8192 ? 16 : 32);
   s.tpr = 4;
@@ -389,13 +391,13 @@ int64_t grid_of(int64_t rows, const Shape& s, int64_t most) {
   return steps < most ? steps : most;
 }
 
-// Workgroups: as many as the 256 CUs hold at once, each walking over rows.  One
-// more round of them with few rows left costs as much as a full one (gradients
-// of 32768 rows of 2048 in bf16: 217 us with 1024 workgroups of four a CU, 289
-// with 1024 where three fitted; forward of 524288 rows of 128: 71 us with 1024,
-// 82 with 2048).
+// Workgroups: as many as the 256 CUs hold at once by their registers, each
+// walking over rows.  A second round of a few costs as much as a full one
+// (gradients of 32768 rows of 2048 in bf16, where three fit a CU: 210 us with
+// 768 workgroups, 267 with 512, 283 with 1024; forward of 524288 rows of 128:
+// 71 us with 1024, 82 with 2048).
 constexpr int64_t kFwdGroups = 1024;
-int64_t bwd_groups(const Shape& s) { return s.nt == 1024 ? 256 : (s.epl == 8 ? 1024 : 512); }
+int64_t bwd_groups(const Shape& s) { return s.nt == 1024 ? 256 : (s.epl == 8 ? 768 : 512); }
 
 template <class IO, int VEC, int EPL, int NT>
 launch_result launch_one(const NormArgs& a, const NormGrads* g, const Shape& s, hipStream_t st) {
