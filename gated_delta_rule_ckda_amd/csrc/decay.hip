@@ -9,7 +9,7 @@
 namespace ckda {
 namespace {
 
-constexpr int kNT = 256;  // 4 waves
+constexpr int kNT = 256;  // of the join
 
 // ---- forward -------------------------------------------------------------------
 // One workgroup walks one (segment, head) over its chunks for DVS columns of
@@ -711,12 +711,17 @@ bool decay_supported(int32_t dk, int32_t dv) {
   return dk >= 8 && dk <= 128 && dk % 8 == 0 && dv >= 8 && dv <= 128 && dv % 8 == 0;
 }
 
-// Tokens of a segment for these sizes (0: sequences are not cut).
+// Tokens of a segment for these sizes (0: sequences are not cut).  Sequences
+// are cut where there are fewer (sequence, head, slab) walks than CUs, into
+// pieces that give each CU one segment of one head: a cut costs another read
+// of k and v.  One prompt of 65536 tokens, 16 heads of 128: 441 us so, 482 with
+// half as many segments, 469 with twice as many, 505 with three quarters (256
+// CUs do not divide into them).  A packed batch is always cut, since its
+// longest sequence would walk alone (40000 tokens, the longest 8191: 298 us).
 int32_t decay_segment(const DecayArgs& a) {
   const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
-  const int64_t parts = static_cast<int64_t>(a.H) * ((a.dv + 63) / 64);
-  if (a.N * parts >= 256 && !a.cu) return 0;
-  int64_t seg = (tokens * a.H / (a.cu ? 384 : 256) + 63) / 64 * 64;
+  if (!a.cu && static_cast<int64_t>(a.N) * a.H * ((a.dv + 63) / 64) >= 256) return 0;
+  int64_t seg = (tokens * a.H / 256 + 63) / 64 * 64;
   if (seg < 512) seg = 512;
   return seg < a.T ? static_cast<int32_t>(seg) : 0;
 }

@@ -14,8 +14,8 @@
 //   a_t da_t = sum_{i >= t} (E_i z_i + sum_{j < t} D_ij M_ij) + sum_{j < t} W_j y_j + g x:
 //
 // sums of terms that all hold the factor a_t, with nothing subtracted, so that
-// dividing by it costs no accuracy.  In a chunk with zero gates, or products
-// beyond 2^60, the factor is left out instead,
+// dividing by it costs no accuracy.  In a chunk with gates of zero or under
+// 2^-30, or products beyond 2^+-60, the factor is left out instead,
 //
 //   R_1(i) = z_i,  R_{t+1}(i) = a_t R_t(i) + M_it     (writes before t, read i)
 //   da_t = sum_{i >= t} D_it R_t(i) + W_t X_t,   X_1 = x,  X_{t+1} = a_t X_t + y_t.

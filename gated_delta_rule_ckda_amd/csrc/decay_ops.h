@@ -187,8 +187,9 @@ __device__ __forceinline__ float exp2_wide(double x) {
 // A chunk's gates in LDS.  L is the running sum of log2|a| (kept in double:
 // with gates near 0.1 a float sum of 64 of them is off by 1e-5), split into an
 // integer and a fraction so that differences of two are exact to float.
-// `fast`: no zero gate and all running products within 2^+-60 of the middle
-// one, so D_ij = er_i ej_j (signs included).
+// `fast`: no gate under 2^-30 (zeros among them) and all running products
+// within 2^+-60 of the middle one, so D_ij = er_i ej_j, signs included, and a
+// sum of terms that hold a gate may be divided by it.
 template <int C>
 struct alignas(16) Gates {
   float E[C], W[C];  // products from the chunk's start, to its end
@@ -214,7 +215,7 @@ __device__ __forceinline__ void gates_fill(Gates<C>& G, float x, bool valid, int
   const int zend = zm ? 63 - __clzll(zm) : -1;
   const float sg = (__popcll(nm & upto) & 1) ? -1.f : 1.f;
   const float sgend = (__popcll(nm) & 1) ? -1.f : 1.f;
-  const bool far = !(fabs(L - mid) <= 60.0);
+  const bool far = !(fabs(L - mid) <= 60.0) || (valid && !(fabsf(gl.l2) <= 30.f));
   const bool fast = zm == 0 && __ballot(far) == 0;
   if (fast) {  // powers of differences up to 60, the others from them
     const float er = sg * __builtin_amdgcn_exp2f(static_cast<float>(L - mid));

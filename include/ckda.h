@@ -422,9 +422,10 @@ ckda_status_t ckda_decay_fwd(const ckda_decay_desc_t* desc, const void* q, const
  * float32, rounded once at the end); dh0 in float32.  With logits dalpha is
  * the gradient of the logits; with alpha_per_head it is summed over all
  * tokens.  dalpha and dh0 may be NULL (not wanted).  dq and dk of a q/k head
- * sum over the value heads that read it.  dalpha is formed with no division
- * by a gate, so zero gates have the gradient of the recurrence.  Every sum
- * runs in a fixed order.
+ * sum over the value heads that read it.  dalpha is formed without
+ * subtracting (blocks with gates of zero or under 2^-30 also without dividing
+ * by one), so every gate, zeros included, has the gradient of the recurrence.
+ * Every sum runs in a fixed order.
  */
 size_t ckda_decay_bwd_workspace_size(const ckda_decay_desc_t* desc, int32_t packed);
 ckda_status_t ckda_decay_bwd(const ckda_decay_desc_t* desc, const void* q, const void* k,

@@ -213,3 +213,17 @@ def test_step(dtype, N, H, Hk, dk, dv, kind, per_head):
     # the step multiplies exact operands in float32: only its output is rounded
     within("o", o, ro[:, 0], ref.HALF[dtype] * np.abs(ro[:, 0]) + 2 * ref.sums(dk, 1) * om[:, 0])
     within("state", new, rh, 2 * ref.sums(dk, 1) * hm)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [64, 150])
+def test_tiny_and_exact_gates(dtype, T):
+    """Gates of 0, +-1, a half and down to the smallest normal float, forward
+    and gradients: products of three of the small ones underflow, where the
+    bounds' own terms vanish with them (2^-126 a term stands beside them)."""
+    c = make(21, 2, T, 2, 2, 64, 64, dtype, h0=True)
+    rng = np.random.default_rng(22)
+    pool = np.array([1, 1, 1, 1, -1, 0.5, 0.999, 0, 1e-9, 1e-12, -1e-20, 1e-30, 2e-38], np.float32)
+    c["alpha"] = rng.choice(pool, c["alpha"].shape).astype(np.float32)
+    check_fwd(c)
+    check_bwd(c)
