@@ -25,6 +25,13 @@
 // wave owns DP / 8 columns of dq, dk and dv for all tokens.  One workgroup
 // fills a CU's LDS, so the next head's or item's rows are on their way into
 // registers while one is computed.
+//
+// P and N rounded to the io type once each, as the states are: half a step of
+// each gradient.  Measured at 8 x 4096 tokens, 16 heads of 128, bf16: 424 us
+// (1.47 GB, 3.5 TB/s).  Without the loads 373 us were left of 540, without the
+// products 422: LDS (half of its cycles busy) and the loads share the time.
+// Four waves took 900 us, loads all at once 528, stores straight from the
+// accumulators 466.
 #include "decay_ops.h"
 
 namespace ckda {

