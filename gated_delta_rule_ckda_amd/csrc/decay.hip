@@ -31,9 +31,11 @@ constexpr int kNT = 256;  // of the join
 //
 // Measured at 8 x 4096 tokens, 16 heads of 128, bf16: 150 us, 3.6 TB/s of the
 // bytes it cannot do without, each read from HBM once (411 MB fetched of 402).
-// Without the loads it takes 119 us, without the products 131: writes into LDS
-// (about 30 bytes a clock and CU) bound the one, what a CU takes in (16 to 22
-// bytes a clock, q and k once a slab) the other, and the two overlap in part.
+// Without the loads it takes 119 us, without the products 131: LDS (58% of its
+// cycles busy, reads of W V across its rows first) bounds the one, what a CU
+// takes in (16 to 22 bytes a clock, q and k once a slab) the other, and the two
+// overlap in part.  Half as many state waves with twice the rows each read W V
+// less but take as long (152 us).
 // Earlier forms: one role and two barriers 246 us, two roles 207, rows loaded
 // two chunks ahead 187, slabs of 64 columns 155.
 template <class Op, int DKP, int DVS>
