@@ -635,7 +635,8 @@ ckda_status_t validate_decay(const ckda_decay_desc_t* d, const int32_t* cu) {
   // a chunk's rows of one tensor are addressed with 32-bit offsets
   if (static_cast<int64_t>(d->H) * (d->dk > d->dv ? d->dk : d->dv) >= (int64_t(1) << 22))
     return fail(CKDA_ERR_UNSUPPORTED, "H * max(dk, dv) of 2^22 or more");
-  if (static_cast<int64_t>(d->B) * d->T >= (int64_t(1) << 31) ||
+  // walks look two chunks past the end
+  if (static_cast<int64_t>(d->B) * d->T >= (int64_t(1) << 31) - 1024 ||
       ckda::decay_grid(decay_args(d, cu), d->io_dtype) >= (int64_t(1) << 31))
     return fail(CKDA_ERR_UNSUPPORTED, "too many (sequence, head) chunks for one launch");
   return ok();

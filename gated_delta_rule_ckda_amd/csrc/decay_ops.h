@@ -134,13 +134,6 @@ __device__ __forceinline__ GateLog gate_log(float x, int gate_input, bool ckda) 
 __device__ __forceinline__ float gate_value(float x, int gate_input, bool ckda) {
   return gate_input == CKDA_GATES_F32 ? x : alpha_from_logit(x, ckda);
 }
-// alpha as it is stored, widened
-__device__ __forceinline__ float gate_stored(const DecayArgs& a, int64_t token, int h) {
-  const int64_t i = a.per_head ? h : token * a.H + h;
-  return a.gate_input == CKDA_GATES_LOGITS_BF16 ? gate_raw<gate_logit_bf16>(a.alpha, i)
-                                                : gate_raw<gate_f32>(a.alpha, i);
-}
-
 // Inclusive sum over the lanes of a wave.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ double dpp_moved(double x) {  // 0 where no lane moves in
@@ -301,18 +294,6 @@ __device__ __forceinline__ void store_piece(rsrc_t r, int off, const uint4& x) {
   typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
   __builtin_amdgcn_raw_buffer_store_b128(u32x4{x.x, x.y, x.z, x.w}, r, off, 0, 0);
 }
-// 4 values in the type of Op (8 or 16 bytes)
-template <class Op>
-__device__ __forceinline__ void store_four(rsrc_t r, int off, const f32x4& x) {
-  alignas(16) typename Op::T y[4];
-  Op::store4(y, x);
-  if constexpr (sizeof(typename Op::T) == 2) {
-    typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-    __builtin_amdgcn_raw_buffer_store_b64(*reinterpret_cast<const u32x2*>(y), r, off, 0, 0);
-  } else {
-    store_piece(r, off, *reinterpret_cast<const uint4*>(y));
-  }
-}
 template <class T, int ROWS, int COLS, int NT>
 struct RowTile {
   static constexpr int EPP = 16 / sizeof(T), PPR = COLS / EPP, NP = ROWS * PPR / NT;
@@ -417,8 +398,6 @@ struct Fr<OpBF16> {
     u.h[1] = *reinterpret_cast<const bf16x4*>(r + 32 * s + 16 + 4 * lq);
     return u.f;
   }
-  // zeros outside the row (guarded loads from memory)
-  static __device__ __forceinline__ F zero() { return F{}; }
 };
 
 template <>
@@ -437,7 +416,6 @@ struct Fr<OpF32> {
     return *reinterpret_cast<const F*>(r + 16 * s + 4 * lq);
   }
   static __device__ __forceinline__ F rowp(const T* r, int s, int lq) { return row(r, s, lq); }
-  static __device__ __forceinline__ F zero() { return F{}; }
 };
 
 // element e of a 16-byte piece, widened

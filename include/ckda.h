@@ -385,7 +385,7 @@ ckda_status_t ckda_l2norm_debug(const void* x, float* y, int64_t rows,
  * cu_seqlens is clamped to [0, T] on the device.
  * Supported: dk and dv multiples of 8 from 8 to 128, in any combination, both
  * io dtypes; others return CKDA_ERR_UNSUPPORTED, as do H * max(dk, dv) of 2^22 or
- * more, B * T of 2^31 or more
+ * more, B * T of 2^31 - 1024 or more
  * and launches of 2^31 or more workgroups.
  */
 typedef struct {
@@ -421,7 +421,8 @@ ckda_status_t ckda_decay_fwd(const ckda_decay_desc_t* desc, const void* q, const
  * k, v and alpha (bf16 inputs: the products run on bf16 operands and sums in
  * float32, rounded once at the end); dh0 in float32.  With logits dalpha is
  * the gradient of the logits; with alpha_per_head it is summed over all
- * tokens.  dalpha and dh0 may be NULL (not wanted).  dq and dk of a q/k head
+ * tokens (in float32; what the tokens' terms cancel stays in proportion to
+ * them, not to the sum).  dalpha and dh0 may be NULL (not wanted).  dq and dk of a q/k head
  * sum over the value heads that read it.  dalpha is formed without
  * subtracting (blocks with gates of zero or under 2^-30 also without dividing
  * by one), so every gate, zeros included, has the gradient of the recurrence.
