@@ -91,11 +91,14 @@ __device__ __forceinline__ Piece piece_of(const DecayArgs& a, int slot, int L, i
 // ---- gates -------------------------------------------------------------------
 constexpr float kLog2e = 1.4426950408889634f;
 
-// log2|a| of a gate, whether it is negative, and whether it is exactly zero
-// (then the logarithm is 0 and the zero is tracked apart).  The logarithm
-// comes from the logit itself where there is one: forming the gate first
-// would lose the distance of a gate from 1, which a memory of thousands of
-// tokens multiplies.
+// log2|a| of a gate, whether it is negative, and whether it is zero (then the
+// logarithm is 0 and the zero is tracked apart).  The logarithm comes from the
+// logit itself where there is one: forming the gate first would lose the
+// distance of a gate from 1, which a memory of thousands of tokens multiplies.
+// A gate under the least float32, 2^-149, is a zero: the single-token step has
+// it so, and a running sum with a logit of -1e9 in it, or of the type's lowest
+// value, would lose the gates behind it.  So no logarithm here is under -150,
+// and a chunk's sum stays within 2^14.
 struct GateLog {
   float l2;
   bool neg, zero;
@@ -115,18 +118,16 @@ __device__ __forceinline__ GateLog gate_log(float x, int gate_input, bool ckda) 
   GateLog r;
   if (gate_input == CKDA_GATES_F32) {
     r.neg = x < 0.f;
-    r.zero = x == 0.f;
     r.l2 = log2_of(fabsf(x));
   } else if (!ckda) {  // sigmoid
     r.neg = false;
-    r.zero = x == -INFINITY;
     r.l2 = (x < 0.f ? x * kLog2e : 0.f) - log2_1p(exp_neg(fabsf(x)));
   } else {  // 2 sigmoid - 1 = tanh(x / 2)
     const float m = fabsf(x), e = exp_neg(m);
     r.neg = x < 0.f;
-    r.zero = x == 0.f;
     r.l2 = m < 0.5f ? log2_of(alpha_from_logit(m, true)) : log2_1p(-e) - log2_1p(e);
   }
+  r.zero = r.l2 < -149.5f;  // -inf of a gate of 0 too
   if (r.zero) r.l2 = 0.f;
   return r;
 }

@@ -377,7 +377,9 @@ ckda_status_t ckda_l2norm_debug(const void* x, float* y, int64_t rows,
  *     gate_range: KDA a = sigmoid, CKDA a = 2 sigmoid - 1).
  * Gates are taken as written: zeros restart the state exactly, negative gates
  * flip it, and a gate's distance from 1 is kept (the products of gates run
- * through logarithms formed from 1 - a, or from the logit itself).
+ * through logarithms formed from 1 - a, or from the logit itself).  A logit
+ * whose gate is under the least float32 (for KDA: -inf, the type's lowest value
+ * and all below about -104) is a gate of zero.
  * A non-finite value in a token's q, k, v or gate reaches the outputs of its
  * own block of 64 tokens (32 in float32 gradients) and of later tokens of its
  * sequence (earlier ones, for gradients); never another sequence.  Tokens

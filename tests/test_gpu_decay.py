@@ -227,3 +227,65 @@ def test_tiny_and_exact_gates(dtype, T):
     c["alpha"] = rng.choice(pool, c["alpha"].shape).astype(np.float32)
     check_fwd(c)
     check_bwd(c)
+
+
+SHUT = [-90.0, -120.0, -200.0, -2e7, -1e9, -1e30, "lowest", -np.inf]
+
+
+def shut(c, low, share=0.04):
+    """Some of the logits set to `low` ("lowest": the type's lowest value)."""
+    if low == "lowest":
+        low = torch.finfo(torch.bfloat16 if c["dtype"] == "bf16" else torch.float32).min
+    rng = np.random.default_rng(31)
+    a = c["alpha"]
+    a[rng.random(a.shape) < share] = low
+    if a.ndim > 1:
+        a[:, 10] = a[:, 11] = a[:, 75] = low
+    else:
+        a[0] = low
+    c["alpha"] = round_bf16(a) if c["dtype"] == "bf16" else a
+    return c
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("low", SHUT)
+@pytest.mark.parametrize("per_head", [False, True])
+def test_logits_that_shut_a_gate(dtype, low, per_head):
+    """Logits so low that the gate is zero in float32 restart the state, as a
+    gate of zero does: prefill and gradients, within the same bounds."""
+    c = shut(make(30, 2, 150, 4, 2, 64, 64, dtype, "logits", "kda", h0=True, per_head=per_head), low)
+    check_fwd(c)
+    check_bwd(c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("low", [-1e9, "lowest", -np.inf])
+def test_shut_gates_across_segments_and_in_steps(dtype, low):
+    """The same in a prompt that is cut into segments, and one token at a time."""
+    c = shut(make(32, 1, 1500, 1, 1, 32, 32, dtype, "logits", "kda", h0=True), low, 0.01)
+    check_fwd(c)
+    c = shut(make(33, 2, 80, 2, 2, 32, 32, dtype, "logits", "kda", h0=True), low)
+    g = on_gpu(c)
+    st = g["h0"].clone()
+    for t in range(80):
+        at = lambda z: z[:, t].contiguous()
+        ck.decay_step(at(g["q"]), at(g["k"]), at(g["v"]), at(g["alpha"]), st, gate="kda", gates="logits",
+                      scale=c["scale"])
+    ht = run_fwd(c)[1]
+    _, rh, _, hm = ref.fwd(c["q"], c["k"], c["v"], gates_of(c)[0], c["h0"], None, c["scale"])
+    # a step rounds a product and a sum, its gate (one power, one reciprocal) is off by three half steps
+    within("steps", st, rh, 5 * 80 * 2.0 ** -24 * hm + 1e-30)
+    within("prefill", ht, rh, ref.bound_state(dtype, hm, 32, 80))
+
+
+@pytest.mark.parametrize("T", [64, 150])
+def test_tiny_logits_of_signed_gates(T):
+    """Logits next to zero, where a signed gate is half of them, down to the
+    least float32, half of which rounds to a gate of zero."""
+    c = make(34, 2, T, 2, 2, 64, 64, "f32", "logits", "ckda", h0=True)
+    rng = np.random.default_rng(35)
+    pool = np.array([1e-45, -1e-45, 3e-45, -1e-40, 1e-38, -1e-30, 0, 4], np.float32)
+    put = rng.random(c["alpha"].shape) < 0.1
+    c["alpha"][put] = rng.choice(pool, int(put.sum()))
+    check_fwd(c)
+    check_bwd(c)
