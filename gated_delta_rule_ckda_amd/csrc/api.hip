@@ -741,7 +741,6 @@ ckda_status_t ckda_decay_bwd(const ckda_decay_desc_t* d, const void* q, const vo
   }
   const size_t need = ckda_decay_bwd_workspace_size(d, cu_seqlens ? 1 : 0);
   if ((st = check_workspace(ts, 12, workspace, workspace_bytes, need)) != CKDA_OK) return st;
-  if (d->num_seqs == 0) return ok();
   ckda::DecayArgs a = decay_args(d, cu_seqlens);
   a.q = q;
   a.k = k;

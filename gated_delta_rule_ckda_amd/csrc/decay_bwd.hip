@@ -397,12 +397,13 @@ __global__ __launch_bounds__(kNT, 2) void decay_grad_kernel(DecayArgs a, DecayGr
 
 // dalpha [H] from the tokens' gradients, in a fixed order: thread t of a
 // head's workgroup takes tokens t, t + 1024, ..., then a tree over threads.
+// Without sequences there is nothing to read: zeros.
 template <class IO>
 __global__ __launch_bounds__(1024) void decay_gate_sum_kernel(DecayArgs a, const float* per_token,
                                                              void* dalpha) {
   __shared__ float part[16];
   const int h = blockIdx.x, t = threadIdx.x;
-  const int64_t n = a.cu ? cu_at(a, a.N) : static_cast<int64_t>(a.B) * a.T;
+  const int64_t n = a.N == 0 ? 0 : a.cu ? cu_at(a, a.N) : static_cast<int64_t>(a.B) * a.T;
   float s = 0.f;
   for (int64_t i = t; i < n; i += 1024) s += per_token[i * a.H + h];
 #pragma unroll
@@ -427,6 +428,14 @@ launch_result launch_grad_t(const DecayArgs& a, const DecayGrads& g, hipStream_t
   const int64_t grid = items < most ? items : most;
   hipLaunchKernelGGL((decay_grad_kernel<Op, DP, C>), dim3(static_cast<unsigned>(grid)), dim3(kNT), lds, s,
                      a, g);
+  return hipGetLastError();
+}
+
+launch_result launch_gate_sum(const DecayArgs& a, const DecayGrads& g, int32_t io_dtype, hipStream_t s) {
+  if (io_dtype == CKDA_DTYPE_BF16)
+    hipLaunchKernelGGL(decay_gate_sum_kernel<io_bf16>, dim3(a.H), dim3(1024), 0, s, a, g.per_token, g.dalpha);
+  else
+    hipLaunchKernelGGL(decay_gate_sum_kernel<io_f32>, dim3(a.H), dim3(1024), 0, s, a, g.per_token, g.dalpha);
   return hipGetLastError();
 }
 
@@ -462,6 +471,8 @@ size_t decay_bwd_workspace(const DecayArgs& a, int32_t io_dtype) {
 
 launch_result launch_decay_bwd(const DecayArgs& a, DecayGrads g, int32_t io_dtype, void* ws,
                                hipStream_t s) {
+  if (a.N == 0)  // one gate a head still has its gradient, a sum over no tokens
+    return g.dalpha && a.per_head ? launch_gate_sum(a, g, io_dtype, s) : hipSuccess;
   DecayArgs f = a;
   lay_out(f, g, io_dtype, static_cast<unsigned char*>(ws));
   f.ht = nullptr;
@@ -481,11 +492,7 @@ launch_result launch_decay_bwd(const DecayArgs& a, DecayGrads g, int32_t io_dtyp
   else
     e = wide ? launch_grad_t<OpF32, 128, CF>(f, g, s) : launch_grad_t<OpF32, 64, CF>(f, g, s);
   if (e != hipSuccess || !g.dalpha || !a.per_head) return e;
-  if (io_dtype == CKDA_DTYPE_BF16)
-    hipLaunchKernelGGL(decay_gate_sum_kernel<io_bf16>, dim3(a.H), dim3(1024), 0, s, f, g.per_token, g.dalpha);
-  else
-    hipLaunchKernelGGL(decay_gate_sum_kernel<io_f32>, dim3(a.H), dim3(1024), 0, s, f, g.per_token, g.dalpha);
-  return hipGetLastError();
+  return launch_gate_sum(f, g, io_dtype, s);
 }
 
 }  // namespace ckda

@@ -424,7 +424,7 @@ ckda_status_t ckda_decay_fwd(const ckda_decay_desc_t* desc, const void* q, const
  * float32, rounded once at the end); dh0 in float32.  With logits dalpha is
  * the gradient of the logits; with alpha_per_head it is summed over all
  * tokens (in float32; what the tokens' terms cancel stays in proportion to
- * them, not to the sum).  dalpha and dh0 may be NULL (not wanted).  dq and dk of a q/k head
+ * them, not to the sum; zeros where num_seqs is 0).  dalpha and dh0 may be NULL (not wanted).  dq and dk of a q/k head
  * sum over the value heads that read it.  dalpha is formed without
  * subtracting (blocks with gates of zero or under 2^-30 also without dividing
  * by one), so every gate, zeros included, has the gradient of the recurrence.

@@ -289,3 +289,19 @@ def test_tiny_logits_of_signed_gates(T):
     c["alpha"][put] = rng.choice(pool, int(put.sum()))
     check_fwd(c)
     check_bwd(c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [0, 5])
+def test_no_sequences_leave_zero_gate_gradients(dtype, T):
+    """A packed batch of no sequences: the sum over no tokens is zero, whatever
+    its memory held before."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, v = torch.ones(1, T, 2, 16, device=DEV, dtype=dt), torch.ones(1, T, 4, 16, device=DEV, dtype=dt)
+    al, cu = torch.full((4,), 0.5, device=DEV), torch.zeros(1, device=DEV, dtype=torch.int32)
+    torch.cuda.synchronize()
+    dirty = [torch.full((4,), float("nan"), device=DEV, dtype=dt) for _ in range(64)]
+    del dirty
+    dal = ck.decay_bwd(q, q, v, al, v, cu_seqlens=cu)[3]
+    torch.cuda.synchronize()
+    assert dal.shape == (4,) and (dal == 0).all()
