@@ -2,8 +2,10 @@
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels behind the C ABI of ``include/ckda.h``.  Tensors are torch CUDA
-(HIP) tensors; calls are asynchronous on the current stream.  If the shared
-library is missing the calls raise -- there is no CPU fallback.
+(HIP) tensors; calls are asynchronous on the current stream, or on ``stream``:
+then the caller orders that stream behind what wrote the inputs, and waits for
+it before the results are read.  If the shared library is missing the calls
+raise -- there is no CPU fallback.
 """
 from __future__ import annotations
 
@@ -466,18 +468,48 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _launch(device, stream, fn, *args):
-    """fn(*args, stream) with the tensors' device current, on the caller's stream
-    or that device's current one."""
+def _launch(device, fn, *args):
+    """fn(*args, stream) with the tensors' device current, on that device's
+    current stream."""
     import torch
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device != device:
-        raise ValueError("the stream belongs to %s, the tensors to %s" % (s.device, device))
+    stream = torch.cuda.current_stream(device).cuda_stream
     if torch.cuda.current_device() == device.index:
-        _check(fn(*args, s.cuda_stream))
+        _check(fn(*args, stream))
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, s.cuda_stream))
+            _check(fn(*args, stream))
+
+
+def _on_stream(call):
+    """`stream` of a call that works on the current stream: the call runs with it
+    current, so what it allocates belongs to it, a workspace that is dropped on
+    return among that.  Tensors that come from or go back to the caller's own
+    stream are recorded on the other one, so that their memory is not given out
+    again while either still uses it."""
+    @functools.wraps(call)
+    def on_stream(*args, stream=None, **named):
+        if stream is None:
+            return call(*args, **named)
+        import torch
+        given = [t for t in args + tuple(named.values()) if isinstance(t, torch.Tensor)]
+        for t in given:
+            if t.device != stream.device:
+                raise ValueError("the stream belongs to %s, the tensors to %s"
+                                 % (stream.device, t.device))
+        caller = torch.cuda.current_stream(stream.device)
+        if stream == caller:
+            return call(*args, **named)
+        try:
+            with torch.cuda.stream(stream):
+                got = call(*args, **named)
+        finally:
+            for t in given:
+                t.record_stream(stream)
+        for t in got if isinstance(got, tuple) else (got,):
+            if t is not None:
+                t.record_stream(caller)
+        return got
+    return on_stream
 
 
 def _state_ok(name, t, shape):
@@ -485,27 +517,6 @@ def _state_ok(name, t, shape):
     if t is not None:
         _require(t.dtype == torch.float32 and tuple(t.shape) == shape,
                  "%s must be float32 of shape %s" % (name, list(shape)))
-
-
-class _on:
-    """The tensors' device made current for a call, and the stream it goes to:
-    the caller's, or that device's current one."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.guard = torch.cuda.device(device)
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        import torch
-        self.guard.__enter__()
-        s = torch.cuda.current_stream(self.device) if self.stream is None else self.stream
-        _require(s.device == self.device, "the stream belongs to %s, the tensors to %s"
-                 % (s.device, self.device))
-        return ctypes.c_void_p(s.cuda_stream)
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
 
 
 @functools.lru_cache(maxsize=256)
@@ -568,6 +579,7 @@ def decay_bwd_workspace_size(desc: DecayDesc, packed: bool) -> int:
     return int(_load().ckda_decay_bwd_workspace_size(ctypes.byref(desc), int(bool(packed))))
 
 
+@_on_stream
 def decay_fwd(q, k, v, alpha, *, h0=None, cu_seqlens=None, gate="ckda", gates="values", scale=1.0,
               output_final_state=True, out=None, final_state=None, workspace=None, stream=None):
     """Linear attention with one decay a head, S_t = a_t S_{t-1} + k_t v_t^T and
@@ -593,12 +605,13 @@ def decay_fwd(q, k, v, alpha, *, h0=None, cu_seqlens=None, gate="ckda", gates="v
     if output_final_state and ht is None:
         ht = torch.empty(shape, device=dev, dtype=torch.float32)
     ws = _workspace(workspace, need_fwd, dev) if need_fwd else None
-    _launch(dev, stream, lib.ckda_decay_fwd, ctypes.byref(desc), _addr(q), _addr(k), _addr(v),
+    _launch(dev, lib.ckda_decay_fwd, ctypes.byref(desc), _addr(q), _addr(k), _addr(v),
             _addr(alpha), _addr(cu_seqlens), _addr(h0), _addr(o), _addr(ht), _addr(ws),
             0 if ws is None else ws.numel())
     return o, ht
 
 
+@_on_stream
 def decay_bwd(q, k, v, alpha, dout, *, h0=None, dht=None, cu_seqlens=None, gate="ckda",
               gates="values", scale=1.0, output_dalpha=True, output_dh0=True, workspace=None,
               stream=None):
@@ -620,12 +633,13 @@ def decay_bwd(q, k, v, alpha, dout, *, h0=None, dht=None, cu_seqlens=None, gate=
     dal = torch.empty(alpha.shape, device=dev, dtype=q.dtype) if output_dalpha else None
     dh0 = torch.empty(shape, device=dev, dtype=torch.float32) if output_dh0 else None
     ws = _workspace(workspace, need_bwd, dev)
-    _launch(dev, stream, lib.ckda_decay_bwd, ctypes.byref(desc), _addr(q), _addr(k), _addr(v),
+    _launch(dev, lib.ckda_decay_bwd, ctypes.byref(desc), _addr(q), _addr(k), _addr(v),
             _addr(alpha), _addr(cu_seqlens), _addr(h0), _addr(dout), _addr(dht), _addr(dq),
             _addr(dkk), _addr(dvv), _addr(dal), _addr(dh0), _addr(ws), ws.numel())
     return dq, dkk, dvv, dal, dh0
 
 
+@_on_stream
 def decay_step(q, k, v, alpha, state, *, gate="ckda", gates="values", scale=1.0, out=None,
                new_state=None, stream=None):
     """One token a sequence of decay_fwd's recurrence: q, k [N,Hk,dk], v
@@ -648,7 +662,7 @@ def decay_step(q, k, v, alpha, state, *, gate="ckda", gates="values", scale=1.0,
         _require(out.dtype == v.dtype and out.shape == v.shape, "out must match v")
     o = torch.empty_like(v) if out is None else out
     dst = state if new_state is None else new_state
-    _launch(dev, stream, lib.ckda_decay_step, N, H, Hk, dk, dv, _dtype_code(q), _gate_code(gate),
+    _launch(dev, lib.ckda_decay_step, N, H, Hk, dk, dv, _dtype_code(q), _gate_code(gate),
             _gate_input(gates, alpha, alpha), int(per_head), float(scale), _addr(q), _addr(k),
             _addr(v), _addr(alpha), _addr(state), _addr(dst), _addr(o))
     return o
@@ -676,6 +690,7 @@ def _norm_args(y, weight, gate, act, residual, scale, next_weight, **more):
     return y.numel() // d, d, 0 if gate is None else _ACTS[act]
 
 
+@_on_stream
 def block_norm(y, weight, *, gate=None, act="sigmoid", residual=None, scale=None,
                next_weight=None, eps=1e-6, out=None, next_out=None, stream=None):
     """The norm after a block, its output gate, the residual stream and the norm
@@ -698,12 +713,13 @@ def block_norm(y, weight, *, gate=None, act="sigmoid", residual=None, scale=None
     n = next_out
     if next_weight is not None and n is None:
         n = torch.empty_like(y)
-    _launch(y.device, stream, lib.ckda_block_norm, rows, d, io, code, float(eps), _addr(y),
+    _launch(y.device, lib.ckda_block_norm, rows, d, io, code, float(eps), _addr(y),
             _addr(weight), _addr(gate), _addr(residual), _addr(scale), _addr(next_weight), _addr(h),
             _addr(n))
     return h, n
 
 
+@_on_stream
 def block_norm_bwd(y, weight, dh, *, dnext=None, gate=None, act="sigmoid", residual=None,
                    scale=None, next_weight=None, eps=1e-6, workspace=None, stream=None):
     """Gradients of block_norm for dL/dh = dh and dL/dn = dnext (given exactly
@@ -727,7 +743,7 @@ def block_norm_bwd(y, weight, dh, *, dnext=None, gate=None, act="sigmoid", resid
     dx = dh if residual is not None and next_weight is None else new(residual)
     need = int(lib.ckda_block_norm_bwd_workspace_size(rows, d, io))
     ws = _workspace(workspace, need, y.device)
-    _launch(y.device, stream, lib.ckda_block_norm_bwd, rows, d, io, code, float(eps), _addr(y),
+    _launch(y.device, lib.ckda_block_norm_bwd, rows, d, io, code, float(eps), _addr(y),
             _addr(weight), _addr(gate), _addr(residual), _addr(scale), _addr(next_weight),
             _addr(dh), _addr(dnext), _addr(dy), _addr(dw), _addr(dg),
             None if dx is dh else _addr(dx), _addr(ds), _addr(dw2), _addr(ws), ws.numel())

@@ -273,3 +273,30 @@ def test_many_tokens_at_the_far_end():
     # the short batch is cut into segments, the long one is not
     assert ((o[-1:].float() - o1.float()).abs().max() / o1.abs().max().float()).item() < 2 ** -6
     assert ((ht[-1:] - h1).abs().max() / h1.abs().max()).item() < 1e-5
+
+
+def test_calls_on_given_streams_keep_their_workspaces():
+    """Calls sent to two streams from one current stream, which goes on
+    allocating and writing: each call's workspace is its own until it ends."""
+    cs = [case(s, T=2000, B=1, H=8, Hk=4, dk=128, dv=128) for s in (11, 12)]
+    x = [torch.randn(4000, 512, device=DEV) for _ in cs]
+    w = torch.rand(512, device=DEV) + 0.5
+
+    def work(c, x, **on):
+        o = ck.decay_fwd(c["q"], c["k"], c["v"], c["alpha"], h0=c["h0"], **on)
+        g = ck.decay_bwd(c["q"], c["k"], c["v"], c["alpha"], c["dout"], h0=c["h0"], dht=c["dht"], **on)
+        n = ck.block_norm_bwd(x, w, x, dnext=x, residual=x, next_weight=w, **on)
+        return o + g + tuple(t for t in n if t is not None)
+
+    want = [work(c, y) for c, y in zip(cs, x)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(3):
+        got = []
+        for c, y, s in zip(cs, x, streams):
+            got.append(work(c, y, stream=s))
+            junk = [torch.full((n,), float("nan"), device=DEV) for n in (1 << 10, 1 << 18, 1 << 20, 1 << 23)]
+            del junk
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))

@@ -223,3 +223,105 @@ def test_norm_reference_against_differences(act):
             down[name][i] -= 1e-5
             want = (loss(up) - loss(down)) / 2e-5
             assert abs(got["d" + name][i] - want) < 1e-7 * max(1, abs(want)), (name, i)
+
+
+class FakeStream:
+    """A stream to be current, without a GPU."""
+    device = torch.device("cpu")
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """Two streams, the first current; what is allocated, with the stream that was
+    current then; what is recorded; the streams that the library was given."""
+    caller, other = FakeStream(1), FakeStream(2)
+    log = dict(caller=caller, other=other, now=caller, made=[], recorded=[], launched=[])
+
+    class current:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            self.before, log["now"] = log["now"], self.s
+
+        def __exit__(self, *exc):
+            log["now"] = self.before
+
+    class Lib:  # the sizes from the library; calls are noted, nothing is launched
+        def __getattr__(self, name):
+            real = getattr(lib, name)
+            if name.endswith("_size") or name.endswith("_supported"):
+                return real
+            return lambda *args: log["launched"].append((name, args[-1])) or 0
+
+    def noting(make):
+        def made(*args, **kw):
+            t = make(*args, **kw)
+            log["made"].append((t.data_ptr(), log["now"]))
+            return t
+        return made
+
+    lib, fake = ck._load(), Lib()
+    monkeypatch.setattr(ck, "_load", lambda: fake)
+    monkeypatch.setattr(ck, "_tensors", lambda *a, **kw: None)
+    monkeypatch.setattr(torch.cuda, "stream", current)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: log["now"])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, s: log["recorded"].append((t.data_ptr(), s)))
+    for name in ("empty", "empty_like"):
+        monkeypatch.setattr(torch, name, noting(getattr(torch, name)))
+    return log
+
+
+def _calls():
+    r = lambda *s: torch.ones(s)
+    q, v, al, st = r(1, 1400, 2, 16), r(1, 1400, 4, 16), r(1, 1400, 4), r(3, 4, 16, 16)
+    y, w = r(6, 32), r(32)
+    return {"decay_fwd": (ck.decay_fwd, (q, q, v, al), {}),
+            "decay_bwd": (ck.decay_bwd, (q, q, v, al, v), {}),
+            "decay_step": (ck.decay_step, (r(3, 2, 16), r(3, 2, 16), r(3, 4, 16), r(3, 4), st), {}),
+            "block_norm": (ck.block_norm, (y, w), dict(residual=y, next_weight=w)),
+            "block_norm_bwd": (ck.block_norm_bwd, (y, w, y), dict(residual=y, dnext=y, next_weight=w))}
+
+
+@pytest.mark.parametrize("name", ["decay_fwd", "decay_bwd", "decay_step", "block_norm", "block_norm_bwd"])
+def test_a_given_stream_owns_what_the_call_allocates(streams, name):
+    """The allocator hands a dropped workspace to the stream that it was allocated
+    on: that has to be the stream that uses it."""
+    fn, args, kw = _calls()[name]
+    got = fn(*args, stream=streams["other"], **kw)
+    assert [s for _, s in streams["launched"]] == [2] and streams["now"] is streams["caller"]
+    assert streams["made"] and all(s is streams["other"] for _, s in streams["made"])
+    for t in list(args) + [t for t in kw.values()]:
+        assert (t.data_ptr(), streams["other"]) in streams["recorded"]
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None:
+            assert (t.data_ptr(), streams["caller"]) in streams["recorded"]
+
+
+@pytest.mark.parametrize("name", ["decay_fwd", "decay_bwd", "decay_step", "block_norm", "block_norm_bwd"])
+def test_no_stream_or_the_current_one(streams, name):
+    fn, args, kw = _calls()[name]
+    fn(*args, **kw)
+    fn(*args, stream=streams["caller"], **kw)
+    assert [s for _, s in streams["launched"]] == [1, 1] and not streams["recorded"]
+
+
+def test_no_rows_are_zeroed_on_the_given_stream(streams, monkeypatch):
+    on = []
+    monkeypatch.setattr(torch.Tensor, "zero_", lambda t: on.append(streams["now"]) or t)
+    e, w = torch.ones(0, 32), torch.ones(32)
+    ck.block_norm_bwd(e, w, e, dnext=e, next_weight=w, stream=streams["other"])
+    assert on and all(s is streams["other"] for s in on)
+
+
+def test_a_stream_of_another_device_is_refused(streams):
+    streams["other"].device = torch.device("meta")
+    for fn, args, kw in _calls().values():
+        with pytest.raises(ValueError, match="stream belongs to"):
+            fn(*args, stream=streams["other"], **kw)
+    assert not streams["launched"] and not streams["made"]
