@@ -9,6 +9,7 @@ raise -- there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -152,10 +153,45 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream(stream=None):
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _record(tensors, stream):
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
+def _on_stream(call):
+    """`stream` of a call that works on the current stream: the call runs with it
+    current, so what it allocates belongs to it, a workspace that is dropped on
+    return among that.  Tensors that come from or go back to the caller's own
+    stream are recorded on the other one, so that their memory is not given out
+    again while either still uses it."""
+    @functools.wraps(call)
+    def on_stream(*args, stream=None, **named):
+        if stream is None:
+            return call(*args, **named)
+        import torch
+        given = [t for t in args + tuple(named.values()) if isinstance(t, torch.Tensor)]
+        for t in given:
+            if t.device != stream.device:
+                raise ValueError("the stream belongs to %s, the tensors to %s"
+                                 % (stream.device, t.device))
+        caller = torch.cuda.current_stream(stream.device)
+        if stream == caller:
+            return call(*args, **named)
+        try:
+            with torch.cuda.stream(stream):
+                got = call(*args, **named)
+        finally:
+            _record(given, stream)
+        _record(got if isinstance(got, tuple) else (got,), caller)
+        return got
+    return on_stream
 
 
 def _gate_code(gate):
@@ -242,6 +278,7 @@ def _fwd_call(q, k, v, alpha, beta, h0, cu_seqlens, chunk_size, use_qk_l2norm, g
     return desc, o, ht
 
 
+@_on_stream
 def chunk_fwd(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_size=64,
               use_qk_l2norm=True, gate="ckda", scale=1.0, output_final_state=True,
               out=None, final_state=None, workspace=None, stream=None, gates="values",
@@ -268,10 +305,11 @@ def chunk_fwd(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_size=64,
              "workspace must be a uint8 device tensor of at least %d bytes" % need)
     _check(lib.ckda_chunk_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha),
                               _ptr(beta), _ptr(cu_seqlens), _ptr(h0), _ptr(o), _ptr(ht),
-                              _ptr(workspace), workspace.numel(), _stream(stream)))
+                              _ptr(workspace), workspace.numel(), _stream()))
     return o, ht
 
 
+@_on_stream
 def chunk_fwd_noalloc(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_size=64,
                       use_qk_l2norm=True, gate="ckda", scale=1.0, output_final_state=True,
                       out=None, final_state=None, stream=None, gates="values",
@@ -285,10 +323,11 @@ def chunk_fwd_noalloc(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_s
                             scale, output_final_state, out, final_state, gates, sign_absorb)
     _check(lib.ckda_chunk_fwd_noalloc(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha),
                                       _ptr(beta), _ptr(cu_seqlens), _ptr(h0), _ptr(o), _ptr(ht),
-                                      _stream(stream)))
+                                      _stream()))
     return o, ht
 
 
+@_on_stream
 def chunk_fwd_save(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_size=64,
                    use_qk_l2norm=True, gate="ckda", scale=1.0, output_final_state=True,
                    out=None, final_state=None, saved=None, stream=None, gates="values"):
@@ -307,7 +346,7 @@ def chunk_fwd_save(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_size
              "saved must be a uint8 device tensor of at least %d bytes" % need)
     _check(lib.ckda_chunk_fwd_save(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha),
                                    _ptr(beta), _ptr(cu_seqlens), _ptr(h0), _ptr(o), _ptr(ht),
-                                   _ptr(saved), saved.numel(), _stream(stream)))
+                                   _ptr(saved), saved.numel(), _stream()))
     return o, ht, saved
 
 
@@ -316,6 +355,7 @@ def chunk_bwd_workspace_size(desc: FwdDesc, packed: bool) -> int:
     return int(_load().ckda_chunk_bwd_workspace_size(ctypes.byref(desc), int(bool(packed))))
 
 
+@_on_stream
 def chunk_bwd(q, k, v, alpha, beta, dout, *, h0=None, dht=None, cu_seqlens=None, chunk_size=64,
               use_qk_l2norm=True, gate="ckda", scale=1.0, output_dh0=True, workspace=None,
               stream=None, gates="values", saved=None):
@@ -373,7 +413,7 @@ def chunk_bwd(q, k, v, alpha, beta, dout, *, h0=None, dht=None, cu_seqlens=None,
     _check(fn(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta),
               _ptr(cu_seqlens), _ptr(h0), _ptr(dout), _ptr(dht), _ptr(dq), _ptr(dkk), _ptr(dvv),
               _ptr(dal), _ptr(dbe), _ptr(dh0), _ptr(workspace), workspace.numel(),
-              _stream(stream)))
+              _stream()))
     return dq, dkk, dvv, dal, dbe, dh0
 
 
@@ -391,12 +431,16 @@ class ChunkFwdPlan:
         self.desc = _make_desc(q, v, H, dk, dv, chunk_size, gate, use_qk_l2norm, scale,
                                cu_seqlens, _gate_input(gates, alpha, beta), sign_absorb)
         self.args = (q, k, v, alpha, beta, h0, cu_seqlens)
-        self.o = torch.empty_like(v) if out is None else out
-        self.ht = (torch.empty((self.desc.num_seqs, H, dk, dv), device=q.device,
-                               dtype=torch.float32) if final_state is None else final_state)
-        need = chunk_fwd_workspace_size(self.desc, cu_seqlens is not None)
-        self.ws = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
         self.stream = stream
+        need = chunk_fwd_workspace_size(self.desc, cu_seqlens is not None)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            self.o = torch.empty_like(v) if out is None else out
+            self.ht = (torch.empty((self.desc.num_seqs, H, dk, dv), device=q.device,
+                                   dtype=torch.float32) if final_state is None else final_state)
+            self.ws = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+        if stream is not None and stream != torch.cuda.current_stream(stream.device):
+            _record(self.args + (out, final_state), stream)
+            _record((self.o, self.ht), torch.cuda.current_stream(stream.device))
 
     def prepare(self):
         q, k, v, alpha, beta, h0, cu = self.args
@@ -413,6 +457,7 @@ class ChunkFwdPlan:
         return self.o, self.ht
 
 
+@_on_stream
 def recurrent_step(q, k, v, alpha, beta, state, *, use_qk_l2norm=True, gate="ckda",
                    scale=1.0, out=None, new_state=None, stream=None, gates="values"):
     """One decode token per sequence: q,k [N,Hk,dk], alpha [N,H,dk], v [N,H,dv],
@@ -435,7 +480,7 @@ def recurrent_step(q, k, v, alpha, beta, state, *, use_qk_l2norm=True, gate="ckd
     _check(lib.ckda_recurrent_step(N, H, Hk, dk, dv, _dtype_code(q), _gate_code(gate), gi,
                                    int(bool(use_qk_l2norm)), float(scale), _ptr(q), _ptr(k),
                                    _ptr(v), _ptr(alpha), _ptr(beta), _ptr(state), _ptr(dst),
-                                   _ptr(o), _stream(stream)))
+                                   _ptr(o), _stream()))
     return o
 
 
@@ -478,38 +523,6 @@ def _launch(device, fn, *args):
     else:
         with torch.cuda.device(device):
             _check(fn(*args, stream))
-
-
-def _on_stream(call):
-    """`stream` of a call that works on the current stream: the call runs with it
-    current, so what it allocates belongs to it, a workspace that is dropped on
-    return among that.  Tensors that come from or go back to the caller's own
-    stream are recorded on the other one, so that their memory is not given out
-    again while either still uses it."""
-    @functools.wraps(call)
-    def on_stream(*args, stream=None, **named):
-        if stream is None:
-            return call(*args, **named)
-        import torch
-        given = [t for t in args + tuple(named.values()) if isinstance(t, torch.Tensor)]
-        for t in given:
-            if t.device != stream.device:
-                raise ValueError("the stream belongs to %s, the tensors to %s"
-                                 % (stream.device, t.device))
-        caller = torch.cuda.current_stream(stream.device)
-        if stream == caller:
-            return call(*args, **named)
-        try:
-            with torch.cuda.stream(stream):
-                got = call(*args, **named)
-        finally:
-            for t in given:
-                t.record_stream(stream)
-        for t in got if isinstance(got, tuple) else (got,):
-            if t is not None:
-                t.record_stream(caller)
-        return got
-    return on_stream
 
 
 def _state_ok(name, t, shape):

@@ -300,3 +300,34 @@ def test_calls_on_given_streams_keep_their_workspaces():
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_delta_rule_calls_on_given_streams_keep_their_workspaces():
+    """The same of the delta rule's calls."""
+    g = torch.Generator(device=DEV).manual_seed(13)
+    r = lambda *s: torch.randn(s, device=DEV, generator=g)
+
+    def inputs():
+        q, k, v, do = (r(1, 2000, 8, 64).to(torch.bfloat16) for _ in range(4))
+        return q, k, v, torch.sigmoid(r(1, 2000, 8, 64) + 4), torch.sigmoid(r(1, 2000, 8)), do
+
+    def work(c, **on):
+        kw = dict(gate="kda", scale=0.125, **on)
+        o = ck.chunk_fwd(*c[:5], **kw)
+        plan = ck.ChunkFwdPlan(*c[:5], **kw)
+        plan.prepare()
+        return o + plan.finish() + ck.chunk_bwd(*c, **kw)
+
+    cs = [inputs() for _ in range(2)]
+    want = [work(c) for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(3):
+        got = []
+        for c, s in zip(cs, streams):
+            got.append(work(c, stream=s))
+            junk = [torch.full((n,), float("nan"), device=DEV) for n in (1 << 10, 1 << 18, 1 << 20, 1 << 23)]
+            del junk
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))

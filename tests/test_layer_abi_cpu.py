@@ -325,3 +325,38 @@ def test_a_stream_of_another_device_is_refused(streams):
         with pytest.raises(ValueError, match="stream belongs to"):
             fn(*args, stream=streams["other"], **kw)
     assert not streams["launched"] and not streams["made"]
+
+
+class Delta:
+    """The delta rule's calls on ones (the device checks see a GPU's tensors)."""
+
+    def __init__(self):
+        r = lambda *s: torch.ones(s)
+        q, v, a, b = r(1, 128, 2, 64), r(1, 128, 2, 64), r(1, 128, 2, 64), r(1, 128, 2)
+        one = [t[0, :3].contiguous() for t in (q, q, v, a, b)]
+        self.calls = {"chunk_fwd": (ck.chunk_fwd, (q, q, v, a, b)), "chunk_fwd_save": (ck.chunk_fwd_save, (q, q, v, a, b)),
+                      "chunk_fwd_noalloc": (ck.chunk_fwd_noalloc, (q, q, v, a, b)),
+                      "chunk_bwd": (ck.chunk_bwd, (q, q, v, a, b, v)),
+                      "recurrent_step": (ck.recurrent_step, (*one, r(3, 2, 64, 64)))}
+        self.inputs = (q, q, v, a, b)
+
+
+@pytest.mark.parametrize("name", ["chunk_fwd", "chunk_fwd_save", "chunk_fwd_noalloc", "chunk_bwd", "recurrent_step", "plan"])
+def test_a_given_stream_owns_what_the_delta_rule_calls_allocate(streams, monkeypatch, name):
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    d = Delta()
+    if name == "plan":
+        plan = ck.ChunkFwdPlan(*d.inputs, stream=streams["other"])
+        plan.prepare()
+        args, got = d.inputs, plan.finish()
+    else:
+        fn, args = d.calls[name]
+        got = fn(*args, stream=streams["other"])
+    handles = [s.value if isinstance(s, ctypes.c_void_p) else s for _, s in streams["launched"]]
+    assert set(handles) == {2} and streams["now"] is streams["caller"]
+    assert streams["made"] and all(s is streams["other"] for _, s in streams["made"])
+    for t in args:
+        assert (t.data_ptr(), streams["other"]) in streams["recorded"]
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None:
+            assert (t.data_ptr(), streams["caller"]) in streams["recorded"]
