@@ -238,7 +238,8 @@ __global__ __launch_bounds__(NT, (EPL == 8 ? 3 : 1)) void norm_bwd_kernel(NormAr
 #pragma unroll
         for (int e = 0; e < VEC; ++e) ss[0] += X::get(vy[k], e) * X::get(vy[k], e);
       row_sum<1, NT>(ss, tpr, red, half);
-      r1 = 1.f / sqrtf(ss[0] * inv_d + a.eps);
+      // with eps = 0 a thread without a row would add inf * 0 to its sums over rows
+      r1 = live ? 1.f / sqrtf(ss[0] * inv_d + a.eps) : 0.f;
     }
     float D[EPL], act[EPL], dact[EPL];
 #pragma unroll
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(NT, (EPL == 8 ? 3 : 1)) void norm_bwd_kernel(NormAr
           ss[1] += X::get(vn[k], e) * w2[j] * h[j];
         }
       row_sum<2, NT>(ss, tpr, red, half);
-      const float r2 = 1.f / sqrtf(ss[0] * inv_d + a.eps), m = ss[1] * r2 * inv_d;
+      const float r2 = live ? 1.f / sqrtf(ss[0] * inv_d + a.eps) : 0.f, m = ss[1] * r2 * inv_d;
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll

@@ -120,3 +120,26 @@ def test_rows_of_zeros_and_no_rows():
     assert ck.block_norm(e, w, next_weight=w)[1].shape == (0, 64)
     r = ck.block_norm_bwd(e, w, e, dnext=e, next_weight=w)
     assert r[0].shape == (0, 64) and (r[1] == 0).all() and (r[5] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,d", [(5, 64), (37, 128), (3, 24), (70, 1001)])
+@pytest.mark.parametrize("parts", ["wgxsn", "w", "xn", "wn"])
+def test_no_eps_and_rows_that_leave_threads_idle(dtype, rows, d, parts):
+    """eps = 0 with rows that do not fill a workgroup: the sums over rows hold
+    the rows there are, and nothing of the idle threads."""
+    c = make(rows, rows, d, dtype, parts)
+    g = on_gpu(c, dtype)
+    kw = dict(gate=g["g"], act="silu", residual=g["x"], scale=g["s"], next_weight=g["w2"], eps=0.0)
+    h, n = ck.block_norm(g["y"], g["w"], **kw)
+    grads = ck.block_norm_bwd(g["y"], g["w"], g["dh"], dnext=g["dn"], **kw)
+    torch.cuda.synchronize()
+    (rh, rn), (hm, nm) = ref.fwd(c["y"], c["w"], c["g"], "silu", c["x"], c["s"], c["w2"], 0.0)
+    within("h", h, rh, hm, HALF[dtype], DEPTH)
+    if n is not None:
+        within("n", n, rn, nm, HALF[dtype], DEPTH)
+    want, mag = ref.bwd(c["y"], c["w"], c["dh"], c["dn"], c["g"], "silu", c["x"], c["s"], c["w2"], 0.0)
+    for name, got in zip(("dy", "dw", "dg", "dx", "ds", "dw2"), grads):
+        if got is not None:
+            vec = name in ("dw", "ds", "dw2")
+            within(name, got, want[name], mag[name], HALF["f32" if vec else dtype], 2 * DEPTH + (rows if vec else 0))
