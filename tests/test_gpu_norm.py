@@ -143,3 +143,28 @@ def test_no_eps_and_rows_that_leave_threads_idle(dtype, rows, d, parts):
         if got is not None:
             vec = name in ("dw", "ds", "dw2")
             within(name, got, want[name], mag[name], HALF["f32" if vec else dtype], 2 * DEPTH + (rows if vec else 0))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_gradients_of_saturated_gates(dtype, act):
+    """Gates far from zero keep the digits of their gradients: dg = dh u act'(g)
+    is a product, so it is off by half a step of its type and DEPTH float32 half
+    steps of the value: u's (as in `h`), a power e = exp(-|g|) (|g| half steps of
+    it, 20 here, where it runs on powers of two), and a few operations on
+    e / (1 + e)^2, which subtracts nothing.  silu' = p + g e / (1 + e)^2 is off by
+    that of the sum of its terms' magnitudes."""
+    c = make(17, 40, 128, dtype, "wg")
+    rng = np.random.default_rng(18)
+    far = rng.uniform(8, 20, c["g"].shape) * rng.choice([-1, 1], c["g"].shape)
+    c["g"] = round_bf16(far.astype(np.float32)) if dtype == "bf16" else far.astype(np.float32)
+    g = on_gpu(c, dtype)
+    got = ck.block_norm_bwd(g["y"], g["w"], g["dh"], gate=g["g"], act=act, eps=EPS)[2]
+    torch.cuda.synchronize()
+    u = ref.parts(c["y"], c["w"], c["g"], act, None, None, EPS)[2]
+    e = np.exp(-np.abs(ref.f64(c["g"])))
+    p, q = np.where(c["g"] >= 0, 1, e) / (1 + e), e / (1 + e) ** 2
+    to = ref.f64(c["dh"]) * u
+    want = to * (q if act == "sigmoid" else p + ref.f64(c["g"]) * q)
+    mag = np.abs(to) * (q if act == "sigmoid" else p + np.abs(ref.f64(c["g"])) * q)
+    announce("dg at %.2g of its bound" % within("dg", got, want, mag, HALF[dtype], 2 * DEPTH))
