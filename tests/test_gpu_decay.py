@@ -305,3 +305,20 @@ def test_no_sequences_leave_zero_gate_gradients(dtype, T):
     dal = ck.decay_bwd(q, q, v, al, v, cu_seqlens=cu)[3]
     torch.cuda.synchronize()
     assert dal.shape == (4,) and (dal == 0).all()
+
+
+CUT = [(1500, None), (1600, [700, 0, 3, 897])]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,lens", CUT)
+@pytest.mark.parametrize("dk,dv", [(128, 128), (72, 104)])
+def test_segments_of_wide_heads(dtype, T, lens, dk, dv):
+    """Long sequences of heads over 64 x 64, whose segment sums hold all columns
+    of the state in one workgroup: forward and gradients."""
+    c = make(40 + dk, 1, T, 2, 1, dk, dv, dtype, lens=lens, h0=True)
+    desc = ck.DecayDesc(1, T, 2, dk, dv, 1 if lens is None else len(lens),
+                        ck.F32 if dtype == "f32" else ck.BF16, 1, 0, 1, 0, 1.0)
+    assert ck.decay_fwd_workspace_size(desc, lens is not None) > 0
+    check_fwd(c)
+    check_bwd(c)
