@@ -604,7 +604,7 @@ ckda::DecayArgs decay_args(const ckda_decay_desc_t* d, const int32_t* cu) {
   return a;
 }
 
-ckda_status_t validate_decay(const ckda_decay_desc_t* d, const int32_t* cu) {
+ckda_status_t validate_decay(const ckda_decay_desc_t* d, const int32_t* cu, ckda::DecayCall call) {
   if (!d) return fail(CKDA_ERR_INVALID_ARGUMENT, "desc is NULL");
   if (d->B <= 0 || d->T < 0 || d->H <= 0 || d->dk <= 0 || d->dv <= 0 || d->num_seqs < 0)
     return fail(CKDA_ERR_INVALID_ARGUMENT,
@@ -637,7 +637,8 @@ ckda_status_t validate_decay(const ckda_decay_desc_t* d, const int32_t* cu) {
     return fail(CKDA_ERR_UNSUPPORTED, "H * max(dk, dv) of 2^22 or more");
   // walks look two chunks past the end
   if (static_cast<int64_t>(d->B) * d->T >= (int64_t(1) << 31) - 1024 ||
-      ckda::decay_grid(decay_args(d, cu), d->io_dtype) >= (int64_t(1) << 31))
+      ckda::decay_grid(decay_args(d, cu), d->io_dtype) >= (int64_t(1) << 31) ||
+      ckda::decay_threads(decay_args(d, cu), d->io_dtype, call) >= (int64_t(1) << 32))
     return fail(CKDA_ERR_UNSUPPORTED, "too many (sequence, head) chunks for one launch");
   return ok();
 }
@@ -678,7 +679,7 @@ size_t ckda_decay_bwd_workspace_size(const ckda_decay_desc_t* d, int32_t packed)
 ckda_status_t ckda_decay_fwd(const ckda_decay_desc_t* d, const void* q, const void* k, const void* v,
                              const void* alpha, const int32_t* cu_seqlens, const float* h0, void* o,
                              float* ht, void* workspace, size_t workspace_bytes, void* stream) {
-  ckda_status_t st = validate_decay(d, cu_seqlens);
+  ckda_status_t st = validate_decay(d, cu_seqlens, ckda::kDecayFwd);
   if (st != CKDA_OK) return st;
   const DecaySizes z = decay_sizes(d);
   const bool some = z.tokens > 0;
@@ -715,7 +716,7 @@ ckda_status_t ckda_decay_bwd(const ckda_decay_desc_t* d, const void* q, const vo
                              const void* dout, const float* dht, void* dq, void* dk, void* dv,
                              void* dalpha, float* dh0, void* workspace, size_t workspace_bytes,
                              void* stream) {
-  ckda_status_t st = validate_decay(d, cu_seqlens);
+  ckda_status_t st = validate_decay(d, cu_seqlens, ckda::kDecayBwd);
   if (st != CKDA_OK) return st;
   const DecaySizes z = decay_sizes(d);
   const bool some = z.tokens > 0;
@@ -761,7 +762,7 @@ ckda_status_t ckda_decay_step(int32_t N, int32_t H, int32_t qk_heads, int32_t dk
   // one token a sequence is a dense batch of N sequences of one token
   const ckda_decay_desc_t d{N > 0 ? N : 1, 1, H, dk, dv, N > 0 ? N : 1, io_dtype, gate_range,
                             gate_input, qk_heads, alpha_per_head, scale};
-  ckda_status_t st = validate_decay(&d, nullptr);
+  ckda_status_t st = validate_decay(&d, nullptr, ckda::kDecayStep);
   if (st != CKDA_OK) return st;
   const int64_t nh = static_cast<int64_t>(N) * H;
   if (nh > (int64_t(1) << 21))

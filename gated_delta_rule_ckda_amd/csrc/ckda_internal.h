@@ -218,6 +218,10 @@ bool decay_supported(int32_t dk, int32_t dv);
 size_t decay_segment_bytes(const DecayArgs& a);
 // Workgroups of the largest launch these sizes need (forward or backward).
 int64_t decay_grid(const DecayArgs& a, int32_t io_dtype);
+// Threads of a call's largest launch.  A launch counts them in 32 bits, and one
+// of a few more than 2^32 has been taken without an error.
+enum DecayCall { kDecayFwd, kDecayBwd, kDecayStep };
+int64_t decay_threads(const DecayArgs& a, int32_t io_dtype, DecayCall call);
 launch_result launch_decay_fwd(DecayArgs a, int32_t io_dtype, void* ws, hipStream_t s);
 launch_result launch_decay_step(const DecayArgs& a, int32_t io_dtype, hipStream_t s);
 // Backward: gradients in the io type, dalpha shaped like alpha.

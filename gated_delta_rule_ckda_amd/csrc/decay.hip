@@ -650,14 +650,16 @@ __global__ __launch_bounds__(64 * NW) void decay_step_kernel(DecayStepArgs a) {
   if (t < 8 && col) IO::store4(static_cast<T*>(a.o) + nh * a.dv + c, y * a.scale);
 }
 
+constexpr int step_waves(int dk) { return dk <= 16 ? 1 : (dk <= 32 ? 2 : (dk <= 64 ? 4 : 8)); }
 template <class IO>
 launch_result launch_step_io(const DecayStepArgs& a, hipStream_t s) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.N) * a.H * ((a.dv + 31) / 32));
-  if (a.dk <= 16)
+  const int waves = step_waves(a.dk);
+  if (waves == 1)
     hipLaunchKernelGGL((decay_step_kernel<IO, 1>), dim3(grid), dim3(64), 0, s, a);
-  else if (a.dk <= 32)
+  else if (waves == 2)
     hipLaunchKernelGGL((decay_step_kernel<IO, 2>), dim3(grid), dim3(128), 0, s, a);
-  else if (a.dk <= 64)
+  else if (waves == 4)
     hipLaunchKernelGGL((decay_step_kernel<IO, 4>), dim3(grid), dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((decay_step_kernel<IO, 8>), dim3(grid), dim3(512), 0, s, a);
@@ -676,18 +678,21 @@ launch_result launch_fwd_t(const DecayArgs& a, hipStream_t s) {
                      Cfg::BYTES, s, a);
   return hipGetLastError();
 }
+// Columns of the state a workgroup of the forward takes.  Slabs of 64 read q and
+// k and form Q K^T half as often as slabs of 32 (8 x 4096 tokens, 16 heads of
+// 128: 155 us against 187); in float32 with rows of 128 only 32 fit the LDS.
+// With few workgroups half the columns each shorten a chunk's step (2 x 100
+// tokens, 4 heads of 64 in float32: 12 us against 18 a call).
+int fwd_slab(const DecayArgs& a, bool bf16) {
+  const int64_t walks = static_cast<int64_t>(a.seg > 0 ? a.slots : a.N) * a.H * ((a.dv + 63) / 64);
+  return a.dv <= 32 || walks <= 128 || (a.dk > 64 && !bf16) ? 32 : 64;
+}
 template <class Op>
 launch_result launch_fwd_op(const DecayArgs& a, hipStream_t s) {
-  // Slabs of 64 columns read q and k and form Q K^T half as often as slabs of
-  // 32 (8 x 4096 tokens, 16 heads of 128: 155 us against 187); in float32 with
-  // rows of 128 only 32 fit the LDS.  With few workgroups half the columns each
-  // shorten a chunk's step (2 x 100 tokens, 4 heads of 64 in float32: 12 us
-  // against 18 a call).
-  constexpr int wide = sizeof(typename Op::T) == 2 ? 64 : 32;
-  const int64_t walks = static_cast<int64_t>(a.seg > 0 ? a.slots : a.N) * a.H * ((a.dv + 63) / 64);
-  const bool narrow = a.dv <= 32 || walks <= 128;
+  constexpr bool bf16 = sizeof(typename Op::T) == 2;
+  const bool narrow = fwd_slab(a, bf16) == 32;
   if (a.dk <= 64) return narrow ? launch_fwd_t<Op, 64, 32>(a, s) : launch_fwd_t<Op, 64, 64>(a, s);
-  return narrow ? launch_fwd_t<Op, 128, 32>(a, s) : launch_fwd_t<Op, 128, wide>(a, s);
+  return narrow ? launch_fwd_t<Op, 128, 32>(a, s) : launch_fwd_t<Op, 128, (bf16 ? 64 : 32)>(a, s);
 }
 
 template <class Op, int DKP, int DVS, int C, bool REV, int MODE>
@@ -783,6 +788,21 @@ int64_t decay_grid(const DecayArgs& a, int32_t io_dtype) {
   const int64_t joins = static_cast<int64_t>(a.N) * a.H * ((static_cast<int64_t>(a.dk) * a.dv / 4 + kNT - 1) / kNT);
   const int64_t m = walks > chunks ? walks : chunks;
   return m > joins ? m : joins;
+}
+
+int64_t decay_threads(const DecayArgs& given, int32_t io_dtype, DecayCall call) {
+  DecayArgs a = given;
+  const int64_t heads = static_cast<int64_t>(a.N) * a.H;
+  if (call == kDecayStep) return heads * ((a.dv + 31) / 32) * 64 * step_waves(a.dk);
+  decay_layout_segments(a, nullptr);
+  const int64_t walks = a.seg > 0 ? decay_slots(a, a.seg) * a.H : heads;
+  const int slab = call == kDecayFwd ? fwd_slab(a, io_dtype == CKDA_DTYPE_BF16) : decay_slab(a.dv);
+  // the forward's walk has four waves more than a state walk's four for every 32 columns
+  const int64_t walk = walks * ((a.dv + slab - 1) / slab) * (8 * slab + (call == kDecayFwd ? 256 : 0));
+  const int64_t sums = a.seg > 0 ? walks * ((a.dv + 63) / 64) * 512 : 0;
+  const int64_t join = a.seg > 0 ? heads * ((static_cast<int64_t>(a.dk) * a.dv / 4 + kNT - 1) / kNT) * kNT : 0;
+  const int64_t m = walk > sums ? walk : sums;
+  return m > join ? m : join;
 }
 
 int decay_dots_per_chunk(int32_t dv) { return (dv + decay_slab(dv) - 1) / decay_slab(dv); }

@@ -387,8 +387,9 @@ ckda_status_t ckda_l2norm_debug(const void* x, float* y, int64_t rows,
  * cu_seqlens is clamped to [0, T] on the device.
  * Supported: dk and dv multiples of 8 from 8 to 128, in any combination, both
  * io dtypes; others return CKDA_ERR_UNSUPPORTED, as do H * max(dk, dv) of 2^22 or
- * more, B * T of 2^31 - 1024 or more
- * and launches of 2^31 or more workgroups.
+ * more, B * T of 2^31 - 1024 or more, 2^31 or more (chunk, head) pairs, and
+ * batches for which a launch would have 2^32 threads (768 for each sequence, head
+ * and 64 columns of dv; in float32 with dk over 64, 512 for each 32 columns).
  */
 typedef struct {
   int32_t B, T, H, dk, dv;
@@ -441,7 +442,7 @@ ckda_status_t ckda_decay_bwd(const ckda_decay_desc_t* desc, const void* q, const
  * One token for each of N sequences:
  *   q, k : [N][Hk][dk]   v, o : [N][H][dv]   alpha : [N][H] or [H]
  *   h0, ht : [N][H][dk][dv] float32; h0 == ht (in place) is allowed.
- * N * H up to 2^21.
+ * N * H up to 2^21 (below it where dk > 64 and dv > 96: fewer than 2^32 threads).
  */
 ckda_status_t ckda_decay_step(int32_t N, int32_t H, int32_t qk_heads, int32_t dk, int32_t dv,
                               int32_t io_dtype, int32_t gate_range, int32_t gate_input,

@@ -360,3 +360,27 @@ def test_a_given_stream_owns_what_the_delta_rule_calls_allocate(streams, monkeyp
     for t in got if isinstance(got, tuple) else (got,):
         if t is not None:
             assert (t.data_ptr(), streams["caller"]) in streams["recorded"]
+
+
+def test_launches_of_two_to_the_32_threads_are_refused():
+    """The last batch that fits passes the checks of sizes (and is refused for a
+    NULL q behind them), the next one does not."""
+    one = dict(T=1, H=1, qk_heads=1)
+
+    def at(which, n, cu=None, **kw):
+        return call(which, desc(B=n, num_seqs=n, **dict(one, **kw)), q=None)
+
+    fits, over = (1, "q must not be NULL"), 2
+    for which, n, kw in (("fwd", (1 << 32) // (768 * 2), {}), ("fwd", (1 << 32) // (512 * 4) - 1, dict(io_dtype=ck.F32)),
+                         ("fwd", (1 << 32) // 768, dict(dk=64, dv=64, io_dtype=ck.F32)), ("fwd", (1 << 32) // 512 - 1, dict(dv=32)),
+                         ("bwd", (1 << 32) // (512 * 2) - 1, {}), ("bwd", (1 << 32) // 256 - 1, dict(dv=24))):
+        assert at(which, n, **kw) == fits, (which, n, kw)
+        st, msg = at(which, n + 1, **kw)
+        assert st == over and "too many" in msg, (which, n, kw)
+    # the states' join of a cut batch: 16 workgroups of 256 a sequence and head
+    for which in ("fwd", "bwd"):
+        for n, want in (((1 << 20) - 1, 1), (1 << 20, 2)):
+            assert call(which, desc(B=1, num_seqs=n, T=1 << 21, H=1, qk_heads=1), cu=CU, q=None)[0] == want
+    for n, dk, dv, want in ((1 << 21, 128, 128, 2), ((1 << 21) - 1, 128, 128, 1), (1 << 21, 72, 104, 2),
+                            (1 << 21, 64, 128, 1), (1 << 21, 128, 96, 1)):
+        assert step(N=n, H=1, Hk=1, dk=dk, dv=dv, q=None)[0] == want, (n, dk, dv)
