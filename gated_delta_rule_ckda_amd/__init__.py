@@ -525,6 +525,11 @@ def _launch(device, fn, *args):
             _check(fn(*args, stream))
 
 
+def _sizes_ok(*sizes):
+    """The library takes 32-bit sizes; a longer one would lose its upper half."""
+    _require(max(sizes) < 1 << 31, "sizes must be below 2^31, got %s" % (sizes,))
+
+
 def _state_ok(name, t, shape):
     import torch
     if t is not None:
@@ -564,6 +569,7 @@ def _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale):
                  "cu_seqlens must be an int32 vector")
         _require(B == 1, "a packed batch has B = 1")
         n = cu_seqlens.numel() - 1
+    _sizes_ok(B, T, H, qs[-1], vs[-1], n)
     return _decay_plan(int(cu_seqlens is not None), B, T, H, qs[-1], vs[-1], n, io, _gate_code(gate),
                        _gate_input(gates, alpha, alpha), Hk, int(per_head), float(scale))
 
@@ -667,6 +673,7 @@ def decay_step(q, k, v, alpha, state, *, gate="ckda", gates="values", scale=1.0,
     _require(k.shape == q.shape and v.shape[0] == N, "shape mismatch")
     per_head = alpha.dim() == 1
     _require(tuple(alpha.shape) == ((H,) if per_head else (N, H)), "alpha must be [N,H] or [H]")
+    _sizes_ok(N, H, Hk, dk, dv)
     dev = q.device
     _tensors(dev, q=q, k=k, v=v, alpha=alpha, state=state, out=out, new_state=new_state)
     _state_ok("state", state, (N, H, dk, dv))
@@ -692,6 +699,7 @@ def _norm_args(y, weight, gate, act, residual, scale, next_weight, **more):
     _require(y.dim() >= 1 and y.shape[-1] > 0, "y must be [..., d]")
     _require(act in _ACTS, "act must be 'none', 'sigmoid' or 'silu'")
     d = y.shape[-1]
+    _sizes_ok(d)
     _tensors(y.device, y=y, weight=weight, gate=gate, residual=residual, scale=scale,
              next_weight=next_weight, **more)
     for name, t in dict(gate=gate, residual=residual, **more).items():

@@ -384,3 +384,21 @@ def test_launches_of_two_to_the_32_threads_are_refused():
     for n, dk, dv, want in ((1 << 21, 128, 128, 2), ((1 << 21) - 1, 128, 128, 1), (1 << 21, 72, 104, 2),
                             (1 << 21, 64, 128, 1), (1 << 21, 128, 96, 1)):
         assert step(N=n, H=1, Hk=1, dk=dk, dv=dv, q=None)[0] == want, (n, dk, dv)
+
+
+def test_sizes_past_32_bits_are_refused():
+    """The descriptors hold 32-bit sizes: 2^32 + 64 tokens are not 64."""
+    n = (1 << 32) + 64
+    z = lambda *s: torch.zeros(1).expand(*s)
+    for q, v, al in ((z(1, n, 1, 8), z(1, n, 1, 8), z(1)), (z(n, 1, 1, 8), z(n, 1, 1, 8), z(1)),
+                     (z(1, 8, 1, n), z(1, 8, 1, 8), z(1)), (z(1, 8, 1, 8), z(1, 8, 1, n), z(1))):
+        with pytest.raises(ValueError, match="below 2.31"):
+            ck.decay_fwd(q, q, v, al)
+        with pytest.raises(ValueError, match="below 2.31"):
+            ck.decay_bwd(q, q, v, al, v)
+    with pytest.raises(ValueError, match="below 2.31"):
+        ck.decay_step(z(n, 1, 8), z(n, 1, 8), z(n, 1, 8), z(1), z(n, 1, 8, 8))
+    with pytest.raises(ValueError, match="below 2.31"):
+        ck.block_norm(z(2, n), z(n))
+    with pytest.raises(ValueError, match="below 2.31"):
+        ck.block_norm_bwd(z(2, n), z(n), z(2, n))
