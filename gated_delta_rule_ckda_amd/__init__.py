@@ -610,7 +610,7 @@ def decay_fwd(q, k, v, alpha, *, h0=None, cu_seqlens=None, gate="ckda", gates="v
     workspace that the caller passes must not be shared by calls that overlap."""
     import torch
     lib = _load()
-    desc, need_fwd, need_bwd = _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale)
+    desc, need, _ = _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale)
     dev = q.device
     _tensors(dev, q=q, k=k, v=v, alpha=alpha, h0=h0, cu_seqlens=cu_seqlens, out=out,
              final_state=final_state)
@@ -623,7 +623,7 @@ def decay_fwd(q, k, v, alpha, *, h0=None, cu_seqlens=None, gate="ckda", gates="v
     ht = final_state
     if output_final_state and ht is None:
         ht = torch.empty(shape, device=dev, dtype=torch.float32)
-    ws = _workspace(workspace, need_fwd, dev) if need_fwd else None
+    ws = _workspace(workspace, need, dev) if need else None
     _launch(dev, lib.ckda_decay_fwd, ctypes.byref(desc), _addr(q), _addr(k), _addr(v),
             _addr(alpha), _addr(cu_seqlens), _addr(h0), _addr(o), _addr(ht), _addr(ws),
             0 if ws is None else ws.numel())
@@ -641,7 +641,7 @@ def decay_bwd(q, k, v, alpha, dout, *, h0=None, dht=None, cu_seqlens=None, gate=
     requested."""
     import torch
     lib = _load()
-    desc, need_fwd, need_bwd = _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale)
+    desc, _, need = _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale)
     dev = q.device
     _tensors(dev, q=q, k=k, v=v, alpha=alpha, dout=dout, h0=h0, dht=dht, cu_seqlens=cu_seqlens)
     shape = (desc.num_seqs, desc.H, desc.dk, desc.dv)
@@ -651,7 +651,7 @@ def decay_bwd(q, k, v, alpha, dout, *, h0=None, dht=None, cu_seqlens=None, gate=
     dq, dkk, dvv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     dal = torch.empty(alpha.shape, device=dev, dtype=q.dtype) if output_dalpha else None
     dh0 = torch.empty(shape, device=dev, dtype=torch.float32) if output_dh0 else None
-    ws = _workspace(workspace, need_bwd, dev)
+    ws = _workspace(workspace, need, dev)
     _launch(dev, lib.ckda_decay_bwd, ctypes.byref(desc), _addr(q), _addr(k), _addr(v),
             _addr(alpha), _addr(cu_seqlens), _addr(h0), _addr(dout), _addr(dht), _addr(dq),
             _addr(dkk), _addr(dvv), _addr(dal), _addr(dh0), _addr(ws), ws.numel())
