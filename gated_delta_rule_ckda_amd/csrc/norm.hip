@@ -38,22 +38,20 @@ __device__ __forceinline__ float sigmoid_of(float x) {
     return 1.f / (1.f + expf(-x));
 }
 
-// sigmoid p and its derivative q = e / (1 + e)^2 from one power e = exp(-|x|):
-// p (1 - p) would lose the digits of q where p is next to 1 (a percent at 12,
-// all of it from 17 on)
+// sigmoid p and its derivative q = e p^2, e = exp(-x): p (1 - p) would lose the
+// digits of q where p is next to 1 (a percent at 12, all of it from 17 on).
+// Where e overflows p is 0, and so is q.
 template <class IO>
 __device__ __forceinline__ void sigmoid_and_slope(float x, float& p, float& q) {
-  float e, r;
+  float e;
   if constexpr (sizeof(typename IO::storage) == 2) {
-    e = exp_neg(fabsf(x));
-    r = __builtin_amdgcn_rcpf(1.f + e);
+    e = exp_neg(x);
+    p = __builtin_amdgcn_rcpf(1.f + e);
   } else {
-    e = expf(-fabsf(x));
-    r = 1.f / (1.f + e);
+    e = expf(-x);
+    p = 1.f / (1.f + e);
   }
-  q = e * r;
-  p = x < 0.f ? q : r;
-  q *= r;
+  q = p == 0.f ? 0.f : e * p * p;
 }
 
 // VEC elements at p (aligned to VEC elements), widened
