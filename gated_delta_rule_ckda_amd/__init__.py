@@ -165,33 +165,28 @@ def _record(tensors, stream):
             t.record_stream(stream)
 
 
-def _on_stream(call):
-    """`stream` of a call that works on the current stream: the call runs with it
-    current, so what it allocates belongs to it, a workspace that is dropped on
-    return among that.  Tensors that come from or go back to the caller's own
-    stream are recorded on the other one, so that their memory is not given out
-    again while either still uses it."""
-    @functools.wraps(call)
-    def on_stream(*args, stream=None, **named):
-        if stream is None:
-            return call(*args, **named)
-        import torch
-        given = [t for t in args + tuple(named.values()) if isinstance(t, torch.Tensor)]
-        for t in given:
-            if t.device != stream.device:
-                raise ValueError("the stream belongs to %s, the tensors to %s"
-                                 % (stream.device, t.device))
-        caller = torch.cuda.current_stream(stream.device)
-        if stream == caller:
-            return call(*args, **named)
-        try:
-            with torch.cuda.stream(stream):
-                got = call(*args, **named)
-        finally:
-            _record(given, stream)
-        _record(got if isinstance(got, tuple) else (got,), caller)
-        return got
-    return on_stream
+def _on_stream(call, named):
+    """call(**named) on named["stream"]: it runs with that stream current, so what it
+    allocates belongs to it, a workspace that is dropped on return among that.
+    Tensors that come from or go back to the caller's own stream are recorded on
+    the other one, so that their memory is not given out again while either
+    still uses it."""
+    import torch
+    stream = named.pop("stream")
+    given = [t for t in named.values() if isinstance(t, torch.Tensor)]
+    for t in given:
+        if t.device != stream.device:
+            raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device, t.device))
+    caller = torch.cuda.current_stream(stream.device)
+    if stream == caller:
+        return call(**named)
+    try:
+        with torch.cuda.stream(stream):
+            got = call(**named)
+    finally:
+        _record(given, stream)
+    _record(got if isinstance(got, tuple) else (got,), caller)
+    return got
 
 
 def _gate_code(gate):
@@ -278,7 +273,6 @@ def _fwd_call(q, k, v, alpha, beta, h0, cu_seqlens, chunk_size, use_qk_l2norm, g
     return desc, o, ht
 
 
-@_on_stream
 def chunk_fwd(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_size=64,
               use_qk_l2norm=True, gate="ckda", scale=1.0, output_final_state=True,
               out=None, final_state=None, workspace=None, stream=None, gates="values",
@@ -294,6 +288,8 @@ def chunk_fwd(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_size=64,
     `workspace`: optional uint8 device tensor of at least
     chunk_fwd_workspace_size() bytes (allocated per call when omitted).
     Returns (o, ht) with ht [N,H,dk,dv] float32 (None if not requested)."""
+    if stream is not None:
+        return _on_stream(chunk_fwd, locals())
     import torch
     lib = _load()
     desc, o, ht = _fwd_call(q, k, v, alpha, beta, h0, cu_seqlens, chunk_size, use_qk_l2norm, gate,
@@ -309,7 +305,6 @@ def chunk_fwd(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_size=64,
     return o, ht
 
 
-@_on_stream
 def chunk_fwd_noalloc(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_size=64,
                       use_qk_l2norm=True, gate="ckda", scale=1.0, output_final_state=True,
                       out=None, final_state=None, stream=None, gates="values",
@@ -318,6 +313,8 @@ def chunk_fwd_noalloc(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_s
     static per-GPU scratch instead (NOALLOC_SCRATCH_BYTES).  The C call
     allocates nothing; pass `out` (and `final_state`) to keep this wrapper
     from allocating them.  Calls on one GPU must not overlap."""
+    if stream is not None:
+        return _on_stream(chunk_fwd_noalloc, locals())
     lib = _load()
     desc, o, ht = _fwd_call(q, k, v, alpha, beta, h0, cu_seqlens, chunk_size, use_qk_l2norm, gate,
                             scale, output_final_state, out, final_state, gates, sign_absorb)
@@ -327,7 +324,6 @@ def chunk_fwd_noalloc(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_s
     return o, ht
 
 
-@_on_stream
 def chunk_fwd_save(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_size=64,
                    use_qk_l2norm=True, gate="ckda", scale=1.0, output_final_state=True,
                    out=None, final_state=None, saved=None, stream=None, gates="values"):
@@ -335,6 +331,8 @@ def chunk_fwd_save(q, k, v, alpha, beta, *, h0=None, cu_seqlens=None, chunk_size
     backward's records kept in `saved` (uint8 device tensor of at least
     chunk_bwd_workspace_size() bytes, allocated when omitted) for
     chunk_bwd(..., saved=saved).  Returns (o, ht, saved)."""
+    if stream is not None:
+        return _on_stream(chunk_fwd_save, locals())
     import torch
     lib = _load()
     desc, o, ht = _fwd_call(q, k, v, alpha, beta, h0, cu_seqlens, chunk_size, use_qk_l2norm, gate,
@@ -355,7 +353,6 @@ def chunk_bwd_workspace_size(desc: FwdDesc, packed: bool) -> int:
     return int(_load().ckda_chunk_bwd_workspace_size(ctypes.byref(desc), int(bool(packed))))
 
 
-@_on_stream
 def chunk_bwd(q, k, v, alpha, beta, dout, *, h0=None, dht=None, cu_seqlens=None, chunk_size=64,
               use_qk_l2norm=True, gate="ckda", scale=1.0, output_dh0=True, workspace=None,
               stream=None, gates="values", saved=None):
@@ -368,6 +365,8 @@ def chunk_bwd(q, k, v, alpha, beta, dout, *, h0=None, dht=None, cu_seqlens=None,
     recomputed, and it serves as the workspace.  Returns float32 (dq, dk, dv,
     dalpha, dbeta, dh0) shaped like q, k, v, alpha, beta and [N,H,dk,dv] (dh0
     None unless output_dh0)."""
+    if stream is not None:
+        return _on_stream(chunk_bwd, locals())
     import torch
     lib = _load()
     H, dk, dv = v.shape[-2], q.shape[-1], v.shape[-1]
@@ -457,12 +456,13 @@ class ChunkFwdPlan:
         return self.o, self.ht
 
 
-@_on_stream
 def recurrent_step(q, k, v, alpha, beta, state, *, use_qk_l2norm=True, gate="ckda",
                    scale=1.0, out=None, new_state=None, stream=None, gates="values"):
     """One decode token per sequence: q,k [N,Hk,dk], alpha [N,H,dk], v [N,H,dv],
     beta [N,H], state [N,H,dk,dv] float32, updated in place unless new_state
     is given.  `gates` as for chunk_fwd.  Returns o [N,H,dv]."""
+    if stream is not None:
+        return _on_stream(recurrent_step, locals())
     import torch
     lib = _load()
     N, Hk, dk = q.shape
@@ -525,9 +525,10 @@ def _launch(device, fn, *args):
             _check(fn(*args, stream))
 
 
-def _sizes_ok(*sizes):
-    """The library takes 32-bit sizes; a longer one would lose its upper half."""
-    _require(max(sizes) < 1 << 31, "sizes must be below 2^31, got %s" % (sizes,))
+def _sizes_ok(sizes):
+    """The library takes 32-bit sizes and would lose the upper half of a longer one;
+    `sizes` has the bits of all of a call's."""
+    _require(sizes < 1 << 31, "sizes must be below 2^31")
 
 
 def _state_ok(name, t, shape):
@@ -538,9 +539,10 @@ def _state_ok(name, t, shape):
 
 
 @functools.lru_cache(maxsize=256)
-def _decay_plan(packed, *fields):
+def _decay_plan(packed, B, T, H, dk, dv, n, *fields):
     """The descriptor of these sizes and the workspaces it needs (forward, backward)."""
-    desc = DecayDesc(*fields)
+    _sizes_ok(B | T | H | dk | dv | n)
+    desc = DecayDesc(B, T, H, dk, dv, n, *fields)
     lib = _load()
     return (desc, int(lib.ckda_decay_fwd_workspace_size(ctypes.byref(desc), packed)),
             int(lib.ckda_decay_bwd_workspace_size(ctypes.byref(desc), packed)))
@@ -569,7 +571,6 @@ def _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale):
                  "cu_seqlens must be an int32 vector")
         _require(B == 1, "a packed batch has B = 1")
         n = cu_seqlens.numel() - 1
-    _sizes_ok(B, T, H, qs[-1], vs[-1], n)
     return _decay_plan(int(cu_seqlens is not None), B, T, H, qs[-1], vs[-1], n, io, _gate_code(gate),
                        _gate_input(gates, alpha, alpha), Hk, int(per_head), float(scale))
 
@@ -598,7 +599,6 @@ def decay_bwd_workspace_size(desc: DecayDesc, packed: bool) -> int:
     return int(_load().ckda_decay_bwd_workspace_size(ctypes.byref(desc), int(bool(packed))))
 
 
-@_on_stream
 def decay_fwd(q, k, v, alpha, *, h0=None, cu_seqlens=None, gate="ckda", gates="values", scale=1.0,
               output_final_state=True, out=None, final_state=None, workspace=None, stream=None):
     """Linear attention with one decay a head, S_t = a_t S_{t-1} + k_t v_t^T and
@@ -608,6 +608,8 @@ def decay_fwd(q, k, v, alpha, *, h0=None, cu_seqlens=None, gate="ckda", gates="v
     (float32) or 'logits' (float32 or bfloat16, activated by `gate`).
     Returns (o, ht) with ht [N,H,dk,dv] float32 (None if not requested).  A
     workspace that the caller passes must not be shared by calls that overlap."""
+    if stream is not None:
+        return _on_stream(decay_fwd, locals())
     import torch
     lib = _load()
     desc, need, _ = _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale)
@@ -630,7 +632,6 @@ def decay_fwd(q, k, v, alpha, *, h0=None, cu_seqlens=None, gate="ckda", gates="v
     return o, ht
 
 
-@_on_stream
 def decay_bwd(q, k, v, alpha, dout, *, h0=None, dht=None, cu_seqlens=None, gate="ckda",
               gates="values", scale=1.0, output_dalpha=True, output_dh0=True, workspace=None,
               stream=None):
@@ -639,6 +640,8 @@ def decay_bwd(q, k, v, alpha, dout, *, h0=None, dht=None, cu_seqlens=None, gate=
     q, k, v and alpha (with logits, the gradient of the logits; with [H], the
     sum over all tokens), dh0 [N,H,dk,dv] float32; dalpha and dh0 None unless
     requested."""
+    if stream is not None:
+        return _on_stream(decay_bwd, locals())
     import torch
     lib = _load()
     desc, _, need = _decay_desc(q, k, v, alpha, cu_seqlens, gate, gates, scale)
@@ -658,12 +661,13 @@ def decay_bwd(q, k, v, alpha, dout, *, h0=None, dht=None, cu_seqlens=None, gate=
     return dq, dkk, dvv, dal, dh0
 
 
-@_on_stream
 def decay_step(q, k, v, alpha, state, *, gate="ckda", gates="values", scale=1.0, out=None,
                new_state=None, stream=None):
     """One token a sequence of decay_fwd's recurrence: q, k [N,Hk,dk], v
     [N,H,dv], alpha [N,H] or [H], state [N,H,dk,dv] float32, updated in place
     unless new_state is given.  Returns o [N,H,dv]."""
+    if stream is not None:
+        return _on_stream(decay_step, locals())
     import torch
     lib = _load()
     _require(q.dim() == 3 and v.dim() == 3, "q and v must be [N,heads,d]")
@@ -673,7 +677,7 @@ def decay_step(q, k, v, alpha, state, *, gate="ckda", gates="values", scale=1.0,
     _require(k.shape == q.shape and v.shape[0] == N, "shape mismatch")
     per_head = alpha.dim() == 1
     _require(tuple(alpha.shape) == ((H,) if per_head else (N, H)), "alpha must be [N,H] or [H]")
-    _sizes_ok(N, H, Hk, dk, dv)
+    _sizes_ok(N | H | Hk | dk | dv)
     dev = q.device
     _tensors(dev, q=q, k=k, v=v, alpha=alpha, state=state, out=out, new_state=new_state)
     _state_ok("state", state, (N, H, dk, dv))
@@ -711,7 +715,6 @@ def _norm_args(y, weight, gate, act, residual, scale, next_weight, **more):
     return y.numel() // d, d, 0 if gate is None else _ACTS[act]
 
 
-@_on_stream
 def block_norm(y, weight, *, gate=None, act="sigmoid", residual=None, scale=None,
                next_weight=None, eps=1e-6, out=None, next_out=None, stream=None):
     """The norm after a block, its output gate, the residual stream and the norm
@@ -723,6 +726,8 @@ def block_norm(y, weight, *, gate=None, act="sigmoid", residual=None, scale=None
     y, gate and residual in bfloat16 or float32, weight, scale and next_weight
     float32 [d].  Any part may be left out.  Returns (h, n), n None without
     next_weight.  out may be the residual itself (updated in place)."""
+    if stream is not None:
+        return _on_stream(block_norm, locals())
     import torch
     lib = _load()
     io = _dtype_code(y)
@@ -740,7 +745,6 @@ def block_norm(y, weight, *, gate=None, act="sigmoid", residual=None, scale=None
     return h, n
 
 
-@_on_stream
 def block_norm_bwd(y, weight, dh, *, dnext=None, gate=None, act="sigmoid", residual=None,
                    scale=None, next_weight=None, eps=1e-6, workspace=None, stream=None):
     """Gradients of block_norm for dL/dh = dh and dL/dn = dnext (given exactly
@@ -748,6 +752,8 @@ def block_norm_bwd(y, weight, dh, *, dnext=None, gate=None, act="sigmoid", resid
     dnext_weight), None where the input was left out; dy, dgate and dresidual
     in y's dtype, the others float32 [d].  Without next_weight dresidual is dh
     itself."""
+    if stream is not None:
+        return _on_stream(block_norm_bwd, locals())
     import torch
     lib = _load()
     io = _dtype_code(y)
