@@ -32,10 +32,13 @@ constexpr int kNT = 256;  // of the join
 // Measured at 8 x 4096 tokens, 16 heads of 128, bf16: 150 us, 3.6 TB/s of the
 // bytes it cannot do without, each read from HBM once (411 MB fetched of 402).
 // Without the loads it takes 119 us, without the products 131: LDS (58% of its
-// cycles busy, reads of W V across its rows first) bounds the one, what a CU
-// takes in (16 to 22 bytes a clock, q and k once a slab) the other, and the two
-// overlap in part.  Half as many state waves with twice the rows each read W V
-// less but take as long (152 us).
+// cycles busy) bounds the one, what a CU takes in (16 to 22 bytes a clock, q and
+// k once a slab) the other, and the two overlap in part.  Nearly half of the LDS
+// cycles are bank conflicts (2.6e7 of 5.4e7): by a model of 64 banks those of
+// the reads across rows of W V (2 ways) and, columns 16 apart, of V (4 ways),
+// whose rows lie 16 bytes past a multiple of 128; K, Q and P have none.  Half
+// as many state waves with twice the rows each read W V less but take as long
+// (152 us).
 // Earlier forms: one role and two barriers 246 us, two roles 207, rows loaded
 // two chunks ahead 187, slabs of 64 columns 155.
 template <class Op, int DKP, int DVS>
@@ -322,7 +325,8 @@ __global__ __launch_bounds__((FwdCfg<Op, DKP, DVS>::NT)) void decay_fwd_kernel(D
 // adjoints and the forward's states).  kSegment over 15/16 of 65536 tokens, 16
 // heads: 168 us with all 128 columns and 64 x 32 a wave, 197 with 32 x 32, 207
 // in slabs of 64 columns; with one of the three terms of W V a third less, so
-// the reads of those terms from LDS bound it.
+// the reads of those terms from LDS bound it, bank conflicts among them (in
+// kChunks 1.3e7 of 2.7e7 LDS cycles; the 128 columns of kSegment conflict more).
 enum { kSegment = 0, kChunks = 1 };
 
 template <class Op, int DKP, int DVS, int C>
@@ -681,8 +685,11 @@ launch_result launch_fwd_t(const DecayArgs& a, hipStream_t s) {
 // Columns of the state a workgroup of the forward takes.  Slabs of 64 read q and
 // k and form Q K^T half as often as slabs of 32 (8 x 4096 tokens, 16 heads of
 // 128: 155 us against 187); in float32 with rows of 128 only 32 fit the LDS.
-// With few workgroups half the columns each shorten a chunk's step (2 x 100
-// tokens, 4 heads of 64 in float32: 12 us against 18 a call).
+// With up to 128 walks half the columns each still find CUs of their own and
+// shorten a chunk's step: 2 x 100 tokens, 4 heads of 64, 11 us against 14 in
+// float32 and 7.3 against 8.1 in bf16; 128 walks of 512 tokens 32 against 42
+// (float32, heads of 64) and 19 against 23 (bf16, heads of 128).  From 256 walks
+// on it is the other way round: 61 against 46, 35 against 25.
 int fwd_slab(const DecayArgs& a, bool bf16) {
   const int64_t walks = static_cast<int64_t>(a.seg > 0 ? a.slots : a.N) * a.H * ((a.dv + 63) / 64);
   return a.dv <= 32 || walks <= 128 || (a.dk > 64 && !bf16) ? 32 : 64;
@@ -744,6 +751,9 @@ bool decay_supported(int32_t dk, int32_t dv) {
 // half as many segments, 469 with twice as many, 505 with three quarters (256
 // CUs do not divide into them).  A packed batch is always cut, since its
 // longest sequence would walk alone (40000 tokens, the longest 8191: 298 us).
+// Batches of little more than 256 walks pay for a second round of CUs: 8, 9, 12
+// and 16 sequences of 4096 tokens, 16 heads of 128, take 160, 258, 265, 308 us,
+// gradients 677, 946, 1118, 1337.
 int32_t decay_segment(const DecayArgs& a) {
   const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
   if (!a.cu && static_cast<int64_t>(a.N) * a.H * ((a.dv + 63) / 64) >= 256) return 0;

@@ -29,7 +29,8 @@
 // P and N rounded to the io type once each, as the states are: half a step of
 // each gradient.  Measured at 8 x 4096 tokens, 16 heads of 128, bf16: 424 us
 // (1.47 GB, 3.5 TB/s).  Without the loads 373 us were left of 540, without the
-// products 422: LDS (half of its cycles busy) and the loads share the time.
+// products 422: LDS (half of its cycles busy, nearly half of those with bank
+// conflicts: 5.4e7 of 1.1e8) and the loads share the time.
 // Four waves took 900 us, loads all at once 528, stores straight from the
 // accumulators 466.
 #include "decay_ops.h"

@@ -20,7 +20,7 @@
 // rows are a thread's own until its last row.  8 elements a thread keep three
 // workgroups of gradients a CU (146 registers); more only where a row is too
 // long for 256 threads.  Measured in bf16: 524288 rows of 128 with a gate 72 us
-// (5.6 TB/s), gradients of 32768 rows of 2048 with all parts 210 us (5.1 TB/s;
+// (5.6 TB/s), gradients of 32768 rows of 2048 with all parts 213 us (5.0 TB/s;
 // a copy of 2 GB runs at 5.0).
 #include "mfma_ops.h"
 
@@ -416,8 +416,8 @@ int64_t grid_of(int64_t rows, const Shape& s, int64_t most) {
 
 // Workgroups: as many as the 256 CUs hold at once by their registers, each
 // walking over rows.  A second round of a few costs as much as a full one
-// (gradients of 32768 rows of 2048 in bf16, where three fit a CU: 210 us with
-// 768 workgroups, 267 with 512, 283 with 1024; forward of 524288 rows of 128:
+// (gradients of 32768 rows of 2048 in bf16, where three fit a CU: 213 us with
+// 768 workgroups, 27% more with 512, 35% more with 1024; forward of 524288 rows of 128:
 // 71 us with 1024, 82 with 2048).
 constexpr int64_t kFwdGroups = 1024;
 int64_t bwd_groups(const Shape& s) { return s.nt == 1024 ? 256 : (s.epl == 8 ? 768 : 512); }
