@@ -20,7 +20,9 @@ __all__ = ["chunk_fwd", "chunk_bwd", "chunk_bwd_workspace_size", "recurrent_step
            "library_path", "abi_version", "chunk_fwd_save", "CkdaError", "BF16", "F32", "GATE_KDA",
            "GATE_CKDA", "GATES_F32", "GATES_LOGITS_F32", "GATES_LOGITS_BF16", "ChunkFwdPlan",
            "decay_fwd", "decay_bwd", "decay_step", "decay_supported",
-           "block_norm", "block_norm_bwd"]
+           "block_norm", "block_norm_bwd", "layer_norm", "layer_norm_bwd",
+           "conv_fwd", "conv_bwd", "conv_step",
+           "scan_fwd", "scan_bwd", "scan_step", "scan_supported"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = os.path.join(_HERE, "libckda.so")
@@ -56,6 +58,21 @@ class DecayDesc(ctypes.Structure):
                 ("io_dtype", ctypes.c_int32), ("gate_range", ctypes.c_int32),
                 ("gate_input", ctypes.c_int32), ("qk_heads", ctypes.c_int32),
                 ("alpha_per_head", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class ConvDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("num_seqs", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("x_stride", ctypes.c_int64)]
+
+
+class ScanDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("S", ctypes.c_int32), ("groups", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("softplus", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64),
+                ("z_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64),
+                ("c_stride", ctypes.c_int64)]
 
 
 def library_path() -> str:
@@ -121,6 +138,32 @@ def _load():
         lib.ckda_block_norm_bwd_workspace_size.argtypes = [i64, i32, i32]
         lib.ckda_block_norm_bwd.restype = i32
         lib.ckda_block_norm_bwd.argtypes = [i64, i32, i32, i32, f32] + [vp] * 15 + [sz, vp]
+        lib.ckda_layer_norm.restype = i32
+        lib.ckda_layer_norm.argtypes = [i64, i32, i32, f32] + [vp] * 7
+        lib.ckda_layer_norm_bwd_workspace_size.restype = sz
+        lib.ckda_layer_norm_bwd_workspace_size.argtypes = [i64, i32, i32]
+        lib.ckda_layer_norm_bwd.restype = i32
+        lib.ckda_layer_norm_bwd.argtypes = [i64, i32, i32, f32] + [vp] * 8 + [sz, vp]
+        cd, sd = ctypes.POINTER(ConvDesc), ctypes.POINTER(ScanDesc)
+        lib.ckda_conv_fwd.restype = i32
+        lib.ckda_conv_fwd.argtypes = [cd] + [vp] * 8
+        lib.ckda_conv_bwd_workspace_size.restype = sz
+        lib.ckda_conv_bwd_workspace_size.argtypes = [cd, i32]
+        lib.ckda_conv_bwd.restype = i32
+        lib.ckda_conv_bwd.argtypes = [cd] + [vp] * 12 + [sz, vp]
+        lib.ckda_conv_step.restype = i32
+        lib.ckda_conv_step.argtypes = [cd] + [vp] * 7
+        lib.ckda_scan_supported.restype = i32
+        lib.ckda_scan_supported.argtypes = [i32]
+        for name in ("ckda_scan_fwd_workspace_size", "ckda_scan_bwd_workspace_size"):
+            getattr(lib, name).restype = sz
+            getattr(lib, name).argtypes = [sd, i32]
+        lib.ckda_scan_fwd.restype = i32
+        lib.ckda_scan_fwd.argtypes = [sd] + [vp] * 13 + [sz, vp]
+        lib.ckda_scan_bwd.restype = i32
+        lib.ckda_scan_bwd.argtypes = [sd] + [vp] * 22 + [sz, vp]
+        lib.ckda_scan_step.restype = i32
+        lib.ckda_scan_step.argtypes = [sd] + [vp] * 12
         lib.ckda_status_string.restype = ctypes.c_char_p
         lib.ckda_status_string.argtypes = [i32]
         lib.ckda_last_error.restype = ctypes.c_char_p
@@ -775,3 +818,341 @@ def block_norm_bwd(y, weight, dh, *, dnext=None, gate=None, act="sigmoid", resid
             _addr(dh), _addr(dnext), _addr(dy), _addr(dw), _addr(dg),
             None if dx is dh else _addr(dx), _addr(ds), _addr(dw2), _addr(ws), ws.numel())
     return dy, dw, dg, dx, ds, dw2
+
+
+# ---- layer norm
+
+def layer_norm(x, weight, bias=None, *, residual=None, eps=1e-5, out=None, residual_out=None, stream=None):
+    """Layer norm over the last axis of x [..., d], after a residual add:
+        h = residual + x           (x itself without a residual)
+        n = (h - mean h) / sqrt(var h + eps) * weight + bias
+    x and residual in bfloat16 or float32, weight and bias float32 [d] (None: 1
+    and 0).  Returns (n, h), h None without a residual.  residual_out may be the
+    residual itself, or x (updated in place)."""
+    if stream is not None:
+        return _on_stream(layer_norm, locals())
+    import torch
+    lib = _load()
+    io = _dtype_code(x)
+    rows, d, _ = _norm_args(x, weight, None, "none", residual, None, bias, out=out, residual_out=residual_out)
+    _require(residual_out is None or residual is not None, "residual_out needs a residual")
+    n = torch.empty_like(x) if out is None else out
+    h = residual_out
+    if residual is not None and h is None:
+        h = torch.empty_like(x)
+    _launch(x.device, lib.ckda_layer_norm, rows, d, io, float(eps), _addr(x), _addr(residual),
+            _addr(weight), _addr(bias), _addr(n), _addr(h))
+    return n, h
+
+
+def layer_norm_bwd(x, weight, dn, *, dh=None, eps=1e-5, output_dbias=True, workspace=None, stream=None):
+    """Gradients of layer_norm for dL/dn = dn and dL/dh = dh (None for zero), from
+    x, the row that was normed (with a residual: layer_norm's h).  Returns (dx,
+    dweight, dbias): dx, the gradient of x and of the residual, in x's dtype, the
+    others float32 [d], None without a weight or unless requested."""
+    if stream is not None:
+        return _on_stream(layer_norm_bwd, locals())
+    import torch
+    lib = _load()
+    io = _dtype_code(x)
+    rows, d, _ = _norm_args(x, weight, None, "none", None, None, None, dn=dn, dh=dh)
+    dx = torch.empty_like(x)
+    dw = None if weight is None else torch.empty_like(weight)
+    db = torch.empty(d, device=x.device, dtype=torch.float32) if output_dbias else None
+    if rows == 0:
+        for t in (dw, db):
+            if t is not None:
+                t.zero_()
+        return dx, dw, db
+    need = int(lib.ckda_layer_norm_bwd_workspace_size(rows, d, io))
+    ws = _workspace(workspace, need, x.device)
+    _launch(x.device, lib.ckda_layer_norm_bwd, rows, d, io, float(eps), _addr(x), _addr(weight),
+            _addr(dn), _addr(dh), _addr(dx), _addr(dw), _addr(db), _addr(ws), ws.numel())
+    return dx, dw, db
+
+
+# ---- short causal convolution and selective scan
+
+def _row_stride(name, t, lead, width):
+    """Elements between the tokens of t, [*lead, ...] with `width` contiguous elements
+    a token (it may be a part of wider rows)."""
+    shape, strides = t.shape, t.stride()
+    want = 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] != 1 and strides[i] != want:
+            raise ValueError("%s must be contiguous within a token" % name)
+        want *= shape[i]
+    step = None  # between tokens, sequences following each other
+    for i in range(lead - 1, -1, -1):
+        if shape[i] != 1:
+            if step is None:
+                step, count = strides[i], shape[i]
+            elif strides[i] != step * count:
+                raise ValueError("%s must have one distance between all its tokens" % name)
+    if step is None or t.numel() == 0:
+        return width
+    _require(step >= width, "%s has tokens that overlap" % name)
+    _require(step < 1 << 31, "sizes must be below 2^31")
+    return step
+
+
+def _batch(x, cu_seqlens):
+    """(leading dimensions of a token, B, T, sequences) of x [B,T,D] or packed [T,D]."""
+    import torch
+    lead = 1 if cu_seqlens is not None and x.dim() == 2 else 2
+    _require(x.dim() == lead + 1, "x must be [B,T,D] (a packed batch may leave B out)")
+    B, T = (1, x.shape[0]) if lead == 1 else x.shape[:2]
+    n = B
+    if cu_seqlens is not None:
+        _require(cu_seqlens.dtype == torch.int32 and cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 1,
+                 "cu_seqlens must be an int32 vector")
+        _require(B == 1, "a packed batch has B = 1")
+        n = cu_seqlens.numel() - 1
+    return lead, B, T, n
+
+
+def _on(device, **named):
+    """Checks that every given tensor is on `device` (a GPU)."""
+    _require(device.type == "cuda", "tensors must be on a GPU, got %s" % device)
+    for name, t in named.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+
+
+def _like(name, t, shape, dtype):
+    if t is not None and (t.dtype != dtype or t.shape != shape):
+        raise ValueError("%s must be %s of shape %s" % (name, dtype, list(shape)))
+
+
+_CONV_ACTS = {"none": 0, "silu": 2}
+
+
+@functools.lru_cache(maxsize=256)
+def _conv_plan(packed, B, T, D, K, n, io, act, stride):
+    """The descriptor of these sizes and the backward's workspace."""
+    _sizes_ok(B | T | D | K | n)
+    desc = ConvDesc(B, T, D, K, n, io, act, stride)
+    return desc, int(_load().ckda_conv_bwd_workspace_size(ctypes.byref(desc), packed))
+
+
+def _conv_desc(x, weight, bias, act, cu_seqlens, step=False):
+    import torch
+    io = _dtype_code(x)
+    if step:
+        _require(x.dim() == 2, "x must be [N,D]")
+        lead, B, T, n = 1, x.shape[0], 1, x.shape[0]
+    else:
+        lead, B, T, n = _batch(x, cu_seqlens)
+    D = x.shape[-1]
+    _require(act in _CONV_ACTS, "act must be 'none' or 'silu'")
+    _require(weight.dim() == 2 and weight.shape[0] == D and weight.dtype == torch.float32,
+             "weight must be float32 [D,K]")
+    _like("bias", bias, (D,), torch.float32)
+    K = weight.shape[1]
+    return _conv_plan(int(cu_seqlens is not None), B, T, D, K, n, io, _CONV_ACTS[act],
+                      _row_stride("x", x, lead, D))
+
+
+def conv_fwd(x, weight, *, bias=None, act="silu", h0=None, cu_seqlens=None, output_final_state=True,
+             out=None, final_state=None, stream=None):
+    """Short causal convolution a channel, y_t = act(bias + sum_j weight[:, j] x_{t-K+1+j}), over
+    whole prompts.  x [B,T,D], packed (cu_seqlens int32 [N+1]) [1,T,D] or [T,D], in bfloat16 or
+    float32; it may be a part of wider rows.  weight [D,K] (K from 2 to 4), bias [D] float32; act
+    'none' or 'silu'; h0 [N,K-1,D] the inputs before each sequence (None: zeros).  Returns (y, ht),
+    y contiguous, ht [N,K-1,D] the last K-1 inputs (None if not requested)."""
+    if stream is not None:
+        return _on_stream(conv_fwd, locals())
+    import torch
+    lib = _load()
+    desc, _ = _conv_desc(x, weight, bias, act, cu_seqlens)
+    dev = x.device
+    _on(dev, x=x)
+    _tensors(dev, weight=weight, bias=bias, h0=h0, cu_seqlens=cu_seqlens, out=out, final_state=final_state)
+    cache = (desc.num_seqs, desc.K - 1, desc.D)
+    _like("h0", h0, cache, x.dtype)
+    _like("final_state", final_state, cache, x.dtype)
+    _like("out", out, x.shape, x.dtype)
+    y = torch.empty(x.shape, device=dev, dtype=x.dtype) if out is None else out
+    ht = final_state
+    if output_final_state and ht is None:
+        ht = torch.empty(cache, device=dev, dtype=x.dtype)
+    _launch(dev, lib.ckda_conv_fwd, ctypes.byref(desc), _addr(x), _addr(weight), _addr(bias),
+            _addr(cu_seqlens), _addr(h0), _addr(y), _addr(ht))
+    return y, ht
+
+
+def conv_bwd(x, weight, dout, *, bias=None, act="silu", h0=None, dht=None, cu_seqlens=None,
+             output_dh0=True, workspace=None, stream=None):
+    """Gradients of conv_fwd for dL/dy = dout and dL/dht = dht (None for zero).
+    Returns (dx, dweight, dbias, dh0): dx and dh0 in x's dtype, dweight and dbias
+    float32; dbias None without a bias, dh0 None unless requested."""
+    if stream is not None:
+        return _on_stream(conv_bwd, locals())
+    import torch
+    lib = _load()
+    desc, need = _conv_desc(x, weight, bias, act, cu_seqlens)
+    dev = x.device
+    _on(dev, x=x)
+    _tensors(dev, weight=weight, bias=bias, h0=h0, dout=dout, dht=dht, cu_seqlens=cu_seqlens)
+    cache = (desc.num_seqs, desc.K - 1, desc.D)
+    _like("h0", h0, cache, x.dtype)
+    _like("dht", dht, cache, x.dtype)
+    _like("dout", dout, x.shape, x.dtype)
+    dx = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    dw = torch.empty_like(weight)
+    db = None if bias is None else torch.empty_like(bias)
+    dh0 = torch.empty(cache, device=dev, dtype=x.dtype) if output_dh0 else None
+    ws = _workspace(workspace, need, dev)
+    _launch(dev, lib.ckda_conv_bwd, ctypes.byref(desc), _addr(x), _addr(weight), _addr(bias),
+            _addr(cu_seqlens), _addr(h0), _addr(dout), _addr(dht), _addr(dx), _addr(dw), _addr(db),
+            _addr(dh0), _addr(ws), ws.numel())
+    return dx, dw, db, dh0
+
+
+def conv_step(x, weight, state, *, bias=None, act="silu", out=None, new_state=None, stream=None):
+    """One token a sequence of conv_fwd: x [N,D], state [N,K-1,D] the last inputs,
+    updated in place unless new_state is given.  Returns y [N,D]."""
+    if stream is not None:
+        return _on_stream(conv_step, locals())
+    import torch
+    lib = _load()
+    desc, _ = _conv_desc(x, weight, bias, act, None, step=True)
+    dev = x.device
+    _on(dev, x=x)
+    _tensors(dev, weight=weight, bias=bias, state=state, out=out, new_state=new_state)
+    cache = (desc.B, desc.K - 1, desc.D)
+    _like("state", state, cache, x.dtype)
+    _like("new_state", new_state, cache, x.dtype)
+    _like("out", out, x.shape, x.dtype)
+    y = torch.empty(x.shape, device=dev, dtype=x.dtype) if out is None else out
+    _launch(dev, lib.ckda_conv_step, ctypes.byref(desc), _addr(x), _addr(weight), _addr(bias),
+            _addr(state), _addr(state if new_state is None else new_state), _addr(y))
+    return y
+
+
+@functools.lru_cache(maxsize=256)
+def _scan_plan(packed, B, T, D, S, G, n, *fields):
+    """The descriptor of these sizes and the workspaces it needs (forward, backward)."""
+    _sizes_ok(B | T | D | S | G | n)
+    desc = ScanDesc(B, T, D, S, G, n, *fields)
+    lib = _load()
+    return (desc, int(lib.ckda_scan_fwd_workspace_size(ctypes.byref(desc), packed)),
+            int(lib.ckda_scan_bwd_workspace_size(ctypes.byref(desc), packed)))
+
+
+def _scan_desc(x, dt, A, B, C, D, z, dt_bias, steps, cu_seqlens, step=False):
+    """The plan of a scan call, after the checks of its inputs' shapes and types."""
+    import torch
+    io = _dtype_code(x)
+    if step:
+        _require(x.dim() == 2, "x must be [N,D]")
+        lead, nb, T, n = 1, x.shape[0], 1, x.shape[0]
+    else:
+        lead, nb, T, n = _batch(x, cu_seqlens)
+    _require(steps in ("logits", "values"), "steps must be 'logits' or 'values'")
+    chans = x.shape[-1]
+    for name, t in (("dt", dt), ("z", z)):
+        _like(name, t, x.shape, x.dtype)
+    _require(A.dim() == 2 and A.shape[0] == chans and A.dtype == torch.float32, "A must be float32 [D,S]")
+    for name, t in (("D", D), ("dt_bias", dt_bias)):
+        _like(name, t, (chans,), torch.float32)
+    S = A.shape[1]
+    G = B.shape[-2] if B.dim() == lead + 2 else 1
+    _require(B.dtype == x.dtype and B.dim() in (lead + 1, lead + 2) and B.shape[:lead] == x.shape[:lead]
+             and B.shape[-1] == S, "B must be [...,groups,S] or [...,S] with the tokens of x")
+    _require(C.dtype == x.dtype and C.shape == B.shape, "C must match B")
+    _require(G > 0 and chans % G == 0, "the groups must divide the channels")
+    _on(x.device, x=x, dt=dt, B=B, C=C, z=z)
+    return _scan_plan(int(cu_seqlens is not None), nb, T, chans, S, G, n, io, int(steps == "logits"),
+                      _row_stride("x", x, lead, chans), _row_stride("dt", dt, lead, chans),
+                      0 if z is None else _row_stride("z", z, lead, chans),
+                      _row_stride("B", B, lead, G * S), _row_stride("C", C, lead, G * S))
+
+
+def scan_supported(S) -> bool:
+    return bool(_load().ckda_scan_supported(S))
+
+
+def scan_fwd(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, steps="logits", h0=None, cu_seqlens=None,
+             output_final_state=True, out=None, final_state=None, workspace=None, stream=None):
+    """Selective scan over whole prompts: S states a channel,
+        d_t = softplus(dt_t + dt_bias)          (steps='values': dt_t + dt_bias)
+        h_t = exp(d_t A) h_{t-1} + d_t x_t B_t,   y_t = (C_t . h_t + D x_t) silu(z_t)
+    x, dt, z [B,T,D], B, C [B,T,G,S] (or [B,T,S]; a group's channels share them),
+    packed (cu_seqlens int32 [N+1]) [1,T,...] or [T,...], in bfloat16 or float32;
+    they may be parts of wider rows.  A [D,S], D, dt_bias [D] float32; h0 [N,D,S]
+    float32.  D, z and dt_bias may be left out.  Returns (y, ht), y contiguous, ht
+    [N,D,S] float32 (None if not requested).  A workspace that the caller passes
+    must not be shared by calls that overlap."""
+    if stream is not None:
+        return _on_stream(scan_fwd, locals())
+    import torch
+    lib = _load()
+    desc, need, _ = _scan_desc(x, dt, A, B, C, D, z, dt_bias, steps, cu_seqlens)
+    dev = x.device
+    _tensors(dev, A=A, D=D, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens, out=out, final_state=final_state)
+    shape = (desc.num_seqs, desc.D, desc.S)
+    _state_ok("h0", h0, shape)
+    _state_ok("final_state", final_state, shape)
+    _like("out", out, x.shape, x.dtype)
+    y = torch.empty(x.shape, device=dev, dtype=x.dtype) if out is None else out
+    ht = final_state
+    if output_final_state and ht is None:
+        ht = torch.empty(shape, device=dev, dtype=torch.float32)
+    ws = _workspace(workspace, need, dev) if need else None
+    _launch(dev, lib.ckda_scan_fwd, ctypes.byref(desc), _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
+            _addr(D), _addr(z), _addr(dt_bias), _addr(cu_seqlens), _addr(h0), _addr(y), _addr(ht), _addr(ws),
+            0 if ws is None else ws.numel())
+    return y, ht
+
+
+def scan_bwd(x, dt, A, B, C, dout, *, D=None, z=None, dt_bias=None, steps="logits", h0=None, dht=None,
+             cu_seqlens=None, output_dh0=True, workspace=None, stream=None):
+    """Gradients of scan_fwd for dL/dy = dout and dL/dht = dht (None for zero).
+    Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0): dx, ddt, dB, dC and dz in
+    x's dtype, contiguous, the others float32; ddt is the gradient of what dt
+    holds.  dD, dz and ddt_bias are None where the input was left out, dh0 unless
+    requested."""
+    if stream is not None:
+        return _on_stream(scan_bwd, locals())
+    import torch
+    lib = _load()
+    desc, _, need = _scan_desc(x, dt, A, B, C, D, z, dt_bias, steps, cu_seqlens)
+    dev = x.device
+    _tensors(dev, A=A, D=D, dt_bias=dt_bias, h0=h0, dout=dout, dht=dht, cu_seqlens=cu_seqlens)
+    shape = (desc.num_seqs, desc.D, desc.S)
+    _state_ok("h0", h0, shape)
+    _state_ok("dht", dht, shape)
+    _like("dout", dout, x.shape, x.dtype)
+    new = lambda t: None if t is None else torch.empty(t.shape, device=dev, dtype=t.dtype)
+    dx, ddt, dA, dB, dC, dD, dz, dbias = (new(t) for t in (x, dt, A, B, C, D, z, dt_bias))
+    dh0 = torch.empty(shape, device=dev, dtype=torch.float32) if output_dh0 else None
+    ws = _workspace(workspace, need, dev)
+    _launch(dev, lib.ckda_scan_bwd, ctypes.byref(desc), _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
+            _addr(D), _addr(z), _addr(dt_bias), _addr(cu_seqlens), _addr(h0), _addr(dout), _addr(dht),
+            _addr(dx), _addr(ddt), _addr(dA), _addr(dB), _addr(dC), _addr(dD), _addr(dz), _addr(dbias),
+            _addr(dh0), _addr(ws), ws.numel())
+    return dx, ddt, dA, dB, dC, dD, dz, dbias, dh0
+
+
+def scan_step(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, steps="logits", out=None,
+              new_state=None, stream=None):
+    """One token a sequence of scan_fwd's recurrence: x, dt, z [N,D], B, C [N,G,S]
+    or [N,S], state [N,D,S] float32, updated in place unless new_state is given.
+    Returns y [N,D]."""
+    if stream is not None:
+        return _on_stream(scan_step, locals())
+    import torch
+    lib = _load()
+    desc, _, _ = _scan_desc(x, dt, A, B, C, D, z, dt_bias, steps, None, step=True)
+    dev = x.device
+    _tensors(dev, A=A, D=D, dt_bias=dt_bias, state=state, out=out, new_state=new_state)
+    shape = (desc.B, desc.D, desc.S)
+    _state_ok("state", state, shape)
+    _state_ok("new_state", new_state, shape)
+    _like("out", out, x.shape, x.dtype)
+    y = torch.empty(x.shape, device=dev, dtype=x.dtype) if out is None else out
+    _launch(dev, lib.ckda_scan_step, ctypes.byref(desc), _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
+            _addr(D), _addr(z), _addr(dt_bias), _addr(state), _addr(state if new_state is None else new_state),
+            _addr(y))
+    return y

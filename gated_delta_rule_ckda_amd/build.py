@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libckda.so")
 OBJDIR = os.path.join(HERE, "_build")
 
 SOURCES = ["api.hip", "decode.hip", "chunk_prep.hip", "chunk_state.hip", "sign_absorb.hip",
-           "chunk_bwd.hip", "bwd_gates.hip", "decay.hip", "decay_bwd.hip", "norm.hip"]
+           "chunk_bwd.hip", "bwd_gates.hip", "decay.hip", "decay_bwd.hip", "norm.hip",
+           "conv.hip", "scan.hip", "scan_bwd.hip", "layer_norm.hip"]
 ARCH = os.environ.get("CKDA_ARCH", "gfx950")
 
 CFLAGS = [

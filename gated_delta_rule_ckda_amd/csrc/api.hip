@@ -545,6 +545,7 @@ struct Tensor {
   Range r;
   bool out;      // written
   bool needed;   // may not be NULL
+  uint32_t align = 16;
 };
 
 // Every tensor aligned and given where needed; no output overlaps an input or
@@ -553,8 +554,8 @@ ckda_status_t check_tensors(const Tensor* ts, int n, int same_a = -1, int same_b
   for (int i = 0; i < n; ++i) {
     if (ts[i].needed && ts[i].r.lo == 0)
       return fail(CKDA_ERR_INVALID_ARGUMENT, "%s must not be NULL", ts[i].r.name);
-    if ((ts[i].r.lo & 15u) != 0)
-      return fail(CKDA_ERR_INVALID_ARGUMENT, "%s is not 16-byte aligned", ts[i].r.name);
+    if ((ts[i].r.lo & (ts[i].align - 1)) != 0)
+      return fail(CKDA_ERR_INVALID_ARGUMENT, "%s is not %u-byte aligned", ts[i].r.name, ts[i].align);
   }
   for (int i = 0; i < n; ++i)
     for (int j = 0; j < n; ++j) {
@@ -873,6 +874,454 @@ ckda_status_t ckda_block_norm_bwd(int64_t rows, int32_t d, int32_t io_dtype, int
   const ckda::NormArgs a{rows, d, act, eps, y, w, g, x, s, w2, nullptr, nullptr};
   const ckda::NormGrads gr{dh, dn, dy, dw, dg, dx, ds, dw2, nullptr};
   return from_hip(ckda::launch_norm_bwd(a, gr, io_dtype, workspace, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---- short convolution ----------------------------------------------------------
+namespace {
+
+// What the calls on sequences of tokens share: the batch, its packing and its size.
+ckda_status_t validate_batch(int32_t B, int32_t T, int32_t num_seqs, int32_t io_dtype, const int32_t* cu) {
+  if (io_dtype != CKDA_DTYPE_BF16 && io_dtype != CKDA_DTYPE_F32)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "io_dtype %d is not a ckda_dtype_t", io_dtype);
+  if (cu) {
+    if (B != 1) return fail(CKDA_ERR_INVALID_ARGUMENT, "cu_seqlens given with B=%d (must be 1)", B);
+    if ((reinterpret_cast<uintptr_t>(cu) & 3u) != 0)
+      return fail(CKDA_ERR_INVALID_ARGUMENT, "cu_seqlens is not 4-byte aligned");
+  } else if (num_seqs != B) {
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "num_seqs=%d must equal B=%d without cu_seqlens", num_seqs, B);
+  }
+  // walks look ahead, and a sequence and its longest piece are added in 32 bits
+  if (static_cast<int64_t>(B) * T >= (int64_t(1) << 31) - 1024 || T >= (1 << 30) ||
+      static_cast<int64_t>(num_seqs) + T >= (int64_t(1) << 31))
+    return fail(CKDA_ERR_UNSUPPORTED, "too many tokens for one launch");
+  return ok();
+}
+
+// The elements between tokens of rows of `width`, 0 meaning contiguous rows.
+bool stride_of(int64_t given, int64_t width, int64_t* stride) {
+  *stride = given == 0 ? width : given;
+  return *stride >= width;
+}
+constexpr int64_t kMaxStride = int64_t(1) << 24;  // a tile of 32 rows is addressed in 31 bits
+
+// A tensor of `tokens` rows of `width` elements, `stride` apart.
+Range rows_range(const char* name, const void* p, int64_t tokens, int64_t stride, int64_t width, int64_t es) {
+  return range(name, p, p && tokens > 0 ? ((tokens - 1) * stride + width) * es : 0);
+}
+
+ckda_status_t no_output_on(const Tensor* ts, int n, const int32_t* cu, int32_t num_seqs) {
+  if (!cu) return ok();
+  const Range rc = range("cu_seqlens", cu, 4 * (static_cast<int64_t>(num_seqs) + 1));
+  for (int i = 0; i < n; ++i)
+    if (ts[i].out && overlap(ts[i].r, rc))
+      return fail(CKDA_ERR_INVALID_ARGUMENT, "%s overlaps cu_seqlens", ts[i].r.name);
+  return ok();
+}
+
+ckda_status_t validate_conv(const ckda_conv_desc_t* d, const int32_t* cu, bool grads, ckda::ConvArgs* a) {
+  if (!d) return fail(CKDA_ERR_INVALID_ARGUMENT, "desc is NULL");
+  if (d->B <= 0 || d->T < 0 || d->D <= 0 || d->K <= 0 || d->num_seqs < 0)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "non-positive size: B=%d T=%d D=%d K=%d num_seqs=%d", d->B, d->T, d->D,
+                d->K, d->num_seqs);
+  if (d->act != CKDA_NORM_GATE_NONE && d->act != CKDA_NORM_GATE_SILU)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "act %d is neither none nor silu", d->act);
+  const ckda_status_t st = validate_batch(d->B, d->T, d->num_seqs, d->io_dtype, cu);
+  if (st != CKDA_OK) return st;
+  *a = ckda::ConvArgs{};
+  if (!stride_of(d->x_stride, d->D, &a->sx))
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "x_stride is below D=%d", d->D);
+  if (d->K < 2 || d->K > 4) return fail(CKDA_ERR_UNSUPPORTED, "no convolution kernel for K=%d (2 to 4)", d->K);
+  if (d->D > (1 << 22) || a->sx >= kMaxStride)
+    return fail(CKDA_ERR_UNSUPPORTED, "D over 2^22 or x_stride of 2^24 or more");
+  a->B = d->B;
+  a->T = d->T;
+  a->D = d->D;
+  a->K = d->K;
+  a->N = d->num_seqs;
+  a->act = d->act == CKDA_NORM_GATE_SILU;
+  a->cu = cu;
+  if (ckda::conv_threads(*a, d->io_dtype, grads) >= (int64_t(1) << 32))
+    return fail(CKDA_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ckda_conv_bwd_workspace_size(const ckda_conv_desc_t* d, int32_t packed) {
+  static const int32_t given = 0;  // only whether the batch is packed matters here
+  ckda::ConvArgs a;
+  std::string kept;  // a size that is asked for is no failed call
+  kept.swap(g_last_error);
+  const ckda_status_t st = validate_conv(d, packed ? &given : nullptr, true, &a);
+  kept.swap(g_last_error);
+  return st == CKDA_OK ? ckda::conv_bwd_workspace(a, d->io_dtype) : 0;
+}
+
+ckda_status_t ckda_conv_fwd(const ckda_conv_desc_t* d, const void* x, const float* w, const float* bias,
+                            const int32_t* cu_seqlens, const void* h0, void* y, void* ht, void* stream) {
+  ckda::ConvArgs a;
+  ckda_status_t st = validate_conv(d, cu_seqlens, false, &a);
+  if (st != CKDA_OK) return st;
+  const int64_t es = elem_bytes(d->io_dtype), tokens = static_cast<int64_t>(d->B) * d->T;
+  const int64_t state = static_cast<int64_t>(d->num_seqs) * (d->K - 1) * d->D * es;
+  const bool some = tokens > 0;
+  const Tensor ts[] = {{rows_range("x", x, tokens, a.sx, d->D, es), false, some, static_cast<uint32_t>(es)},
+                       {range("w", w, w ? 4 * static_cast<int64_t>(d->D) * d->K : 0), false, true},
+                       {range("bias", bias, bias ? 4 * static_cast<int64_t>(d->D) : 0), false, false},
+                       {range("h0", h0, h0 ? state : 0), false, false},
+                       {rows_range("y", y, tokens, d->D, d->D, es), true, some},
+                       {range("ht", ht, ht ? state : 0), true, false}};
+  if ((st = check_tensors(ts, 6, 3, 5)) != CKDA_OK) return st;
+  if ((st = no_output_on(ts, 6, cu_seqlens, d->num_seqs)) != CKDA_OK) return st;
+  if (d->num_seqs == 0) return ok();
+  a.x = x;
+  a.w = w;
+  a.bias = bias;
+  a.h0 = h0;
+  a.y = y;
+  a.ht = ht;
+  return from_hip(ckda::launch_conv_fwd(a, d->io_dtype, static_cast<hipStream_t>(stream)));
+}
+
+ckda_status_t ckda_conv_bwd(const ckda_conv_desc_t* d, const void* x, const float* w, const float* bias,
+                            const int32_t* cu_seqlens, const void* h0, const void* dy, const void* dht, void* dx,
+                            float* dw, float* dbias, void* dh0, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  ckda::ConvArgs a;
+  ckda_status_t st = validate_conv(d, cu_seqlens, true, &a);
+  if (st != CKDA_OK) return st;
+  const int64_t es = elem_bytes(d->io_dtype), tokens = static_cast<int64_t>(d->B) * d->T;
+  const int64_t state = static_cast<int64_t>(d->num_seqs) * (d->K - 1) * d->D * es;
+  const int64_t taps = 4 * static_cast<int64_t>(d->D) * d->K, vec = 4 * static_cast<int64_t>(d->D);
+  const bool some = tokens > 0;
+  const Tensor ts[] = {{rows_range("x", x, tokens, a.sx, d->D, es), false, some, static_cast<uint32_t>(es)},
+                       {range("w", w, w ? taps : 0), false, true},
+                       {range("bias", bias, bias ? vec : 0), false, false},
+                       {range("h0", h0, h0 ? state : 0), false, false},
+                       {rows_range("dy", dy, tokens, d->D, d->D, es), false, some},
+                       {range("dht", dht, dht ? state : 0), false, false},
+                       {rows_range("dx", dx, tokens, d->D, d->D, es), true, some},
+                       {range("dw", dw, dw ? taps : 0), true, true},
+                       {range("dbias", dbias, dbias ? vec : 0), true, false},
+                       {range("dh0", dh0, dh0 ? state : 0), true, false}};
+  if ((st = check_tensors(ts, 10)) != CKDA_OK) return st;
+  if ((st = no_output_on(ts, 10, cu_seqlens, d->num_seqs)) != CKDA_OK) return st;
+  const size_t need = ckda::conv_bwd_workspace(a, d->io_dtype);
+  if ((st = check_workspace(ts, 10, workspace, workspace_bytes, need)) != CKDA_OK) return st;
+  a.x = x;
+  a.w = w;
+  a.bias = bias;
+  a.h0 = h0;
+  const ckda::ConvGrads g{dy, dht, dx, dw, dbias, dh0, nullptr};
+  return from_hip(ckda::launch_conv_bwd(a, g, d->io_dtype, workspace, static_cast<hipStream_t>(stream)));
+}
+
+ckda_status_t ckda_conv_step(const ckda_conv_desc_t* d, const void* x, const float* w, const float* bias,
+                             const void* h0, void* ht, void* y, void* stream) {
+  if (d && d->B == 0 && d->num_seqs == 0) return ok();
+  ckda::ConvArgs a;
+  ckda_status_t st = validate_conv(d, nullptr, false, &a);
+  if (st != CKDA_OK) return st;
+  if (d->T != 1) return fail(CKDA_ERR_INVALID_ARGUMENT, "T=%d must be 1", d->T);
+  const int64_t es = elem_bytes(d->io_dtype), state = static_cast<int64_t>(d->B) * (d->K - 1) * d->D * es;
+  const Tensor ts[] = {{rows_range("x", x, d->B, a.sx, d->D, es), false, true, static_cast<uint32_t>(es)},
+                       {range("w", w, 4 * static_cast<int64_t>(d->D) * d->K), false, true},
+                       {range("bias", bias, bias ? 4 * static_cast<int64_t>(d->D) : 0), false, false},
+                       {range("h0", h0, state), false, true},
+                       {range("ht", ht, state), true, true},
+                       {rows_range("y", y, d->B, d->D, d->D, es), true, true}};
+  if ((st = check_tensors(ts, 6, 3, 4)) != CKDA_OK) return st;
+  a.x = x;
+  a.w = w;
+  a.bias = bias;
+  a.h0 = h0;
+  a.y = y;
+  a.ht = ht;
+  return from_hip(ckda::launch_conv_step(a, d->io_dtype, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---- selective scan ---------------------------------------------------------------
+namespace {
+
+enum ScanCall { kScanFwd, kScanBwd, kScanStep };
+
+ckda_status_t validate_scan(const ckda_scan_desc_t* d, const int32_t* cu, ScanCall call, ckda::ScanArgs* a) {
+  if (!d) return fail(CKDA_ERR_INVALID_ARGUMENT, "desc is NULL");
+  if (d->B <= 0 || d->T < 0 || d->D <= 0 || d->S <= 0 || d->num_seqs < 0)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "non-positive size: B=%d T=%d D=%d S=%d num_seqs=%d", d->B, d->T, d->D,
+                d->S, d->num_seqs);
+  if (d->groups <= 0 || d->D % d->groups != 0)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "groups %d does not divide D=%d", d->groups, d->D);
+  if (d->softplus != 0 && d->softplus != 1) return fail(CKDA_ERR_INVALID_ARGUMENT, "softplus must be 0 or 1");
+  const ckda_status_t st = validate_batch(d->B, d->T, d->num_seqs, d->io_dtype, cu);
+  if (st != CKDA_OK) return st;
+  if (!ckda::scan_supported(d->S)) return fail(CKDA_ERR_UNSUPPORTED, "no scan kernel for S=%d (1 to 64)", d->S);
+  if (d->D > (1 << 20)) return fail(CKDA_ERR_UNSUPPORTED, "D over 2^20");
+  *a = ckda::ScanArgs{};
+  const int64_t bc = static_cast<int64_t>(d->groups) * d->S;
+  if (!stride_of(d->x_stride, d->D, &a->sx) || !stride_of(d->dt_stride, d->D, &a->sdt) ||
+      !stride_of(d->z_stride, d->D, &a->sz) || !stride_of(d->b_stride, bc, &a->sb) ||
+      !stride_of(d->c_stride, bc, &a->sc))
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "a stride is below its row");
+  for (int64_t s : {a->sx, a->sdt, a->sz, a->sb, a->sc})
+    if (s >= kMaxStride) return fail(CKDA_ERR_UNSUPPORTED, "a stride of 2^24 or more");
+  a->B = d->B;
+  a->T = d->T;
+  a->D = d->D;
+  a->S = d->S;
+  a->G = d->groups;
+  a->N = d->num_seqs;
+  a->softplus = d->softplus;
+  a->cu = cu;
+  if ((call == kScanStep ? ckda::scan_step_threads(*a) : ckda::scan_threads(*a, call == kScanBwd)) >= (int64_t(1) << 32))
+    return fail(CKDA_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
+  return ok();
+}
+
+size_t scan_workspace(const ckda_scan_desc_t* d, int32_t packed, ScanCall call) {
+  static const int32_t given = 0;  // only whether the batch is packed matters here
+  ckda::ScanArgs a;
+  std::string kept;  // a size that is asked for is no failed call
+  kept.swap(g_last_error);
+  const ckda_status_t st = validate_scan(d, packed ? &given : nullptr, call, &a);
+  kept.swap(g_last_error);
+  if (st != CKDA_OK || (call == kScanFwd && d->num_seqs == 0)) return 0;
+  return call == kScanFwd ? ckda::scan_fwd_workspace(a) : ckda::scan_bwd_workspace(a);
+}
+
+struct ScanSizes {
+  int64_t es, tokens, bc, state, A, vec;  // bytes of an element, tokens, states of a token's groups; bytes
+};
+ScanSizes scan_sizes(const ckda_scan_desc_t* d) {
+  ScanSizes z;
+  z.es = elem_bytes(d->io_dtype);
+  z.tokens = static_cast<int64_t>(d->B) * d->T;
+  z.bc = static_cast<int64_t>(d->groups) * d->S;
+  z.A = 4 * static_cast<int64_t>(d->D) * d->S;
+  z.state = z.A * d->num_seqs;
+  z.vec = 4 * static_cast<int64_t>(d->D);
+  return z;
+}
+
+// Whether rows can move in 16-byte accesses: every base and stride a multiple,
+// and every group's channels whole vectors.
+bool scan_vec(const ckda::ScanArgs& a, int64_t es) {
+  const int64_t n = 8;  // a thread's channels at most, in either type
+  const auto fits = [&](const void* p, int64_t stride) { return aligned16(p) && stride * es % 16 == 0; };
+  return (a.D / a.G) % n == 0 && fits(a.x, a.sx) && fits(a.dt, a.sdt) && (!a.z || fits(a.z, a.sz));
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t ckda_scan_supported(int32_t S) { return ckda::scan_supported(S) ? 1 : 0; }
+
+size_t ckda_scan_fwd_workspace_size(const ckda_scan_desc_t* d, int32_t packed) {
+  return scan_workspace(d, packed, kScanFwd);
+}
+size_t ckda_scan_bwd_workspace_size(const ckda_scan_desc_t* d, int32_t packed) {
+  return scan_workspace(d, packed, kScanBwd);
+}
+
+ckda_status_t ckda_scan_fwd(const ckda_scan_desc_t* d, const void* x, const void* dt, const float* A,
+                            const void* B, const void* C, const float* D, const void* z, const float* dt_bias,
+                            const int32_t* cu_seqlens, const float* h0, void* y, float* ht, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  ckda::ScanArgs a;
+  ckda_status_t st = validate_scan(d, cu_seqlens, kScanFwd, &a);
+  if (st != CKDA_OK) return st;
+  const ScanSizes s = scan_sizes(d);
+  const bool some = s.tokens > 0;
+  const uint32_t el = static_cast<uint32_t>(s.es);
+  const Tensor ts[] = {{rows_range("x", x, s.tokens, a.sx, d->D, s.es), false, some, el},
+                       {rows_range("dt", dt, s.tokens, a.sdt, d->D, s.es), false, some, el},
+                       {range("A", A, A ? s.A : 0), false, true},
+                       {rows_range("B", B, s.tokens, a.sb, s.bc, s.es), false, some, el},
+                       {rows_range("C", C, s.tokens, a.sc, s.bc, s.es), false, some, el},
+                       {range("D", D, D ? s.vec : 0), false, false},
+                       {rows_range("z", z, s.tokens, a.sz, d->D, s.es), false, false, el},
+                       {range("dt_bias", dt_bias, dt_bias ? s.vec : 0), false, false},
+                       {range("h0", h0, h0 ? s.state : 0), false, false},
+                       {rows_range("y", y, s.tokens, d->D, d->D, s.es), true, some},
+                       {range("ht", ht, ht ? s.state : 0), true, false}};
+  if ((st = check_tensors(ts, 11, 8, 10)) != CKDA_OK) return st;
+  if ((st = no_output_on(ts, 11, cu_seqlens, d->num_seqs)) != CKDA_OK) return st;
+  const size_t need = d->num_seqs == 0 ? 0 : ckda::scan_fwd_workspace(a);
+  if ((st = check_workspace(ts, 11, workspace, workspace_bytes, need)) != CKDA_OK) return st;
+  if (d->num_seqs == 0) return ok();
+  a.x = x;
+  a.dt = dt;
+  a.A = A;
+  a.Bm = B;
+  a.Cm = C;
+  a.Dv = D;
+  a.z = z;
+  a.bias = dt_bias;
+  a.h0 = h0;
+  a.y = y;
+  a.ht = ht;
+  a.vec = scan_vec(a, s.es);
+  return from_hip(ckda::launch_scan_fwd(a, d->io_dtype, workspace, static_cast<hipStream_t>(stream)));
+}
+
+ckda_status_t ckda_scan_bwd(const ckda_scan_desc_t* d, const void* x, const void* dt, const float* A,
+                            const void* B, const void* C, const float* D, const void* z, const float* dt_bias,
+                            const int32_t* cu_seqlens, const float* h0, const void* dy, const float* dht, void* dx,
+                            void* ddt, float* dA, void* dB, void* dC, float* dD, void* dz, float* ddt_bias,
+                            float* dh0, void* workspace, size_t workspace_bytes, void* stream) {
+  ckda::ScanArgs a;
+  ckda_status_t st = validate_scan(d, cu_seqlens, kScanBwd, &a);
+  if (st != CKDA_OK) return st;
+  const ScanSizes s = scan_sizes(d);
+  const bool some = s.tokens > 0;
+  if (some && (z == nullptr) != (dz == nullptr))
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "dz is given exactly with z");
+  if ((D == nullptr) != (dD == nullptr)) return fail(CKDA_ERR_INVALID_ARGUMENT, "dD is given exactly with D");
+  if ((dt_bias == nullptr) != (ddt_bias == nullptr))
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "ddt_bias is given exactly with dt_bias");
+  const uint32_t el = static_cast<uint32_t>(s.es);
+  const Tensor ts[] = {{rows_range("x", x, s.tokens, a.sx, d->D, s.es), false, some, el},
+                       {rows_range("dt", dt, s.tokens, a.sdt, d->D, s.es), false, some, el},
+                       {range("A", A, A ? s.A : 0), false, true},
+                       {rows_range("B", B, s.tokens, a.sb, s.bc, s.es), false, some, el},
+                       {rows_range("C", C, s.tokens, a.sc, s.bc, s.es), false, some, el},
+                       {range("D", D, D ? s.vec : 0), false, false},
+                       {rows_range("z", z, s.tokens, a.sz, d->D, s.es), false, false, el},
+                       {range("dt_bias", dt_bias, dt_bias ? s.vec : 0), false, false},
+                       {range("h0", h0, h0 ? s.state : 0), false, false},
+                       {rows_range("dy", dy, s.tokens, d->D, d->D, s.es), false, some},
+                       {range("dht", dht, dht ? s.state : 0), false, false},
+                       {rows_range("dx", dx, s.tokens, d->D, d->D, s.es), true, some},
+                       {rows_range("ddt", ddt, s.tokens, d->D, d->D, s.es), true, some},
+                       {range("dA", dA, dA ? s.A : 0), true, true},
+                       {rows_range("dB", dB, s.tokens, s.bc, s.bc, s.es), true, some},
+                       {rows_range("dC", dC, s.tokens, s.bc, s.bc, s.es), true, some},
+                       {range("dD", dD, dD ? s.vec : 0), true, false},
+                       {rows_range("dz", dz, s.tokens, d->D, d->D, s.es), true, false},
+                       {range("ddt_bias", ddt_bias, ddt_bias ? s.vec : 0), true, false},
+                       {range("dh0", dh0, dh0 ? s.state : 0), true, false}};
+  if ((st = check_tensors(ts, 20)) != CKDA_OK) return st;
+  if ((st = no_output_on(ts, 20, cu_seqlens, d->num_seqs)) != CKDA_OK) return st;
+  const size_t need = ckda::scan_bwd_workspace(a);
+  if ((st = check_workspace(ts, 20, workspace, workspace_bytes, need)) != CKDA_OK) return st;
+  a.x = x;
+  a.dt = dt;
+  a.A = A;
+  a.Bm = B;
+  a.Cm = C;
+  a.Dv = D;
+  a.z = z;
+  a.bias = dt_bias;
+  a.h0 = h0;
+  a.dy = dy;
+  a.dht = dht;
+  a.dx = dx;
+  a.ddt = ddt;
+  a.dA = dA;
+  a.dB = dB;
+  a.dC = dC;
+  a.dD = dD;
+  a.dz = dz;
+  a.dbias = ddt_bias;
+  a.dh0 = dh0;
+  a.vec = scan_vec(a, s.es);
+  return from_hip(ckda::launch_scan_bwd(a, d->io_dtype, workspace, static_cast<hipStream_t>(stream)));
+}
+
+ckda_status_t ckda_scan_step(const ckda_scan_desc_t* d, const void* x, const void* dt, const float* A,
+                             const void* B, const void* C, const float* D, const void* z, const float* dt_bias,
+                             const float* h0, float* ht, void* y, void* stream) {
+  if (d && d->B == 0 && d->num_seqs == 0) return ok();
+  ckda::ScanArgs a;
+  ckda_status_t st = validate_scan(d, nullptr, kScanStep, &a);
+  if (st != CKDA_OK) return st;
+  if (d->T != 1) return fail(CKDA_ERR_INVALID_ARGUMENT, "T=%d must be 1", d->T);
+  const ScanSizes s = scan_sizes(d);
+  if (s.state > (int64_t(1) << 33))
+    return fail(CKDA_ERR_UNSUPPORTED, "N * D * S exceeds 2^31 for one decode launch");
+  const uint32_t el = static_cast<uint32_t>(s.es);
+  const Tensor ts[] = {{rows_range("x", x, s.tokens, a.sx, d->D, s.es), false, true, el},
+                       {rows_range("dt", dt, s.tokens, a.sdt, d->D, s.es), false, true, el},
+                       {range("A", A, s.A), false, true},
+                       {rows_range("B", B, s.tokens, a.sb, s.bc, s.es), false, true, el},
+                       {rows_range("C", C, s.tokens, a.sc, s.bc, s.es), false, true, el},
+                       {range("D", D, D ? s.vec : 0), false, false},
+                       {rows_range("z", z, s.tokens, a.sz, d->D, s.es), false, false, el},
+                       {range("dt_bias", dt_bias, dt_bias ? s.vec : 0), false, false},
+                       {range("h0", h0, s.state), false, true},
+                       {range("ht", ht, s.state), true, true},
+                       {rows_range("y", y, s.tokens, d->D, d->D, s.es), true, true}};
+  if ((st = check_tensors(ts, 11, 8, 9)) != CKDA_OK) return st;
+  a.x = x;
+  a.dt = dt;
+  a.A = A;
+  a.Bm = B;
+  a.Cm = C;
+  a.Dv = D;
+  a.z = z;
+  a.bias = dt_bias;
+  a.h0 = h0;
+  a.ht = ht;
+  a.y = y;
+  return from_hip(ckda::launch_scan_step(a, d->io_dtype, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---- layer norm ---------------------------------------------------------------------
+extern "C" {
+
+size_t ckda_layer_norm_bwd_workspace_size(int64_t rows, int32_t d, int32_t io_dtype) {
+  if (rows <= 0 || d <= 0 || d > 16384) return 0;
+  if (io_dtype != CKDA_DTYPE_BF16 && io_dtype != CKDA_DTYPE_F32) return 0;
+  return ckda::layer_norm_bwd_workspace(rows, d, io_dtype);
+}
+
+ckda_status_t ckda_layer_norm(int64_t rows, int32_t d, int32_t io_dtype, float eps, const void* x, const void* r,
+                              const float* w, const float* b, void* n, void* h, void* stream) {
+  ckda_status_t st = validate_norm(rows, d, io_dtype, CKDA_NORM_GATE_NONE, eps, nullptr);
+  if (st != CKDA_OK) return st;
+  if ((r == nullptr) != (h == nullptr) && rows > 0)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "h is given exactly with r");
+  const int64_t by = rows * d * elem_bytes(io_dtype), v = 4 * static_cast<int64_t>(d);
+  const bool some = rows > 0;
+  // h may be the very buffer of r or of x: a row is read before it is written
+  const bool same = h != nullptr && (h == r || h == x);
+  const Tensor ts[] = {{range("x", x, x ? by : 0), false, some}, {range("r", r, r ? by : 0), false, false},
+                       {range("w", w, w ? v : 0), false, false}, {range("b", b, b ? v : 0), false, false},
+                       {range("n", n, n ? by : 0), true, some},  {range("h", h, h ? by : 0), true, false}};
+  if ((st = check_tensors(ts, 6, same && h == x ? 0 : 1, 5)) != CKDA_OK) return st;
+  if (rows == 0) return ok();
+  const ckda::LayerNormArgs a{rows, d, eps, x, r, w, b, n, h};
+  return from_hip(ckda::launch_layer_norm(a, io_dtype, static_cast<hipStream_t>(stream)));
+}
+
+ckda_status_t ckda_layer_norm_bwd(int64_t rows, int32_t d, int32_t io_dtype, float eps, const void* x,
+                                  const float* w, const void* dn, const void* dh, void* dx, float* dw, float* db,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  ckda_status_t st = validate_norm(rows, d, io_dtype, CKDA_NORM_GATE_NONE, eps, nullptr);
+  if (st != CKDA_OK) return st;
+  if (rows == 0)
+    return fail(CKDA_ERR_INVALID_ARGUMENT, "no rows: the sums over rows would not be written");
+  if ((w == nullptr) != (dw == nullptr)) return fail(CKDA_ERR_INVALID_ARGUMENT, "dw is given exactly with w");
+  const int64_t by = rows * d * elem_bytes(io_dtype), v = 4 * static_cast<int64_t>(d);
+  const Tensor ts[] = {{range("x", x, x ? by : 0), false, true},   {range("w", w, w ? v : 0), false, false},
+                       {range("dn", dn, dn ? by : 0), false, true}, {range("dh", dh, dh ? by : 0), false, false},
+                       {range("dx", dx, dx ? by : 0), true, true}, {range("dw", dw, dw ? v : 0), true, false},
+                       {range("db", db, db ? v : 0), true, false}};
+  if ((st = check_tensors(ts, 7)) != CKDA_OK) return st;
+  const size_t need = ckda_layer_norm_bwd_workspace_size(rows, d, io_dtype);
+  if ((st = check_workspace(ts, 7, workspace, workspace_bytes, need)) != CKDA_OK) return st;
+  const ckda::LayerNormArgs a{rows, d, eps, x, nullptr, w, nullptr, nullptr, nullptr};
+  const ckda::LayerNormGrads g{dn, dh, dx, dw, db, nullptr};
+  return from_hip(ckda::launch_layer_norm_bwd(a, g, io_dtype, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

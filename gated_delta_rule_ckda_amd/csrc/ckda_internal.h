@@ -270,6 +270,112 @@ size_t norm_bwd_workspace(int64_t rows, int32_t d, int32_t io_dtype);
 launch_result launch_norm_fwd(const NormArgs& a, int32_t io_dtype, hipStream_t s);
 launch_result launch_norm_bwd(const NormArgs& a, NormGrads g, int32_t io_dtype, void* ws, hipStream_t s);
 
+// Short causal convolution (conv.hip).  Sequences are cut into tiles of tokens,
+// one a thread and vector of channels.
+struct ConvArgs {
+  int32_t B, T, D, K, N;
+  int32_t act;         // 1: silu
+  int64_t sx;          // elements between the tokens of x
+  const void* x;
+  const float* w;      // [D][K]
+  const float* bias;   // [D] or null
+  const int32_t* cu;   // null for a dense batch
+  const void* h0;      // [N][K-1][D] or null
+  void* y;
+  void* ht;
+  int32_t tile, slots; // tokens of a tile, tile slots over all sequences
+};
+struct ConvGrads {
+  const void* dy;
+  const void* dht;
+  void* dx;
+  float* dw;
+  float* dbias;
+  void* dh0;
+  float* part;         // [workgroups along the slots][K + 1][D]
+};
+// Threads of a call's largest launch (a launch counts them in 32 bits).
+int64_t conv_threads(const ConvArgs& a, int32_t io_dtype, bool grads);
+size_t conv_bwd_workspace(const ConvArgs& a, int32_t io_dtype);
+launch_result launch_conv_fwd(ConvArgs a, int32_t io_dtype, hipStream_t s);
+launch_result launch_conv_bwd(ConvArgs a, ConvGrads g, int32_t io_dtype, void* ws, hipStream_t s);
+launch_result launch_conv_step(const ConvArgs& a, int32_t io_dtype, hipStream_t s);
+
+// Selective scan (scan.hip, scan_bwd.hip).
+struct ScanArgs {
+  int32_t B, T, D, S, G, N;
+  int32_t softplus;    // 1: steps are softplus(dt + bias), 0: dt + bias
+  int32_t vec;         // 1: the rows of x, dt, z, y and their gradients move in 16-byte accesses
+  int64_t sx, sdt, sz, sb, sc;  // elements between the tokens of x, dt, z, B and C
+  const void* x;
+  const void* dt;
+  const float* A;      // [D][S]
+  const void* Bm;      // [tokens][G][S], as Cm
+  const void* Cm;
+  const float* Dv;     // [D] or null, as bias
+  const void* z;       // or null
+  const float* bias;
+  const int32_t* cu;   // null for a dense batch
+  const float* h0;     // [N][D][S] or null
+  void* y;
+  float* ht;
+  // pieces of a sequence run side by side (seg: tokens of a piece)
+  int32_t seg, slots;
+  int32_t cut;         // 1: sequences may have more than one piece
+  float* entry;        // [slots][blocks][SP][CH] what enters a piece
+  float* span;         // [slots][blocks][CH] the sum of a piece's steps
+  float* marks;        // [mark slots][blocks][SP][CH] the state entering every 16 tokens
+  int32_t mslots;
+  // gradients
+  const void* dy;
+  const float* dht;
+  void* dx;
+  void* ddt;
+  void* dB;
+  void* dC;
+  void* dz;
+  float* dA;
+  float* dD;
+  float* dbias;
+  float* dh0;
+  float* partbc;       // [blocks][tokens][2][SP] sums over a block's channels for dB and dC
+  float* partA;        // [slots][blocks][SP][CH]
+  float* partD;        // [slots][blocks][2][CH]
+};
+bool scan_supported(int32_t S);
+int64_t scan_threads(const ScanArgs& a, bool grads);
+int64_t scan_step_threads(const ScanArgs& a);
+size_t scan_fwd_workspace(const ScanArgs& a);
+size_t scan_bwd_workspace(const ScanArgs& a);
+launch_result launch_scan_fwd(ScanArgs a, int32_t io_dtype, void* ws, hipStream_t s);
+launch_result launch_scan_bwd(ScanArgs a, int32_t io_dtype, void* ws, hipStream_t s);
+launch_result launch_scan_step(const ScanArgs& a, int32_t io_dtype, hipStream_t s);
+
+// Layer norm (layer_norm.hip); null: that part is absent.
+struct LayerNormArgs {
+  int64_t rows;
+  int32_t d;
+  float eps;
+  const void* x;       // [rows][d], as r, n and h
+  const void* r;
+  const float* w;      // [d], as b
+  const float* b;
+  void* n;
+  void* h;
+};
+struct LayerNormGrads {
+  const void* dn;
+  const void* dh;
+  void* dx;
+  float* dw;
+  float* db;
+  float* part;         // [workgroups][2][d]
+};
+size_t layer_norm_bwd_workspace(int64_t rows, int32_t d, int32_t io_dtype);
+launch_result launch_layer_norm(const LayerNormArgs& a, int32_t io_dtype, hipStream_t s);
+launch_result launch_layer_norm_bwd(const LayerNormArgs& a, LayerNormGrads g, int32_t io_dtype, void* ws,
+                                    hipStream_t s);
+
 // ---- small device helpers shared by the kernels --------------------------
 
 // bf16 <-> f32.  Conversion to bf16 rounds to nearest even (finite inputs).

@@ -1,0 +1,305 @@
+// Layer norm of rows of d elements, with the residual add before it:
+//
+//   h = r + x                         (x itself without r)
+//   n = (h - mean h) rstd w + b       rstd = 1 / sqrt(mean (h - mean h)^2 + eps)
+//
+// n is formed from h before its rounding; the variance is that of the centred
+// row, so a mean far above the spread costs no digits.  Backwards, with
+// c = (h - mean h) rstd and m = dn w,
+//
+//   dw = sum_rows dn c,  db = sum_rows dn
+//   dx = dh + rstd (m - mean m - c mean(m c))
+//
+// Bound by HBM: every activation is read and written once.  Layout of threads
+// and rows as for the norms around a block: TPR threads a row, weights and sums
+// over rows in registers, workgroups walking over rows.
+#include "row_ops.h"
+
+namespace ckda {
+namespace {
+
+template <class IO, int VEC, int EPL, int NT>
+__global__ __launch_bounds__(NT) void layer_norm_kernel(LayerNormArgs a, int tpr) {
+  constexpr int K = EPL / VEC;
+  using X = Vec<IO, VEC>;
+  __shared__ float red[4 * (NT / 64)];
+  int half = 0;
+  const int t = threadIdx.x, lane = t & (tpr - 1);
+  const int rpb = NT / tpr;  // rows a workgroup and step
+  float w[EPL], b[EPL];
+  bool ok[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (lane + tpr * k) * VEC;
+    ok[k] = c < a.d;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      w[k * VEC + e] = a.w && ok[k] ? a.w[c + e] : 1.f;
+      b[k * VEC + e] = a.b && ok[k] ? a.b[c + e] : 0.f;
+    }
+  }
+  const float inv_d = 1.f / a.d;
+  // every thread of a workgroup takes the same number of steps (barriers)
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * rpb) {
+    const int64_t row = r0 + t / tpr;
+    const bool live = row < a.rows;
+    typename X::V vx[K], vr[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = row * a.d + (lane + tpr * k) * VEC;
+      vx[k] = typename X::V{};
+      vr[k] = vx[k];
+      if (live && ok[k]) {
+        vx[k] = X::load(a.x, i);
+        if (a.r) vr[k] = X::load(a.r, i);
+      }
+    }
+    float h[EPL], s[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int j = k * VEC + e;
+        h[j] = X::get(vx[k], e) + (a.r ? X::get(vr[k], e) : 0.f);
+        s[0] += h[j];
+      }
+    if (a.h && live) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (ok[k]) X::store(a.h, row * a.d + (lane + tpr * k) * VEC, h + k * VEC);
+    }
+    row_sum<1, NT>(s, tpr, red, half);
+    const float mean = s[0] * inv_d;
+    s[0] = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int j = k * VEC + e;
+        h[j] = ok[k] ? h[j] - mean : 0.f;
+        s[0] += h[j] * h[j];
+      }
+    row_sum<1, NT>(s, tpr, red, half);
+    const float rstd = 1.f / sqrtf(s[0] * inv_d + a.eps);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) h[j] = h[j] * rstd * w[j] + b[j];
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (ok[k]) X::store(a.n, row * a.d + (lane + tpr * k) * VEC, h + k * VEC);
+    }
+  }
+}
+
+// Gradients; each workgroup leaves its rows' sums for dw and db in
+// part[workgroup][2][d].
+template <class IO, int VEC, int EPL, int NT>
+__global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(LayerNormArgs a, LayerNormGrads g, int tpr) {
+  constexpr int K = EPL / VEC;
+  using X = Vec<IO, VEC>;
+  __shared__ float red[2 * 3 * (NT / 64)];
+  extern __shared__ float cols[];  // [rows a step][d] for rows of less than a workgroup
+  int half = 0;
+  const int t = threadIdx.x, lane = t & (tpr - 1);
+  const int rpb = NT / tpr;
+  float w[EPL], dw[EPL], db[EPL];
+  bool ok[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (lane + tpr * k) * VEC;
+    ok[k] = c < a.d;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      w[k * VEC + e] = ok[k] ? (a.w ? a.w[c + e] : 1.f) : 0.f;
+      dw[k * VEC + e] = db[k * VEC + e] = 0.f;
+    }
+  }
+  const float inv_d = 1.f / a.d;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rpb; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * rpb) {
+    const int64_t row = r0 + t / tpr;
+    const bool live = row < a.rows;
+    typename X::V vx[K], vn[K], vh[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t i = row * a.d + (lane + tpr * k) * VEC;
+      vx[k] = typename X::V{};
+      vn[k] = vh[k] = vx[k];
+      if (live && ok[k]) {
+        vx[k] = X::load(a.x, i);
+        vn[k] = X::load(g.dn, i);
+        if (g.dh) vh[k] = X::load(g.dh, i);
+      }
+    }
+    float h[EPL], s1[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        h[k * VEC + e] = X::get(vx[k], e);
+        s1[0] += h[k * VEC + e];
+      }
+    row_sum<1, NT, 3>(s1, tpr, red, half);
+    const float mean = s1[0] * inv_d;
+    float s[3] = {0.f, 0.f, 0.f};  // of (h - mean)^2, m, m (h - mean)
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int j = k * VEC + e;
+        h[j] = ok[k] ? h[j] - mean : 0.f;
+        const float m = X::get(vn[k], e) * w[j];
+        s[0] += h[j] * h[j];
+        s[1] += m;
+        s[2] += m * h[j];
+      }
+    row_sum<3, NT, 3>(s, tpr, red, half);
+    // with eps = 0 a thread without a row would add inf * 0 to its sums over rows
+    const float rstd = live ? 1.f / sqrtf(s[0] * inv_d + a.eps) : 0.f;
+    const float mm = s[1] * inv_d, mc = s[2] * inv_d * rstd;
+    float dx[EPL];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int j = k * VEC + e;
+        const float c = h[j] * rstd, dn = X::get(vn[k], e);
+        dw[j] += dn * c;
+        db[j] += dn;
+        dx[j] = rstd * (dn * w[j] - mm - c * mc);
+        if (g.dh) dx[j] += X::get(vh[k], e);
+      }
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (ok[k]) X::store(g.dx, row * a.d + (lane + tpr * k) * VEC, dx + k * VEC);
+    }
+  }
+  // sums over the rows of this workgroup, row groups in order
+  float* out = g.part + static_cast<int64_t>(blockIdx.x) * 2 * a.d;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if (!(q == 0 ? g.dw : g.db)) continue;
+    const float* sum = q == 0 ? dw : db;
+    if (rpb == 1) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (ok[k])
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) out[q * a.d + (lane + tpr * k) * VEC + e] = sum[k * VEC + e];
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (ok[k])
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) cols[(t / tpr) * a.d + (lane + tpr * k) * VEC + e] = sum[k * VEC + e];
+      __syncthreads();
+      for (int c = t; c < a.d; c += NT) {
+        float v = 0.f;
+        for (int j = 0; j < rpb; ++j) v += cols[j * a.d + c];
+        out[q * a.d + c] = v;
+      }
+    }
+  }
+}
+
+// out[c] = sum over workgroups of part[.][q][c]: 32 columns a workgroup, its
+// 32 groups of lanes taking every 32nd workgroup's; their sums are added in order.
+__global__ __launch_bounds__(1024) void layer_norm_cols_kernel(const float* part, int parts, int d, float* dw,
+                                                               float* db) {
+  __shared__ float red[32][33];
+  const int q = blockIdx.y, l = threadIdx.x & 31, c = blockIdx.x * 32 + l, grp = threadIdx.x >> 5;
+  float* out = q == 0 ? dw : db;
+  if (!out) return;
+  float v = 0.f;
+  if (c < d)
+    for (int p = grp; p < parts; p += 32) v += part[(static_cast<int64_t>(p) * 2 + q) * d + c];
+  red[grp][l] = v;
+  __syncthreads();
+  if (grp == 0 && c < d) {
+    for (int i = 1; i < 32; ++i) v += red[i][l];
+    out[c] = v;
+  }
+}
+
+// How rows of d elements are held: EPL elements a thread, TPR threads.
+struct Shape {
+  int vec, epl, tpr, nt;
+};
+Shape shape_of(int d, int es) {
+  Shape s;
+  s.vec = 16 / es;
+  while (d % s.vec != 0) s.vec /= 2;
+  s.nt = d > 8192 ? 1024 : 256;
+  s.epl = d <= 2048 ? 8 : (d <= 4096 || d > 8192 ? 16 : 32);
+  s.tpr = 4;
+  while (s.tpr * s.epl < d) s.tpr *= 2;
+  return s;
+}
+
+int64_t grid_of(int64_t rows, const Shape& s, int64_t most) {
+  const int64_t steps = (rows + s.nt / s.tpr - 1) / (s.nt / s.tpr);
+  return steps < most ? steps : most;
+}
+
+constexpr int64_t kFwdGroups = 1024;
+int64_t bwd_groups(const Shape& s) { return s.nt == 1024 ? 256 : (s.epl == 8 ? 1024 : 512); }
+
+template <class IO, int VEC, int EPL, int NT>
+launch_result launch_one(const LayerNormArgs& a, const LayerNormGrads* g, const Shape& s, hipStream_t st) {
+  if (!g) {
+    hipLaunchKernelGGL((layer_norm_kernel<IO, VEC, EPL, NT>),
+                       dim3(static_cast<unsigned>(grid_of(a.rows, s, kFwdGroups))), dim3(NT), 0, st, a, s.tpr);
+    return hipGetLastError();
+  }
+  const int64_t grid = grid_of(a.rows, s, bwd_groups(s));
+  const int rpb = NT / s.tpr;
+  const size_t lds = rpb > 1 ? static_cast<size_t>(rpb) * a.d * 4 : 0;
+  hipLaunchKernelGGL((layer_norm_bwd_kernel<IO, VEC, EPL, NT>), dim3(static_cast<unsigned>(grid)), dim3(NT), lds,
+                     st, a, *g, s.tpr);
+  const launch_result e = hipGetLastError();
+  if (e != hipSuccess || (!g->dw && !g->db)) return e;
+  hipLaunchKernelGGL(layer_norm_cols_kernel, dim3((a.d + 31) / 32, 2), dim3(1024), 0, st, g->part,
+                     static_cast<int>(grid), a.d, g->dw, g->db);
+  return hipGetLastError();
+}
+
+template <class IO, int VEC>
+launch_result launch_vec(const LayerNormArgs& a, const LayerNormGrads* g, const Shape& s, hipStream_t st) {
+  if (s.nt == 1024) return launch_one<IO, VEC, 16, 1024>(a, g, s, st);
+  if (s.epl == 8) return launch_one<IO, VEC, 8, 256>(a, g, s, st);
+  if (s.epl == 16) return launch_one<IO, VEC, 16, 256>(a, g, s, st);
+  return launch_one<IO, VEC, 32, 256>(a, g, s, st);
+}
+
+launch_result launch(const LayerNormArgs& a, const LayerNormGrads* g, int32_t io_dtype, hipStream_t st) {
+  const Shape s = shape_of(a.d, io_dtype == CKDA_DTYPE_BF16 ? 2 : 4);
+  if (io_dtype == CKDA_DTYPE_BF16) {
+    if (s.vec == 8) return launch_vec<io_bf16, 8>(a, g, s, st);
+    if (s.vec == 4) return launch_vec<io_bf16, 4>(a, g, s, st);
+    if (s.vec == 2) return launch_vec<io_bf16, 2>(a, g, s, st);
+    return launch_vec<io_bf16, 1>(a, g, s, st);
+  }
+  if (s.vec == 4) return launch_vec<io_f32, 4>(a, g, s, st);
+  if (s.vec == 2) return launch_vec<io_f32, 2>(a, g, s, st);
+  return launch_vec<io_f32, 1>(a, g, s, st);
+}
+
+}  // namespace
+
+size_t layer_norm_bwd_workspace(int64_t rows, int32_t d, int32_t io_dtype) {
+  const Shape s = shape_of(d, io_dtype == CKDA_DTYPE_BF16 ? 2 : 4);
+  return static_cast<size_t>(grid_of(rows, s, bwd_groups(s))) * 2 * d * 4;
+}
+
+launch_result launch_layer_norm(const LayerNormArgs& a, int32_t io_dtype, hipStream_t s) {
+  return launch(a, nullptr, io_dtype, s);
+}
+
+launch_result launch_layer_norm_bwd(const LayerNormArgs& a, LayerNormGrads g, int32_t io_dtype, void* ws,
+                                    hipStream_t s) {
+  g.part = static_cast<float*>(ws);
+  return launch(a, &g, io_dtype, s);
+}
+
+}  // namespace ckda

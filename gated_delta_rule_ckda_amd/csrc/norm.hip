@@ -22,96 +22,12 @@
 // long for 256 threads.  Measured in bf16: 524288 rows of 128 with a gate 72 us
 // (5.6 TB/s), gradients of 32768 rows of 2048 with all parts 213 us (5.0 TB/s;
 // a copy of 2 GB runs at 5.0).
-#include "mfma_ops.h"
+#include "row_ops.h"
 
 namespace ckda {
 namespace {
 
 enum { kActNone = 0, kActSigmoid = 1, kActSilu = 2 };
-
-template <class IO>
-__device__ __forceinline__ float sigmoid_of(float x) {
-  // off by 1e-6 of the value at most in the fast form, far below bf16's rounding
-  if constexpr (sizeof(typename IO::storage) == 2)
-    return __builtin_amdgcn_rcpf(1.f + exp_neg(x));
-  else
-    return 1.f / (1.f + expf(-x));
-}
-
-// sigmoid p and its derivative q = e p^2, e = exp(-x): p (1 - p) would lose the
-// digits of q where p is next to 1 (a percent at 12, all of it from 17 on).
-// Where e overflows p is 0, and so is q.
-template <class IO>
-__device__ __forceinline__ void sigmoid_and_slope(float x, float& p, float& q) {
-  float e;
-  if constexpr (sizeof(typename IO::storage) == 2) {
-    e = exp_neg(x);
-    p = __builtin_amdgcn_rcpf(1.f + e);
-  } else {
-    e = expf(-x);
-    p = 1.f / (1.f + e);
-  }
-  q = p == 0.f ? 0.f : e * p * p;
-}
-
-// VEC elements at p (aligned to VEC elements), widened
-template <class IO, int VEC>
-struct Vec {
-  using T = typename IO::storage;
-  typedef T V __attribute__((ext_vector_type(VEC)));
-  static __device__ __forceinline__ V load(const void* p, int64_t i) {
-    return __builtin_nontemporal_load(reinterpret_cast<const V*>(static_cast<const T*>(p) + i));
-  }
-  static __device__ __forceinline__ float get(const V& v, int e) {
-    T x;
-    if constexpr (VEC == 1)
-      x = v[0];
-    else
-      x = v[e];
-    if constexpr (sizeof(T) == 2)
-      return bf16_to_f32(x);
-    else
-      return x;
-  }
-  static __device__ __forceinline__ void store(void* p, int64_t i, const float* x) {
-    V v;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      if constexpr (sizeof(T) == 2) {
-        const __bf16 b = static_cast<__bf16>(x[e]);
-        v[e] = __builtin_bit_cast(uint16_t, b);
-      } else {
-        v[e] = x[e];
-      }
-    }
-    __builtin_nontemporal_store(v, reinterpret_cast<V*>(static_cast<T*>(p) + i));
-  }
-};
-
-// Sums of N values over the TPR threads of a row (a power of two); `red` holds
-// 16 * N floats and is used alternately (two halves), so one barrier a sum.
-template <int N, int NT>
-__device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float* red, int& half) {
-  const int wide = tpr < 64 ? tpr : 64;
-  for (int m = wide >> 1; m >= 1; m >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], m, 64);
-  if (tpr <= 64) return;
-  const int t = threadIdx.x, wave = t >> 6, waves = tpr >> 6;
-  float* r = red + half * (NT / 64) * 2;
-  half ^= 1;
-  if ((t & 63) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[2 * wave + i] = v[i];
-  __syncthreads();
-  // the row's waves are the whole workgroup (tpr = NT) or an aligned part of it
-  const int first = wave & ~(waves - 1);
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int j = 0; j < waves; ++j)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += r[2 * (first + j) + i];
-}
 
 template <class IO, int VEC, int EPL, int NT>
 __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormArgs a, int tpr) {

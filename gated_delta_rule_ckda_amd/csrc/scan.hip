@@ -1,0 +1,464 @@
+// Selective scan: whole prompts, and one token a sequence (see scan_ops.h for the
+// formulas and how a workgroup holds channels and states).
+#include "scan_ops.h"
+
+namespace ckda {
+namespace {
+
+// What a walk over a piece leaves behind.
+enum Walk {
+  kOutputs,   // y, and ht after a sequence's last piece
+  kSums,      // the state it would end in from zero, and the sum of its steps
+  kMarks,     // the states entering every kMark tokens
+};
+
+template <class IO, class C, int WALK>
+__global__ __launch_bounds__(256, 2) void scan_walk_kernel(ScanArgs a) {
+  constexpr int CH = C::CH, NR = C::NR, NL = C::NL, SP = C::SP, NSL = C::NSL;
+  constexpr int TT = 32, EP = TT * CH / 256, EB = TT * SP / 256;
+  constexpr int ES = sizeof(typename IO::storage);
+  constexpr bool kY = WALK == kOutputs;
+  using Row = RowBits<IO, EP>;
+  __shared__ __align__(16) float sd[TT][CH], su[TT][CH], sB[TT][SP], sC[kY ? TT : 1][SP], sY[kY ? NSL : 1][TT][CH];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const ScanBlock<C> b(a);
+  const Piece p = piece_of(a, b.slot, a.seg, lane);
+  if (p.n < 0) return;
+  // nothing enters a piece after a sequence's last one
+  if (WALK == kSums && p.s == p.count - 1) return;
+
+  const int ch = lane % CH, sl = wave * NL + lane / CH;
+  const bool mine = ch < b.cols;
+  const int64_t chan = b.chan + ch;
+  const int64_t own = (static_cast<int64_t>(b.slot) * scan_blocks(a.D, a.G, CH) + b.blk) * SP + sl * NR;
+  float A2[NR], h[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int n = sl * NR + i;
+    const bool ok = mine && n < a.S;
+    A2[i] = ok ? a.A[chan * a.S + n] * kLog2e : 0.f;
+    h[i] = 0.f;
+    if (WALK != kSums) {
+      if (a.cut)
+        h[i] = a.entry[(own + i) * CH + ch];
+      else if (a.h0 && ok)
+        h[i] = a.h0[(static_cast<int64_t>(p.n) * a.D + chan) * a.S + n];
+    }
+  }
+  // this thread's part of a tile of TT tokens: EP channels of one row
+  const int row = tid / (CH / EP), col = tid % (CH / EP) * EP, left = b.cols - col;
+  float bias[EP], Dv[EP];
+#pragma unroll
+  for (int e = 0; e < EP; ++e) {
+    bias[e] = a.bias && e < left ? a.bias[b.chan + col + e] : 0.f;
+    Dv[e] = kY && a.Dv && e < left ? a.Dv[b.chan + col + e] : 0.f;
+  }
+
+  Row rx, rdt, rz, nx, ndt, nz;
+  uint32_t rB[EB], rC[EB];
+  const auto load = [&](int t0) {
+    const int rows = p.len - t0 < TT ? (p.len - t0 > 0 ? p.len - t0 : 0) : TT;
+    const int64_t at = p.begin + (rows > 0 ? t0 : 0);
+    const bool ok = row < rows && left > 0;
+    nx.load(rows_rsrc<IO>(a.x, at, a.sx, b.chan, rows, b.cols), ok ? static_cast<int>(row * a.sx + col) * ES : kOut, left, a.vec);
+    ndt.load(rows_rsrc<IO>(a.dt, at, a.sdt, b.chan, rows, b.cols), ok ? static_cast<int>(row * a.sdt + col) * ES : kOut, left, a.vec);
+    if (kY && a.z)
+      nz.load(rows_rsrc<IO>(a.z, at, a.sz, b.chan, rows, b.cols), ok ? static_cast<int>(row * a.sz + col) * ES : kOut, left, a.vec);
+    const rsrc_t rb = rows_rsrc<IO>(a.Bm, at, a.sb, static_cast<int64_t>(b.g) * a.S, rows, a.S);
+    const rsrc_t rc = rows_rsrc<IO>(kY ? a.Cm : a.Bm, at, kY ? a.sc : a.sb, static_cast<int64_t>(b.g) * a.S, rows, a.S);
+#pragma unroll
+    for (int i = 0; i < EB; ++i) {
+      const int t = (tid + 256 * i) / SP, n = (tid + 256 * i) % SP;
+      const bool in = t < rows && n < a.S;
+      ldraw<ES>(rb, in ? static_cast<int>(t * a.sb + n) * ES : kOut, rB + i);
+      if (kY) ldraw<ES>(rc, in ? static_cast<int>(t * a.sc + n) * ES : kOut, rC + i);
+    }
+  };
+  const int mark0 = WALK == kMarks ? first_slot(a, p.n, kMark) + static_cast<int>(static_cast<int64_t>(p.s) * a.seg / kMark) : 0;
+  float span = 0.f;
+  load(0);
+  for (int t0 = 0; t0 < p.len; t0 += TT) {
+    const int rows = p.len - t0 < TT ? p.len - t0 : TT;
+    rx = nx;
+    rdt = ndt;
+    rz = nz;
+    {
+      float d[EP], u[EP];
+#pragma unroll
+      for (int e = 0; e < EP; ++e) {
+        const float v = rdt.get(e) + bias[e];
+        float slope;
+        d[e] = v;
+        if (a.softplus) softplus_and_slope<IO>(v, d[e], slope);
+        if (row >= rows) d[e] = 0.f;
+        u[e] = d[e] * rx.get(e);
+      }
+      lds_put<EP>(&sd[row][col], d);
+      lds_put<EP>(&su[row][col], u);
+#pragma unroll
+      for (int i = 0; i < EB; ++i) {
+        const int t = (tid + 256 * i) / SP, n = (tid + 256 * i) % SP;
+        sB[t][n] = dec<IO>(rB + i, 0);
+        if (kY) sC[t][n] = dec<IO>(rC + i, 0);
+      }
+    }
+    __syncthreads();
+    load(t0 + TT);
+    for (int tb = 0; tb < rows; tb += 4) {
+      if (WALK == kMarks && (tb & (kMark - 1)) == 0) {
+        const int64_t m = mark0 + (t0 + tb) / kMark;
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+          a.marks[((m * scan_blocks(a.D, a.G, CH) + b.blk) * SP + sl * NR + i) * CH + ch] = h[i];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int t = tb + k;
+        const float d = sd[t][ch], u = su[t][ch];
+        float B[NR], Cv[NR], y = 0.f;
+        lds_run<NR>(&sB[t][sl * NR], B);
+        if (kY) lds_run<NR>(&sC[t][sl * NR], Cv);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const float e = __builtin_amdgcn_exp2f(d * A2[i]);
+          h[i] = __builtin_fmaf(e, h[i], u * B[i]);
+          if (kY) y = __builtin_fmaf(Cv[i], h[i], y);
+        }
+        if (kY) sY[sl][t][ch] = y;
+        if (WALK == kSums) span += d;
+      }
+    }
+    __syncthreads();
+    if (kY && row < rows && left > 0) {
+      float y[EP];
+#pragma unroll
+      for (int e = 0; e < EP; ++e) y[e] = Dv[e] * rx.get(e);
+#pragma unroll
+      for (int s = 0; s < NSL; ++s) lds_add<EP>(&sY[s][row][col], y);
+      if (a.z)
+#pragma unroll
+        for (int e = 0; e < EP; ++e) y[e] *= silu_of<IO>(rz.get(e));
+      Row::store(rows_rsrc<IO>(a.y, p.begin + t0, a.D, b.chan, rows, b.cols),
+                 static_cast<int>(static_cast<int64_t>(row) * a.D + col) * ES, left, a.vec, y);
+    }
+  }
+  if (WALK == kSums) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) a.entry[(own + i) * CH + ch] = h[i];
+    if (sl == 0) a.span[(static_cast<int64_t>(b.slot) * scan_blocks(a.D, a.G, CH) + b.blk) * CH + ch] = span;
+  }
+  if (WALK == kOutputs && a.ht && p.s == p.count - 1 && mine) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+      if (sl * NR + i < a.S) a.ht[(static_cast<int64_t>(p.n) * a.D + chan) * a.S + sl * NR + i] = h[i];
+  }
+}
+
+// The adjoint a piece would hand to the one before it from zero, and the sum of
+// its steps: G_t = c_t + g_t C_t, c_{t-1} = exp(d_t A) G_t, with g_t = dy_t silu(z_t).
+template <class IO, class C>
+__global__ __launch_bounds__(256, 2) void scan_back_kernel(ScanArgs a) {
+  constexpr int CH = C::CH, NR = C::NR, NL = C::NL, SP = C::SP;
+  constexpr int TT = 32, EP = TT * CH / 256, EB = TT * SP / 256;
+  constexpr int ES = sizeof(typename IO::storage);
+  using Row = RowBits<IO, EP>;
+  __shared__ __align__(16) float sd[TT][CH], sg[TT][CH], sC[TT][SP];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const ScanBlock<C> b(a);
+  const Piece p = piece_of(a, b.slot, a.seg, lane);
+  if (p.n < 0 || p.s == 0) return;  // nothing comes before a sequence's first piece
+  const int ch = lane % CH, sl = wave * NL + lane / CH;
+  const bool mine = ch < b.cols;
+  float A2[NR], c[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int n = sl * NR + i;
+    A2[i] = mine && n < a.S ? a.A[static_cast<int64_t>(b.chan + ch) * a.S + n] * kLog2e : 0.f;
+    c[i] = 0.f;
+  }
+  const int row = tid / (CH / EP), col = tid % (CH / EP) * EP, left = b.cols - col;
+  float bias[EP];
+#pragma unroll
+  for (int e = 0; e < EP; ++e) bias[e] = a.bias && e < left ? a.bias[b.chan + col + e] : 0.f;
+  float span = 0.f;
+  for (int t0 = (p.len - 1) / TT * TT; t0 >= 0; t0 -= TT) {
+    const int rows = p.len - t0 < TT ? p.len - t0 : TT;
+    const int64_t at = p.begin + t0;
+    const bool ok = row < rows && left > 0;
+    Row rdt, rdy, rz;
+    rdt.load(rows_rsrc<IO>(a.dt, at, a.sdt, b.chan, rows, b.cols), ok ? static_cast<int>(row * a.sdt + col) * ES : kOut, left, a.vec);
+    rdy.load(rows_rsrc<IO>(a.dy, at, a.D, b.chan, rows, b.cols), ok ? static_cast<int>(static_cast<int64_t>(row) * a.D + col) * ES : kOut, left, a.vec);
+    if (a.z) rz.load(rows_rsrc<IO>(a.z, at, a.sz, b.chan, rows, b.cols), ok ? static_cast<int>(row * a.sz + col) * ES : kOut, left, a.vec);
+    const rsrc_t rc = rows_rsrc<IO>(a.Cm, at, a.sc, static_cast<int64_t>(b.g) * a.S, rows, a.S);
+    uint32_t rC[EB];
+#pragma unroll
+    for (int i = 0; i < EB; ++i) {
+      const int t = (tid + 256 * i) / SP, n = (tid + 256 * i) % SP;
+      ldraw<ES>(rc, t < rows && n < a.S ? static_cast<int>(t * a.sc + n) * ES : kOut, rC + i);
+    }
+    float d[EP], g[EP];
+#pragma unroll
+    for (int e = 0; e < EP; ++e) {
+      const float v = rdt.get(e) + bias[e];
+      float slope;
+      d[e] = v;
+      if (a.softplus) softplus_and_slope<IO>(v, d[e], slope);
+      if (row >= rows) d[e] = 0.f;
+      g[e] = rdy.get(e);
+      if (a.z) g[e] *= silu_of<IO>(rz.get(e));
+    }
+    __syncthreads();
+    lds_put<EP>(&sd[row][col], d);
+    lds_put<EP>(&sg[row][col], g);
+#pragma unroll
+    for (int i = 0; i < EB; ++i) sC[(tid + 256 * i) / SP][(tid + 256 * i) % SP] = dec<IO>(rC + i, 0);
+    __syncthreads();
+    for (int tb = (rows - 1) / 4 * 4; tb >= 0; tb -= 4) {
+#pragma unroll
+      for (int k = 3; k >= 0; --k) {
+        const int t = tb + k;
+        const float dd = sd[t][ch], gg = sg[t][ch];
+        float Cv[NR];
+        lds_run<NR>(&sC[t][sl * NR], Cv);
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+          c[i] = __builtin_amdgcn_exp2f(dd * A2[i]) * __builtin_fmaf(gg, Cv[i], c[i]);
+        span += dd;
+      }
+    }
+  }
+  const int64_t own = static_cast<int64_t>(b.slot) * scan_blocks(a.D, a.G, CH) + b.blk;
+#pragma unroll
+  for (int i = 0; i < NR; ++i) a.entry[(own * SP + sl * NR + i) * CH + ch] = c[i];
+  if (sl == 0) a.span[own * CH + ch] = span;
+}
+
+// entry[s], the pieces' own sums, become what enters them: R <- exp(A span_s) R + sum_s
+// along a sequence's pieces (backwards: against them), from h0 (dht).
+template <class C, bool REV>
+__global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a) {
+  constexpr int CH = C::CH, SP = C::SP;
+  const int blocks = scan_blocks(a.D, a.G, CH), per = a.D / a.G, nb = (per + CH - 1) / CH;
+  const int n = blockIdx.x / blocks, blk = blockIdx.x - n * blocks, g = blk / nb, c0 = (blk - g * nb) * CH;
+  const Seq q = sequence(a, n);
+  const int first = first_slot(a, n, a.seg), count = q.len > 0 ? (q.len + a.seg - 1) / a.seg : 1;
+  const float* from = REV ? a.dht : a.h0;
+  for (int k = threadIdx.x; k < SP * CH; k += 256) {
+    const int st = k / CH, ch = k % CH;
+    const bool ok = c0 + ch < per && st < a.S;
+    const int64_t chan = static_cast<int64_t>(g) * per + c0 + ch;
+    const float A2 = ok ? a.A[chan * a.S + st] * kLog2e : 0.f;
+    float R = ok && from ? from[(static_cast<int64_t>(n) * a.D + chan) * a.S + st] : 0.f;
+    for (int j = 0; j < count; ++j) {
+      const int64_t own = static_cast<int64_t>(first + (REV ? count - 1 - j : j)) * blocks + blk;
+      float* at = a.entry + own * SP * CH + k;
+      const bool last = j == count - 1;  // its own sum enters no piece and was not formed
+      const float sum = last ? 0.f : *at;
+      const float gain = last ? 0.f : __builtin_amdgcn_exp2f(a.span[own * CH + ch] * A2);
+      *at = R;
+      R = __builtin_fmaf(gain, R, sum);
+    }
+  }
+}
+
+// One token a sequence.  LPC lanes hold the S states of a channel, VEC each.
+template <class IO, int VEC>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, int lpc) {
+  typedef float V __attribute__((ext_vector_type(VEC)));
+  const int64_t id = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / lpc;
+  const int s = (threadIdx.x & (lpc - 1)) * VEC;
+  const int64_t n = id / a.D;
+  if (n >= a.N) return;
+  const int c = static_cast<int>(id - n * a.D), g = c / (a.D / a.G);
+  using T = typename IO::storage;
+  const float x = IO::load(static_cast<const T*>(a.x), n * a.sx + c);
+  float d = IO::load(static_cast<const T*>(a.dt), n * a.sdt + c) + (a.bias ? a.bias[c] : 0.f), slope;
+  float y = 0.f;
+  if (a.softplus) softplus_and_slope<IO>(d, d, slope);
+  if (s < a.S) {
+    const int64_t at = (n * a.D + c) * a.S + s;
+    V h;
+    if constexpr (VEC == 1)
+      h[0] = a.h0[at];
+    else
+      h = __builtin_nontemporal_load(reinterpret_cast<const V*>(a.h0 + at));
+    const float u = d * x;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const float e = __builtin_amdgcn_exp2f(d * (a.A[static_cast<int64_t>(c) * a.S + s + i] * kLog2e));
+      const float B = IO::load(static_cast<const T*>(a.Bm), n * a.sb + static_cast<int64_t>(g) * a.S + s + i);
+      const float Cv = IO::load(static_cast<const T*>(a.Cm), n * a.sc + static_cast<int64_t>(g) * a.S + s + i);
+      h[i] = __builtin_fmaf(e, h[i], u * B);
+      y = __builtin_fmaf(Cv, h[i], y);
+    }
+    if constexpr (VEC == 1)
+      a.ht[at] = h[0];
+    else
+      __builtin_nontemporal_store(h, reinterpret_cast<V*>(a.ht + at));
+  }
+  for (int m = lpc >> 1; m >= 1; m >>= 1) y += __shfl_xor(y, m, 64);
+  if (s == 0) {
+    y += (a.Dv ? a.Dv[c] : 0.f) * x;
+    if (a.z) y *= silu_of<IO>(IO::load(static_cast<const T*>(a.z), n * a.sz + c));
+    const __bf16 b = static_cast<__bf16>(y);
+    if constexpr (sizeof(T) == 2)
+      static_cast<T*>(a.y)[n * a.D + c] = __builtin_bit_cast(uint16_t, b);
+    else
+      static_cast<T*>(a.y)[n * a.D + c] = y;
+  }
+}
+
+struct StepShape {
+  int vec, lpc;
+};
+StepShape step_shape(int S) {
+  StepShape r;
+  r.vec = S % 4 == 0 ? 4 : 1;
+  r.lpc = 1;
+  while (r.lpc * r.vec < S) r.lpc *= 2;
+  return r;
+}
+
+template <class IO>
+launch_result launch_walk(const ScanArgs& a, const ScanPlan& p, Walk walk, hipStream_t s) {
+  return scan_config(p.which, [&](auto cfg) -> launch_result {
+    using C = decltype(cfg);
+    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(p.slots) * p.blocks));
+    if (walk == kOutputs)
+      hipLaunchKernelGGL((scan_walk_kernel<IO, C, kOutputs>), grid, dim3(256), 0, s, a);
+    else if (walk == kSums)
+      hipLaunchKernelGGL((scan_walk_kernel<IO, C, kSums>), grid, dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((scan_walk_kernel<IO, C, kMarks>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+  });
+}
+launch_result launch_walk_io(const ScanArgs& a, const ScanPlan& p, Walk walk, int32_t io_dtype, hipStream_t s) {
+  return io_dtype == CKDA_DTYPE_BF16 ? launch_walk<io_bf16>(a, p, walk, s) : launch_walk<io_f32>(a, p, walk, s);
+}
+
+}  // namespace
+
+bool scan_supported(int32_t S) { return S >= 1 && S <= 64; }
+
+ScanPlan scan_plan(const ScanArgs& a, bool grads) {
+  ScanPlan p;
+  const int per = a.D / a.G;
+  const auto wide = [&](int CH) { return static_cast<int64_t>(a.N) * a.G * ((per + CH - 1) / CH); };
+  if (a.S <= 8)
+    p.which = 0;
+  else if (a.S <= 16)
+    p.which = wide(64) < 512 ? 2 : 1;
+  else
+    p.which = a.S <= 32 ? 3 : 4;
+  p.CH = p.which <= 1 ? 64 : (p.which <= 3 ? 32 : 16);
+  p.SP = p.which == 0 ? 8 : (p.which <= 2 ? 16 : (p.which == 3 ? 32 : 64));
+  p.blocks = scan_blocks(a.D, a.G, p.CH);
+  // pieces: enough for two workgroups a CU, of 128 tokens at least
+  const int64_t want = 512;
+  const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
+  p.seg = scan_whole(a.T);
+  p.cut = 0;
+  if (a.N > 0 && a.T > 256 && (a.cu || static_cast<int64_t>(a.N) * p.blocks * 2 <= want)) {
+    int64_t L = tokens * p.blocks / want;
+    L = L < 128 ? 128 : (L + 31) / 32 * 32;
+    if (L < a.T) {
+      p.seg = static_cast<int>(L);
+      p.cut = 1;
+    }
+  }
+  p.slots = a.cu ? a.T / p.seg + a.N : a.N * (a.T > 0 ? (a.T + p.seg - 1) / p.seg : 1);
+  if (a.N == 0) p.slots = 0;  // a packed batch of no sequences
+  p.mslots = grads && a.N > 0 ? (a.cu ? a.T / kMark + a.N : a.N * (a.T > 0 ? (a.T + kMark - 1) / kMark : 1)) : 0;
+  return p;
+}
+
+int64_t scan_threads(const ScanArgs& a, bool grads) {
+  // slots and threads in 64 bits, for narrow blocks and pieces of 128 tokens
+  const int64_t blocks = static_cast<int64_t>(a.G) * ((a.D / a.G + 15) / 16);
+  const int64_t slots = a.cu ? a.T / 128 + static_cast<int64_t>(a.N) : static_cast<int64_t>(a.N) * (a.T / 128 + 1);
+  return slots * blocks * 256;
+}
+int64_t scan_step_threads(const ScanArgs& a) {
+  return static_cast<int64_t>(a.N) * a.D * step_shape(a.S).lpc;
+}
+
+namespace {
+// entry and span of the pieces, at ws; returns the bytes taken
+size_t layout_pieces(ScanArgs& a, const ScanPlan& p, unsigned char* ws) {
+  a.seg = p.seg;
+  a.slots = p.slots;
+  a.cut = p.cut;
+  if (!p.cut) return 0;
+  const size_t n = static_cast<size_t>(p.slots) * p.blocks * p.CH * 4;
+  const size_t entry = (n * p.SP + 255) & ~size_t(255), span = (n + 255) & ~size_t(255);
+  a.entry = reinterpret_cast<float*>(ws);
+  a.span = reinterpret_cast<float*>(ws + entry);
+  return entry + span;
+}
+}  // namespace
+
+size_t scan_fwd_workspace(const ScanArgs& a0) {
+  ScanArgs a = a0;
+  return layout_pieces(a, scan_plan(a, false), nullptr);
+}
+
+launch_result launch_scan_pieces(const ScanArgs& a, const ScanPlan& p, int32_t io_dtype, bool rev, hipStream_t s) {
+  launch_result e;
+  if (!rev) {
+    e = launch_walk_io(a, p, kSums, io_dtype, s);
+  } else {
+    e = scan_config(p.which, [&](auto cfg) -> launch_result {
+      using C = decltype(cfg);
+      const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(p.slots) * p.blocks));
+      if (io_dtype == CKDA_DTYPE_BF16)
+        hipLaunchKernelGGL((scan_back_kernel<io_bf16, C>), grid, dim3(256), 0, s, a);
+      else
+        hipLaunchKernelGGL((scan_back_kernel<io_f32, C>), grid, dim3(256), 0, s, a);
+      return hipGetLastError();
+    });
+  }
+  if (e != hipSuccess) return e;
+  return scan_config(p.which, [&](auto cfg) -> launch_result {
+    using C = decltype(cfg);
+    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.N) * p.blocks));
+    if (rev)
+      hipLaunchKernelGGL((scan_join_kernel<C, true>), grid, dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((scan_join_kernel<C, false>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+  });
+}
+
+launch_result launch_scan_marks(const ScanArgs& a, const ScanPlan& p, int32_t io_dtype, hipStream_t s) {
+  return launch_walk_io(a, p, kMarks, io_dtype, s);
+}
+
+launch_result launch_scan_fwd(ScanArgs a, int32_t io_dtype, void* ws, hipStream_t s) {
+  const ScanPlan p = scan_plan(a, false);
+  layout_pieces(a, p, static_cast<unsigned char*>(ws));
+  if (p.cut) {
+    const launch_result e = launch_scan_pieces(a, p, io_dtype, false, s);
+    if (e != hipSuccess) return e;
+  }
+  return launch_walk_io(a, p, kOutputs, io_dtype, s);
+}
+
+launch_result launch_scan_step(const ScanArgs& a, int32_t io_dtype, hipStream_t s) {
+  const StepShape r = step_shape(a.S);
+  const dim3 grid(static_cast<unsigned>((scan_step_threads(a) + 255) / 256));
+  if (io_dtype == CKDA_DTYPE_BF16) {
+    if (r.vec == 4)
+      hipLaunchKernelGGL((scan_step_kernel<io_bf16, 4>), grid, dim3(256), 0, s, a, r.lpc);
+    else
+      hipLaunchKernelGGL((scan_step_kernel<io_bf16, 1>), grid, dim3(256), 0, s, a, r.lpc);
+  } else {
+    if (r.vec == 4)
+      hipLaunchKernelGGL((scan_step_kernel<io_f32, 4>), grid, dim3(256), 0, s, a, r.lpc);
+    else
+      hipLaunchKernelGGL((scan_step_kernel<io_f32, 1>), grid, dim3(256), 0, s, a, r.lpc);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace ckda

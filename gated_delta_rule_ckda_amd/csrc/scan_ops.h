@@ -1,0 +1,233 @@
+// Device building blocks of the selective scan: for every channel with S states,
+//
+//   d_t = softplus(dt_t + bias)   (or dt_t + bias itself)
+//   h_t = exp(d_t A) h_{t-1} + d_t x_t B_t,     y_t = C_t . h_t + D x_t
+//
+// and, with a gate, y_t silu(z_t).  B and C are shared by the channels of a group.
+//
+// A workgroup of four waves walks over the tokens of one piece of a sequence for
+// CH channels.  Lanes hold channels, and the states of a channel are dealt out to
+// the workgroup's 4 NL slices (NL slices a wave, side by side in its lanes), NR a
+// lane, so that a lane's sums over states are its own and only 4 NL partial sums
+// a token and channel meet in LDS.
+#pragma once
+
+#include "decay_ops.h"
+#include "row_ops.h"
+
+namespace ckda {
+
+template <int NL_, int NR_>
+struct ScanCfg {
+  static constexpr int NL = NL_, NR = NR_;
+  static constexpr int CH = 64 / NL;     // channels of a workgroup
+  static constexpr int NSL = 4 * NL;     // slices of the states
+  static constexpr int SP = NSL * NR;    // states, the last ones possibly padding
+};
+
+// softplus and its derivative, the sigmoid.  log1p(e) is formed so that it keeps
+// the digits of a small e; -inf gives 0.
+template <class IO>
+__device__ __forceinline__ void softplus_and_slope(float v, float& d, float& slope) {
+  const float m = fabsf(v);
+  float e, l, r;
+  if constexpr (sizeof(typename IO::storage) == 2) {
+    e = exp_neg(m);
+    l = log2_1p(e) * 0.6931471805599453f;
+    r = __builtin_amdgcn_rcpf(1.f + e);
+  } else {
+    e = expf(-m);
+    l = log1pf(e);
+    r = 1.f / (1.f + e);
+  }
+  d = fmaxf(v, 0.f) + l;
+  slope = v < 0.f ? e * r : r;
+}
+
+// ---- rows in memory --------------------------------------------------------
+// EP consecutive channels of a row as they lie in memory.  Offsets that are out
+// of the resource's range load zeros and store nothing; kOut is one.
+constexpr int kOut = 0x7ffffff0;
+
+template <class IO, int EP>
+struct RowBits {
+  static constexpr int ES = sizeof(typename IO::storage), BYTES = EP * ES, W = BYTES >= 4 ? BYTES / 4 : 1;
+  uint32_t w[W];
+  // off: bytes to the first channel (kOut: none); cols: channels left in the row
+  __device__ __forceinline__ void load(rsrc_t r, int off, int cols, bool vec) {
+    if (vec) {
+      if constexpr (BYTES >= 32) {
+        ldraw<16, kStream>(r, off, w);
+        ldraw<16, kStream>(r, off == kOut ? kOut : off + 16, w + 4);
+      } else {
+        ldraw<BYTES, kStream>(r, off, w);
+      }
+    } else if constexpr (ES == 4) {
+#pragma unroll
+      for (int e = 0; e < EP; ++e) ldraw<4>(r, e < cols && off != kOut ? off + 4 * e : kOut, w + e);
+    } else {
+      uint32_t x[EP];
+#pragma unroll
+      for (int e = 0; e < EP; ++e) ldraw<2>(r, e < cols && off != kOut ? off + 2 * e : kOut, x + e);
+#pragma unroll
+      for (int e = 0; e < EP; e += 2) w[e / 2] = (x[e] & 0xffffu) | (e + 1 < EP ? x[e + 1 < EP ? e + 1 : e] << 16 : 0);
+    }
+  }
+  __device__ __forceinline__ float get(int e) const { return dec<IO>(w, e); }
+  static __device__ __forceinline__ void store(rsrc_t r, int off, int cols, bool vec, const float* x) {
+    if constexpr (ES == 4) {
+      if (vec) {
+        if constexpr (EP >= 4) {
+#pragma unroll
+          for (int e = 0; e < EP; e += 4) {
+            typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+            const u4 v = {__float_as_uint(x[e]), __float_as_uint(x[e + 1]), __float_as_uint(x[e + 2]), __float_as_uint(x[e + 3])};
+            __builtin_amdgcn_raw_buffer_store_b128(v, r, off == kOut ? kOut : off + 4 * e, 0, kStream);
+          }
+          return;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < EP; ++e)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[e]), r, e < cols && off != kOut ? off + 4 * e : kOut, 0, 0);
+    } else {
+      uint32_t u[W];
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        bf16x2 b;
+        b[0] = static_cast<__bf16>(x[2 * k]);
+        b[1] = static_cast<__bf16>(x[2 * k + 1 < EP ? 2 * k + 1 : 2 * k]);
+        u[k] = __builtin_bit_cast(uint32_t, b);
+      }
+      if (vec) {
+        if constexpr (EP == 8) {
+          typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+          __builtin_amdgcn_raw_buffer_store_b128(u4{u[0], u[1], u[2], u[3]}, r, off, 0, kStream);
+          return;
+        } else if constexpr (EP == 4) {
+          typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+          __builtin_amdgcn_raw_buffer_store_b64(u2{u[0], u[1]}, r, off, 0, kStream);
+          return;
+        } else if constexpr (EP == 2) {
+          __builtin_amdgcn_raw_buffer_store_b32(u[0], r, off, 0, kStream);
+          return;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < EP; ++e)
+        __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(u[e / 2] >> (16 * (e & 1))), r,
+                                              e < cols && off != kOut ? off + 2 * e : kOut, 0, 0);
+    }
+  }
+};
+
+// The resource of `rows` rows of `cols` channels from channel c of token t on.
+template <class IO>
+__device__ __forceinline__ rsrc_t rows_rsrc(const void* p, int64_t t, int64_t stride, int64_t c, int rows, int cols) {
+  constexpr int ES = sizeof(typename IO::storage);
+  const int64_t at = uniform64((t * stride + c) * ES);
+  const int bytes = rows > 0 ? static_cast<int>((rows - 1) * stride + cols) * ES : 0;
+  return make_rsrc(static_cast<const char*>(p) + at, uniform32(bytes));
+}
+
+// ---- workgroups ------------------------------------------------------------
+// Blocks of channels: CH of one group each.
+__host__ __device__ __forceinline__ int scan_blocks(int D, int G, int CH) { return G * ((D / G + CH - 1) / CH); }
+
+// Workgroups whose channels share 128-byte lines are put on one XCD (workgroups
+// go to the 8 XCDs in turn): NL neighbours 8 apart.
+template <int NL>
+__device__ __forceinline__ int scan_order(int id, int total) {
+  const int span = 8 * NL, base = id / span * span;
+  if (NL == 1 || base + span > total) return id;
+  const int r = id - base;
+  return base + (r & 7) * NL + (r >> 3);
+}
+
+template <class C>
+struct ScanBlock {
+  int slot, blk;   // piece slot, block of channels
+  int g, chan, cols;  // group, first channel, channels of the block
+  __device__ __forceinline__ ScanBlock(const ScanArgs& a) {
+    const int per = a.D / a.G, nb = (per + C::CH - 1) / C::CH, blocks = a.G * nb;
+    const int id = scan_order<C::NL>(blockIdx.x, gridDim.x);
+    slot = id / blocks;
+    blk = id - slot * blocks;
+    g = blk / nb;
+    const int c0 = (blk - g * nb) * C::CH;
+    chan = g * per + c0;
+    cols = per - c0 < C::CH ? per - c0 : C::CH;
+  }
+};
+
+// NR consecutive floats in LDS (16-byte aligned rows), the same for all lanes of a slice
+template <int NR>
+__device__ __forceinline__ void lds_run(const float* p, float* v) {
+  if constexpr (NR % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < NR; i += 4) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(p + i);
+      v[i] = x[0]; v[i + 1] = x[1]; v[i + 2] = x[2]; v[i + 3] = x[3];
+    }
+  } else {
+    static_assert(NR == 2, "states a lane");
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    v[0] = x.x;
+    v[1] = x.y;
+  }
+}
+template <int EP>
+__device__ __forceinline__ void lds_put(float* p, const float* v) {
+  if constexpr (EP % 4 == 0) {
+#pragma unroll
+    for (int e = 0; e < EP; e += 4) *reinterpret_cast<f32x4*>(p + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
+  } else if constexpr (EP == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  } else {
+    p[0] = v[0];
+  }
+}
+template <int EP>
+__device__ __forceinline__ void lds_add(const float* p, float* v) {
+  if constexpr (EP % 4 == 0) {
+#pragma unroll
+    for (int e = 0; e < EP; e += 4) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(p + e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[e + i] += x[i];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < EP; ++e) v[e] += p[e];
+  }
+}
+
+constexpr int kMark = 16;  // tokens between the states kept for the gradients
+
+// Tokens of a piece where sequences are not cut: past every sequence's end.
+__host__ __device__ __forceinline__ int scan_whole(int T) { return T + 1; }
+
+// What the kernels of one call share out: which lanes hold which states.
+template <class F>
+launch_result scan_config(int which, F f) {
+  switch (which) {
+    case 0: return f(ScanCfg<1, 2>{});
+    case 1: return f(ScanCfg<1, 4>{});
+    case 2: return f(ScanCfg<2, 2>{});
+    case 3: return f(ScanCfg<2, 4>{});
+    default: return f(ScanCfg<4, 4>{});
+  }
+}
+struct ScanPlan {
+  int which, CH, SP;
+  int blocks, slots, seg, cut, mslots;
+};
+ScanPlan scan_plan(const ScanArgs& a, bool grads);
+
+// The pieces' own sums and what enters each (launched where sequences are cut):
+// forwards, or backwards for the adjoint.
+launch_result launch_scan_pieces(const ScanArgs& a, const ScanPlan& p, int32_t io_dtype, bool rev, hipStream_t s);
+// The states entering every kMark tokens.
+launch_result launch_scan_marks(const ScanArgs& a, const ScanPlan& p, int32_t io_dtype, hipStream_t s);
+
+}  // namespace ckda

@@ -54,7 +54,7 @@
 extern "C" {
 #endif
 
-#define CKDA_ABI_VERSION 10
+#define CKDA_ABI_VERSION 11
 
 typedef enum {
   CKDA_OK = 0,
@@ -494,6 +494,169 @@ ckda_status_t ckda_block_norm_bwd(int64_t rows, int32_t d, int32_t io_dtype, int
                                   const float* s, const float* w2, const void* dh, const void* dn,
                                   void* dy, float* dw, void* dg, void* dx, float* ds, float* dw2,
                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Short causal convolution, one filter of K taps a channel (the step before a
+ * recurrent mixer: on q, k and v of the layers above, on x of the selective scan):
+ *
+ *     y_t = act(bias + sum_j w_j x_{t-K+1+j}),      j = 0 .. K-1
+ *
+ *   x : [B][T][D] with x_stride elements between tokens   y : [B][T][D]
+ *   w : [D][K] float32   bias : [D] float32 (NULL: zero)
+ *   h0, ht : [num_seqs][K-1][D], the last K-1 inputs before a sequence and at its
+ *     end (h0 NULL: zeros; ht NULL: not written; they may be the same buffer)
+ * x, y, h0 and ht in the io dtype; act 0 (none) or CKDA_NORM_GATE_SILU.  Packed
+ * batches as above (B = 1, cu_seqlens clamped to [0, T] on the device; tokens past
+ * its end are neither read nor written).  A non-finite input reaches the outputs
+ * (backwards: gradients) of its own channel up to K-1 tokens on, of its own
+ * sequence only.
+ * Supported: K from 2 to 4, D up to 2^22 and x_stride below 2^24, B * T below
+ * 2^31 - 1024, T below 2^30; others return CKDA_ERR_UNSUPPORTED, as do batches for which a
+ * launch would have 2^32 threads (about a token and channel in 32).  x needs only
+ * its elements' alignment; 16-byte accesses are used where its base, its stride
+ * and D are multiples of 16 bytes.
+ */
+typedef struct {
+  int32_t B, T, D, K;
+  int32_t num_seqs;   /* B for a dense batch */
+  int32_t io_dtype;   /* ckda_dtype_t */
+  int32_t act;        /* CKDA_NORM_GATE_NONE or CKDA_NORM_GATE_SILU */
+  int64_t x_stride;   /* elements between tokens of x (at least D); 0 = D */
+} ckda_conv_desc_t;
+
+ckda_status_t ckda_conv_fwd(const ckda_conv_desc_t* desc, const void* x, const float* w,
+                            const float* bias, const int32_t* cu_seqlens, const void* h0, void* y,
+                            void* ht, void* stream);
+
+/*
+ * Its gradients, given dy = dL/dy and dht = dL/dht (io dtype; NULL for zero):
+ * dx [B][T][D] and dh0 (NULL: not wanted) in the io dtype, dw [D][K] and dbias
+ * [D] (NULL: not wanted) in float32, summed over all tokens in a fixed order.
+ * `workspace`: ckda_conv_bwd_workspace_size bytes, 256-byte aligned.
+ */
+size_t ckda_conv_bwd_workspace_size(const ckda_conv_desc_t* desc, int32_t packed);
+ckda_status_t ckda_conv_bwd(const ckda_conv_desc_t* desc, const void* x, const float* w,
+                            const float* bias, const int32_t* cu_seqlens, const void* h0,
+                            const void* dy, const void* dht, void* dx, float* dw, float* dbias,
+                            void* dh0, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token for each of N sequences (desc: B = num_seqs = N, T = 1): x [N][D]
+ * with x_stride elements between sequences; the cache [N][K-1][D] loses its
+ * oldest input and gains this one (h0 == ht, in place, is allowed).
+ */
+ckda_status_t ckda_conv_step(const ckda_conv_desc_t* desc, const void* x, const float* w,
+                             const float* bias, const void* h0, void* ht, void* y, void* stream);
+
+/*
+ * Selective scan: a recurrence of S states a channel whose decay, write and
+ * read-out depend on the token,
+ *
+ *     d_t = softplus(dt_t + dt_bias)           (dt_t + dt_bias without softplus)
+ *     h_t = exp(d_t A) h_{t-1} + d_t x_t B_t
+ *     y_t = (C_t . h_t + D x_t) silu(z_t)      (D NULL: 0; z NULL: no gate)
+ *
+ *   x, dt, z, y : [B][T][D]   A : [D][S] float32   D, dt_bias : [D] float32
+ *   B, C : [B][T][groups][S], shared by the D / groups channels of a group
+ *   h0, ht : [num_seqs][D][S] float32 (h0 NULL: zeros; ht NULL: not written; they
+ *     may be the same buffer)
+ * x, dt, z, B, C and y in the io dtype.  The inputs may be parts of wider rows
+ * (a projection's output): the strides are the elements between tokens, the
+ * channels and the groups' states being contiguous.  States, decays and sums are
+ * kept in float32.  A is taken as written (negative for a decay) and must be
+ * finite.  A step of exactly 0 (with softplus: a logit of -inf, the type's lowest
+ * value and all below about -104) leaves the states as they are where the
+ * token's x and B are finite.  A non-finite value in a token's x, dt, z, B or C
+ * reaches outputs of its own sequence only.  Packed batches as above: cu_seqlens
+ * clamped to [0, T] on the device, tokens past its end neither read nor written.
+ * Supported: S from 1 to 64, groups dividing D, D up to 2^20, strides below 2^24,
+ * B * T below 2^31 - 1024, T below 2^30; others return CKDA_ERR_UNSUPPORTED, as do batches
+ * for which a launch would have 2^32 threads (256 for each sequence, 128 tokens
+ * of it and 16 channels).  x, dt, z, B and C need only their elements'
+ * alignment; 16-byte accesses are used where the bases and strides of x, dt and
+ * z, D and D / groups are multiples of 16 bytes.
+ */
+typedef struct {
+  int32_t B, T, D, S;
+  int32_t groups;
+  int32_t num_seqs;   /* B for a dense batch */
+  int32_t io_dtype;   /* ckda_dtype_t */
+  int32_t softplus;   /* 1: dt holds logits of the steps, 0: the steps */
+  /* elements between tokens; 0 = contiguous */
+  int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;
+} ckda_scan_desc_t;
+
+/* 1 if the scan calls have kernels for S states a channel, else 0. */
+int32_t ckda_scan_supported(int32_t S);
+
+/*
+ * The forward over whole sequences.  The workspace (0 bytes where there are
+ * sequences and channels enough to fill the GPU; then NULL is fine) holds the
+ * states entering the pieces that long sequences are cut into: 256-byte aligned,
+ * overlapping no tensor.
+ */
+size_t ckda_scan_fwd_workspace_size(const ckda_scan_desc_t* desc, int32_t packed);
+ckda_status_t ckda_scan_fwd(const ckda_scan_desc_t* desc, const void* x, const void* dt,
+                            const float* A, const void* B, const void* C, const float* D,
+                            const void* z, const float* dt_bias, const int32_t* cu_seqlens,
+                            const float* h0, void* y, float* ht, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients, given dy = dL/dy (io dtype, contiguous) and dht = dL/dht
+ * (float32, NULL for zero): dx, ddt, dz [B][T][D] and dB, dC [B][T][groups][S]
+ * in the io dtype, contiguous; dA [D][S], dD, ddt_bias [D] and dh0 in float32.
+ * ddt is the gradient of what dt holds.  dz, dD and ddt_bias are given exactly
+ * where z, D and dt_bias are; dh0 may be NULL (not wanted).  The states are
+ * formed again from the inputs.  Every sum runs in a fixed order.
+ */
+size_t ckda_scan_bwd_workspace_size(const ckda_scan_desc_t* desc, int32_t packed);
+ckda_status_t ckda_scan_bwd(const ckda_scan_desc_t* desc, const void* x, const void* dt,
+                            const float* A, const void* B, const void* C, const float* D,
+                            const void* z, const float* dt_bias, const int32_t* cu_seqlens,
+                            const float* h0, const void* dy, const float* dht, void* dx, void* ddt,
+                            float* dA, void* dB, void* dC, float* dD, void* dz, float* ddt_bias,
+                            float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token for each of N sequences (desc: B = num_seqs = N, T = 1; the strides
+ * are between sequences): x, dt, z, y [N][D], B, C [N][groups][S], states
+ * [N][D][S]; h0 == ht (in place) is allowed.  N * D * S up to 2^31.
+ */
+ckda_status_t ckda_scan_step(const ckda_scan_desc_t* desc, const void* x, const void* dt,
+                             const float* A, const void* B, const void* C, const float* D,
+                             const void* z, const float* dt_bias, const float* h0, float* ht, void* y,
+                             void* stream);
+
+/*
+ * Layer norm of `rows` rows of d elements with the residual add before it, in
+ * float32:
+ *
+ *   h = r + x                                           (r NULL: h = x)
+ *   n = (h - mean h) / sqrt(mean (h - mean h)^2 + eps) * w + b   (w NULL: 1, b NULL: 0)
+ *
+ * n is formed from h before its rounding.  x, r, n, h: [rows][d] in the io
+ * dtype; w, b: [d] float32.  h is given exactly with r, and may be r's buffer or x's
+ * (updated in place); other overlaps with an output are refused.
+ * d from 1 to 16384, any; rows whose d is a multiple of 8 (bf16) or 4 (float32)
+ * move in 16-byte accesses.
+ */
+ckda_status_t ckda_layer_norm(int64_t rows, int32_t d, int32_t io_dtype, float eps, const void* x,
+                              const void* r, const float* w, const float* b, void* n, void* h,
+                              void* stream);
+
+/*
+ * Its gradients for dn = dL/dn and dh = dL/dh (NULL: zero, as without a
+ * residual), from x, the normed row (the forward's h where there was a
+ * residual): dx, which is the gradient of both x and r, in the io dtype; dw, db
+ * [d] float32, summed over the rows in a fixed order (dw is given exactly where
+ * w is; db may be NULL).  No output overlaps an input or another output.
+ * `workspace`: ckda_layer_norm_bwd_workspace_size bytes, 256-byte aligned.
+ */
+size_t ckda_layer_norm_bwd_workspace_size(int64_t rows, int32_t d, int32_t io_dtype);
+ckda_status_t ckda_layer_norm_bwd(int64_t rows, int32_t d, int32_t io_dtype, float eps, const void* x,
+                                  const float* w, const void* dn, const void* dh, void* dx, float* dw,
+                                  float* db, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* ckda_status_string(int32_t status);
