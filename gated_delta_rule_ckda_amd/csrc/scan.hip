@@ -12,40 +12,129 @@ enum Walk {
   kMarks,     // the states entering every kMark tokens
 };
 
+// The operands of four tokens on their way from LDS to the states.
+template <int NR, bool Y>
+struct Four {
+  float d[4], u[4], B[4][NR], C[4][NR];
+  __device__ __forceinline__ void load(const float* sd, const float* su, const float* sB, const float* sC, int CH, int SP) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      d[j] = sd[j * CH];
+      u[j] = su[j * CH];
+      lds_run<NR>(sB + j * SP, B[j]);
+      if (Y) lds_run<NR>(sC + j * SP, C[j]);
+    }
+  }
+};
+
+// W waves walk the states over a tile of TT tokens; four more, spread over the same
+// SIMDs, form the steps and writes of tiles to come in LDS and finish the outputs
+// of the one before.  Tiles are laid down two
+// ahead, so that the states' operands are asked for four tokens ahead across
+// tiles.
 template <class IO, class C, int WALK>
-__global__ __launch_bounds__(256, 2) void scan_walk_kernel(ScanArgs a) {
+__global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs a) {
   constexpr int CH = C::CH, NR = C::NR, NL = C::NL, SP = C::SP, NSL = C::NSL;
-  constexpr int TT = 32, EP = TT * CH / 256, EB = TT * SP / 256;
+  constexpr int TT = 16, EP = TT * CH / 256, EB = (TT * SP + 255) / 256;
   constexpr int ES = sizeof(typename IO::storage);
   constexpr bool kY = WALK == kOutputs;
   using Row = RowBits<IO, EP>;
-  __shared__ __align__(16) float sd[TT][CH], su[TT][CH], sB[TT][SP], sC[kY ? TT : 1][SP], sY[kY ? NSL : 1][TT][CH];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ __align__(16) float sd[3][TT][CH], su[3][TT][CH], sB[3][TT][SP], sC[kY ? 3 : 1][kY ? TT : 1][SP];
+  __shared__ __align__(16) float sY[2][kY ? NSL : 1][TT][CH];
+  const int lane = threadIdx.x & 63, wave = uniform32(threadIdx.x >> 6);
   const ScanBlock<C> b(a);
   const Piece p = piece_of(a, b.slot, a.seg, lane);
   if (p.n < 0) return;
   // nothing enters a piece after a sequence's last one
   if (WALK == kSums && p.s == p.count - 1) return;
+  const int tiles = (p.len + TT - 1) / TT;
+  const int64_t blocks = scan_blocks(a.D, a.G, CH);
 
-  const int ch = lane % CH, sl = wave * NL + lane / CH;
-  const bool mine = ch < b.cols;
-  const int64_t chan = b.chan + ch;
-  const int64_t own = (static_cast<int64_t>(b.slot) * scan_blocks(a.D, a.G, CH) + b.blk) * SP + sl * NR;
-  float A2[NR], h[NR];
+  if (wave < C::W) {
+    // ---- states
+    const int ch = lane % CH, sl = wave * NL + lane / CH;
+    const bool mine = ch < b.cols;
+    const int64_t chan = b.chan + ch;
+    const int64_t own = (b.slot * blocks + b.blk) * SP + sl * NR;
+    float A2[NR], h[NR];
 #pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int n = sl * NR + i;
-    const bool ok = mine && n < a.S;
-    A2[i] = ok ? a.A[chan * a.S + n] * kLog2e : 0.f;
-    h[i] = 0.f;
-    if (WALK != kSums) {
-      if (a.cut)
-        h[i] = a.entry[(own + i) * CH + ch];
-      else if (a.h0 && ok)
-        h[i] = a.h0[(static_cast<int64_t>(p.n) * a.D + chan) * a.S + n];
+    for (int i = 0; i < NR; ++i) {
+      const int n = sl * NR + i;
+      const bool ok = mine && n < a.S;
+      A2[i] = ok ? a.A[chan * a.S + n] * kLog2e : 0.f;
+      h[i] = 0.f;
+      if (WALK != kSums) {
+        if (a.cut)
+          h[i] = a.entry[(own + i) * CH + ch];
+        else if (a.h0 && ok)
+          h[i] = a.h0[(static_cast<int64_t>(p.n) * a.D + chan) * a.S + n];
+      }
     }
+    const int64_t mark0 = WALK == kMarks ? first_slot(a, p.n, kMark) + static_cast<int64_t>(p.s) * a.seg / kMark : 0;
+    float span = 0.f;
+    Four<NR, kY> ops[2];
+    const auto fetch = [&](Four<NR, kY>& o, int q, int t) {
+      o.load(&sd[q][t][ch], &su[q][t][ch], &sB[q][t][sl * NR], kY ? &sC[kY ? q : 0][kY ? t : 0][sl * NR] : nullptr, CH, SP);
+    };
+    __syncthreads();
+    int q = 0, half = 0;
+    if (tiles > 0) fetch(ops[0], 0, 0);
+    for (int k = 0; k < tiles; ++k) {
+      if (WALK == kMarks) {
+        static_assert(TT == kMark, "a state a tile");
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+          a.marks[(((mark0 + k) * blocks + b.blk) * SP + sl * NR + i) * CH + ch] = h[i];
+      }
+      const int next = q == 2 ? 0 : q + 1;
+#pragma unroll
+      for (int g = 0; g < TT / 4; ++g) {
+        Four<NR, kY>& o = ops[g & 1];
+        float e[4][NR];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < NR; ++i) e[j][i] = o.d[j] * A2[i];
+        // past the last tile this reads what an earlier one left
+        fetch(ops[(g + 1) & 1], g + 1 < TT / 4 ? q : next, (g + 1) % (TT / 4) * 4);
+        __builtin_amdgcn_sched_barrier(0);
+        // powers run together: a switch between them and other operations costs both
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < NR; ++i) e[j][i] = __builtin_amdgcn_exp2f(e[j][i]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float y = 0.f;
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            h[i] = __builtin_fmaf(e[j][i], h[i], o.u[j] * o.B[j][i]);
+            if (kY) y = __builtin_fmaf(o.C[j][i], h[i], y);
+          }
+          if (kY) sY[half][sl][4 * g + j][ch] = y;
+          if (WALK == kSums) span += o.d[j];
+        }
+      }
+      q = next;
+      half ^= 1;
+      __syncthreads();
+    }
+    if (WALK == kSums) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i) a.entry[(own + i) * CH + ch] = h[i];
+      if (sl == 0) a.span[(b.slot * blocks + b.blk) * CH + ch] = span;
+    }
+    if (WALK == kOutputs && a.ht && p.s == p.count - 1 && mine) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+        if (sl * NR + i < a.S) a.ht[(static_cast<int64_t>(p.n) * a.D + chan) * a.S + sl * NR + i] = h[i];
+    }
+    return;
   }
-  // this thread's part of a tile of TT tokens: EP channels of one row
+
+  // ---- inputs and outputs: this thread's part of a tile is EP channels of one row
+  const int tid = threadIdx.x - 64 * C::W;
   const int row = tid / (CH / EP), col = tid % (CH / EP) * EP, left = b.cols - col;
   float bias[EP], Dv[EP];
 #pragma unroll
@@ -53,8 +142,8 @@ __global__ __launch_bounds__(256, 2) void scan_walk_kernel(ScanArgs a) {
     bias[e] = a.bias && e < left ? a.bias[b.chan + col + e] : 0.f;
     Dv[e] = kY && a.Dv && e < left ? a.Dv[b.chan + col + e] : 0.f;
   }
-
-  Row rx, rdt, rz, nx, ndt, nz;
+  Row nx, ndt, nz;
+  Row x0, x1, x2, z0, z1, z2;  // of the tiles whose outputs are to come
   uint32_t rB[EB], rC[EB];
   const auto load = [&](int t0) {
     const int rows = p.len - t0 < TT ? (p.len - t0 > 0 ? p.len - t0 : 0) : TT;
@@ -74,92 +163,78 @@ __global__ __launch_bounds__(256, 2) void scan_walk_kernel(ScanArgs a) {
       if (kY) ldraw<ES>(rc, in ? static_cast<int>(t * a.sc + n) * ES : kOut, rC + i);
     }
   };
-  const int mark0 = WALK == kMarks ? first_slot(a, p.n, kMark) + static_cast<int>(static_cast<int64_t>(p.s) * a.seg / kMark) : 0;
-  float span = 0.f;
+  const auto stage = [&](int k, int q) {
+    const int rows = p.len - k * TT;
+    float d[EP], u[EP];
+#pragma unroll
+    for (int e = 0; e < EP; ++e) d[e] = ndt.get(e) + bias[e];
+    if (a.softplus)
+#pragma unroll
+      for (int e = 0; e < EP; ++e) d[e] = softplus_of(d[e]);
+#pragma unroll
+    for (int e = 0; e < EP; ++e) {
+      d[e] = row < rows ? d[e] : 0.f;
+      u[e] = d[e] * nx.get(e);
+    }
+    lds_put<EP>(&sd[q][row][col], d);
+    lds_put<EP>(&su[q][row][col], u);
+#pragma unroll
+    for (int i = 0; i < EB; ++i) {
+      const int j = tid + 256 * i;
+      if (TT * SP % 256 == 0 || j < TT * SP) {
+        sB[q][j / SP][j % SP] = dec<IO>(rB + i, 0);
+        if (kY) sC[q][j / SP][j % SP] = dec<IO>(rC + i, 0);
+      }
+    }
+  };
+  const auto outputs = [&](int k, const Row& rx, const Row& rz) {
+    const int rows = p.len - k * TT < TT ? p.len - k * TT : TT;
+    if (row >= rows || left <= 0) return;
+    float y[EP];
+#pragma unroll
+    for (int e = 0; e < EP; ++e) y[e] = Dv[e] * rx.get(e);
+#pragma unroll
+    for (int s = 0; s < NSL; ++s) lds_add<EP>(&sY[k & 1][s][row][col], y);
+    if (a.z)
+#pragma unroll
+      for (int e = 0; e < EP; ++e) y[e] *= silu_of<IO>(rz.get(e));
+    Row::store(rows_rsrc<IO>(a.y, p.begin + k * TT, a.D, b.chan, rows, b.cols),
+               static_cast<int>(static_cast<int64_t>(row) * a.D + col) * ES, left, a.vec, y);
+  };
+  // before tile k: tiles k and k+1 lie in LDS, k+2 is on its way
   load(0);
-  for (int t0 = 0; t0 < p.len; t0 += TT) {
-    const int rows = p.len - t0 < TT ? p.len - t0 : TT;
-    rx = nx;
-    rdt = ndt;
-    rz = nz;
-    {
-      float d[EP], u[EP];
-#pragma unroll
-      for (int e = 0; e < EP; ++e) {
-        const float v = rdt.get(e) + bias[e];
-        float slope;
-        d[e] = v;
-        if (a.softplus) softplus_and_slope<IO>(v, d[e], slope);
-        if (row >= rows) d[e] = 0.f;
-        u[e] = d[e] * rx.get(e);
-      }
-      lds_put<EP>(&sd[row][col], d);
-      lds_put<EP>(&su[row][col], u);
-#pragma unroll
-      for (int i = 0; i < EB; ++i) {
-        const int t = (tid + 256 * i) / SP, n = (tid + 256 * i) % SP;
-        sB[t][n] = dec<IO>(rB + i, 0);
-        if (kY) sC[t][n] = dec<IO>(rC + i, 0);
-      }
-    }
+  stage(0, 0);
+  x1 = nx;
+  z1 = nz;
+  load(TT);
+  stage(1, 1);
+  x2 = nx;
+  z2 = nz;
+  load(2 * TT);
+  __syncthreads();
+  int q = 2;
+  for (int k = 0; k < tiles; ++k) {
+    if (k + 2 < tiles) stage(k + 2, q);
+    q = q == 2 ? 0 : q + 1;
+    if (kY && k > 0) outputs(k - 1, x0, z0);
+    x0 = x1;
+    z0 = z1;
+    x1 = x2;
+    z1 = z2;
+    x2 = nx;
+    z2 = nz;
+    if (k + 2 < tiles) load((k + 3) * TT);
     __syncthreads();
-    load(t0 + TT);
-    for (int tb = 0; tb < rows; tb += 4) {
-      if (WALK == kMarks && (tb & (kMark - 1)) == 0) {
-        const int64_t m = mark0 + (t0 + tb) / kMark;
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-          a.marks[((m * scan_blocks(a.D, a.G, CH) + b.blk) * SP + sl * NR + i) * CH + ch] = h[i];
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int t = tb + k;
-        const float d = sd[t][ch], u = su[t][ch];
-        float B[NR], Cv[NR], y = 0.f;
-        lds_run<NR>(&sB[t][sl * NR], B);
-        if (kY) lds_run<NR>(&sC[t][sl * NR], Cv);
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const float e = __builtin_amdgcn_exp2f(d * A2[i]);
-          h[i] = __builtin_fmaf(e, h[i], u * B[i]);
-          if (kY) y = __builtin_fmaf(Cv[i], h[i], y);
-        }
-        if (kY) sY[sl][t][ch] = y;
-        if (WALK == kSums) span += d;
-      }
-    }
-    __syncthreads();
-    if (kY && row < rows && left > 0) {
-      float y[EP];
-#pragma unroll
-      for (int e = 0; e < EP; ++e) y[e] = Dv[e] * rx.get(e);
-#pragma unroll
-      for (int s = 0; s < NSL; ++s) lds_add<EP>(&sY[s][row][col], y);
-      if (a.z)
-#pragma unroll
-        for (int e = 0; e < EP; ++e) y[e] *= silu_of<IO>(rz.get(e));
-      Row::store(rows_rsrc<IO>(a.y, p.begin + t0, a.D, b.chan, rows, b.cols),
-                 static_cast<int>(static_cast<int64_t>(row) * a.D + col) * ES, left, a.vec, y);
-    }
   }
-  if (WALK == kSums) {
-#pragma unroll
-    for (int i = 0; i < NR; ++i) a.entry[(own + i) * CH + ch] = h[i];
-    if (sl == 0) a.span[(static_cast<int64_t>(b.slot) * scan_blocks(a.D, a.G, CH) + b.blk) * CH + ch] = span;
-  }
-  if (WALK == kOutputs && a.ht && p.s == p.count - 1 && mine) {
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-      if (sl * NR + i < a.S) a.ht[(static_cast<int64_t>(p.n) * a.D + chan) * a.S + sl * NR + i] = h[i];
-  }
+  if (kY && tiles > 0) outputs(tiles - 1, x0, z0);
 }
 
 // The adjoint a piece would hand to the one before it from zero, and the sum of
 // its steps: G_t = c_t + g_t C_t, c_{t-1} = exp(d_t A) G_t, with g_t = dy_t silu(z_t).
 template <class IO, class C>
-__global__ __launch_bounds__(256, 2) void scan_back_kernel(ScanArgs a) {
+__global__ __launch_bounds__(64 * C::W, 2) void scan_back_kernel(ScanArgs a) {
   constexpr int CH = C::CH, NR = C::NR, NL = C::NL, SP = C::SP;
-  constexpr int TT = 32, EP = TT * CH / 256, EB = TT * SP / 256;
+  constexpr int TT = 32, NT = 64 * C::W, EP = TT * CH / NT, EB = TT * SP / NT;
   constexpr int ES = sizeof(typename IO::storage);
   using Row = RowBits<IO, EP>;
   __shared__ __align__(16) float sd[TT][CH], sg[TT][CH], sC[TT][SP];
@@ -193,16 +268,14 @@ __global__ __launch_bounds__(256, 2) void scan_back_kernel(ScanArgs a) {
     uint32_t rC[EB];
 #pragma unroll
     for (int i = 0; i < EB; ++i) {
-      const int t = (tid + 256 * i) / SP, n = (tid + 256 * i) % SP;
+      const int t = (tid + NT * i) / SP, n = (tid + NT * i) % SP;
       ldraw<ES>(rc, t < rows && n < a.S ? static_cast<int>(t * a.sc + n) * ES : kOut, rC + i);
     }
     float d[EP], g[EP];
 #pragma unroll
     for (int e = 0; e < EP; ++e) {
-      const float v = rdt.get(e) + bias[e];
-      float slope;
-      d[e] = v;
-      if (a.softplus) softplus_and_slope<IO>(v, d[e], slope);
+      d[e] = rdt.get(e) + bias[e];
+      if (a.softplus) d[e] = softplus_of(d[e]);
       if (row >= rows) d[e] = 0.f;
       g[e] = rdy.get(e);
       if (a.z) g[e] *= silu_of<IO>(rz.get(e));
@@ -211,7 +284,7 @@ __global__ __launch_bounds__(256, 2) void scan_back_kernel(ScanArgs a) {
     lds_put<EP>(&sd[row][col], d);
     lds_put<EP>(&sg[row][col], g);
 #pragma unroll
-    for (int i = 0; i < EB; ++i) sC[(tid + 256 * i) / SP][(tid + 256 * i) % SP] = dec<IO>(rC + i, 0);
+    for (int i = 0; i < EB; ++i) sC[(tid + NT * i) / SP][(tid + NT * i) % SP] = dec<IO>(rC + i, 0);
     __syncthreads();
     for (int tb = (rows - 1) / 4 * 4; tb >= 0; tb -= 4) {
 #pragma unroll
@@ -272,9 +345,8 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, int lpc) {
   const int c = static_cast<int>(id - n * a.D), g = c / (a.D / a.G);
   using T = typename IO::storage;
   const float x = IO::load(static_cast<const T*>(a.x), n * a.sx + c);
-  float d = IO::load(static_cast<const T*>(a.dt), n * a.sdt + c) + (a.bias ? a.bias[c] : 0.f), slope;
-  float y = 0.f;
-  if (a.softplus) softplus_and_slope<IO>(d, d, slope);
+  float d = IO::load(static_cast<const T*>(a.dt), n * a.sdt + c) + (a.bias ? a.bias[c] : 0.f), y = 0.f;
+  if (a.softplus) d = softplus_of(d);
   if (s < a.S) {
     const int64_t at = (n * a.D + c) * a.S + s;
     V h;
@@ -325,11 +397,11 @@ launch_result launch_walk(const ScanArgs& a, const ScanPlan& p, Walk walk, hipSt
     using C = decltype(cfg);
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(p.slots) * p.blocks));
     if (walk == kOutputs)
-      hipLaunchKernelGGL((scan_walk_kernel<IO, C, kOutputs>), grid, dim3(256), 0, s, a);
+      hipLaunchKernelGGL((scan_walk_kernel<IO, C, kOutputs>), grid, dim3(64 * (C::W + 4)), 0, s, a);
     else if (walk == kSums)
-      hipLaunchKernelGGL((scan_walk_kernel<IO, C, kSums>), grid, dim3(256), 0, s, a);
+      hipLaunchKernelGGL((scan_walk_kernel<IO, C, kSums>), grid, dim3(64 * (C::W + 4)), 0, s, a);
     else
-      hipLaunchKernelGGL((scan_walk_kernel<IO, C, kMarks>), grid, dim3(256), 0, s, a);
+      hipLaunchKernelGGL((scan_walk_kernel<IO, C, kMarks>), grid, dim3(64 * (C::W + 4)), 0, s, a);
     return hipGetLastError();
   });
 }
@@ -344,22 +416,25 @@ bool scan_supported(int32_t S) { return S >= 1 && S <= 64; }
 ScanPlan scan_plan(const ScanArgs& a, bool grads) {
   ScanPlan p;
   const int per = a.D / a.G;
-  const auto wide = [&](int CH) { return static_cast<int64_t>(a.N) * a.G * ((per + CH - 1) / CH); };
+  // Workgroups of 64 channels for whole sequences; a GPU holds two a CU
+  const int64_t whole = static_cast<int64_t>(a.N) * a.G * ((per + 63) / 64);
+  const int64_t want = a.cu ? 1024 : 512;
+  // Sequences are cut where they leave CUs idle, and in packed batches, whose
+  // lengths are not known here.
+  const bool few = a.T > 256 && (a.cu || whole < 192);
   if (a.S <= 8)
     p.which = 0;
   else if (a.S <= 16)
-    p.which = wide(64) < 512 ? 2 : 1;
+    p.which = !few && whole < 512 ? 2 : 1;
   else
     p.which = a.S <= 32 ? 3 : 4;
-  p.CH = p.which <= 1 ? 64 : (p.which <= 3 ? 32 : 16);
+  p.CH = p.which <= 1 ? 64 : 32;
   p.SP = p.which == 0 ? 8 : (p.which <= 2 ? 16 : (p.which == 3 ? 32 : 64));
   p.blocks = scan_blocks(a.D, a.G, p.CH);
-  // pieces: enough for two workgroups a CU, of 128 tokens at least
-  const int64_t want = 512;
   const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
   p.seg = scan_whole(a.T);
   p.cut = 0;
-  if (a.N > 0 && a.T > 256 && (a.cu || static_cast<int64_t>(a.N) * p.blocks * 2 <= want)) {
+  if (a.N > 0 && few) {
     int64_t L = tokens * p.blocks / want;
     L = L < 128 ? 128 : (L + 31) / 32 * 32;
     if (L < a.T) {
@@ -367,17 +442,17 @@ ScanPlan scan_plan(const ScanArgs& a, bool grads) {
       p.cut = 1;
     }
   }
-  p.slots = a.cu ? a.T / p.seg + a.N : a.N * (a.T > 0 ? (a.T + p.seg - 1) / p.seg : 1);
-  if (a.N == 0) p.slots = 0;  // a packed batch of no sequences
+  // none in a packed batch of no sequences
+  p.slots = a.N == 0 ? 0 : (a.cu ? a.T / p.seg + a.N : a.N * (a.T > 0 ? (a.T + p.seg - 1) / p.seg : 1));
   p.mslots = grads && a.N > 0 ? (a.cu ? a.T / kMark + a.N : a.N * (a.T > 0 ? (a.T + kMark - 1) / kMark : 1)) : 0;
   return p;
 }
 
 int64_t scan_threads(const ScanArgs& a, bool grads) {
   // slots and threads in 64 bits, for narrow blocks and pieces of 128 tokens
-  const int64_t blocks = static_cast<int64_t>(a.G) * ((a.D / a.G + 15) / 16);
+  const int64_t blocks = static_cast<int64_t>(a.G) * ((a.D / a.G + 31) / 32);
   const int64_t slots = a.cu ? a.T / 128 + static_cast<int64_t>(a.N) : static_cast<int64_t>(a.N) * (a.T / 128 + 1);
-  return slots * blocks * 256;
+  return slots * blocks * 768;
 }
 int64_t scan_step_threads(const ScanArgs& a) {
   return static_cast<int64_t>(a.N) * a.D * step_shape(a.S).lpc;
@@ -412,9 +487,9 @@ launch_result launch_scan_pieces(const ScanArgs& a, const ScanPlan& p, int32_t i
       using C = decltype(cfg);
       const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(p.slots) * p.blocks));
       if (io_dtype == CKDA_DTYPE_BF16)
-        hipLaunchKernelGGL((scan_back_kernel<io_bf16, C>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((scan_back_kernel<io_bf16, C>), grid, dim3(64 * C::W), 0, s, a);
       else
-        hipLaunchKernelGGL((scan_back_kernel<io_f32, C>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((scan_back_kernel<io_f32, C>), grid, dim3(64 * C::W), 0, s, a);
       return hipGetLastError();
     });
   }

@@ -16,9 +16,10 @@ namespace ckda {
 namespace {
 
 template <class IO, class C>
-__global__ __launch_bounds__(256, 2) void scan_grads_kernel(ScanArgs a) {
+__global__ __launch_bounds__(64 * C::W, 2) void scan_grads_kernel(ScanArgs a) {
   constexpr int CH = C::CH, NR = C::NR, NL = C::NL, SP = C::SP, NSL = C::NSL;
-  constexpr int TT = kMark, EP = TT * CH / 256, EB = TT * SP / 256 > 0 ? TT * SP / 256 : 1;
+  constexpr int TT = kMark, NT = 64 * C::W, EP = TT * CH / NT, EB = (TT * SP + NT - 1) / NT;
+  constexpr int GV = 16 / NL, TG = GV / (2 * NR);  // values summed over channels at a time, their tokens
   constexpr int ES = sizeof(typename IO::storage);
   constexpr float kLn2 = 0.6931471805599453f;
   using Row = RowBits<IO, EP>;
@@ -58,6 +59,10 @@ __global__ __launch_bounds__(256, 2) void scan_grads_kernel(ScanArgs a) {
   const int64_t mark0 = p.n >= 0 ? first_slot(a, p.n, kMark) + static_cast<int64_t>(p.s) * a.seg / kMark : 0;
   const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
 
+  // where this lane's sum over channels goes: (token, dB or dC, state) of sbc
+  const int vi = sum_index<NL>(lane);
+  const int sum_at = (vi / (2 * NR) * 2 + vi / NR % 2) * SP + sl * NR + vi % NR;
+
   Row nx, ndt, ndy, nz;
   uint32_t rB[EB], rC[EB];
   float nh[NR];
@@ -75,7 +80,7 @@ __global__ __launch_bounds__(256, 2) void scan_grads_kernel(ScanArgs a) {
     const rsrc_t rc = rows_rsrc<IO>(a.Cm, at, a.sc, static_cast<int64_t>(b.g) * a.S, rows, a.S);
 #pragma unroll
     for (int i = 0; i < EB; ++i) {
-      const int t = (tid + 256 * i) / SP, n = (tid + 256 * i) % SP;
+      const int t = (tid + NT * i) / SP, n = (tid + NT * i) % SP;
       const bool in = t < rows && n < a.S;
       ldraw<ES>(rb, in ? static_cast<int>(t * a.sb + n) * ES : kOut, rB + i);
       ldraw<ES>(rc, in ? static_cast<int>(t * a.sc + n) * ES : kOut, rC + i);
@@ -95,27 +100,33 @@ __global__ __launch_bounds__(256, 2) void scan_grads_kernel(ScanArgs a) {
 #pragma unroll
       for (int e = 0; e < EP; ++e) {
         x[e] = nx.get(e);
-        const float v = ndt.get(e) + bias[e];
-        d[e] = v;
+        d[e] = ndt.get(e) + bias[e];
         slope[e] = 1.f;
-        if (a.softplus) softplus_and_slope<IO>(v, d[e], slope[e]);
-        if (row >= rows) d[e] = 0.f;
-        u[e] = d[e] * x[e];
         g[e] = ndy.get(e);
         dz[e] = 0.f;
-        if (a.z) {
+      }
+      if (a.softplus)
+#pragma unroll
+        for (int e = 0; e < EP; ++e) softplus_and_slope(d[e], d[e], slope[e]);
+      if (a.z)
+#pragma unroll
+        for (int e = 0; e < EP; ++e) {
           float act, s;
           silu_and_slope<IO>(nz.get(e), act, s);
           dz[e] = g[e] * s;
           g[e] *= act;
         }
+#pragma unroll
+      for (int e = 0; e < EP; ++e) {
+        d[e] = row < rows ? d[e] : 0.f;
+        u[e] = d[e] * x[e];
       }
       lds_put<EP>(&sd[row][col], d);
       lds_put<EP>(&su[row][col], u);
       lds_put<EP>(&sg[row][col], g);
 #pragma unroll
       for (int i = 0; i < EB; ++i) {
-        const int k = tid + 256 * i;
+        const int k = tid + NT * i;
         if (k < TT * SP) {
           sB[k / SP][k % SP] = dec<IO>(rB + i, 0);
           sC[k / SP][k % SP] = dec<IO>(rC + i, 0);
@@ -142,35 +153,34 @@ __global__ __launch_bounds__(256, 2) void scan_grads_kernel(ScanArgs a) {
       sP[2][sl][t][ch] = y;
     }
 #pragma unroll
-    for (int t = TT - 1; t >= 0; --t) {
-      const float dd = sd[t][ch], uu = su[t][ch], gg = sg[t][ch];
-      float B[NR], Cv[NR], gb = 0.f, wa = 0.f;
-      lds_run<NR>(&sB[t][sl * NR], B);
-      lds_run<NR>(&sC[t][sl * NR], Cv);
+    for (int tg = TT / TG - 1; tg >= 0; --tg) {
+      float v[GV];
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const float G = __builtin_fmaf(gg, Cv[i], c[i]);
-        gb = __builtin_fmaf(G, B[i], gb);
-        c[i] = ex[t][i] * G;
-        const float w = c[i] * h[t][i];
-        wa = __builtin_fmaf(w, A2[i], wa);
-        dA[i] = __builtin_fmaf(w, dd, dA[i]);
-        float vb = G * uu, vc = gg * h[t + 1][i];
+      for (int j = TG - 1; j >= 0; --j) {
+        const int t = tg * TG + j;
+        const float dd = sd[t][ch], uu = su[t][ch], gg = sg[t][ch];
+        float B[NR], Cv[NR], gb = 0.f, wa = 0.f;
+        lds_run<NR>(&sB[t][sl * NR], B);
+        lds_run<NR>(&sC[t][sl * NR], Cv);
 #pragma unroll
-        for (int m = CH / 2; m >= 1; m /= 2) {
-          vb += __shfl_xor(vb, m, 64);
-          vc += __shfl_xor(vc, m, 64);
+        for (int i = 0; i < NR; ++i) {
+          const float G = __builtin_fmaf(gg, Cv[i], c[i]);
+          gb = __builtin_fmaf(G, B[i], gb);
+          c[i] = ex[t][i] * G;
+          const float w = c[i] * h[t][i];
+          wa = __builtin_fmaf(w, A2[i], wa);
+          dA[i] = __builtin_fmaf(w, dd, dA[i]);
+          v[(j * 2) * NR + i] = G * uu;
+          v[(j * 2 + 1) * NR + i] = gg * h[t + 1][i];
         }
-        if (ch == 0) {
-          sbc[t][0][sl * NR + i] = vb;
-          sbc[t][1][sl * NR + i] = vc;
-        }
+        sP[0][sl][t][ch] = gb;
+        sP[1][sl][t][ch] = wa;
       }
-      sP[0][sl][t][ch] = gb;
-      sP[1][sl][t][ch] = wa;
+      const float sum = sum_channels<NL>(v);
+      if ((lane & 3) == 0) (&sbc[0][0][0])[tg * TG * 2 * SP + sum_at] = sum;
     }
     __syncthreads();
-    for (int k = tid; k < rows * 2 * SP; k += 256)
+    for (int k = tid; k < rows * 2 * SP; k += NT)
       a.partbc[(static_cast<int64_t>(b.blk) * tokens + p.begin + t0) * 2 * SP + k] = (&sbc[0][0][0])[k];
     if (row < rows && left > 0) {
       float gb[EP], wa[EP], y[EP], dx[EP], dt[EP];
@@ -216,7 +226,7 @@ __global__ __launch_bounds__(256, 2) void scan_grads_kernel(ScanArgs a) {
     red[(TT + row) * CH + col + e] = db[e];
   }
   __syncthreads();
-  for (int k = tid; k < 2 * CH; k += 256) {
+  for (int k = tid; k < 2 * CH; k += NT) {
     float v = 0.f;
     for (int r = 0; r < TT; ++r) v += red[((k / CH) * TT + r) * CH + k % CH];
     a.partD[own * 2 * CH + k] = v;
@@ -302,7 +312,7 @@ launch_result launch_io(const ScanArgs& a, const ScanPlan& p, hipStream_t s) {
     using C = decltype(cfg);
     if (p.slots > 0) {
       hipLaunchKernelGGL((scan_grads_kernel<IO, C>), dim3(static_cast<unsigned>(static_cast<int64_t>(p.slots) * p.blocks)),
-                         dim3(256), 0, s, a);
+                         dim3(64 * C::W), 0, s, a);
       const launch_result e = hipGetLastError();
       if (e != hipSuccess) return e;
     }

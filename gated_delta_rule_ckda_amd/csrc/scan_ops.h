@@ -5,11 +5,11 @@
 //
 // and, with a gate, y_t silu(z_t).  B and C are shared by the channels of a group.
 //
-// A workgroup of four waves walks over the tokens of one piece of a sequence for
-// CH channels.  Lanes hold channels, and the states of a channel are dealt out to
-// the workgroup's 4 NL slices (NL slices a wave, side by side in its lanes), NR a
-// lane, so that a lane's sums over states are its own and only 4 NL partial sums
-// a token and channel meet in LDS.
+// W waves of a workgroup walk over the tokens of one piece of a sequence for CH
+// channels.  Lanes hold channels, and the states of a channel are dealt out to W NL
+// slices (NL slices a wave, side by side in its lanes), NR a lane, so that a
+// lane's sums over states are its own and only W NL partial sums a token and
+// channel meet in LDS.
 #pragma once
 
 #include "decay_ops.h"
@@ -17,30 +17,33 @@
 
 namespace ckda {
 
-template <int NL_, int NR_>
+template <int W_, int NL_, int NR_>
 struct ScanCfg {
-  static constexpr int NL = NL_, NR = NR_;
+  static constexpr int W = W_, NL = NL_, NR = NR_;
   static constexpr int CH = 64 / NL;     // channels of a workgroup
-  static constexpr int NSL = 4 * NL;     // slices of the states
+  static constexpr int NSL = W * NL;     // slices of the states
   static constexpr int SP = NSL * NR;    // states, the last ones possibly padding
 };
 
-// softplus and its derivative, the sigmoid.  log1p(e) is formed so that it keeps
-// the digits of a small e; -inf gives 0.
-template <class IO>
+// exp(-m) for m >= 0, the rounding of m log2(e) undone (it would cost m / 2 half
+// steps of the value); zeros from about 87 on.
+__device__ __forceinline__ float exp_minus(float m) {
+  m = fminf(m, 200.f);
+  const float t = m * -kLog2e, e = __builtin_amdgcn_exp2f(t);
+  const float r = __builtin_fmaf(m, -kLog2e, -t);  // what t lost
+  return __builtin_fmaf(e * 0.6931471805599453f, r, e);
+}
+// softplus: max(v, 0) + log(1 + e), e = exp(-|v|).  u = 1 + e is off by c, which
+// the last step puts back, so a small e keeps its digits (c counts 1 / u times;
+// leaving that out costs less than half a step).  -inf gives 0, NaN stays.
+__device__ __forceinline__ float softplus_of(float v) {
+  const float e = exp_minus(fabsf(v)), u = 1.f + e, c = e - (u - 1.f);
+  return (v < 0.f ? 0.f : v) + __builtin_fmaf(__builtin_amdgcn_logf(u), 0.6931471805599453f, c);
+}
+// with its derivative, the sigmoid
 __device__ __forceinline__ void softplus_and_slope(float v, float& d, float& slope) {
-  const float m = fabsf(v);
-  float e, l, r;
-  if constexpr (sizeof(typename IO::storage) == 2) {
-    e = exp_neg(m);
-    l = log2_1p(e) * 0.6931471805599453f;
-    r = __builtin_amdgcn_rcpf(1.f + e);
-  } else {
-    e = expf(-m);
-    l = log1pf(e);
-    r = 1.f / (1.f + e);
-  }
-  d = fmaxf(v, 0.f) + l;
+  const float e = exp_minus(fabsf(v)), u = 1.f + e, c = e - (u - 1.f), r = __builtin_amdgcn_rcpf(u);
+  d = (v < 0.f ? 0.f : v) + __builtin_fmaf(__builtin_amdgcn_logf(u), 0.6931471805599453f, c);
   slope = v < 0.f ? e * r : r;
 }
 
@@ -202,6 +205,51 @@ __device__ __forceinline__ void lds_add(const float* p, float* v) {
   }
 }
 
+// ---- sums over a wave's channels ---------------------------------------------
+// 16 / NL values a lane, to be summed over the lanes of each slice: halves of the
+// wave and neighbouring rows of 16 lanes are added while pairs of values become one
+// register, then the lanes of a row, four registers becoming one.  Lane l, for l a
+// multiple of 4, ends with the sum of value sum_index(l) of slice l / (64 / NL).
+template <int NL>
+__device__ __forceinline__ float sum_channels(const float (&v)[16 / NL]) {
+  const auto swap = [](float x, float y, auto f) {
+    const auto r = f(__float_as_uint(x), __float_as_uint(y));
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  };
+  const auto halves = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane32_swap(x, y, false, false); };
+  const auto rows = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane16_swap(x, y, false, false); };
+  float s[8], q[4];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s[k] = NL == 1 ? swap(v[2 * k], v[NL == 1 ? 2 * k + 1 : 0], halves) : v[NL == 1 ? 0 : k];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) q[k] = swap(s[2 * k], s[2 * k + 1], rows);
+  // banks of 4 lanes: 0 and 1 from q0 (q2), 2 and 3 from q1 (q3); then bank 1 from
+  // q0, 3 from q1, 0 from q2, 2 from q3; then all four lanes of a bank.  A lane's
+  // register is read by its neighbours two wait states after it is written.
+  float t0, t1, r;
+  asm("s_nop 1\n\t"
+      "v_add_f32_dpp %0, %3, %3 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %1, %5, %5 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %0, %4, %4 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %1, %6, %6 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "s_nop 1\n\t"
+      "v_add_f32_dpp %2, %0, %0 row_ror:4 row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %2, %1, %1 row_ror:12 row_mask:0xf bank_mask:0x5\n\t"
+      "s_nop 1\n\t"
+      "v_add_f32_dpp %2, %2, %2 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "s_nop 1\n\t"
+      "v_add_f32_dpp %2, %2, %2 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf"
+      : "=&v"(t0), "=&v"(t1), "=&v"(r)
+      : "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3]));
+  return r;
+}
+template <int NL>
+__device__ __forceinline__ int sum_index(int lane) {
+  const int row = lane >> 4, bank = (lane >> 2) & 3, q = (0x1302 >> (4 * bank)) & 3;  // 2, 0, 3, 1
+  if (NL == 1) return 4 * q + ((row & 1) << 1 | row >> 1);
+  return 2 * q + (row & 1);
+}
+
 constexpr int kMark = 16;  // tokens between the states kept for the gradients
 
 // Tokens of a piece where sequences are not cut: past every sequence's end.
@@ -211,11 +259,11 @@ __host__ __device__ __forceinline__ int scan_whole(int T) { return T + 1; }
 template <class F>
 launch_result scan_config(int which, F f) {
   switch (which) {
-    case 0: return f(ScanCfg<1, 2>{});
-    case 1: return f(ScanCfg<1, 4>{});
-    case 2: return f(ScanCfg<2, 2>{});
-    case 3: return f(ScanCfg<2, 4>{});
-    default: return f(ScanCfg<4, 4>{});
+    case 0: return f(ScanCfg<4, 1, 2>{});
+    case 1: return f(ScanCfg<4, 1, 4>{});
+    case 2: return f(ScanCfg<4, 2, 2>{});
+    case 3: return f(ScanCfg<4, 2, 4>{});
+    default: return f(ScanCfg<8, 2, 4>{});
   }
 }
 struct ScanPlan {
