@@ -543,7 +543,8 @@ def l2norm_debug(x, stream=None):
 
 def _tensors(device, **named):
     """Checks that every given tensor is contiguous on `device` (a GPU)."""
-    _require(device.type == "cuda", "tensors must be on a GPU, got %s" % device)
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a GPU, got %s" % device)
     for name, t in named.items():
         if t is not None:
             if t.device != device:
@@ -566,6 +567,14 @@ def _launch(device, fn, *args):
     else:
         with torch.cuda.device(device):
             _check(fn(*args, stream))
+
+
+def _new(like):
+    """An uninitialised contiguous tensor of `like`'s shape, type and device."""
+    import torch
+    if like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(like.shape, device=like.device, dtype=like.dtype)
 
 
 def _sizes_ok(sizes):
@@ -820,6 +829,25 @@ def block_norm_bwd(y, weight, dh, *, dnext=None, gate=None, act="sigmoid", resid
     return dy, dw, dg, dx, ds, dw2
 
 
+# torch's accessor of the current stream's bare handle, where it has one: 0.1 us
+# of a call, where a Stream object takes 1.8 (a call with small tensors: 12)
+def _bare_stream(device):
+    import torch
+    bare = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(device).cuda_stream if bare is None else bare(device.index)
+
+
+def _launch_bare(device, fn, *args):
+    """_launch, with the stream's handle by _bare_stream."""
+    import torch
+    stream = _bare_stream(device)
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream))
+
+
 # ---- layer norm
 
 def layer_norm(x, weight, bias=None, *, residual=None, eps=1e-5, out=None, residual_out=None, stream=None):
@@ -840,7 +868,7 @@ def layer_norm(x, weight, bias=None, *, residual=None, eps=1e-5, out=None, resid
     h = residual_out
     if residual is not None and h is None:
         h = torch.empty_like(x)
-    _launch(x.device, lib.ckda_layer_norm, rows, d, io, float(eps), _addr(x), _addr(residual),
+    _launch_bare(x.device, lib.ckda_layer_norm, rows, d, io, float(eps), _addr(x), _addr(residual),
             _addr(weight), _addr(bias), _addr(n), _addr(h))
     return n, h
 
@@ -866,7 +894,7 @@ def layer_norm_bwd(x, weight, dn, *, dh=None, eps=1e-5, output_dbias=True, works
         return dx, dw, db
     need = int(lib.ckda_layer_norm_bwd_workspace_size(rows, d, io))
     ws = _workspace(workspace, need, x.device)
-    _launch(x.device, lib.ckda_layer_norm_bwd, rows, d, io, float(eps), _addr(x), _addr(weight),
+    _launch_bare(x.device, lib.ckda_layer_norm_bwd, rows, d, io, float(eps), _addr(x), _addr(weight),
             _addr(dn), _addr(dh), _addr(dx), _addr(dw), _addr(db), _addr(ws), ws.numel())
     return dx, dw, db
 
@@ -876,6 +904,8 @@ def layer_norm_bwd(x, weight, dn, *, dh=None, eps=1e-5, output_dbias=True, works
 def _row_stride(name, t, lead, width):
     """Elements between the tokens of t, [*lead, ...] with `width` contiguous elements
     a token (it may be a part of wider rows)."""
+    if t.is_contiguous():
+        return width
     shape, strides = t.shape, t.stride()
     want = 1
     for i in range(len(shape) - 1, lead - 1, -1):
@@ -911,12 +941,13 @@ def _batch(x, cu_seqlens):
     return lead, B, T, n
 
 
-def _on(device, **named):
+def _on(device, *tensors):
     """Checks that every given tensor is on `device` (a GPU)."""
-    _require(device.type == "cuda", "tensors must be on a GPU, got %s" % device)
-    for name, t in named.items():
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a GPU, got %s" % device)
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+            raise ValueError("a tensor is on %s, not on %s" % (t.device, device))
 
 
 def _like(name, t, shape, dtype):
@@ -966,17 +997,17 @@ def conv_fwd(x, weight, *, bias=None, act="silu", h0=None, cu_seqlens=None, outp
     lib = _load()
     desc, _ = _conv_desc(x, weight, bias, act, cu_seqlens)
     dev = x.device
-    _on(dev, x=x)
+    _on(dev, x)
     _tensors(dev, weight=weight, bias=bias, h0=h0, cu_seqlens=cu_seqlens, out=out, final_state=final_state)
     cache = (desc.num_seqs, desc.K - 1, desc.D)
     _like("h0", h0, cache, x.dtype)
     _like("final_state", final_state, cache, x.dtype)
     _like("out", out, x.shape, x.dtype)
-    y = torch.empty(x.shape, device=dev, dtype=x.dtype) if out is None else out
+    y = _new(x) if out is None else out
     ht = final_state
     if output_final_state and ht is None:
         ht = torch.empty(cache, device=dev, dtype=x.dtype)
-    _launch(dev, lib.ckda_conv_fwd, ctypes.byref(desc), _addr(x), _addr(weight), _addr(bias),
+    _launch_bare(dev, lib.ckda_conv_fwd, ctypes.byref(desc), _addr(x), _addr(weight), _addr(bias),
             _addr(cu_seqlens), _addr(h0), _addr(y), _addr(ht))
     return y, ht
 
@@ -992,18 +1023,18 @@ def conv_bwd(x, weight, dout, *, bias=None, act="silu", h0=None, dht=None, cu_se
     lib = _load()
     desc, need = _conv_desc(x, weight, bias, act, cu_seqlens)
     dev = x.device
-    _on(dev, x=x)
+    _on(dev, x)
     _tensors(dev, weight=weight, bias=bias, h0=h0, dout=dout, dht=dht, cu_seqlens=cu_seqlens)
     cache = (desc.num_seqs, desc.K - 1, desc.D)
     _like("h0", h0, cache, x.dtype)
     _like("dht", dht, cache, x.dtype)
     _like("dout", dout, x.shape, x.dtype)
-    dx = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    dx = _new(x)
     dw = torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
     dh0 = torch.empty(cache, device=dev, dtype=x.dtype) if output_dh0 else None
     ws = _workspace(workspace, need, dev)
-    _launch(dev, lib.ckda_conv_bwd, ctypes.byref(desc), _addr(x), _addr(weight), _addr(bias),
+    _launch_bare(dev, lib.ckda_conv_bwd, ctypes.byref(desc), _addr(x), _addr(weight), _addr(bias),
             _addr(cu_seqlens), _addr(h0), _addr(dout), _addr(dht), _addr(dx), _addr(dw), _addr(db),
             _addr(dh0), _addr(ws), ws.numel())
     return dx, dw, db, dh0
@@ -1014,18 +1045,17 @@ def conv_step(x, weight, state, *, bias=None, act="silu", out=None, new_state=No
     updated in place unless new_state is given.  Returns y [N,D]."""
     if stream is not None:
         return _on_stream(conv_step, locals())
-    import torch
     lib = _load()
     desc, _ = _conv_desc(x, weight, bias, act, None, step=True)
     dev = x.device
-    _on(dev, x=x)
+    _on(dev, x)
     _tensors(dev, weight=weight, bias=bias, state=state, out=out, new_state=new_state)
     cache = (desc.B, desc.K - 1, desc.D)
     _like("state", state, cache, x.dtype)
     _like("new_state", new_state, cache, x.dtype)
     _like("out", out, x.shape, x.dtype)
-    y = torch.empty(x.shape, device=dev, dtype=x.dtype) if out is None else out
-    _launch(dev, lib.ckda_conv_step, ctypes.byref(desc), _addr(x), _addr(weight), _addr(bias),
+    y = _new(x) if out is None else out
+    _launch_bare(dev, lib.ckda_conv_step, ctypes.byref(desc), _addr(x), _addr(weight), _addr(bias),
             _addr(state), _addr(state if new_state is None else new_state), _addr(y))
     return y
 
@@ -1062,7 +1092,7 @@ def _scan_desc(x, dt, A, B, C, D, z, dt_bias, steps, cu_seqlens, step=False):
              and B.shape[-1] == S, "B must be [...,groups,S] or [...,S] with the tokens of x")
     _require(C.dtype == x.dtype and C.shape == B.shape, "C must match B")
     _require(G > 0 and chans % G == 0, "the groups must divide the channels")
-    _on(x.device, x=x, dt=dt, B=B, C=C, z=z)
+    _on(x.device, x, dt, B, C, z)
     return _scan_plan(int(cu_seqlens is not None), nb, T, chans, S, G, n, io, int(steps == "logits"),
                       _row_stride("x", x, lead, chans), _row_stride("dt", dt, lead, chans),
                       0 if z is None else _row_stride("z", z, lead, chans),
@@ -1095,12 +1125,12 @@ def scan_fwd(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, steps="logits", h0
     _state_ok("h0", h0, shape)
     _state_ok("final_state", final_state, shape)
     _like("out", out, x.shape, x.dtype)
-    y = torch.empty(x.shape, device=dev, dtype=x.dtype) if out is None else out
+    y = _new(x) if out is None else out
     ht = final_state
     if output_final_state and ht is None:
         ht = torch.empty(shape, device=dev, dtype=torch.float32)
     ws = _workspace(workspace, need, dev) if need else None
-    _launch(dev, lib.ckda_scan_fwd, ctypes.byref(desc), _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
+    _launch_bare(dev, lib.ckda_scan_fwd, ctypes.byref(desc), _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
             _addr(D), _addr(z), _addr(dt_bias), _addr(cu_seqlens), _addr(h0), _addr(y), _addr(ht), _addr(ws),
             0 if ws is None else ws.numel())
     return y, ht
@@ -1124,11 +1154,11 @@ def scan_bwd(x, dt, A, B, C, dout, *, D=None, z=None, dt_bias=None, steps="logit
     _state_ok("h0", h0, shape)
     _state_ok("dht", dht, shape)
     _like("dout", dout, x.shape, x.dtype)
-    new = lambda t: None if t is None else torch.empty(t.shape, device=dev, dtype=t.dtype)
+    new = lambda t: None if t is None else _new(t)
     dx, ddt, dA, dB, dC, dD, dz, dbias = (new(t) for t in (x, dt, A, B, C, D, z, dt_bias))
     dh0 = torch.empty(shape, device=dev, dtype=torch.float32) if output_dh0 else None
     ws = _workspace(workspace, need, dev)
-    _launch(dev, lib.ckda_scan_bwd, ctypes.byref(desc), _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
+    _launch_bare(dev, lib.ckda_scan_bwd, ctypes.byref(desc), _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
             _addr(D), _addr(z), _addr(dt_bias), _addr(cu_seqlens), _addr(h0), _addr(dout), _addr(dht),
             _addr(dx), _addr(ddt), _addr(dA), _addr(dB), _addr(dC), _addr(dD), _addr(dz), _addr(dbias),
             _addr(dh0), _addr(ws), ws.numel())
@@ -1142,7 +1172,6 @@ def scan_step(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, steps="log
     Returns y [N,D]."""
     if stream is not None:
         return _on_stream(scan_step, locals())
-    import torch
     lib = _load()
     desc, _, _ = _scan_desc(x, dt, A, B, C, D, z, dt_bias, steps, None, step=True)
     dev = x.device
@@ -1151,8 +1180,8 @@ def scan_step(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, steps="log
     _state_ok("state", state, shape)
     _state_ok("new_state", new_state, shape)
     _like("out", out, x.shape, x.dtype)
-    y = torch.empty(x.shape, device=dev, dtype=x.dtype) if out is None else out
-    _launch(dev, lib.ckda_scan_step, ctypes.byref(desc), _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
+    y = _new(x) if out is None else out
+    _launch_bare(dev, lib.ckda_scan_step, ctypes.byref(desc), _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
             _addr(D), _addr(z), _addr(dt_bias), _addr(state), _addr(state if new_state is None else new_state),
             _addr(y))
     return y

@@ -942,7 +942,7 @@ ckda_status_t validate_conv(const ckda_conv_desc_t* d, const int32_t* cu, bool g
   a->N = d->num_seqs;
   a->act = d->act == CKDA_NORM_GATE_SILU;
   a->cu = cu;
-  if (ckda::conv_threads(*a, d->io_dtype, grads) >= (int64_t(1) << 32))
+  if (ckda::conv_threads(*a, grads) >= (int64_t(1) << 32))
     return fail(CKDA_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
   return ok();
 }
@@ -958,7 +958,7 @@ size_t ckda_conv_bwd_workspace_size(const ckda_conv_desc_t* d, int32_t packed) {
   kept.swap(g_last_error);
   const ckda_status_t st = validate_conv(d, packed ? &given : nullptr, true, &a);
   kept.swap(g_last_error);
-  return st == CKDA_OK ? ckda::conv_bwd_workspace(a, d->io_dtype) : 0;
+  return st == CKDA_OK ? ckda::conv_bwd_workspace(a) : 0;
 }
 
 ckda_status_t ckda_conv_fwd(const ckda_conv_desc_t* d, const void* x, const float* w, const float* bias,
@@ -1010,7 +1010,7 @@ ckda_status_t ckda_conv_bwd(const ckda_conv_desc_t* d, const void* x, const floa
                        {range("dh0", dh0, dh0 ? state : 0), true, false}};
   if ((st = check_tensors(ts, 10)) != CKDA_OK) return st;
   if ((st = no_output_on(ts, 10, cu_seqlens, d->num_seqs)) != CKDA_OK) return st;
-  const size_t need = ckda::conv_bwd_workspace(a, d->io_dtype);
+  const size_t need = ckda::conv_bwd_workspace(a);
   if ((st = check_workspace(ts, 10, workspace, workspace_bytes, need)) != CKDA_OK) return st;
   a.x = x;
   a.w = w;
@@ -1281,7 +1281,7 @@ extern "C" {
 size_t ckda_layer_norm_bwd_workspace_size(int64_t rows, int32_t d, int32_t io_dtype) {
   if (rows <= 0 || d <= 0 || d > 16384) return 0;
   if (io_dtype != CKDA_DTYPE_BF16 && io_dtype != CKDA_DTYPE_F32) return 0;
-  return ckda::layer_norm_bwd_workspace(rows, d, io_dtype);
+  return ckda::layer_norm_bwd_workspace(rows, d);
 }
 
 ckda_status_t ckda_layer_norm(int64_t rows, int32_t d, int32_t io_dtype, float eps, const void* x, const void* r,

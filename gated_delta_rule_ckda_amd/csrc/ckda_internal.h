@@ -295,8 +295,8 @@ struct ConvGrads {
   float* part;         // [workgroups along the slots][K + 1][D]
 };
 // Threads of a call's largest launch (a launch counts them in 32 bits).
-int64_t conv_threads(const ConvArgs& a, int32_t io_dtype, bool grads);
-size_t conv_bwd_workspace(const ConvArgs& a, int32_t io_dtype);
+int64_t conv_threads(const ConvArgs& a, bool grads);
+size_t conv_bwd_workspace(const ConvArgs& a);
 launch_result launch_conv_fwd(ConvArgs a, int32_t io_dtype, hipStream_t s);
 launch_result launch_conv_bwd(ConvArgs a, ConvGrads g, int32_t io_dtype, void* ws, hipStream_t s);
 launch_result launch_conv_step(const ConvArgs& a, int32_t io_dtype, hipStream_t s);
@@ -371,7 +371,7 @@ struct LayerNormGrads {
   float* db;
   float* part;         // [workgroups][2][d]
 };
-size_t layer_norm_bwd_workspace(int64_t rows, int32_t d, int32_t io_dtype);
+size_t layer_norm_bwd_workspace(int64_t rows, int32_t d);
 launch_result launch_layer_norm(const LayerNormArgs& a, int32_t io_dtype, hipStream_t s);
 launch_result launch_layer_norm_bwd(const LayerNormArgs& a, LayerNormGrads g, int32_t io_dtype, void* ws,
                                     hipStream_t s);

@@ -18,37 +18,30 @@
 namespace ckda {
 namespace {
 
-// One row of VEC channels, widened.
-template <class IO, int VEC>
-__device__ __forceinline__ void row_f32(const void* p, int64_t i, float* x) {
-  const auto v = Vec<IO, VEC>::load(p, i);
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) x[e] = Vec<IO, VEC>::get(v, e);
-}
-
 template <int VEC, int K>
 struct Taps {
   float w[VEC][K], b[VEC];
   __device__ __forceinline__ Taps(const ConvArgs& a, int c) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
+      const int64_t at = c + e < a.D ? c + e : 0;
 #pragma unroll
-      for (int j = 0; j < K; ++j) w[e][j] = a.w[static_cast<int64_t>(c + e) * K + j];
-      b[e] = a.bias ? a.bias[c + e] : 0.f;
+      for (int j = 0; j < K; ++j) w[e][j] = a.w[at * K + j];
+      b[e] = a.bias ? a.bias[at] : 0.f;
     }
   }
 };
 
 // The K-1 inputs before token t0 of sequence n, whose tokens begin at `begin`.
-template <class IO, int VEC, int K>
+template <class X, int VEC, int K>
 __device__ __forceinline__ void window(const ConvArgs& a, int n, int64_t begin, int t0, int c, float (&x)[K - 1][VEC]) {
 #pragma unroll
   for (int r = 0; r < K - 1; ++r) {
     const int t = t0 - (K - 1) + r;
     if (t >= 0) {
-      row_f32<IO, VEC>(a.x, (begin + t) * a.sx + c, x[r]);
+      X::row(a.x, (begin + t) * a.sx + c, a.D - c, x[r]);
     } else if (a.h0) {
-      row_f32<IO, VEC>(a.h0, (static_cast<int64_t>(n) * (K - 1) + (K - 1 + t)) * a.D + c, x[r]);
+      X::row(a.h0, (static_cast<int64_t>(n) * (K - 1) + (K - 1 + t)) * a.D + c, a.D - c, x[r]);
     } else {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) x[r][e] = 0.f;
@@ -56,9 +49,9 @@ __device__ __forceinline__ void window(const ConvArgs& a, int n, int64_t begin, 
   }
 }
 
-template <class IO, int VEC, int K>
+template <class IO, int VEC, bool ALIGNED, int K>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int cx, int ny) {
-  using X = Vec<IO, VEC>;
+  using X = Chans<IO, VEC, ALIGNED>;
   constexpr int U = 4;
   const int chunk = blockIdx.x % ny, py = 256 / cx;
   const int slot = (blockIdx.x / ny) * py + threadIdx.x / cx;
@@ -71,7 +64,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int cx, int n
   float x[K - 1 + U][VEC];
   {
     float first[K - 1][VEC];
-    window<IO, VEC, K>(a, p.n, q.begin, p.s * a.tile, c, first);
+    window<X, VEC, K>(a, p.n, q.begin, p.s * a.tile, c, first);
 #pragma unroll
     for (int r = 0; r < K - 1; ++r)
 #pragma unroll
@@ -82,7 +75,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int cx, int n
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       next[u] = typename X::V{};
-      if (t + u < p.len) next[u] = X::load(a.x, (p.begin + t + u) * a.sx + c);
+      if (t + u < p.len) next[u] = X::load(a.x, (p.begin + t + u) * a.sx + c, a.D - c);
     }
   };
   load(0);
@@ -103,7 +96,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int cx, int n
         for (int j = 0; j < K; ++j) s += w.w[e][j] * x[u + j][e];
         y[e] = a.act ? silu_of<IO>(s) : s;
       }
-      X::store(a.y, (p.begin + t + u) * a.D + c, y);
+      X::store(a.y, (p.begin + t + u) * a.D + c, a.D - c, y);
     }
 #pragma unroll
     for (int r = 0; r < K - 1; ++r)
@@ -118,14 +111,14 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int cx, int n
       const int t = q.len - (K - 1) + r;
       float v[VEC];
       if (t >= 0) {
-        row_f32<IO, VEC>(a.x, (q.begin + t) * a.sx + c, v);
+        X::row(a.x, (q.begin + t) * a.sx + c, a.D - c, v);
       } else if (a.h0) {
-        row_f32<IO, VEC>(a.h0, at + static_cast<int64_t>(K - 1 + t) * a.D, v);
+        X::row(a.h0, at + static_cast<int64_t>(K - 1 + t) * a.D, a.D - c, v);
       } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[e] = 0.f;
       }
-      X::store(a.ht, at + static_cast<int64_t>(r) * a.D, v);
+      X::store(a.ht, at + static_cast<int64_t>(r) * a.D, a.D - c, v);
     }
   }
 }
@@ -134,9 +127,9 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int cx, int n
 // gradient of the input K-1 tokens back, whose last tap g_t was; it walks K-1
 // tokens past its tile for the inputs at the tile's end.  Each workgroup leaves
 // its tiles' sums for dw and db in part[workgroup][K + 1][D].
-template <class IO, int VEC, int K>
+template <class IO, int VEC, bool ALIGNED, int K>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, ConvGrads gr, int cx, int ny) {
-  using X = Vec<IO, VEC>;
+  using X = Chans<IO, VEC, ALIGNED>;
   __shared__ float red[256 * VEC];
   const int chunk = blockIdx.x % ny, py = 256 / cx, grp = blockIdx.x / ny;
   const int slot = grp * py + threadIdx.x / cx;
@@ -158,7 +151,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, ConvGrads gr,
     float x[K][VEC], g[K][VEC];  // inputs t-K+1..t, gradients g_{t-K+1}..g_t
     {
       float first[K - 1][VEC];
-      window<IO, VEC, K>(a, p.n, q.begin, t0, c, first);
+      window<X, VEC, K>(a, p.n, q.begin, t0, c, first);
 #pragma unroll
       for (int r = 0; r < K; ++r)
 #pragma unroll
@@ -170,8 +163,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, ConvGrads gr,
     typename X::V nx = typename X::V{}, ng = nx;
     const auto load = [&](int t) {
       if (t < q.len) {
-        nx = X::load(a.x, (q.begin + t) * a.sx + c);
-        ng = X::load(gr.dy, (q.begin + t) * a.D + c);
+        nx = X::load(a.x, (q.begin + t) * a.sx + c, a.D - c);
+        ng = X::load(gr.dy, (q.begin + t) * a.D + c, a.D - c);
       }
     };
     const int end = t0 + p.len + K - 1;
@@ -219,14 +212,14 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, ConvGrads gr,
       }
       if (gr.dht && t >= q.len) {
         float more[VEC];
-        row_f32<IO, VEC>(gr.dht, (static_cast<int64_t>(p.n) * (K - 1) + (t - q.len)) * a.D + c, more);
+        X::row(gr.dht, (static_cast<int64_t>(p.n) * (K - 1) + (t - q.len)) * a.D + c, a.D - c, more);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) dx[e] += more[e];
       }
       if (s >= 0)
-        X::store(gr.dx, (q.begin + s) * a.D + c, dx);
+        X::store(gr.dx, (q.begin + s) * a.D + c, a.D - c, dx);
       else if (t0 == 0)
-        X::store(gr.dh0, (static_cast<int64_t>(p.n) * (K - 1) + t) * a.D + c, dx);
+        X::store(gr.dh0, (static_cast<int64_t>(p.n) * (K - 1) + t) * a.D + c, a.D - c, dx);
     }
   }
   // sums over the workgroup's tiles, in order
@@ -243,7 +236,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, ConvGrads gr,
       for (int e = 0; e < VEC; ++e) {
         float v = j < K ? dw[j < K ? j : 0][e] : db[e];
         for (int r = 1; r < py; ++r) v += red[(threadIdx.x + r * cx) * VEC + e];
-        gr.part[(static_cast<int64_t>(grp) * (K + 1) + j) * a.D + c + e] = v;
+        if (c + e < a.D) gr.part[(static_cast<int64_t>(grp) * (K + 1) + j) * a.D + c + e] = v;
       }
     }
   }
@@ -272,9 +265,9 @@ __global__ __launch_bounds__(1024) void conv_cols_kernel(const float* part, int 
 }
 
 // One token a sequence: the cache moves up a row in place.
-template <class IO, int VEC, int K>
+template <class IO, int VEC, bool ALIGNED, int K>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int nv) {
-  using X = Vec<IO, VEC>;
+  using X = Chans<IO, VEC, ALIGNED>;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t n = i / nv;
   const int c = static_cast<int>(i - n * nv) * VEC;
@@ -282,8 +275,8 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int nv) {
   const int64_t at = n * (K - 1) * a.D + c;
   float x[K][VEC], y[VEC];
 #pragma unroll
-  for (int r = 0; r < K - 1; ++r) row_f32<IO, VEC>(a.h0, at + static_cast<int64_t>(r) * a.D, x[r]);
-  row_f32<IO, VEC>(a.x, n * a.sx + c, x[K - 1]);
+  for (int r = 0; r < K - 1; ++r) X::row(a.h0, at + static_cast<int64_t>(r) * a.D, a.D - c, x[r]);
+  X::row(a.x, n * a.sx + c, a.D - c, x[K - 1]);
   const Taps<VEC, K> w(a, c);
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
@@ -292,19 +285,14 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int nv) {
     for (int j = 0; j < K; ++j) s += w.w[e][j] * x[j][e];
     y[e] = a.act ? silu_of<IO>(s) : s;
   }
-  X::store(a.y, n * a.D + c, y);
+  X::store(a.y, n * a.D + c, a.D - c, y);
 #pragma unroll
-  for (int r = 0; r < K - 1; ++r) X::store(a.ht, at + static_cast<int64_t>(r) * a.D, x[r + 1]);
+  for (int r = 0; r < K - 1; ++r) X::store(a.ht, at + static_cast<int64_t>(r) * a.D, a.D - c, x[r + 1]);
 }
 
-bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
-
-// Channels a thread: 16 bytes where the width and the tokens of x allow it.
-int vec_of(const ConvArgs& a, int es) {
-  const int wide = 16 / es;
-  if (a.D % wide == 0 && a.sx % wide == 0 && aligned(a.x, 16)) return wide;
-  if (es == 2 && a.D % 2 == 0 && a.sx % 2 == 0 && aligned(a.x, 4)) return 2;
-  return 1;
+// Whether every vector of VEC channels lies at a multiple of its size.
+bool aligned(const ConvArgs& a, int vec, int es) {
+  return a.D % vec == 0 && a.sx % vec == 0 && reinterpret_cast<uintptr_t>(a.x) % (vec * es) == 0;
 }
 
 struct Grid {
@@ -312,7 +300,7 @@ struct Grid {
   int64_t groups;     // workgroups over slots
 };
 Grid grid_of(const ConvArgs& a, int vec) {
-  const int nv = a.D / vec;
+  const int nv = (a.D + vec - 1) / vec;
   Grid g{1, 0, 0};
   while (g.cx < 64 && g.cx < nv) g.cx *= 2;
   g.ny = (nv + g.cx - 1) / g.cx;
@@ -321,31 +309,44 @@ Grid grid_of(const ConvArgs& a, int vec) {
   return g;
 }
 
-constexpr int kFwdTile = 32, kBwdTile = 64;
+constexpr int kVec = 4;  // channels a thread
+
 int32_t slots_of(const ConvArgs& a, int tile) {
   if (a.N == 0) return 0;  // a packed batch of no sequences
   if (a.cu) return a.T / tile + a.N;
   return a.N * (a.T > 0 ? (a.T + tile - 1) / tile : 1);
 }
+// Tokens of a tile: long ones read fewer rows twice and leave fewer partial sums,
+// but there have to be waves enough to hide the loads.  Measured: gradients of
+// 2 x 4096 tokens of 2001 channels (1000 waves with tiles of 64) 82 us with 64,
+// 54 with 32; of 8 x 4096 of 2048 in bf16 (4096 waves) 96 with 64, 106 with 32;
+// forward of the latter 53 with 32 and with 64, 55 with 16.
+void set_tile(ConvArgs& a, bool grads) {
+  const int64_t nv = (a.D + kVec - 1) / kVec;
+  a.tile = grads ? 64 : 32;
+  while (a.tile > 8 && slots_of(a, a.tile) * nv < 2048 * 64) a.tile /= 2;
+  a.slots = slots_of(a, a.tile);
+}
 
 enum Pass { kFwd, kBwd, kStep };
 
-template <class IO, int VEC, int K>
+template <class IO, int VEC, bool ALIGNED, int K>
 launch_result launch_one(const ConvArgs& a, const ConvGrads* g, Pass pass, hipStream_t s) {
   if (pass == kStep) {
-    const int nv = a.D / VEC;
+    const int nv = (a.D + VEC - 1) / VEC;
     const int64_t grid = (static_cast<int64_t>(a.N) * nv + 255) / 256;
-    hipLaunchKernelGGL((conv_step_kernel<IO, VEC, K>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a, nv);
+    hipLaunchKernelGGL((conv_step_kernel<IO, VEC, ALIGNED, K>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a,
+                       nv);
     return hipGetLastError();
   }
   const Grid r = grid_of(a, VEC);
   const dim3 grid(static_cast<unsigned>(r.groups * r.ny));
   if (pass == kFwd) {
-    hipLaunchKernelGGL((conv_fwd_kernel<IO, VEC, K>), grid, dim3(256), 0, s, a, r.cx, r.ny);
+    hipLaunchKernelGGL((conv_fwd_kernel<IO, VEC, ALIGNED, K>), grid, dim3(256), 0, s, a, r.cx, r.ny);
     return hipGetLastError();
   }
   if (r.groups > 0) {
-    hipLaunchKernelGGL((conv_bwd_kernel<IO, VEC, K>), grid, dim3(256), 0, s, a, *g, r.cx, r.ny);
+    hipLaunchKernelGGL((conv_bwd_kernel<IO, VEC, ALIGNED, K>), grid, dim3(256), 0, s, a, *g, r.cx, r.ny);
     const launch_result e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -355,53 +356,47 @@ launch_result launch_one(const ConvArgs& a, const ConvGrads* g, Pass pass, hipSt
   return hipGetLastError();
 }
 
-template <class IO, int VEC>
+template <class IO, int VEC, bool ALIGNED>
 launch_result launch_taps(const ConvArgs& a, const ConvGrads* g, Pass pass, hipStream_t s) {
-  if (a.K == 2) return launch_one<IO, VEC, 2>(a, g, pass, s);
-  if (a.K == 3) return launch_one<IO, VEC, 3>(a, g, pass, s);
-  return launch_one<IO, VEC, 4>(a, g, pass, s);
+  if (a.K == 2) return launch_one<IO, VEC, ALIGNED, 2>(a, g, pass, s);
+  if (a.K == 3) return launch_one<IO, VEC, ALIGNED, 3>(a, g, pass, s);
+  return launch_one<IO, VEC, ALIGNED, 4>(a, g, pass, s);
 }
 
+template <class IO>
+launch_result launch_io(const ConvArgs& a, const ConvGrads* g, Pass pass, hipStream_t s) {
+  if (aligned(a, kVec, sizeof(typename IO::storage))) return launch_taps<IO, kVec, true>(a, g, pass, s);
+  return launch_taps<IO, kVec, false>(a, g, pass, s);
+}
 launch_result launch(const ConvArgs& a, const ConvGrads* g, int32_t io_dtype, Pass pass, hipStream_t s) {
-  if (io_dtype == CKDA_DTYPE_BF16) {
-    const int v = vec_of(a, 2);
-    if (v == 8) return launch_taps<io_bf16, 8>(a, g, pass, s);
-    if (v == 2) return launch_taps<io_bf16, 2>(a, g, pass, s);
-    return launch_taps<io_bf16, 1>(a, g, pass, s);
-  }
-  if (vec_of(a, 4) == 4) return launch_taps<io_f32, 4>(a, g, pass, s);
-  return launch_taps<io_f32, 1>(a, g, pass, s);
+  return io_dtype == CKDA_DTYPE_BF16 ? launch_io<io_bf16>(a, g, pass, s) : launch_io<io_f32>(a, g, pass, s);
 }
 
 }  // namespace
 
-int64_t conv_threads(const ConvArgs& a0, int32_t io_dtype, bool grads) {
-  // one channel a thread, the most there can be
+int64_t conv_threads(const ConvArgs& a0, bool grads) {
   ConvArgs a = a0;
-  const int tile = grads ? kBwdTile : kFwdTile;
-  if (static_cast<int64_t>(a.N) * (static_cast<int64_t>(a.T) / tile + 1) >= (int64_t(1) << 31)) return int64_t(1) << 62;
-  a.slots = slots_of(a, tile);
-  const Grid g = grid_of(a, 1);
+  const int64_t most = a.cu ? a.T / 8 + static_cast<int64_t>(a.N) : static_cast<int64_t>(a.N) * (a.T / 8 + 1);
+  if (most >= (int64_t(1) << 31)) return int64_t(1) << 62;
+  set_tile(a, grads);
+  const Grid g = grid_of(a, kVec);
   return g.groups * g.ny * 256;
 }
 
-// A column sum a workgroup: there are most workgroups with one channel a thread,
-// so this does not depend on how the tensors are aligned.
-size_t conv_bwd_workspace(const ConvArgs& a0, int32_t io_dtype) {
+// A column sum a workgroup.
+size_t conv_bwd_workspace(const ConvArgs& a0) {
   ConvArgs a = a0;
-  a.slots = slots_of(a, kBwdTile);
-  return static_cast<size_t>(grid_of(a, 1).groups) * (a.K + 1) * a.D * 4;
+  set_tile(a, true);
+  return static_cast<size_t>(grid_of(a, kVec).groups) * (a.K + 1) * a.D * 4;
 }
 
 launch_result launch_conv_fwd(ConvArgs a, int32_t io_dtype, hipStream_t s) {
-  a.tile = kFwdTile;
-  a.slots = slots_of(a, a.tile);
+  set_tile(a, false);
   return launch(a, nullptr, io_dtype, kFwd, s);
 }
 
 launch_result launch_conv_bwd(ConvArgs a, ConvGrads g, int32_t io_dtype, void* ws, hipStream_t s) {
-  a.tile = kBwdTile;
-  a.slots = slots_of(a, a.tile);
+  set_tile(a, true);
   g.part = static_cast<float*>(ws);
   return launch(a, &g, io_dtype, kBwd, s);
 }

@@ -79,6 +79,66 @@ struct Vec {
   }
 };
 
+// VEC elements of a row.  ALIGNED: whole vectors at multiples of their size,
+// streamed.  Otherwise they may lie anywhere and the row's last one may hold fewer
+// (n elements): wide accesses all the same, which the memory path splits where they
+// cross a line, and cached ones, since neighbours share lines.  Measured on 40000
+// rows of 1001 float32: a convolution takes 67 us so, 128 an element at a time.
+template <class IO, int VEC, bool ALIGNED>
+struct Chans {
+  using T = typename IO::storage;
+  typedef T V __attribute__((ext_vector_type(VEC)));
+  struct __attribute__((packed)) Any {
+    T x[VEC];
+  };
+  static __device__ __forceinline__ V load(const void* p, int64_t i, int n) {
+    const T* at = static_cast<const T*>(p) + i;
+    if constexpr (ALIGNED) return __builtin_nontemporal_load(reinterpret_cast<const V*>(at));
+    V v = V{};
+    if (n >= VEC) {
+      const Any a = *reinterpret_cast<const Any*>(at);
+      v = __builtin_bit_cast(V, a);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e < n) v[e] = at[e];
+    }
+    return v;
+  }
+  static __device__ __forceinline__ float get(const V& v, int e) {
+    if constexpr (sizeof(T) == 2)
+      return bf16_to_f32(v[e]);
+    else
+      return v[e];
+  }
+  static __device__ __forceinline__ void store(void* p, int64_t i, int n, const float* x) {
+    T* at = static_cast<T*>(p) + i;
+    V v;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if constexpr (sizeof(T) == 2)
+        v[e] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(x[e]));
+      else
+        v[e] = x[e];
+    }
+    if constexpr (ALIGNED) {
+      __builtin_nontemporal_store(v, reinterpret_cast<V*>(at));
+    } else if (n >= VEC) {
+      *reinterpret_cast<Any*>(at) = __builtin_bit_cast(Any, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e < n) at[e] = v[e];
+    }
+  }
+  // widened
+  static __device__ __forceinline__ void row(const void* p, int64_t i, int n, float* x) {
+    const V v = load(p, i, n);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[e] = get(v, e);
+  }
+};
+
 // Sums of N values over the TPR threads of a row (a power of two); `red` holds
 // 2 * MOST floats a wave and is used alternately (two halves), so one barrier a sum.
 template <int N, int NT, int MOST = 2>
