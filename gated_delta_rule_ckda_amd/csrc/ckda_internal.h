@@ -322,9 +322,12 @@ struct ScanArgs {
   // pieces of a sequence run side by side (seg: tokens of a piece)
   int32_t seg, slots;
   int32_t cut;         // 1: sequences may have more than one piece
-  float* entry;        // [slots][blocks][SP][CH] what enters a piece
+  float* entry;        // [slots][blocks][SP][CH] the state entering a piece
+  float* leave;        // the adjoint entering it from behind
   float* span;         // [slots][blocks][CH] the sum of a piece's steps
-  float* marks;        // [mark slots][blocks][SP][CH] the state entering every 16 tokens
+  float* marks;        // [mark slots][blocks][SP][CH] the state entering every 16 tokens,
+                       // where sequences are cut as far as the piece itself wrote it
+  float* mspan;        // [mark slots][blocks][CH] the sum of the piece's steps up to there
   int32_t mslots;
   // gradients
   const void* dy;

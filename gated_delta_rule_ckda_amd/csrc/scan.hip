@@ -9,7 +9,10 @@ namespace {
 enum Walk {
   kOutputs,   // y, and ht after a sequence's last piece
   kSums,      // the state it would end in from zero, and the sum of its steps
-  kMarks,     // the states entering every kMark tokens
+  kMarks,     // the states entering every kMark tokens; in a piece of a cut sequence
+              // from zero, with the sums of steps up to them, and what kSums leaves
+  kBack,      // kSums for the adjoint, against the tokens:
+              //   c_{t-1} = exp(d_t A) (c_t + g_t C_t),  g_t = dy_t silu(z_t)
 };
 
 // The operands of four tokens on their way from LDS to the states.
@@ -37,7 +40,7 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
   constexpr int CH = C::CH, NR = C::NR, NL = C::NL, SP = C::SP, NSL = C::NSL;
   constexpr int TT = 16, EP = TT * CH / 256, EB = (TT * SP + 255) / 256;
   constexpr int ES = sizeof(typename IO::storage);
-  constexpr bool kY = WALK == kOutputs;
+  constexpr bool kY = WALK == kOutputs, kRev = WALK == kBack, kSum = WALK == kSums || kRev;
   using Row = RowBits<IO, EP>;
   __shared__ __align__(16) float sd[3][TT][CH], su[3][TT][CH], sB[3][TT][SP], sC[kY ? 3 : 1][kY ? TT : 1][SP];
   __shared__ __align__(16) float sY[2][kY ? NSL : 1][TT][CH];
@@ -45,12 +48,14 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
   const ScanBlock<C> b(a);
   const Piece p = piece_of(a, b.slot, a.seg, lane);
   if (p.n < 0) return;
-  // nothing enters a piece after a sequence's last one
+  // nothing enters a piece after a sequence's last one, or from before its first
   if (WALK == kSums && p.s == p.count - 1) return;
+  if (kRev && p.s == 0) return;
   const int tiles = (p.len + TT - 1) / TT;
   const int64_t blocks = scan_blocks(a.D, a.G, CH);
 
   if (wave < C::W) {
+    __builtin_amdgcn_s_setprio(2);  // the others have a tile's time
     // ---- states
     const int ch = lane % CH, sl = wave * NL + lane / CH;
     const bool mine = ch < b.cols;
@@ -63,7 +68,7 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
       const bool ok = mine && n < a.S;
       A2[i] = ok ? a.A[chan * a.S + n] * kLog2e : 0.f;
       h[i] = 0.f;
-      if (WALK != kSums) {
+      if (!kSum && !(WALK == kMarks && a.cut)) {
         if (a.cut)
           h[i] = a.entry[(own + i) * CH + ch];
         else if (a.h0 && ok)
@@ -78,13 +83,14 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
     };
     __syncthreads();
     int q = 0, half = 0;
-    if (tiles > 0) fetch(ops[0], 0, 0);
+    if (tiles > 0) fetch(ops[0], 0, kRev ? TT - 4 : 0);
     for (int k = 0; k < tiles; ++k) {
       if (WALK == kMarks) {
         static_assert(TT == kMark, "a state a tile");
 #pragma unroll
         for (int i = 0; i < NR; ++i)
           a.marks[(((mark0 + k) * blocks + b.blk) * SP + sl * NR + i) * CH + ch] = h[i];
+        if (a.cut && sl == 0) a.mspan[((mark0 + k) * blocks + b.blk) * CH + ch] = span;
       }
       const int next = q == 2 ? 0 : q + 1;
 #pragma unroll
@@ -96,7 +102,8 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
 #pragma unroll
           for (int i = 0; i < NR; ++i) e[j][i] = o.d[j] * A2[i];
         // past the last tile this reads what an earlier one left
-        fetch(ops[(g + 1) & 1], g + 1 < TT / 4 ? q : next, (g + 1) % (TT / 4) * 4);
+        const int to = (g + 1) % (TT / 4) * 4;
+        fetch(ops[(g + 1) & 1], g + 1 < TT / 4 ? q : next, kRev ? TT - 4 - to : to);
         __builtin_amdgcn_sched_barrier(0);
         // powers run together: a switch between them and other operations costs both
 #pragma unroll
@@ -105,24 +112,29 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
           for (int i = 0; i < NR; ++i) e[j][i] = __builtin_amdgcn_exp2f(e[j][i]);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int jj = 0; jj < 4; ++jj) {
+          const int j = kRev ? 3 - jj : jj;
           float y = 0.f;
 #pragma unroll
           for (int i = 0; i < NR; ++i) {
-            h[i] = __builtin_fmaf(e[j][i], h[i], o.u[j] * o.B[j][i]);
+            if (kRev)
+              h[i] = e[j][i] * __builtin_fmaf(o.u[j], o.B[j][i], h[i]);
+            else
+              h[i] = __builtin_fmaf(e[j][i], h[i], o.u[j] * o.B[j][i]);
             if (kY) y = __builtin_fmaf(o.C[j][i], h[i], y);
           }
           if (kY) sY[half][sl][4 * g + j][ch] = y;
-          if (WALK == kSums) span += o.d[j];
+          if (kSum || WALK == kMarks) span += o.d[j];
         }
       }
       q = next;
       half ^= 1;
       __syncthreads();
     }
-    if (WALK == kSums) {
+    if (kSum || (WALK == kMarks && a.cut)) {
+      float* to = kRev ? a.leave : a.entry;
 #pragma unroll
-      for (int i = 0; i < NR; ++i) a.entry[(own + i) * CH + ch] = h[i];
+      for (int i = 0; i < NR; ++i) to[(own + i) * CH + ch] = h[i];
       if (sl == 0) a.span[(b.slot * blocks + b.blk) * CH + ch] = span;
     }
     if (WALK == kOutputs && a.ht && p.s == p.count - 1 && mine) {
@@ -145,26 +157,32 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
   Row nx, ndt, nz;
   Row x0, x1, x2, z0, z1, z2;  // of the tiles whose outputs are to come
   uint32_t rB[EB], rC[EB];
-  const auto load = [&](int t0) {
-    const int rows = p.len - t0 < TT ? (p.len - t0 > 0 ? p.len - t0 : 0) : TT;
+  // against the tokens the writes are dy's gated and B's place is C's
+  const void* px = kRev ? a.dy : a.x;
+  const int64_t sx = kRev ? a.D : a.sx, sb = kRev ? a.sc : a.sb;
+  // tile k in the order of the walk
+  const auto first = [&](int k) { return (kRev ? tiles - 1 - k : k) * TT; };
+  const auto load = [&](int k) {
+    const int t0 = k < tiles ? first(k) : p.len;
+    const int rows = p.len - t0 < TT ? p.len - t0 : TT;
     const int64_t at = p.begin + (rows > 0 ? t0 : 0);
     const bool ok = row < rows && left > 0;
-    nx.load(rows_rsrc<IO>(a.x, at, a.sx, b.chan, rows, b.cols), ok ? static_cast<int>(row * a.sx + col) * ES : kOut, left, a.vec);
+    nx.load(rows_rsrc<IO>(px, at, sx, b.chan, rows, b.cols), ok ? static_cast<int>(row * sx + col) * ES : kOut, left, a.vec);
     ndt.load(rows_rsrc<IO>(a.dt, at, a.sdt, b.chan, rows, b.cols), ok ? static_cast<int>(row * a.sdt + col) * ES : kOut, left, a.vec);
-    if (kY && a.z)
+    if ((kY || kRev) && a.z)
       nz.load(rows_rsrc<IO>(a.z, at, a.sz, b.chan, rows, b.cols), ok ? static_cast<int>(row * a.sz + col) * ES : kOut, left, a.vec);
-    const rsrc_t rb = rows_rsrc<IO>(a.Bm, at, a.sb, static_cast<int64_t>(b.g) * a.S, rows, a.S);
+    const rsrc_t rb = rows_rsrc<IO>(kRev ? a.Cm : a.Bm, at, sb, static_cast<int64_t>(b.g) * a.S, rows, a.S);
     const rsrc_t rc = rows_rsrc<IO>(kY ? a.Cm : a.Bm, at, kY ? a.sc : a.sb, static_cast<int64_t>(b.g) * a.S, rows, a.S);
 #pragma unroll
     for (int i = 0; i < EB; ++i) {
       const int t = (tid + 256 * i) / SP, n = (tid + 256 * i) % SP;
       const bool in = t < rows && n < a.S;
-      ldraw<ES>(rb, in ? static_cast<int>(t * a.sb + n) * ES : kOut, rB + i);
+      ldraw<ES>(rb, in ? static_cast<int>(t * sb + n) * ES : kOut, rB + i);
       if (kY) ldraw<ES>(rc, in ? static_cast<int>(t * a.sc + n) * ES : kOut, rC + i);
     }
   };
   const auto stage = [&](int k, int q) {
-    const int rows = p.len - k * TT;
+    const int rows = k < tiles ? p.len - first(k) : 0;
     float d[EP], u[EP];
 #pragma unroll
     for (int e = 0; e < EP; ++e) d[e] = ndt.get(e) + bias[e];
@@ -174,8 +192,11 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
 #pragma unroll
     for (int e = 0; e < EP; ++e) {
       d[e] = row < rows ? d[e] : 0.f;
-      u[e] = d[e] * nx.get(e);
+      u[e] = kRev ? nx.get(e) : d[e] * nx.get(e);
     }
+    if (kRev && a.z)
+#pragma unroll
+      for (int e = 0; e < EP; ++e) u[e] *= silu_of<IO>(nz.get(e));
     lds_put<EP>(&sd[q][row][col], d);
     lds_put<EP>(&su[q][row][col], u);
 #pragma unroll
@@ -206,11 +227,11 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
   stage(0, 0);
   x1 = nx;
   z1 = nz;
-  load(TT);
+  load(1);
   stage(1, 1);
   x2 = nx;
   z2 = nz;
-  load(2 * TT);
+  load(2);
   __syncthreads();
   int q = 2;
   for (int k = 0; k < tiles; ++k) {
@@ -223,87 +244,10 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
     z1 = z2;
     x2 = nx;
     z2 = nz;
-    if (k + 2 < tiles) load((k + 3) * TT);
+    if (k + 2 < tiles) load(k + 3);
     __syncthreads();
   }
   if (kY && tiles > 0) outputs(tiles - 1, x0, z0);
-}
-
-// The adjoint a piece would hand to the one before it from zero, and the sum of
-// its steps: G_t = c_t + g_t C_t, c_{t-1} = exp(d_t A) G_t, with g_t = dy_t silu(z_t).
-template <class IO, class C>
-__global__ __launch_bounds__(64 * C::W, 2) void scan_back_kernel(ScanArgs a) {
-  constexpr int CH = C::CH, NR = C::NR, NL = C::NL, SP = C::SP;
-  constexpr int TT = 32, NT = 64 * C::W, EP = TT * CH / NT, EB = TT * SP / NT;
-  constexpr int ES = sizeof(typename IO::storage);
-  using Row = RowBits<IO, EP>;
-  __shared__ __align__(16) float sd[TT][CH], sg[TT][CH], sC[TT][SP];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const ScanBlock<C> b(a);
-  const Piece p = piece_of(a, b.slot, a.seg, lane);
-  if (p.n < 0 || p.s == 0) return;  // nothing comes before a sequence's first piece
-  const int ch = lane % CH, sl = wave * NL + lane / CH;
-  const bool mine = ch < b.cols;
-  float A2[NR], c[NR];
-#pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int n = sl * NR + i;
-    A2[i] = mine && n < a.S ? a.A[static_cast<int64_t>(b.chan + ch) * a.S + n] * kLog2e : 0.f;
-    c[i] = 0.f;
-  }
-  const int row = tid / (CH / EP), col = tid % (CH / EP) * EP, left = b.cols - col;
-  float bias[EP];
-#pragma unroll
-  for (int e = 0; e < EP; ++e) bias[e] = a.bias && e < left ? a.bias[b.chan + col + e] : 0.f;
-  float span = 0.f;
-  for (int t0 = (p.len - 1) / TT * TT; t0 >= 0; t0 -= TT) {
-    const int rows = p.len - t0 < TT ? p.len - t0 : TT;
-    const int64_t at = p.begin + t0;
-    const bool ok = row < rows && left > 0;
-    Row rdt, rdy, rz;
-    rdt.load(rows_rsrc<IO>(a.dt, at, a.sdt, b.chan, rows, b.cols), ok ? static_cast<int>(row * a.sdt + col) * ES : kOut, left, a.vec);
-    rdy.load(rows_rsrc<IO>(a.dy, at, a.D, b.chan, rows, b.cols), ok ? static_cast<int>(static_cast<int64_t>(row) * a.D + col) * ES : kOut, left, a.vec);
-    if (a.z) rz.load(rows_rsrc<IO>(a.z, at, a.sz, b.chan, rows, b.cols), ok ? static_cast<int>(row * a.sz + col) * ES : kOut, left, a.vec);
-    const rsrc_t rc = rows_rsrc<IO>(a.Cm, at, a.sc, static_cast<int64_t>(b.g) * a.S, rows, a.S);
-    uint32_t rC[EB];
-#pragma unroll
-    for (int i = 0; i < EB; ++i) {
-      const int t = (tid + NT * i) / SP, n = (tid + NT * i) % SP;
-      ldraw<ES>(rc, t < rows && n < a.S ? static_cast<int>(t * a.sc + n) * ES : kOut, rC + i);
-    }
-    float d[EP], g[EP];
-#pragma unroll
-    for (int e = 0; e < EP; ++e) {
-      d[e] = rdt.get(e) + bias[e];
-      if (a.softplus) d[e] = softplus_of(d[e]);
-      if (row >= rows) d[e] = 0.f;
-      g[e] = rdy.get(e);
-      if (a.z) g[e] *= silu_of<IO>(rz.get(e));
-    }
-    __syncthreads();
-    lds_put<EP>(&sd[row][col], d);
-    lds_put<EP>(&sg[row][col], g);
-#pragma unroll
-    for (int i = 0; i < EB; ++i) sC[(tid + NT * i) / SP][(tid + NT * i) % SP] = dec<IO>(rC + i, 0);
-    __syncthreads();
-    for (int tb = (rows - 1) / 4 * 4; tb >= 0; tb -= 4) {
-#pragma unroll
-      for (int k = 3; k >= 0; --k) {
-        const int t = tb + k;
-        const float dd = sd[t][ch], gg = sg[t][ch];
-        float Cv[NR];
-        lds_run<NR>(&sC[t][sl * NR], Cv);
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-          c[i] = __builtin_amdgcn_exp2f(dd * A2[i]) * __builtin_fmaf(gg, Cv[i], c[i]);
-        span += dd;
-      }
-    }
-  }
-  const int64_t own = static_cast<int64_t>(b.slot) * scan_blocks(a.D, a.G, CH) + b.blk;
-#pragma unroll
-  for (int i = 0; i < NR; ++i) a.entry[(own * SP + sl * NR + i) * CH + ch] = c[i];
-  if (sl == 0) a.span[own * CH + ch] = span;
 }
 
 // entry[s], the pieces' own sums, become what enters them: R <- exp(A span_s) R + sum_s
@@ -324,7 +268,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a) {
     float R = ok && from ? from[(static_cast<int64_t>(n) * a.D + chan) * a.S + st] : 0.f;
     for (int j = 0; j < count; ++j) {
       const int64_t own = static_cast<int64_t>(first + (REV ? count - 1 - j : j)) * blocks + blk;
-      float* at = a.entry + own * SP * CH + k;
+      float* at = (REV ? a.leave : a.entry) + own * SP * CH + k;
       const bool last = j == count - 1;  // its own sum enters no piece and was not formed
       const float sum = last ? 0.f : *at;
       const float gain = last ? 0.f : __builtin_amdgcn_exp2f(a.span[own * CH + ch] * A2);
@@ -400,6 +344,8 @@ launch_result launch_walk(const ScanArgs& a, const ScanPlan& p, Walk walk, hipSt
       hipLaunchKernelGGL((scan_walk_kernel<IO, C, kOutputs>), grid, dim3(64 * (C::W + 4)), 0, s, a);
     else if (walk == kSums)
       hipLaunchKernelGGL((scan_walk_kernel<IO, C, kSums>), grid, dim3(64 * (C::W + 4)), 0, s, a);
+    else if (walk == kBack)
+      hipLaunchKernelGGL((scan_walk_kernel<IO, C, kBack>), grid, dim3(64 * (C::W + 4)), 0, s, a);
     else
       hipLaunchKernelGGL((scan_walk_kernel<IO, C, kMarks>), grid, dim3(64 * (C::W + 4)), 0, s, a);
     return hipGetLastError();
@@ -418,10 +364,10 @@ ScanPlan scan_plan(const ScanArgs& a, bool grads) {
   const int per = a.D / a.G;
   // Workgroups of 64 channels for whole sequences; a GPU holds two a CU
   const int64_t whole = static_cast<int64_t>(a.N) * a.G * ((per + 63) / 64);
-  const int64_t want = a.cu ? 1024 : 512;
+  const int64_t want = a.cu || grads ? 1024 : 512;
   // Sequences are cut where they leave CUs idle, and in packed batches, whose
   // lengths are not known here.
-  const bool few = a.T > 256 && (a.cu || whole < 192);
+  const bool few = a.T > 256 && (a.cu || whole < (grads ? 512 : 192));
   if (a.S <= 8)
     p.which = 0;
   else if (a.S <= 16)
@@ -478,22 +424,7 @@ size_t scan_fwd_workspace(const ScanArgs& a0) {
   return layout_pieces(a, scan_plan(a, false), nullptr);
 }
 
-launch_result launch_scan_pieces(const ScanArgs& a, const ScanPlan& p, int32_t io_dtype, bool rev, hipStream_t s) {
-  launch_result e;
-  if (!rev) {
-    e = launch_walk_io(a, p, kSums, io_dtype, s);
-  } else {
-    e = scan_config(p.which, [&](auto cfg) -> launch_result {
-      using C = decltype(cfg);
-      const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(p.slots) * p.blocks));
-      if (io_dtype == CKDA_DTYPE_BF16)
-        hipLaunchKernelGGL((scan_back_kernel<io_bf16, C>), grid, dim3(64 * C::W), 0, s, a);
-      else
-        hipLaunchKernelGGL((scan_back_kernel<io_f32, C>), grid, dim3(64 * C::W), 0, s, a);
-      return hipGetLastError();
-    });
-  }
-  if (e != hipSuccess) return e;
+launch_result launch_scan_join(const ScanArgs& a, const ScanPlan& p, bool rev, hipStream_t s) {
   return scan_config(p.which, [&](auto cfg) -> launch_result {
     using C = decltype(cfg);
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.N) * p.blocks));
@@ -506,14 +437,19 @@ launch_result launch_scan_pieces(const ScanArgs& a, const ScanPlan& p, int32_t i
 }
 
 launch_result launch_scan_marks(const ScanArgs& a, const ScanPlan& p, int32_t io_dtype, hipStream_t s) {
-  return launch_walk_io(a, p, kMarks, io_dtype, s);
+  launch_result e = launch_walk_io(a, p, kMarks, io_dtype, s);
+  if (e != hipSuccess || !p.cut) return e;
+  e = launch_scan_join(a, p, false, s);
+  if (e == hipSuccess) e = launch_walk_io(a, p, kBack, io_dtype, s);
+  return e == hipSuccess ? launch_scan_join(a, p, true, s) : e;
 }
 
 launch_result launch_scan_fwd(ScanArgs a, int32_t io_dtype, void* ws, hipStream_t s) {
   const ScanPlan p = scan_plan(a, false);
   layout_pieces(a, p, static_cast<unsigned char*>(ws));
   if (p.cut) {
-    const launch_result e = launch_scan_pieces(a, p, io_dtype, false, s);
+    launch_result e = launch_walk_io(a, p, kSums, io_dtype, s);
+    if (e == hipSuccess) e = launch_scan_join(a, p, false, s);
     if (e != hipSuccess) return e;
   }
   return launch_walk_io(a, p, kOutputs, io_dtype, s);

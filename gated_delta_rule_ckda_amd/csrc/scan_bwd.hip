@@ -9,7 +9,9 @@
 //
 // The states are formed again: a first walk leaves the one entering every kMark
 // tokens, and the walk backwards takes kMark tokens at a time, forwards into
-// registers and then back.
+// registers and then back.  In a cut sequence the pieces' first walks start from
+// zero, and what enters a piece is added to its marks, decayed over the steps
+// since, as they are read: so the states are walked once.
 #include "scan_ops.h"
 
 namespace ckda {
@@ -43,7 +45,7 @@ __global__ __launch_bounds__(64 * C::W, 2) void scan_grads_kernel(ScanArgs a) {
     dA[i] = c[i] = 0.f;
     if (p.n >= 0) {
       if (a.cut)
-        c[i] = a.entry[(own * SP + n) * CH + ch];
+        c[i] = a.leave[(own * SP + n) * CH + ch];
       else if (a.dht && ok)
         c[i] = a.dht[(static_cast<int64_t>(p.n) * a.D + chan) * a.S + n];
     }
@@ -65,7 +67,7 @@ __global__ __launch_bounds__(64 * C::W, 2) void scan_grads_kernel(ScanArgs a) {
 
   Row nx, ndt, ndy, nz;
   uint32_t rB[EB], rC[EB];
-  float nh[NR];
+  float nh[NR], ne[NR], ns = 0.f;  // a tile's first state: the piece's part, what entered, the steps since
   const auto load = [&](int t0) {
     const bool some = t0 >= 0;
     const int rows = !some ? 0 : (p.len - t0 < TT ? p.len - t0 : TT);
@@ -86,20 +88,24 @@ __global__ __launch_bounds__(64 * C::W, 2) void scan_grads_kernel(ScanArgs a) {
       ldraw<ES>(rc, in ? static_cast<int>(t * a.sc + n) * ES : kOut, rC + i);
     }
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
+    for (int i = 0; i < NR; ++i) {
       nh[i] = some ? a.marks[(((mark0 + t0 / kMark) * blocks + b.blk) * SP + sl * NR + i) * CH + ch] : 0.f;
+      if (a.cut) ne[i] = a.entry[(own * SP + sl * NR + i) * CH + ch];
+    }
+    if (a.cut && some) ns = a.mspan[((mark0 + t0 / kMark) * blocks + b.blk) * CH + ch];
   };
 
   const int last = p.n >= 0 && p.len > 0 ? (p.len - 1) / TT * TT : -1;
   if (last >= 0) load(last);
   for (int t0 = last; t0 >= 0; t0 -= TT) {
     const int rows = p.len - t0 < TT ? p.len - t0 : TT;
-    float x[EP], d[EP], slope[EP], g[EP], dz[EP];
+    // kept for the outputs; d and g are read back from this thread's places in LDS
+    const Row rx = nx;
+    float slope[EP], dz[EP];
     {
-      float u[EP];
+      float u[EP], d[EP], g[EP];
 #pragma unroll
       for (int e = 0; e < EP; ++e) {
-        x[e] = nx.get(e);
         d[e] = ndt.get(e) + bias[e];
         slope[e] = 1.f;
         g[e] = ndy.get(e);
@@ -119,7 +125,7 @@ __global__ __launch_bounds__(64 * C::W, 2) void scan_grads_kernel(ScanArgs a) {
 #pragma unroll
       for (int e = 0; e < EP; ++e) {
         d[e] = row < rows ? d[e] : 0.f;
-        u[e] = d[e] * x[e];
+        u[e] = d[e] * rx.get(e);
       }
       lds_put<EP>(&sd[row][col], d);
       lds_put<EP>(&su[row][col], u);
@@ -135,7 +141,8 @@ __global__ __launch_bounds__(64 * C::W, 2) void scan_grads_kernel(ScanArgs a) {
     }
     float h[TT + 1][NR], ex[TT][NR];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) h[0][i] = nh[i];
+    for (int i = 0; i < NR; ++i)
+      h[0][i] = a.cut ? __builtin_fmaf(__builtin_amdgcn_exp2f(ns * A2[i]), ne[i], nh[i]) : nh[i];
     __syncthreads();
     load(t0 - TT);
 #pragma unroll
@@ -183,12 +190,15 @@ __global__ __launch_bounds__(64 * C::W, 2) void scan_grads_kernel(ScanArgs a) {
     for (int k = tid; k < rows * 2 * SP; k += NT)
       a.partbc[(static_cast<int64_t>(b.blk) * tokens + p.begin + t0) * 2 * SP + k] = (&sbc[0][0][0])[k];
     if (row < rows && left > 0) {
-      float gb[EP], wa[EP], y[EP], dx[EP], dt[EP];
+      float gb[EP], wa[EP], y[EP], dx[EP], dt[EP], x[EP], d[EP], g[EP];
 #pragma unroll
       for (int e = 0; e < EP; ++e) {
-        gb[e] = wa[e] = 0.f;
+        gb[e] = wa[e] = d[e] = g[e] = 0.f;
+        x[e] = rx.get(e);
         y[e] = Dv[e] * x[e];
       }
+      lds_add<EP>(&sd[row][col], d);
+      lds_add<EP>(&sg[row][col], g);
 #pragma unroll
       for (int s = 0; s < NSL; ++s) {
         lds_add<EP>(&sP[0][s][row][col], gb);
@@ -298,6 +308,8 @@ size_t layout(ScanArgs& a, const ScanPlan& p, unsigned char* ws) {
     return r;
   };
   a.entry = take(p.cut ? at * p.slots : 0);
+  a.leave = take(p.cut ? at * p.slots : 0);
+  a.mspan = take(p.cut ? lanes * p.mslots : 0);
   a.span = take(p.cut ? lanes * p.slots : 0);
   a.marks = take(at * p.mslots);
   a.partbc = take(static_cast<size_t>(p.blocks) * a.B * a.T * 2 * p.SP * 4);
@@ -342,10 +354,7 @@ launch_result launch_scan_bwd(ScanArgs a, int32_t io_dtype, void* ws, hipStream_
   const ScanPlan p = scan_plan(a, true);
   layout(a, p, static_cast<unsigned char*>(ws));
   if (p.slots > 0) {
-    launch_result e = hipSuccess;
-    if (p.cut) e = launch_scan_pieces(a, p, io_dtype, false, s);
-    if (e == hipSuccess) e = launch_scan_marks(a, p, io_dtype, s);
-    if (e == hipSuccess && p.cut) e = launch_scan_pieces(a, p, io_dtype, true, s);
+    const launch_result e = launch_scan_marks(a, p, io_dtype, s);
     if (e != hipSuccess) return e;
   }
   return io_dtype == CKDA_DTYPE_BF16 ? launch_io<io_bf16>(a, p, s) : launch_io<io_f32>(a, p, s);

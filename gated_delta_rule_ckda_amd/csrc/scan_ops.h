@@ -272,10 +272,8 @@ struct ScanPlan {
 };
 ScanPlan scan_plan(const ScanArgs& a, bool grads);
 
-// The pieces' own sums and what enters each (launched where sequences are cut):
-// forwards, or backwards for the adjoint.
-launch_result launch_scan_pieces(const ScanArgs& a, const ScanPlan& p, int32_t io_dtype, bool rev, hipStream_t s);
-// The states entering every kMark tokens.
+// What the gradients need of the states: the marks and, where sequences are cut,
+// the state and the adjoint entering every piece.
 launch_result launch_scan_marks(const ScanArgs& a, const ScanPlan& p, int32_t io_dtype, hipStream_t s);
 
 }  // namespace ckda
