@@ -1079,7 +1079,7 @@ ckda_status_t validate_scan(const ckda_scan_desc_t* d, const int32_t* cu, ScanCa
   a->N = d->num_seqs;
   a->softplus = d->softplus;
   a->cu = cu;
-  if ((call == kScanStep ? ckda::scan_step_threads(*a) : ckda::scan_threads(*a, call == kScanBwd)) >= (int64_t(1) << 32))
+  if ((call == kScanStep ? ckda::scan_step_threads(*a) : ckda::scan_threads(*a)) >= (int64_t(1) << 32))
     return fail(CKDA_ERR_UNSUPPORTED, "too many tokens and channels for one launch");
   return ok();
 }

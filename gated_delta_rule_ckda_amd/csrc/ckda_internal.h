@@ -346,7 +346,7 @@ struct ScanArgs {
   float* partD;        // [slots][blocks][2][CH]
 };
 bool scan_supported(int32_t S);
-int64_t scan_threads(const ScanArgs& a, bool grads);
+int64_t scan_threads(const ScanArgs& a);
 int64_t scan_step_threads(const ScanArgs& a);
 size_t scan_fwd_workspace(const ScanArgs& a);
 size_t scan_bwd_workspace(const ScanArgs& a);
