@@ -100,7 +100,7 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < NR; ++i) e[j][i] = o.d[j] * A2[i];
+          for (int i = 0; i < NR; ++i) e[j][i] = decay_arg(o.d[j], A2[i]);
         // past the last tile this reads what an earlier one left
         const int to = (g + 1) % (TT / 4) * 4;
         fetch(ops[(g + 1) & 1], g + 1 < TT / 4 ? q : next, kRev ? TT - 4 - to : to);
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a) {
       float* at = (REV ? a.leave : a.entry) + own * SP * CH + k;
       const bool last = j == count - 1;  // its own sum enters no piece and was not formed
       const float sum = last ? 0.f : *at;
-      const float gain = last ? 0.f : __builtin_amdgcn_exp2f(a.span[own * CH + ch] * A2);
+      const float gain = last ? 0.f : decay_by(a.span[own * CH + ch], A2);
       *at = R;
       R = __builtin_fmaf(gain, R, sum);
     }
@@ -307,7 +307,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, int lpc, int
     const float u = d * x;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[i]), h[i], u * B[i]);
+      h[i] = __builtin_fmaf(decay_by(d, A2[i]), h[i], u * B[i]);
       y = __builtin_fmaf(Cv[i], h[i], y);
     }
     State::store(a.ht, at, VEC, h);

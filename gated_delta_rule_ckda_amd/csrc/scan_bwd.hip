@@ -142,7 +142,7 @@ __global__ __launch_bounds__(64 * C::W, 2) void scan_grads_kernel(ScanArgs a) {
     float h[TT + 1][NR], ex[TT][NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i)
-      h[0][i] = a.cut ? __builtin_fmaf(__builtin_amdgcn_exp2f(ns * A2[i]), ne[i], nh[i]) : nh[i];
+      h[0][i] = a.cut ? __builtin_fmaf(decay_by(ns, A2[i]), ne[i], nh[i]) : nh[i];
     __syncthreads();
     load(t0 - TT);
 #pragma unroll
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(64 * C::W, 2) void scan_grads_kernel(ScanArgs a) {
       lds_run<NR>(&sC[t][sl * NR], Cv);
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
-        ex[t][i] = __builtin_amdgcn_exp2f(dd * A2[i]);
+        ex[t][i] = decay_by(dd, A2[i]);
         h[t + 1][i] = __builtin_fmaf(ex[t][i], h[t][i], uu * B[i]);
         y = __builtin_fmaf(Cv[i], h[t + 1][i], y);
       }

@@ -25,6 +25,16 @@ struct ScanCfg {
   static constexpr int SP = NSL * NR;    // states, the last ones possibly padding
 };
 
+// The decay of a step d by A = A2 ln 2.  v_exp_f32 is low by 6.8e-9 of the value on
+// average for arguments next to 0, 3.5e-9 at -0.01 and 2e-9 to 4e-9 from there on
+// (measured over 2^20 arguments each; its rounding is 1.8e-8): nothing in one step,
+// but a product over a memory of a thousand tokens keeps every step's.  The sum
+// with kLift, in the product's own rounding, takes most of it back; an argument of
+// 0 still gives 1.
+constexpr float kLift = 8e-9f;
+__device__ __forceinline__ float decay_arg(float d, float A2) { return __builtin_fmaf(d, A2, kLift); }
+__device__ __forceinline__ float decay_by(float d, float A2) { return __builtin_amdgcn_exp2f(decay_arg(d, A2)); }
+
 // exp(-m) for m >= 0, the rounding of m log2(e) undone (it would cost m / 2 half
 // steps of the value); zeros from about 87 on.
 __device__ __forceinline__ float exp_minus(float m) {
