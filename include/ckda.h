@@ -565,14 +565,14 @@ ckda_status_t ckda_conv_step(const ckda_conv_desc_t* desc, const void* x, const 
  * channels and the groups' states being contiguous.  States, decays and sums are
  * kept in float32.  A is taken as written (negative for a decay) and must be
  * finite.  A step of exactly 0 (with softplus: a logit of -inf, the type's lowest
- * value and all below about -104) leaves the states as they are where the
+ * value and all below about -88) leaves the states as they are where the
  * token's x and B are finite.  A non-finite value in a token's x, dt, z, B or C
  * reaches outputs of its own sequence only.  Packed batches as above: cu_seqlens
  * clamped to [0, T] on the device, tokens past its end neither read nor written.
  * Supported: S from 1 to 64, groups dividing D, D up to 2^20, strides below 2^24,
  * B * T below 2^31 - 1024, T below 2^30; others return CKDA_ERR_UNSUPPORTED, as do batches
- * for which a launch would have 2^32 threads (256 for each sequence, 128 tokens
- * of it and 16 channels).  x, dt, z, B and C need only their elements'
+ * for which a launch would have 2^32 threads (768 for each sequence, 128 tokens
+ * of it and 32 channels).  x, dt, z, B and C need only their elements'
  * alignment; 16-byte accesses are used where the bases and strides of x, dt and
  * z, D and D / groups are multiples of 16 bytes.
  */

@@ -94,6 +94,14 @@ def test_long_tiles():
     check(make(500, 8, 600, 1028, 4, "bf16", states=False))
 
 
+def test_no_tokens():
+    x, h0 = torch.ones(2, 0, 8, device="cuda"), torch.randn(2, 3, 8, device="cuda")
+    w = torch.ones(8, 4, device="cuda")
+    y, ht = ck.conv_fwd(x, w, h0=h0)
+    dx, dw, db, dh0 = ck.conv_bwd(x, w, x, bias=w[:, 0].contiguous(), h0=h0, dht=2 * h0)
+    assert y.shape == (2, 0, 8) and torch.equal(ht, h0) and torch.equal(dh0, 2 * h0) and (dw == 0).all() and (db == 0).all()
+
+
 def test_no_sequences():
     x = torch.full((1, 6, 8), 3.0, device="cuda")
     w, b = torch.ones(8, 4, device="cuda"), torch.ones(8, device="cuda")

@@ -194,3 +194,40 @@ def test_prompt_then_steps_are_one_prompt():
     torch.cuda.synchronize()
     within("y", torch.cat(ys, 1), *want["y"], HALF["f32"])
     within("state", st, *want["ht"], HALF["f32"])
+
+
+def test_batches_of_no_tokens():
+    """T = 0: the states pass through, forwards and backwards; the sums are zeros."""
+    c = make_scan(990, 2, 1, 24, 16, 1, "bf16")
+    g = scan_tensors(c)
+    none = lambda m: g[m][:, :0]
+    kw = dict(scan_kw(c, g), z=none("z"))
+    y, ht = ck.scan_fwd(none("x"), none("dt"), g["A"], none("B"), none("C"), **kw)
+    r = dict(zip(GRADS, ck.scan_bwd(none("x"), none("dt"), g["A"], none("B"), none("C"), none("dy"), dht=g["dht"], **kw)))
+    torch.cuda.synchronize()
+    assert y.shape == (2, 0, 24) and torch.equal(ht, g["h0"]) and torch.equal(r["dh0"], g["dht"])
+    assert all((r[m] == 0).all() for m in ("dA", "dD", "dbias"))
+    e = ck.scan_step(none("x")[0], none("dt")[0], g["A"], none("B")[0], none("C")[0], g["h0"][:0])
+    assert e.shape == (0, 24)
+
+
+def test_long_rows_and_late_tokens():
+    """Tokens past 2^31 elements of a tensor: the last sequence of a batch whose rows
+    are far apart."""
+    c = make_scan(991, 1, 40, 24, 16, 1, "bf16")
+    g = scan_tensors(c)
+    kw = scan_kw(c, g)
+    y, ht = ck.scan_fwd(g["x"], g["dt"], g["A"], g["B"], g["C"], **kw)
+    stride, T = (1 << 20) + 8, 2240
+    wide = torch.zeros(T * stride, device="cuda", dtype=torch.bfloat16)
+    far = wide.as_strided((1, T, 24), (T * stride, stride, 1))
+    far[:, -40:] = g["x"]
+    assert (T - 40) * stride > 1 << 31
+    put = lambda t: torch.cat([torch.zeros(1, T - 40, *t.shape[2:], device="cuda", dtype=t.dtype), t], 1)
+    cu = torch.tensor([0, T - 40, T], dtype=torch.int32, device="cuda")
+    two = dict(D=g["D"], z=put(g["z"]), dt_bias=g["bias"], cu_seqlens=cu, h0=torch.cat([torch.zeros_like(g["h0"]), g["h0"]]))
+    y2, ht2 = ck.scan_fwd(far, put(g["dt"]), g["A"], put(g["B"]), put(g["C"]), **two)
+    cy, _ = ck.conv_fwd(g["x"], torch.ones(24, 4, device="cuda"))
+    cy2, _ = ck.conv_fwd(far, torch.ones(24, 4, device="cuda"), cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2[:, -40:]) and torch.equal(ht[0], ht2[1]) and torch.equal(cy, cy2[:, -40:])
