@@ -11,7 +11,10 @@
 // Bound by HBM: x is read and y written once.  A thread walks over a tile of
 // tokens for a vector of channels with the last K-1 rows in registers, so a row
 // is read again only at tile edges, and consecutive threads take consecutive
-// channels, so a wave reads whole lines.
+// channels, so a wave reads whole lines.  Four channels a thread: eight leave two
+// waves a SIMD (forward 60 us instead of 54), two read half as much at a time
+// (gradients 133 us instead of 96).  8 x 4096 tokens of 2048 channels in bf16, 4
+// taps: 54 us (4.9 TB/s), gradients 96 us (4.2).
 #include "row_ops.h"
 #include "spans.h"
 
@@ -250,8 +253,10 @@ __global__ __launch_bounds__(1024) void conv_cols_kernel(const float* part, int 
   const int l = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int64_t cols = static_cast<int64_t>(K + 1) * D, i = static_cast<int64_t>(blockIdx.x) * 32 + l;
   float v = 0.f;
-  if (i < cols)
+  if (i < cols) {
+#pragma unroll 8
     for (int p = grp; p < parts; p += 32) v += part[p * cols + i];
+  }
   red[grp][l] = v;
   __syncthreads();
   if (grp == 0 && i < cols) {

@@ -16,7 +16,7 @@
 // with the row ahead that is faster in bf16 than wide accesses at odd addresses
 // (32768 rows of 2001 with a residual: 119 us against 148; 1001 float32: 105 and
 // 101).  Measured in bf16: 32768 rows of 2048 with a residual 99 us (5.4 TB/s),
-// their gradients 115 us (4.7), 524288 rows of 128 60 us (4.5).
+// their gradients 110 us (4.9), 524288 rows of 128 60 us (4.5).
 #include "row_ops.h"
 
 namespace ckda {
@@ -251,8 +251,10 @@ __global__ __launch_bounds__(1024) void layer_norm_cols_kernel(const float* part
   float* out = q == 0 ? dw : db;
   if (!out) return;
   float v = 0.f;
-  if (c < d)
+  if (c < d) {
+#pragma unroll 8
     for (int p = grp; p < parts; p += 32) v += part[(static_cast<int64_t>(p) * 2 + q) * d + c];
+  }
   red[grp][l] = v;
   __syncthreads();
   if (grp == 0 && c < d) {
