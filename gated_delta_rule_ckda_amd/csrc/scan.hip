@@ -79,7 +79,7 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
     for (int i = 0; i < NR; ++i) {
       const int n = sl * NR + i;
       const bool ok = mine && n < a.S;
-      A2[i] = ok ? a.A[chan * a.S + n] * kLog2e : 0.f;
+      A2[i] = ok ? log2_rate(a.A[chan * a.S + n]) : 0.f;
       h[i] = 0.f;
       if (!kSum && !(WALK == kMarks && a.cut)) {
         if (a.cut)
@@ -278,7 +278,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a) {
     const int st = k / CH, ch = k % CH;
     const bool ok = c0 + ch < per && st < a.S;
     const int64_t chan = static_cast<int64_t>(g) * per + c0 + ch;
-    const float A2 = ok ? a.A[chan * a.S + st] * kLog2e : 0.f;
+    const float A2 = ok ? log2_rate(a.A[chan * a.S + st]) : 0.f;
     float R = ok && from ? from[(static_cast<int64_t>(n) * a.D + chan) * a.S + st] : 0.f;
     for (int j = 0; j < count; ++j) {
       const int64_t own = static_cast<int64_t>(first + (REV ? count - 1 - j : j)) * blocks + blk;
@@ -316,7 +316,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, int lpc, int
     Token::row(a.Bm, n * a.sb + group, VEC, B);
     Token::row(a.Cm, n * a.sc + group, VEC, Cv);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) A2[i] = a.A[static_cast<int64_t>(c) * a.S + s + i] * kLog2e;
+    for (int i = 0; i < VEC; ++i) A2[i] = log2_rate(a.A[static_cast<int64_t>(c) * a.S + s + i]);
     if (a.softplus) d = softplus_of(d);
     const float u = d * x;
 #pragma unroll

@@ -44,7 +44,7 @@ __global__ __launch_bounds__(64 * C::W, 2) void scan_grads_kernel(ScanArgs a) {
   for (int i = 0; i < NR; ++i) {
     const int n = sl * NR + i;
     const bool ok = mine && n < a.S;
-    A2[i] = ok ? a.A[chan * a.S + n] * kLog2e : 0.f;
+    A2[i] = ok ? log2_rate(a.A[chan * a.S + n]) : 0.f;
     dA[i] = c[i] = 0.f;
     if (p.n >= 0) {
       if (a.cut)

@@ -25,6 +25,13 @@ struct ScanCfg {
   static constexpr int SP = NSL * NR;    // states, the last ones possibly padding
 };
 
+// A / ln 2, kept finite for the largest A: an infinite one would make no number of a
+// step of 0, of the rows that fill a tile's end, and of its product with a decay of 0.
+__device__ __forceinline__ float log2_rate(float A) {
+  const float r = A * kLog2e, most = 3.4028234663852886e38f;
+  return r < -most ? -most : (r > most ? most : r);
+}
+
 // The decay of a step d by A = A2 ln 2.  v_exp_f32 is low by 6.8e-9 of the value on
 // average for arguments next to 0, 3.5e-9 at -0.01 and 2e-9 to 4e-9 from there on
 // (measured over 2^20 arguments each; its rounding is 1.8e-8): nothing in one step,

@@ -231,3 +231,25 @@ def test_long_rows_and_late_tokens():
     cy2, _ = ck.conv_fwd(far, torch.ones(24, 4, device="cuda"), cu_seqlens=cu)
     torch.cuda.synchronize()
     assert torch.equal(y, y2[:, -40:]) and torch.equal(ht[0], ht2[1]) and torch.equal(cy, cy2[:, -40:])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,steps", [(1, "values"), (37, "values"), (37, "logits"), (300, "values")])
+def test_decay_rates_of_the_lowest_value(dtype, T, steps):
+    """A of float32's lowest value forgets the state at once, whatever the step; a step
+    of exactly 0 keeps it all the same."""
+    c = make_scan(995 + T, 1, T, 24, 16, 1, dtype, steps=steps)
+    low = np.finfo(np.float32).min
+    c["A"][::3], c["A"][1::3, 5] = low, low
+    check(c, cut=128 if T > 256 else 0)
+    if steps == "values":
+        c["dt"][:, T // 2:T // 2 + 3] = 0
+        check(c, grads=False, cut=128 if T > 256 else 0)  # dL/dstep of such a step is A itself
+    if T == 1:
+        g, want = scan_tensors(c), scan_reference(c, False)
+        state = g["h0"].clone()
+        y = ck.scan_step(g["x"][:, 0], g["dt"][:, 0], g["A"], g["B"][:, 0], g["C"][:, 0], state, D=g["D"], z=g["z"][:, 0],
+                         steps=steps)
+        torch.cuda.synchronize()
+        within("y", y[:, None], *want["y"], HALF[dtype])
+        within("state", state, *want["ht"], HALF["f32"])
