@@ -11,10 +11,10 @@
 // Bound by HBM: x is read and y written once.  A thread walks over a tile of
 // tokens for a vector of channels with the last K-1 rows in registers, so a row
 // is read again only at tile edges, and consecutive threads take consecutive
-// channels, so a wave reads whole lines.  Four channels a thread: eight leave two
-// waves a SIMD (forward 60 us instead of 54), two read half as much at a time
-// (gradients 133 us instead of 96).  8 x 4096 tokens of 2048 channels in bf16, 4
-// taps: 54 us (4.9 TB/s), gradients 96 us (4.2).
+// channels, so a wave reads whole lines.  Four channels a thread: with two
+// and with eight the forward took 56 and 60 us instead of 55, the gradients 133 and
+// 105 instead of 98.  8 x 4096 tokens of 2048 channels in bf16, 4 taps: 54 us (4.9
+// TB/s), gradients 96 us (4.2).
 #include "row_ops.h"
 #include "spans.h"
 

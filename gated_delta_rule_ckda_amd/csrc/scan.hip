@@ -6,7 +6,7 @@
 // costs 8.4 cycles a wave, the others 2.5 to 2.9 where two waves or more take turns
 // and about 4 where powers come between them, which is why they run in groups.  B
 // and C, the same for all channels, reach the lanes as broadcast reads, so a lane
-// holds as many states as there are waves to spare.  8 x 4096 tokens of 2048
+// holds several states.  8 x 4096 tokens of 2048
 // channels and 16 states in bf16: 365 us (1.5 TB/s; the bytes alone would take 106,
 // the instructions alone 131).
 #include "scan_ops.h"
@@ -376,26 +376,39 @@ bool scan_supported(int32_t S) { return S >= 1 && S <= 64; }
 ScanPlan scan_plan(const ScanArgs& a, bool grads) {
   ScanPlan p;
   const int per = a.D / a.G;
-  // Workgroups of 64 channels for whole sequences; a GPU holds two a CU
-  const int64_t whole = static_cast<int64_t>(a.N) * a.G * ((per + 63) / 64);
+  // Workgroups for whole sequences, of 64 channels or, past 16 states, of 32; a GPU
+  // holds two a CU (of 32 channels and 16 states three), 512 at a time.
+  const int wide = a.S <= 16 ? 64 : 32;
+  const int64_t whole = static_cast<int64_t>(a.N) * a.G * ((per + wide - 1) / wide);
   const int64_t want = a.cu || grads ? 1024 : 512;
-  // Sequences are cut where they leave CUs idle, and in packed batches, whose
-  // lengths are not known here.
-  const bool few = a.T > 256 && (a.cu || whole < (grads ? 512 : 192));
+  // Sequences are cut where whole ones leave CUs idle, and in packed batches, whose
+  // lengths are not known here.  Measured in us on sequences of 2048 tokens, cut and
+  // whole, 16 states: forward of 128 workgroups 134 and 149, of 160 209 and 182; gradients
+  // of 256 669 and 745, of 320 885 and 1110, of 384 1130 and 1119, of 480 1341 and
+  // 1132.  32 states: forward of 64 76 and 185, of 192 197 and 190; gradients of 256
+  // 651 and 826, of 512 1221 and 1112.
+  const bool few = a.T > 256 && (a.cu || whole <= (grads ? 341 : 128));
+  // 8 to 16 states of whole sequences: 32 channels a workgroup use more CUs (forward
+  // of 256 workgroups of 64: 186 us, 203 with 64; of 384 245 and 276), up to where
+  // they no longer fit in one round (of 416 368 and 276; gradients of 256 745 and
+  // 869, of 384 1160 and 1119).
   if (a.S <= 8)
     p.which = 0;
   else if (a.S <= 16)
-    p.which = !few && whole < 512 ? 2 : 1;
+    p.which = !few && whole <= (grads ? 341 : 384) ? 2 : 1;
   else
     p.which = a.S <= 32 ? 3 : 4;
   p.CH = p.which <= 1 ? 64 : 32;
   p.SP = p.which == 0 ? 8 : (p.which <= 2 ? 16 : (p.which == 3 ? 32 : 64));
   p.blocks = scan_blocks(a.D, a.G, p.CH);
-  const int64_t tokens = static_cast<int64_t>(a.B) * a.T;
   p.seg = scan_whole(a.T);
   p.cut = 0;
   if (a.N > 0 && few) {
-    int64_t L = tokens * p.blocks / want;
+    // no more than `want` workgroups, in pieces of one length: a last round of a
+    // few, or a short last piece, would leave the rest waiting (forward of 96
+    // workgroups whole: 112 us in 5 pieces, 136 in 6; gradients of 160: 487 and 506)
+    const int64_t own = static_cast<int64_t>(a.N) * p.blocks, pieces = want > own ? want / own : 1;
+    int64_t L = a.cu ? static_cast<int64_t>(a.T) * p.blocks / want : (a.T + pieces - 1) / pieces;
     L = L < 128 ? 128 : (L + 31) / 32 * 32;
     if (L < a.T) {
       p.seg = static_cast<int>(L);

@@ -12,9 +12,9 @@
 // registers and then back.  In a cut sequence the pieces' first walks start from
 // zero, and what enters a piece is added to its marks, decayed over the steps
 // since, as they are read: so the states are walked once.  Bound by vector
-// instructions, 16 a token, channel and state, 4 of them for the sums over channels.
-// 8 x 4096 tokens of 2048 channels and 16 states in bf16: 1296 us, of which this
-// kernel 860, the walks of states and adjoints 215 and 160, dB and dC 37.
+// instructions, 22 a token, channel and state here, 4 of them for the sums over
+// channels.  8 x 4096 tokens of 2048 channels and 16 states in bf16: 1296 us, of
+// which this kernel 870, the walks of states and adjoints 216 and 160, dB and dC 37.
 #include "scan_ops.h"
 
 namespace ckda {

@@ -253,3 +253,8 @@ def test_decay_rates_of_the_lowest_value(dtype, T, steps):
         torch.cuda.synchronize()
         within("y", y[:, None], *want["y"], HALF[dtype])
         within("state", state, *want["ht"], HALF["f32"])
+
+
+def test_pieces_longer_than_the_shortest():
+    """Sequences in a few pieces each, the last one ending inside a tile."""
+    check(make_scan(998, 4, 530, 1984, 9, 1, "bf16"), grads=False, cut=160)
