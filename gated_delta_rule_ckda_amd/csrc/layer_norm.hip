@@ -3,9 +3,12 @@
 //   h = r + x                         (x itself without r)
 //   n = (h - mean h) rstd w + b       rstd = 1 / sqrt(mean (h - mean h)^2 + eps)
 //
-// n is formed from h before its rounding; the variance is that of the centred
-// row, so a mean far above the spread costs no digits.  Backwards, with
-// c = (h - mean h) rstd and m = dn w,
+// n is formed from h before its rounding.  The row is centred twice: a mean far
+// above the spread is off by several 2^-24 of itself, which the centred row would keep
+// as a shift (a row of 77777.7 gave n = 0.9).  What the centred row's own mean is,
+// summed beside its squares, is taken out of both, so such a mean costs no
+// digits, and no further round of sums (gradients of 32768 rows of 2048: 110 us
+// before, 112 now).  Backwards, with c = (h - mean h) rstd and m = dn w,
 //
 //   dw = sum_rows dn c,  db = sum_rows dn
 //   dx = dh + rstd (m - mean m - c mean(m c))
@@ -16,11 +19,18 @@
 // with the row ahead that is faster in bf16 than wide accesses at odd addresses
 // (32768 rows of 2001 with a residual: 119 us against 148; 1001 float32: 105 and
 // 101).  Measured in bf16: 32768 rows of 2048 with a residual 99 us (5.4 TB/s),
-// their gradients 110 us (4.9), 524288 rows of 128 60 us (4.5).
+// their gradients 112 us (4.8), 524288 rows of 128 60 us (4.5).
 #include "row_ops.h"
 
 namespace ckda {
 namespace {
+
+// The mean square about the mean, from a mean square and what is left of the mean:
+// a row of one value may leave less than nothing.  NaN stays.
+__device__ __forceinline__ float centred_square(float square, float left) {
+  const float v = __builtin_fmaf(-left, left, square);
+  return v < 0.f ? 0.f : v;
+}
 
 template <class IO, bool ALIGNED, int EPL, int NT>
 __global__ __launch_bounds__(NT) void layer_norm_kernel(LayerNormArgs a, int tpr) {
@@ -74,23 +84,23 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(LayerNormArgs a, int tpr
       vr[k] = nr[k];
     }
     if (kAhead) load(r0 + step);  // a row ahead, while this one's sums go around
-    float h[EPL], s[1] = {0.f};
+    float h[EPL], s1[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const int j = k * VEC + e;
         h[j] = X::get(vx[k], e) + (a.r ? X::get(vr[k], e) : 0.f);
-        s[0] += h[j];
+        s1[0] += h[j];
       }
     if (a.h && live) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
         if (ok[k]) X::store(a.h, row * a.d + (lane + tpr * k) * VEC, a.d - (lane + tpr * k) * VEC, h + k * VEC);
     }
-    row_sum<1, NT>(s, tpr, red, half);
-    const float mean = s[0] * inv_d;
-    s[0] = 0.f;
+    row_sum<1, NT>(s1, tpr, red, half);
+    const float mean = s1[0] * inv_d;
+    float s[2] = {0.f, 0.f};  // of (h - mean)^2 and h - mean
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -98,11 +108,13 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(LayerNormArgs a, int tpr
         const int j = k * VEC + e;
         h[j] = in(k, e) ? h[j] - mean : 0.f;
         s[0] += h[j] * h[j];
+        s[1] += h[j];
       }
-    row_sum<1, NT>(s, tpr, red, half);
-    const float rstd = 1.f / sqrtf(s[0] * inv_d + a.eps);
+    row_sum<2, NT>(s, tpr, red, half);
+    const float left = s[1] * inv_d;
+    const float rstd = 1.f / sqrtf(centred_square(s[0] * inv_d, left) + a.eps);
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) h[j] = h[j] * rstd * w[j] + b[j];
+    for (int j = 0; j < EPL; ++j) h[j] = __builtin_fmaf(h[j], rstd, -left * rstd) * w[j] + b[j];
     if (live) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
@@ -118,7 +130,7 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(LayerNormArgs a, Lay
   constexpr int VEC = ALIGNED ? 16 / sizeof(typename IO::storage) : 1, K = EPL / VEC;
   constexpr bool kAhead = NT == 256;  // more threads leave no registers for it
   using X = Chans<IO, VEC, ALIGNED>;
-  __shared__ float red[2 * 3 * (NT / 64)];
+  __shared__ float red[2 * 4 * (NT / 64)];
   extern __shared__ float cols[];  // [rows a step][d] for rows of less than a workgroup
   int half = 0;
   const int t = threadIdx.x, lane = t & (tpr - 1);
@@ -175,9 +187,9 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(LayerNormArgs a, Lay
         h[k * VEC + e] = X::get(vx[k], e);
         s1[0] += h[k * VEC + e];
       }
-    row_sum<1, NT, 3>(s1, tpr, red, half);
+    row_sum<1, NT, 4>(s1, tpr, red, half);
     const float mean = s1[0] * inv_d;
-    float s[3] = {0.f, 0.f, 0.f};  // of (h - mean)^2, m, m (h - mean)
+    float s[4] = {0.f, 0.f, 0.f, 0.f};  // of (h - mean)^2, m, m (h - mean), h - mean
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -188,18 +200,20 @@ __global__ __launch_bounds__(NT) void layer_norm_bwd_kernel(LayerNormArgs a, Lay
         s[0] += h[j] * h[j];
         s[1] += m;
         s[2] += m * h[j];
+        s[3] += h[j];
       }
-    row_sum<3, NT, 3>(s, tpr, red, half);
+    row_sum<4, NT, 4>(s, tpr, red, half);
+    const float left = s[3] * inv_d, mm = s[1] * inv_d;
     // with eps = 0 a thread without a row would add inf * 0 to its sums over rows
-    const float rstd = live ? 1.f / sqrtf(s[0] * inv_d + a.eps) : 0.f;
-    const float mm = s[1] * inv_d, mc = s[2] * inv_d * rstd;
+    const float rstd = live ? 1.f / sqrtf(centred_square(s[0] * inv_d, left) + a.eps) : 0.f;
+    const float mc = (s[2] * inv_d - left * mm) * rstd;
     float dx[EPL];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const int j = k * VEC + e;
-        const float c = h[j] * rstd, dn = X::get(vn[k], e);
+        const float c = __builtin_fmaf(h[j], rstd, -left * rstd), dn = X::get(vn[k], e);
         dw[j] += dn * c;
         db[j] += dn;
         dx[j] = rstd * (dn * w[j] - mm - c * mc);

@@ -159,6 +159,10 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float* red, int&
   const int first = wave & ~(waves - 1);
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.f;
+  // two waves' at a time: the compiler's eight hold 8 N registers at the kernels' tightest
+  // place (gradients of 4096 rows of 16384 in bf16: block norm 5956 us against 1128 so;
+  // layer norm, with a sum more, 421 against 366 at 16383 elements)
+#pragma unroll 2
   for (int j = 0; j < waves; ++j)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += r[MOST * (first + j) + i];
