@@ -265,30 +265,51 @@ __global__ __launch_bounds__(64 * (C::W + 4), 4) void scan_walk_kernel(ScanArgs 
 }
 
 // entry[s], the pieces' own sums, become what enters them: R <- exp(A span_s) R + sum_s
-// along a sequence's pieces (backwards: against them), from h0 (dht).
+// along a sequence's pieces (backwards: against them), from h0 (dht).  A thread takes
+// N states of one channel, whose loads share the wait, and asks for the next piece's
+// before it stores this one's.
 template <class C, bool REV>
 __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a) {
-  constexpr int CH = C::CH, SP = C::SP;
+  constexpr int CH = C::CH, SP = C::SP, N = SP * CH / 256;
+  static_assert(256 % CH == 0 && SP * CH % 256 == 0, "a thread's states are of one channel");
   const int blocks = scan_blocks(a.D, a.G, CH), per = a.D / a.G, nb = (per + CH - 1) / CH;
   const int n = blockIdx.x / blocks, blk = blockIdx.x - n * blocks, g = blk / nb, c0 = (blk - g * nb) * CH;
   const Seq q = sequence(a, n);
   const int first = first_slot(a, n, a.seg), count = q.len > 0 ? (q.len + a.seg - 1) / a.seg : 1;
   const float* from = REV ? a.dht : a.h0;
-  for (int k = threadIdx.x; k < SP * CH; k += 256) {
-    const int st = k / CH, ch = k % CH;
+  float* const to = REV ? a.leave : a.entry;
+  const int ch = threadIdx.x % CH;
+  const int64_t chan = static_cast<int64_t>(g) * per + c0 + ch;
+  float A2[N], R[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int st = (threadIdx.x + 256 * i) / CH;
     const bool ok = c0 + ch < per && st < a.S;
-    const int64_t chan = static_cast<int64_t>(g) * per + c0 + ch;
-    const float A2 = ok ? log2_rate(a.A[chan * a.S + st]) : 0.f;
-    float R = ok && from ? from[(static_cast<int64_t>(n) * a.D + chan) * a.S + st] : 0.f;
-    for (int j = 0; j < count; ++j) {
-      const int64_t own = static_cast<int64_t>(first + (REV ? count - 1 - j : j)) * blocks + blk;
-      float* at = (REV ? a.leave : a.entry) + own * SP * CH + k;
-      const bool last = j == count - 1;  // its own sum enters no piece and was not formed
-      const float sum = last ? 0.f : *at;
-      const float gain = last ? 0.f : decay_by(a.span[own * CH + ch], A2);
-      *at = R;
-      R = __builtin_fmaf(gain, R, sum);
-    }
+    A2[i] = ok ? log2_rate(a.A[chan * a.S + st]) : 0.f;
+    R[i] = ok && from ? from[(static_cast<int64_t>(n) * a.D + chan) * a.S + st] : 0.f;
+  }
+  // the last one's own sum enters no piece and was not formed
+  const auto slot = [&](int j) { return static_cast<int64_t>(first + (REV ? count - 1 - j : j)) * blocks + blk; };
+  float sum[N], span = 0.f;
+  const auto load = [&](int j) {
+    const bool some = j < count - 1;
+    const int64_t own = slot(some ? j : 0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum[i] = some ? to[own * SP * CH + threadIdx.x + 256 * i] : 0.f;
+    span = some ? a.span[own * CH + ch] : 0.f;
+  };
+  load(0);
+  for (int j = 0; j < count; ++j) {
+    float own[N], h[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) own[i] = sum[i];
+    const float d = span;
+    load(j + 1);
+#pragma unroll
+    for (int i = 0; i < N; ++i) to[slot(j) * SP * CH + threadIdx.x + 256 * i] = R[i];
+    enter(d, A2, R, own, h);
+#pragma unroll
+    for (int i = 0; i < N; ++i) R[i] = h[i];
   }
 }
 

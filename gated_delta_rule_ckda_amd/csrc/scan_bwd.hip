@@ -144,8 +144,8 @@ __global__ __launch_bounds__(64 * C::W, 2) void scan_grads_kernel(ScanArgs a) {
     }
     float h[TT + 1][NR], ex[TT][NR];
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
-      h[0][i] = a.cut ? __builtin_fmaf(decay_by(ns, A2[i]), ne[i], nh[i]) : nh[i];
+    for (int i = 0; i < NR; ++i) h[0][i] = nh[i];
+    if (a.cut) enter(ns, A2, ne, nh, h[0]);
     __syncthreads();
     load(t0 - TT);
 #pragma unroll

@@ -42,6 +42,37 @@ constexpr float kLift = 8e-9f;
 __device__ __forceinline__ float decay_arg(float d, float A2) { return __builtin_fmaf(d, A2, kLift); }
 __device__ __forceinline__ float decay_by(float d, float A2) { return __builtin_amdgcn_exp2f(decay_arg(d, A2)); }
 
+// h = own + R exp(span A): the states R that enter a part of a sequence added to the
+// part's own, whose steps sum to `span`.  For rates that grow the power may leave
+// float32 where its product with R does not: past 2^126 the exponent's whole part
+// goes to the product instead, and an R of 0 stays 0 (all lanes then take that
+// path, as few as need it; without a branch gradients of a layer took 1326 us, not
+// 1297).  Decays take the one power.  Steps of the largest finite size may sum to
+// infinity, of which a rate of 0 would make no number.
+template <int N>
+__device__ __forceinline__ void enter(float span, const float (&A2)[N], const float (&R)[N], const float (&own)[N],
+                                      float (&h)[N]) {
+  constexpr float kMost = 3.4028234663852886e38f;
+  span = __builtin_amdgcn_fmed3f(span, -kMost, kMost);
+  float x[N], top = -kMost;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = decay_arg(span, A2[i]);
+    top = fmaxf(top, x[i]);
+  }
+  if (__any(top > 126.f)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      // more than 2^277 takes the least float32 past the largest
+      const float y = __builtin_amdgcn_fmed3f(x[i], -300.f, 300.f), k = rintf(y);
+      h[i] = own[i] + __builtin_amdgcn_ldexpf(R[i] * __builtin_amdgcn_exp2f(y - k), static_cast<int>(k));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(x[i]), R[i], own[i]);
+  }
+}
+
 // exp(-m) for m >= 0, the rounding of m log2(e) undone (it would cost m / 2 half
 // steps of the value); zeros from about 87 on.
 __device__ __forceinline__ float exp_minus(float m) {

@@ -564,7 +564,8 @@ ckda_status_t ckda_conv_step(const ckda_conv_desc_t* desc, const void* x, const 
  * (a projection's output): the strides are the elements between tokens, the
  * channels and the groups' states being contiguous.  States, decays and sums are
  * kept in float32.  A is taken as written (negative for a decay) and must be
- * finite.  A step of exactly 0 (with softplus: a logit of -inf, the type's lowest
+ * finite; a rate that grows (d_t A > 0) is one as well, while exp(d_t A) and what
+ * the recurrence forms of it stay in float32.  A step of exactly 0 (with softplus: a logit of -inf, the type's lowest
  * value and all below about -88) leaves the states as they are where the
  * token's x and B are finite.  A non-finite value in a token's x, dt, z, B or C
  * reaches outputs of its own sequence only.  Packed batches as above: cu_seqlens
