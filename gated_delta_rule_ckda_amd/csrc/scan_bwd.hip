@@ -211,7 +211,8 @@ __global__ __launch_bounds__(64 * C::W, 2) void scan_grads_kernel(ScanArgs a) {
 #pragma unroll
       for (int e = 0; e < EP; ++e) {
         dx[e] = __builtin_fmaf(d[e], gb[e], Dv[e] * g[e]);
-        dt[e] = __builtin_fmaf(x[e], gb[e], wa[e] * kLn2) * slope[e];
+        // a slope of 0 is a masked token's, whose w . A may have left float32
+        dt[e] = slope[e] == 0.f ? 0.f : __builtin_fmaf(x[e], gb[e], wa[e] * kLn2) * slope[e];
         dz[e] *= y[e];
         dD[e] = __builtin_fmaf(g[e], x[e], dD[e]);
         db[e] += dt[e];

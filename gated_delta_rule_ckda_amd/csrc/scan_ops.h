@@ -25,8 +25,9 @@ struct ScanCfg {
   static constexpr int SP = NSL * NR;    // states, the last ones possibly padding
 };
 
-// A / ln 2, kept finite for the largest A: an infinite one would make no number of a
-// step of 0, of the rows that fill a tile's end, and of its product with a decay of 0.
+// A / ln 2, kept finite for the largest A (past 2.358e38 rates count as that one): an
+// infinite one would make no number of a step of 0, of the rows that fill a tile's
+// end, and of its product with a decay of 0.
 __device__ __forceinline__ float log2_rate(float A) {
   const float r = A * kLog2e, most = 3.4028234663852886e38f;
   return r < -most ? -most : (r > most ? most : r);

@@ -565,7 +565,8 @@ ckda_status_t ckda_conv_step(const ckda_conv_desc_t* desc, const void* x, const 
  * channels and the groups' states being contiguous.  States, decays and sums are
  * kept in float32.  A is taken as written (negative for a decay) and must be
  * finite; a rate that grows (d_t A > 0) is one as well, while exp(d_t A) and what
- * the recurrence forms of it stay in float32.  A step of exactly 0 (with softplus: a logit of -inf, the type's lowest
+ * the recurrence forms of it stay in float32.  Rates past 2.358e38 (float32's largest
+ * over log2 e) count as that one, which forgets a state at once.  A step of exactly 0 (with softplus: a logit of -inf, the type's lowest
  * value and all below about -88) leaves the states as they are where the
  * token's x and B are finite.  A non-finite value in a token's x, dt, z, B or C
  * reaches outputs of its own sequence only.  Packed batches as above: cu_seqlens
@@ -607,9 +608,11 @@ ckda_status_t ckda_scan_fwd(const ckda_scan_desc_t* desc, const void* x, const v
  * Its gradients, given dy = dL/dy (io dtype, contiguous) and dht = dL/dht
  * (float32, NULL for zero): dx, ddt, dz [B][T][D] and dB, dC [B][T][groups][S]
  * in the io dtype, contiguous; dA [D][S], dD, ddt_bias [D] and dh0 in float32.
- * ddt is the gradient of what dt holds.  dz, dD and ddt_bias are given exactly
- * where z, D and dt_bias are; dh0 may be NULL (not wanted).  The states are
- * formed again from the inputs.  Every sum runs in a fixed order.
+ * ddt is the gradient of what dt holds, a sum of products with A (infinite or no
+ * number where one of them leaves float32), and 0 for a logit whose softplus has no
+ * slope.  dz, dD and ddt_bias are given exactly where z, D and dt_bias are; dh0 may
+ * be NULL (not wanted).  The states are formed again from the inputs.  Every sum
+ * runs in a fixed order.
  */
 size_t ckda_scan_bwd_workspace_size(const ckda_scan_desc_t* desc, int32_t packed);
 ckda_status_t ckda_scan_bwd(const ckda_scan_desc_t* desc, const void* x, const void* dt,
