@@ -267,33 +267,46 @@ __global__ __launch_bounds__(256) void scan_bc_kernel(ScanArgs a) {
 }
 
 // dA (what = 0) and dD, dbias (what = 1): the pieces' sums, 32 columns a
-// workgroup, its 32 groups of lanes taking every 32nd piece's; their sums are
-// added in order.
+// workgroup at a time, its 32 groups of lanes taking every 32nd piece's; their sums
+// are added in order.
 template <class C>
 __global__ __launch_bounds__(1024) void scan_cols_kernel(ScanArgs a, int what) {
   constexpr int CH = C::CH, SP = C::SP;
   __shared__ float red[32][33];
   const int per = a.D / a.G, nb = (per + CH - 1) / CH, blocks = a.G * nb;
   const int l = threadIdx.x & 31, grp = threadIdx.x >> 5, rows = what ? 2 : SP;
-  const int64_t cols = static_cast<int64_t>(blocks) * rows * CH, i = static_cast<int64_t>(blockIdx.x) * 32 + l;
+  const int64_t cols = static_cast<int64_t>(blocks) * rows * CH;
   const float* part = what ? a.partD : a.partA;
-  float v = 0.f;
-  if (i < cols)
-    for (int s = grp; s < a.slots; s += 32) v += part[s * cols + i];
-  red[grp][l] = v;
-  __syncthreads();
-  if (grp != 0 || i >= cols) return;
-  for (int r = 1; r < 32; ++r) v += red[r][l];
-  const int blk = static_cast<int>(i / (rows * CH)), k = static_cast<int>(i - static_cast<int64_t>(blk) * rows * CH);
-  const int n = k / CH, g = blk / nb, c = (blk - g * nb) * CH + k % CH;
-  if (c >= per) return;
-  const int64_t chan = static_cast<int64_t>(g) * per + c;
-  if (what == 0) {
-    if (n < a.S) a.dA[chan * a.S + n] = v;
-  } else {
-    float* out = n == 0 ? a.dD : a.dbias;
-    if (out) out[chan] = v;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * 32; first < cols; first += static_cast<int64_t>(gridDim.x) * 32) {
+    const int64_t i = first + l;
+    float v = 0.f;
+    if (i < cols)
+      for (int s = grp; s < a.slots; s += 32) v += part[s * cols + i];
+    red[grp][l] = v;
+    __syncthreads();
+    if (grp == 0 && i < cols) {
+      for (int r = 1; r < 32; ++r) v += red[r][l];
+      const int blk = static_cast<int>(i / (rows * CH)), k = static_cast<int>(i - static_cast<int64_t>(blk) * rows * CH);
+      const int n = k / CH, g = blk / nb, c = (blk - g * nb) * CH + k % CH;
+      const int64_t chan = static_cast<int64_t>(g) * per + c;
+      if (c < per) {
+        if (what == 0) {
+          if (n < a.S) a.dA[chan * a.S + n] = v;
+        } else {
+          float* out = n == 0 ? a.dD : a.dbias;
+          if (out) out[chan] = v;
+        }
+      }
+    }
+    __syncthreads();
   }
+}
+
+// Workgroups for the sums of `rows` values a channel: a launch counts its threads in 32
+// bits, which groups of a channel each, at 64 columns a group, would pass.
+dim3 cols_grid(int64_t cols, int rows) {
+  const int64_t n = (cols * rows + 31) / 32;
+  return dim3(static_cast<unsigned>(n < (1 << 20) ? n : 1 << 20));
 }
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -339,10 +352,10 @@ launch_result launch_io(const ScanArgs& a, const ScanPlan& p, hipStream_t s) {
       if (e != hipSuccess) return e;
     }
     const int64_t cols = static_cast<int64_t>(p.blocks) * C::CH;
-    hipLaunchKernelGGL((scan_cols_kernel<C>), dim3(static_cast<unsigned>((cols * C::SP + 31) / 32)), dim3(1024), 0, s, a, 0);
+    hipLaunchKernelGGL((scan_cols_kernel<C>), cols_grid(cols, C::SP), dim3(1024), 0, s, a, 0);
     const launch_result e = hipGetLastError();
     if (e != hipSuccess || (!a.dD && !a.dbias)) return e;
-    hipLaunchKernelGGL((scan_cols_kernel<C>), dim3(static_cast<unsigned>((cols * 2 + 31) / 32)), dim3(1024), 0, s, a, 1);
+    hipLaunchKernelGGL((scan_cols_kernel<C>), cols_grid(cols, 2), dim3(1024), 0, s, a, 1);
     return hipGetLastError();
   });
 }
