@@ -1109,11 +1109,13 @@ ScanSizes scan_sizes(const ckda_scan_desc_t* d) {
   return z;
 }
 
-// Whether rows can move in 16-byte accesses: every base and stride a multiple,
-// and every group's channels whole vectors.
+// Whether a thread's channels can move at once: every base and stride a multiple of
+// their size, and every group's channels whole vectors.
 bool scan_vec(const ckda::ScanArgs& a, int64_t es) {
-  const int64_t n = 8;  // a thread's channels at most, in either type
-  const auto fits = [&](const void* p, int64_t stride) { return aligned16(p) && stride * es % 16 == 0; };
+  const int64_t n = 4;  // a thread's channels at most, in either type
+  const auto fits = [&](const void* p, int64_t stride) {
+    return reinterpret_cast<uintptr_t>(p) % (n * es) == 0 && stride % n == 0;
+  };
   return (a.D / a.G) % n == 0 && fits(a.x, a.sx) && fits(a.dt, a.sdt) && (!a.z || fits(a.z, a.sz));
 }
 

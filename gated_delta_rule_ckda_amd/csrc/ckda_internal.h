@@ -305,7 +305,9 @@ launch_result launch_conv_step(const ConvArgs& a, int32_t io_dtype, hipStream_t 
 struct ScanArgs {
   int32_t B, T, D, S, G, N;
   int32_t softplus;    // 1: steps are softplus(dt + bias), 0: dt + bias
-  int32_t vec;         // 1: the rows of x, dt, z, y and their gradients move in 16-byte accesses
+  int32_t vec;         // 1: a thread's channels (4 at most) of x, dt, z, y and their gradients move at once
+  int32_t seg, slots;  // tokens of a piece, pieces
+  int32_t cut;         // 1: sequences may have more than one piece
   int64_t sx, sdt, sz, sb, sc;  // elements between the tokens of x, dt, z, B and C
   const void* x;
   const void* dt;
@@ -319,16 +321,13 @@ struct ScanArgs {
   const float* h0;     // [N][D][S] or null
   void* y;
   float* ht;
-  // pieces of a sequence run side by side (seg: tokens of a piece)
-  int32_t seg, slots;
-  int32_t cut;         // 1: sequences may have more than one piece
+  // pieces of a sequence run side by side
   float* entry;        // [slots][blocks][SP][CH] the state entering a piece
   float* leave;        // the adjoint entering it from behind
   float* span;         // [slots][blocks][CH] the sum of a piece's steps
   float* marks;        // [mark slots][blocks][SP][CH] the state entering every 16 tokens,
                        // where sequences are cut as far as the piece itself wrote it
   float* mspan;        // [mark slots][blocks][CH] the sum of the piece's steps up to there
-  int32_t mslots;
   // gradients
   const void* dy;
   const float* dht;

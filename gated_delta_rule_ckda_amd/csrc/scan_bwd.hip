@@ -316,7 +316,6 @@ size_t layout(ScanArgs& a, const ScanPlan& p, unsigned char* ws) {
   a.seg = p.seg;
   a.slots = p.slots;
   a.cut = p.cut;
-  a.mslots = p.mslots;
   const size_t lanes = static_cast<size_t>(p.blocks) * p.CH * 4, at = lanes * p.SP;
   size_t n = 0;
   const auto take = [&](size_t bytes) {

@@ -107,13 +107,9 @@ struct RowBits {
   uint32_t w[W];
   // off: bytes to the first channel (kOut: none); cols: channels left in the row
   __device__ __forceinline__ void load(rsrc_t r, int off, int cols, bool vec) {
+    static_assert(EP == 1 || EP == 2 || EP == 4, "channels a thread");
     if (vec) {
-      if constexpr (BYTES >= 32) {
-        ldraw<16, kStream>(r, off, w);
-        ldraw<16, kStream>(r, off == kOut ? kOut : off + 16, w + 4);
-      } else {
-        ldraw<BYTES, kStream>(r, off, w);
-      }
+      ldraw<BYTES, kStream>(r, off, w);
     } else if constexpr (ES == 4) {
 #pragma unroll
       for (int e = 0; e < EP; ++e) ldraw<4>(r, e < cols && off != kOut ? off + 4 * e : kOut, w + e);
@@ -129,13 +125,10 @@ struct RowBits {
   static __device__ __forceinline__ void store(rsrc_t r, int off, int cols, bool vec, const float* x) {
     if constexpr (ES == 4) {
       if (vec) {
-        if constexpr (EP >= 4) {
-#pragma unroll
-          for (int e = 0; e < EP; e += 4) {
-            typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-            const u4 v = {__float_as_uint(x[e]), __float_as_uint(x[e + 1]), __float_as_uint(x[e + 2]), __float_as_uint(x[e + 3])};
-            __builtin_amdgcn_raw_buffer_store_b128(v, r, off == kOut ? kOut : off + 4 * e, 0, kStream);
-          }
+        if constexpr (EP == 4) {
+          typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+          const u4 v = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+          __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, kStream);
           return;
         }
       }
@@ -152,11 +145,7 @@ struct RowBits {
         u[k] = __builtin_bit_cast(uint32_t, b);
       }
       if (vec) {
-        if constexpr (EP == 8) {
-          typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-          __builtin_amdgcn_raw_buffer_store_b128(u4{u[0], u[1], u[2], u[3]}, r, off, 0, kStream);
-          return;
-        } else if constexpr (EP == 4) {
+        if constexpr (EP == 4) {
           typedef uint32_t u2 __attribute__((ext_vector_type(2)));
           __builtin_amdgcn_raw_buffer_store_b64(u2{u[0], u[1]}, r, off, 0, kStream);
           return;

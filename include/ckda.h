@@ -512,9 +512,10 @@ ckda_status_t ckda_block_norm_bwd(int64_t rows, int32_t d, int32_t io_dtype, int
  * sequence only.
  * Supported: K from 2 to 4, D up to 2^22 and x_stride below 2^24, B * T below
  * 2^31 - 1024, T below 2^30; others return CKDA_ERR_UNSUPPORTED, as do batches for which a
- * launch would have 2^32 threads (about a token and channel in 32).  x needs only
- * its elements' alignment; 16-byte accesses are used where its base, its stride
- * and D are multiples of 16 bytes.
+ * launch would have 2^32 threads (of 4 channels and 32 tokens each, with gradients 64,
+ * and a tile at least a sequence).  x needs only its elements' alignment; 4 channels
+ * are one access (8 bytes in bf16, 16 in float32), which is aligned where its base,
+ * its stride and D are multiples of 4 elements.
  */
 typedef struct {
   int32_t B, T, D, K;
@@ -575,8 +576,9 @@ ckda_status_t ckda_conv_step(const ckda_conv_desc_t* desc, const void* x, const 
  * B * T below 2^31 - 1024, T below 2^30; others return CKDA_ERR_UNSUPPORTED, as do batches
  * for which a launch would have 2^32 threads (768 for each sequence, 128 tokens
  * of it and 32 channels).  x, dt, z, B and C need only their elements'
- * alignment; 16-byte accesses are used where the bases and strides of x, dt and
- * z, D and D / groups are multiples of 16 bytes.
+ * alignment; up to 4 channels move at once (8 bytes in bf16, 16 in float32) where
+ * the bases and strides of x, dt and z and D / groups are multiples of 4 elements,
+ * else one at a time.
  */
 typedef struct {
   int32_t B, T, D, S;
