@@ -3,10 +3,12 @@ states), with several blocks of channels, groups and sequences: forward and grad
 against the recurrence in float64 within its bounds (scan_fp64.py)."""
 import ctypes
 
+import numpy as np
 import pytest
+import torch
 
 import gated_delta_rule_ckda_amd as ck
-from tests.ssm_util import make_scan
+from tests.ssm_util import make_scan, scan_kw, scan_tensors
 from tests.test_gpu_scan import check
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +47,27 @@ def test_parts(dtype, S):
                                               (5376, 1, 1, 0, [1500, 5, 0, 997, 500], 256)])
 def test_longer_pieces(D, S, B, T, lens, cut):
     check(make_scan(1900 + S, B, T, D, S, 1, "bf16", lens=lens), cut=cut)
+
+
+@pytest.mark.parametrize("S", [5, 16, 40])
+def test_non_finite_values_stay_in_their_sequence(S):
+    """NaN, infinities and the lowest value in a few tokens of the middle sequence of three,
+    each of which is cut: the others keep their bits, forward and backwards."""
+    c = make_scan(2100 + S, 1, 0, 72, S, 1, "bf16", lens=[300, 290, 200])
+    g = scan_tensors(c)
+    kw = scan_kw(c, g)
+    run = lambda t, k: (ck.scan_fwd(t["x"], t["dt"], t["A"], t["B"], t["C"], **k),
+                        ck.scan_bwd(t["x"], t["dt"], t["A"], t["B"], t["C"], t["dy"], dht=t["dht"], **k))
+    (y, ht), r = run(g, kw)
+    other = np.r_[0:300, 590:790]
+    for m in ("x", "dt", "B", "C", "z", "dy"):
+        for value in (float("nan"), float("inf"), float("-inf"), float(torch.finfo(torch.bfloat16).min)):
+            bad = dict(g)
+            bad[m] = g[m].clone()
+            bad[m][0, 430:433] = value
+            (y2, ht2), r2 = run(bad, dict(kw, z=bad["z"]))
+            torch.cuda.synchronize()
+            assert torch.equal(y[:, other], y2[:, other]) and torch.equal(ht[[0, 2]], ht2[[0, 2]]), (m, value)
+            for i in (0, 1, 3, 4, 6):  # dx, ddt, dB, dC, dz
+                assert torch.equal(r[i][:, other], r2[i][:, other]), (m, value, i)
+            assert torch.equal(r[8][[0, 2]], r2[8][[0, 2]]), (m, value)
