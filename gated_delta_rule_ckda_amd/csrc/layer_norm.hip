@@ -17,9 +17,13 @@
 // row, EPL elements each, weights and sums over rows in registers; workgroups walk
 // over rows and load a row ahead.  Rows of odd widths move an element at a time:
 // with the row ahead that is faster in bf16 than wide accesses at odd addresses
-// (32768 rows of 2001 with a residual: 119 us against 148; 1001 float32: 105 and
-// 101).  Measured in bf16: 32768 rows of 2048 with a residual 99 us (5.4 TB/s),
-// their gradients 112 us (4.8), 524288 rows of 128 60 us (4.5).
+// (32768 rows with a residual, of 2001 in bf16: 119 us against 148; of 1001 in float32:
+// 105 and 101).  Measured, 32768 rows of 2048 with a residual: bf16 99 us (5.4
+// TB/s), gradients 112 (4.8); float32 195 (5.5), gradients 206 (5.2).  524288 rows of
+// 128 in bf16: 60 us (4.5).  Gradients past 8192 elements have 128 registers a thread
+// and keep 96 bytes a lane in scratch in float32, 208 at odd widths of either type
+// (4096 rows of 16384 with a residual: bf16 136 us, float32 251; of 16383: 361
+// and 418); odd widths from 4097 to 8192 run one wave a SIMD.
 #include "row_ops.h"
 
 namespace ckda {

@@ -20,7 +20,7 @@
 // rows are a thread's own until its last row.  8 elements a thread keep three
 // workgroups of gradients a CU (146 registers); more only where a row is too
 // long for 256 threads.  Measured in bf16: 524288 rows of 128 with a gate 72 us
-// (5.6 TB/s), gradients of 32768 rows of 2048 with all parts 213 us (5.0 TB/s;
+// (5.6 TB/s), gradients of 32768 rows of 2048 with all parts 206 us (5.2 TB/s;
 // a copy of 2 GB runs at 5.0).
 #include "row_ops.h"
 

@@ -6,9 +6,9 @@
 // costs 8.4 cycles a wave, the others 2.5 to 2.9 where two waves or more take turns
 // and about 4 where powers come between them, which is why they run in groups.  B
 // and C, the same for all channels, reach the lanes as broadcast reads, so a lane
-// holds several states.  8 x 4096 tokens of 2048
-// channels and 16 states in bf16: 365 us (1.5 TB/s; the bytes alone would take 106,
-// the instructions alone 131).
+// holds several states.  8 x 4096 tokens of 2048 channels and 16 states: bf16 364 us
+// (1.5 TB/s), float32 394 (2.7).  The bytes alone would take 106 (212) us, the
+// states' instructions 131, with the input waves' (38% of all) about 200.
 #include "scan_ops.h"
 
 namespace ckda {
@@ -403,11 +403,20 @@ ScanPlan scan_plan(const ScanArgs& a, bool grads) {
   const int64_t whole = static_cast<int64_t>(a.N) * a.G * ((per + wide - 1) / wide);
   const int64_t want = a.cu || grads ? 1024 : 512;
   // Sequences are cut where whole ones leave CUs idle, and in packed batches, whose
-  // lengths are not known here.  Measured in us on sequences of 2048 tokens, cut and
-  // whole, 16 states: forward of 128 workgroups 134 and 149, of 160 209 and 182; gradients
-  // of 256 669 and 745, of 320 885 and 1110, of 384 1130 and 1119, of 480 1341 and
-  // 1132.  32 states: forward of 64 76 and 185, of 192 197 and 190; gradients of 256
-  // 651 and 826, of 512 1221 and 1112.
+  // lengths are not known here.  Measured in us on sequences of 2048 tokens of 2048 channels
+  // in bf16, by workgroups of whole sequences, cut and whole:
+  //   forward     up to 128                            160 and more
+  //    8 states   128: 106, 169                        160: 139, 169   192: 194, 170
+  //   16          128: 133, 149                        160: 175, 182   192: 248, 184
+  //   32           64: 70, 192     128: 122, 198       192: 225, 199
+  //   64           64: 137, 284    128: 249, 287       192: 386, 289
+  //   gradients   up to 341                            352 and more
+  //    8 states   256: 494, 674    320: 648, 803       384: 759, 806
+  //   16          256: 662, 753    320: 883, 1158      384: 1103, 1116  480: 1280, 1127
+  //   32          256: 652, 841    320: 874, 1085      384: 1047, 1095  512: 1232, 1114
+  //   64          192: 1088, 1125  320: 1758, 2199     384: 1921, 2206
+  // One rule for all of them: it gives up a fifth at 160 workgroups and 8 states, and
+  // an eighth at 384 and 64 with gradients, which cuts would have gained.
   const bool few = a.T > 256 && (a.cu || whole <= (grads ? 341 : 128));
   // 8 to 16 states of whole sequences: 32 channels a workgroup use more CUs (forward
   // of 256 workgroups of 64: 186 us, 203 with 64; of 384 245 and 276), up to where

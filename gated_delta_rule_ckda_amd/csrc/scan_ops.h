@@ -46,10 +46,10 @@ __device__ __forceinline__ float decay_by(float d, float A2) { return __builtin_
 // h = own + R exp(span A): the states R that enter a part of a sequence added to the
 // part's own, whose steps sum to `span`.  For rates that grow the power may leave
 // float32 where its product with R does not: past 2^126 the exponent's whole part
-// goes to the product instead, and an R of 0 stays 0 (all lanes then take that
-// path, as few as need it; without a branch gradients of a layer took 1326 us, not
-// 1297).  Decays take the one power.  Steps of the largest finite size may sum to
-// infinity, of which a rate of 0 would make no number.
+// goes to the product instead, and an R of 0 stays 0.  Decays take the one power: a
+// wave branches where any of its lanes grows that far (both ways in every lane:
+// gradients of a layer 1326 us against 1297).  Steps of the largest finite size may
+// sum to infinity, of which a rate of 0 would make no number.
 template <int N>
 __device__ __forceinline__ void enter(float span, const float (&A2)[N], const float (&R)[N], const float (&own)[N],
                                       float (&h)[N]) {
